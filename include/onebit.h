@@ -451,6 +451,73 @@ size_t onebit_workspace_bytes(int64_t N, int32_t n, int32_t n_seg);
  * about N / 1024 bytes (0 if N < 0, N is not a multiple of 4 or n_seg < 1). */
 size_t frozen_v_workspace_bytes(int64_t N, int32_t n_seg);
 
+/*
+ * Training operators beside the optimizer
+ * ---------------------------------------
+ * The calls below compute parts of the model whose gradients the calls above
+ * compress.  Tensors carry one of the element types
+ */
+typedef enum { ONEBIT_F32 = 0, ONEBIT_BF16 = 1, ONEBIT_F16 = 2 } onebit_dtype;
+
+/*
+ * Dropout with a mask that is drawn again wherever it is needed:
+ *   u(r, c) = half word c & 7 (low half of a word first) of
+ *             Philox4x32-10(counter = (c / 8, R lo32, R hi32, step'),
+ *                           key = (seed lo32, seed hi32 xor 0x44524F50)),
+ *             R = row0 + r, step' = step + (step_dev ? *step_dev : 0) mod 2^32
+ *   T = max(1, floor((1 - p) 65536 + 1/2))
+ *   k = u(r, c) < T ? x[r][c] * (65536 / T) : +0   (whatever a dropped x held)
+ *   y = residual ? residual + k : k
+ * in binary32, rounded once to the element type.  The kept share T / 65536 is
+ * exact and the scale is its inverse (rounded once to binary32); p = 0 keeps
+ * everything.  The gradient with respect to x is the same call on the
+ * gradient, without a residual; the residual's is the gradient itself.
+ * The mask depends on (seed, step', R, c) alone: a part of the rows, given
+ * its row0, gets the whole tensor's mask on any rank.  A captured graph that
+ * passes step_dev draws new masks on each replay as the caller changes it.
+ *
+ * x, residual, y: rows of `cols` elements, ld_* elements apart (ld >= cols);
+ * aligned to their element.  y may be x or residual itself (same ld).
+ * residual may be NULL (ld_r unread), step_dev too (device, 4-byte aligned).
+ * 0 <= p < 1, row0 >= 0, rows * ceil(cols / 8) < 2^31.  No rows or columns:
+ * a no-op.
+ */
+int dropout_apply(const void* x, const void* residual, void* y, int32_t dtype, int64_t rows,
+                  int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_y, float p, uint64_t seed,
+                  uint32_t step, const uint32_t* step_dev, int64_t row0, hipStream_t stream);
+
+/*
+ * A relative position bias learned per (bucket, head), as a map over the
+ * scores of Tq queries and Tk keys:
+ *   out[h][i][j] = table[map[clamp(d, -radius, radius) + radius]][h],
+ *   d = j - (i + q_pos)             (query i stands at position i + q_pos)
+ * table [n_buckets][H] float; map [2 radius + 1] int32, device memory: the
+ * bucket of each distance (a bucket outside 0 ... n_buckets - 1 counts as no
+ * bias); out [H][Tq][Tk] of the element type, aligned to its element.
+ * 1 <= radius <= 1024, 1 <= n_buckets <= 1024, 1 <= H <= 65535, lengths up to
+ * 2^29, |q_pos| <= 2^29, Tq * ceil(Tk / 8) < 2^31.
+ */
+int rel_bias_expand(const float* table, const int32_t* map, void* out, int32_t dtype, int32_t H,
+                    int32_t n_buckets, int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos,
+                    hipStream_t stream);
+
+/*
+ * The gradient of that bias from the gradient of the scores:
+ *   dtable[b][h] = (accumulate ? dtable[b][h] : 0)
+ *                  + sum of ds[n][h][i][j] over n and every (i, j) of bucket b
+ * ds [B][H][Tq][Tk] of the element type; dtable [n_buckets][H] float.  The
+ * sums are binary32 within a workgroup and binary64 over workgroups, in an
+ * order fixed by the sizes.  Where ds is empty the sums are 0.
+ * ws: at least rel_bias_workspace_bytes(...) bytes, 256-byte aligned, scratch.
+ */
+int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtable, int32_t B,
+                  int32_t H, int32_t n_buckets, int32_t radius, int32_t Tq, int32_t Tk,
+                  int32_t q_pos, int32_t accumulate, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+/* Workspace bytes of rel_bias_grad (0 if the sizes are invalid). */
+size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t radius);
+
 /* Static description of a status code. */
 const char* onebit_strerror(int status);
 

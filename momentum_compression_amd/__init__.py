@@ -27,4 +27,8 @@ from .onebit import (  # noqa: F401
     warmup_adam_step,
     warmup_lamb_step,
     warmup_workspace_bytes,
+    dropout_apply,
+    rel_bias_expand,
+    rel_bias_grad,
+    rel_bias_workspace_bytes,
 )

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "train.h"
 
 using namespace onebit;
 
@@ -493,6 +494,114 @@ int lamb_momentum_scale(const float* m, int64_t N, const int64_t* seg_off, int32
     drop_stale_error();
     return hip_status(
         launch_momentum_scale(m, N, seg_off, n_seg, k, split_warmup_ws(ws, N, n_seg), stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- training operators
+
+namespace {
+
+constexpr int64_t kMaxPositions = (int64_t)1 << 29;  // lengths and positions: 32-bit differences
+constexpr int64_t kMaxLd = (int64_t)1 << 40;         // strides: 64-bit offsets stay in range
+
+// bytes of an element, 0 for an unknown type
+size_t type_size(int32_t dtype) {
+    return dtype == ONEBIT_F32 ? 4 : dtype == ONEBIT_BF16 || dtype == ONEBIT_F16 ? 2 : 0;
+}
+
+// rows of `cols` elements in groups of 8 columns, as the row kernels count
+// them: below 2^31
+bool row_groups_ok(int64_t rows, int64_t cols) {
+    const int64_t per_row = ceil_div(cols, 8);
+    return rows <= INT32_MAX && per_row <= INT32_MAX && rows * per_row <= INT32_MAX;
+}
+
+int check_lengths(int32_t Tq, int32_t Tk) {
+    return Tq < 0 || Tk < 0 || Tq > kMaxPositions || Tk > kMaxPositions ? ONEBIT_E_SIZE : ONEBIT_OK;
+}
+
+int check_bias_sizes(int32_t H, int32_t n_buckets, int32_t radius) {
+    if (H < 1 || H > 65535) return ONEBIT_E_SIZE;
+    if (n_buckets < 1 || n_buckets > kMaxBuckets || radius < 1 || radius > kMaxRadius)
+        return ONEBIT_E_SIZE;
+    return ONEBIT_OK;
+}
+
+bool position_ok(int32_t q_pos) { return q_pos >= -kMaxPositions && q_pos <= kMaxPositions; }
+
+// distances' sums of every part of every head
+size_t bias_grad_ws_bytes(int64_t parts, int32_t H, int32_t radius) {
+    return round_up((size_t)parts * H * (2 * (size_t)radius + 1) * sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
+int dropout_apply(const void* x, const void* residual, void* y, int32_t dtype, int64_t rows,
+                  int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_y, float p, uint64_t seed,
+                  uint32_t step, const uint32_t* step_dev, int64_t row0, hipStream_t stream) {
+    const size_t size = type_size(dtype);
+    if (!size) return ONEBIT_E_ARG;
+    if (rows < 0 || cols < 0 || row0 < 0) return ONEBIT_E_SIZE;
+    if (!(p >= 0.0f && p < 1.0f)) return ONEBIT_E_ARG;
+    if (rows == 0 || cols == 0) return ONEBIT_OK;
+    if (!x || !y) return ONEBIT_E_NULL;
+    if (!row_groups_ok(rows, cols)) return ONEBIT_E_SIZE;
+    if (ld_x < cols || ld_y < cols || (residual && ld_r < cols) || ld_x > kMaxLd || ld_y > kMaxLd ||
+        (residual && ld_r > kMaxLd))
+        return ONEBIT_E_SIZE;
+    if (!aligned(x, size) || !aligned(y, size) || !aligned(residual, size) || !aligned(step_dev, 4))
+        return ONEBIT_E_ALIGN;
+    drop_stale_error();
+    return hip_status(launch_dropout(x, residual, y, dtype, rows, cols, ld_x, ld_r, ld_y, row0, p,
+                                     seed, step, step_dev, stream));
+}
+
+int rel_bias_expand(const float* table, const int32_t* map, void* out, int32_t dtype, int32_t H,
+                    int32_t n_buckets, int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos,
+                    hipStream_t stream) {
+    const size_t size = type_size(dtype);
+    if (!size || !position_ok(q_pos)) return ONEBIT_E_ARG;
+    int st = check_lengths(Tq, Tk);
+    if (st || (st = check_bias_sizes(H, n_buckets, radius))) return st;
+    if (Tq == 0 || Tk == 0) return ONEBIT_OK;
+    if (!table || !map || !out) return ONEBIT_E_NULL;
+    if (!row_groups_ok(Tq, Tk)) return ONEBIT_E_SIZE;
+    if (!aligned(table, 4) || !aligned(map, 4) || !aligned(out, size)) return ONEBIT_E_ALIGN;
+    drop_stale_error();
+    return hip_status(launch_rel_bias(RelBias{table, map, n_buckets, radius, H}, out, dtype, Tq, Tk,
+                                      q_pos, stream));
+}
+
+size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t radius) {
+    if (B < 0 || check_lengths(Tq, Tk) || check_bias_sizes(H, 1, radius)) return 0;
+    if (B == 0 || Tq == 0 || Tk == 0) return 256;
+    return bias_grad_ws_bytes(bias_grad_plan(B, H, Tq, Tk).parts(), H, radius);
+}
+
+int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtable, int32_t B,
+                  int32_t H, int32_t n_buckets, int32_t radius, int32_t Tq, int32_t Tk,
+                  int32_t q_pos, int32_t accumulate, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+    const size_t size = type_size(dtype);
+    if (!size || !position_ok(q_pos) || (accumulate != 0 && accumulate != 1)) return ONEBIT_E_ARG;
+    int st = B < 0 ? ONEBIT_E_SIZE : check_lengths(Tq, Tk);
+    if (st || (st = check_bias_sizes(H, n_buckets, radius))) return st;
+    const bool empty = B == 0 || Tq == 0 || Tk == 0;
+    if (!map || !dtable || (!ds && !empty)) return ONEBIT_E_NULL;
+    if (!aligned(ds, size) || !aligned(map, 4) || !aligned(dtable, 4)) return ONEBIT_E_ALIGN;
+    if (!empty && !groups_ok(bias_grad_plan(B, H, Tq, Tk).parts())) return ONEBIT_E_SIZE;
+    if (!ws || ws_bytes < rel_bias_workspace_bytes(B, H, Tq, Tk, radius)) return ONEBIT_E_WORKSPACE;
+    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    drop_stale_error();
+    if (empty)  // sums over nothing
+        return hip_status(launch_bias_join(static_cast<float*>(ws), map, dtable, H, 0, n_buckets,
+                                           radius, accumulate != 0, stream));
+    return hip_status(launch_rel_bias_grad(ds, dtype, map, dtable, B, H, n_buckets, radius, Tq, Tk,
+                                           q_pos, accumulate != 0, static_cast<float*>(ws),
+                                           stream));
 }
 
 }  // extern "C"

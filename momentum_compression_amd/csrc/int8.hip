@@ -8,39 +8,12 @@
 // quantisation block of B elements spans B/4 lanes; its max |g'| is a
 // butterfly over those lanes (B <= 256) or, for B = 512 / 1024, combined
 // across waves through LDS.
-//
-// Philox4x32-10 is the SC'11 construction: per round two 32x32->64
-// multiplies of counter words 0 and 2, xor of the high halves with the other
-// words and the round key; key bumped by the two Weyl constants.
 #include "common.h"
+#include "philox.h"
 
 namespace onebit {
 
 namespace {
-
-__device__ __forceinline__ void philox_round(uint32_t& c0, uint32_t& c1, uint32_t& c2,
-                                             uint32_t& c3, uint32_t k0, uint32_t k1) {
-    const uint64_t p0 = (uint64_t)0xD2511F53u * c0;
-    const uint64_t p1 = (uint64_t)0xCD9E8D57u * c2;
-    const uint32_t n0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-    const uint32_t n1 = (uint32_t)p1;
-    const uint32_t n2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-    const uint32_t n3 = (uint32_t)p0;
-    c0 = n0;
-    c1 = n1;
-    c2 = n2;
-    c3 = n3;
-}
-
-__device__ __forceinline__ void philox10(uint32_t& c0, uint32_t& c1, uint32_t& c2, uint32_t& c3,
-                                         uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        philox_round(c0, c1, c2, c3, k0, k1);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-}
 
 template <int B>
 __device__ __forceinline__ float group_max(float v, float* lds) {

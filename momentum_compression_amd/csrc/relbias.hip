@@ -1,0 +1,289 @@
+// A relative position bias learned per (bucket, head), written out as a map,
+// and its gradient.
+//
+//   out[h][i][j]    = table[map[clamp(d, -R, R) + R]][h],  d = j - (i + q_pos)
+//   dtable[b][h] (+)= sum of ds[.][h][i][j] over every (i, j) of bucket b
+//
+// The map from distances to buckets is whole numbers made once by the caller,
+// so no logarithm decides a bucket on the device.  A map entry outside the
+// table counts as no bias.
+#include "train.h"
+
+namespace onebit {
+
+namespace {
+
+__device__ __forceinline__ float bias_value(const RelBias& b, int x, int h) {
+    const int m = b.map[x];
+    return (uint32_t)m < (uint32_t)b.n_buckets ? b.table[(int64_t)m * b.H + h] : 0.0f;
+}
+
+// LDS slot of a distance: one word of padding after eight, so that lanes that
+// are eight distances apart read different banks.
+__device__ __forceinline__ int slot(int x) { return x + (x >> 3); }
+
+constexpr int kExpandGroups = 4;  // groups of 8 columns per lane
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rel_bias_kernel(RelBias b, T* __restrict__ out,
+                                                           uint32_t groups, FastDiv per_row,
+                                                           int32_t Tq, int32_t Tk, int32_t q_pos) {
+    __shared__ float vals[2 * kMaxRadius + 1 + (2 * kMaxRadius + 1) / 8 + 1];
+    const int h = blockIdx.y, R = b.radius;
+    for (int x = threadIdx.x; x <= 2 * R; x += kThreads) vals[slot(x)] = bias_value(b, x, h);
+    __syncthreads();
+    T* head = out + (int64_t)h * Tq * Tk;
+#pragma unroll
+    for (int u = 0; u < kExpandGroups; ++u) {
+        const uint32_t g = (blockIdx.x * kExpandGroups + u) * (uint32_t)kThreads + threadIdx.x;
+        if (g >= groups) break;
+        const uint32_t i = per_row.div(g);
+        const int32_t c = 8 * (int32_t)(g - i * per_row.d);
+        const int32_t d = c - (int32_t)i - q_pos;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int32_t x = d + e < -R ? -R : (d + e > R ? R : d + e);
+            v[e] = vals[slot(x + R)];
+        }
+        T* p = head + (int64_t)i * Tk + c;
+        if (c + 8 <= Tk) {
+            store8(p, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + e < Tk) p[e] = (T)v[e];
+        }
+    }
+}
+
+// Gradient.  One pass over ds.  A wave holds 8 rows of 8 * W columns: a lane
+// has 8 columns of each row, whose 64 values fall on 15 diagonals, so it keeps
+// 15 sums in registers over all its sequences.  Neighbouring lanes' diagonals
+// overlap and are joined by one shuffle each; what is left are 8 distances a
+// lane, added to the wave's own bins in LDS without atomics (no two lanes own
+// the same distance), so the result does not depend on timing.  Narrow maps
+// give the other 64 / W parts of the wave other sequences.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void bias_grad_kernel(const T* __restrict__ ds,
+                                                            float* __restrict__ partials,
+                                                            BiasGradPlan plan, int32_t B, int32_t H,
+                                                            int32_t radius, int32_t Tq, int32_t Tk,
+                                                            int32_t q_pos) {
+    extern __shared__ float lds[];  // [4][2 radius + 1]
+    const int R = radius, bins_n = 2 * R + 1;
+    const int wave = threadIdx.x >> 6, lane = lane_id();
+    const int col = lane % W, sub = lane / W;
+    constexpr int subs = 64 / W;
+    float* bins = lds + wave * bins_n;
+    for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
+    const int h = blockIdx.y;
+    int64_t part = blockIdx.x;
+    const int bb = (int)(part % plan.batch_blocks);
+    part /= plan.batch_blocks;
+    const int cb = (int)(part % plan.col_blocks);
+    const int rb = (int)(part / plan.col_blocks);
+    const int32_t c0 = cb * (8 * W) + 8 * col;
+    const int32_t b1 = (bb + 1) * plan.batches < B ? (bb + 1) * plan.batches : B;
+    const bool whole = c0 + 8 <= Tk;
+    float far_lo = 0.0f, far_hi = 0.0f;
+    for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows; i0 += 32) {
+        float acc[15];
+#pragma unroll
+        for (int k = 0; k < 15; ++k) acc[k] = 0.0f;
+        for (int32_t b = bb * plan.batches + sub; b < b1; b += subs) {
+            const T* p = ds + (((int64_t)b * H + h) * Tq + i0) * (int64_t)Tk + c0;
+            Vec8<T> v[8];
+            if (whole && i0 + 8 <= Tq) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] = load8(p + (int64_t)r * Tk);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    v[r] = Vec8<T>{};
+                    if (i0 + r >= Tq) continue;
+                    v[r] = whole ? load8(p + (int64_t)r * Tk)
+                                 : load_tail(p + (int64_t)r * Tk, Tk - c0);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e - r + 7] += (float)v[r].v[e];
+        }
+#pragma unroll
+        for (int off = W; off < 64; off <<= 1)
+#pragma unroll
+            for (int k = 0; k < 15; ++k) acc[k] += __shfl_xor(acc[k], off, 64);
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {
+            const float next = __shfl_down(acc[k], 1, 64);
+            if (col + 1 < W) acc[k + 8] += next;
+        }
+        // acc[k] is the sum of distance d0 + k
+        const int32_t d0 = c0 - i0 - q_pos - 7;
+        if (sub == 0) {
+#pragma unroll
+            for (int k = 0; k < 15; ++k) {
+                if (k < 7 && col != 0) continue;
+                const int32_t d = d0 + k;
+                if (d <= -R) far_lo += acc[k];
+                else if (d >= R) far_hi += acc[k];
+                else bins[d + R] += acc[k];
+            }
+        }
+        // the next rows' distances lie with other lanes
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    for (int off = 32; off > 0; off >>= 1) {
+        far_lo += __shfl_xor(far_lo, off, 64);
+        far_hi += __shfl_xor(far_hi, off, 64);
+    }
+    if (lane == 0) {
+        bins[0] += far_lo;
+        bins[2 * R] += far_hi;
+    }
+    __syncthreads();
+    float* to = partials + ((int64_t)h * gridDim.x + blockIdx.x) * bins_n;
+    for (int x = threadIdx.x; x < bins_n; x += kThreads)
+        to[x] = (lds[x] + lds[bins_n + x]) + (lds[2 * bins_n + x] + lds[3 * bins_n + x]);
+}
+
+constexpr int kJoinThreads = 1024;
+
+// One workgroup per head: each distance's sum over the parts in binary64 (as
+// many threads a distance as the workgroup has room for), then each bucket's
+// over its distances, in the order of the distances.
+__global__ __launch_bounds__(kJoinThreads) void bias_join_kernel(const float* __restrict__ partials,
+                                                                const int32_t* __restrict__ map,
+                                                                float* __restrict__ dtable,
+                                                                int32_t H, int64_t parts,
+                                                                int32_t n_buckets, int32_t radius,
+                                                                int32_t accumulate) {
+    __shared__ double sums[2 * kMaxRadius + 1];
+    __shared__ int32_t where[2 * kMaxRadius + 1];
+    const int h = blockIdx.x, n = 2 * radius + 1;
+    const float* from = partials + (int64_t)h * parts * n;
+    const int slices = n <= kJoinThreads ? kJoinThreads / n : 1;
+    for (int t = threadIdx.x; t < n * slices; t += kJoinThreads) {
+        const int x = t % n, s = t / n;
+        double v = 0.0;
+#pragma unroll 8
+        for (int64_t q = s; q < parts; q += slices) v += (double)from[q * n + x];
+        sums[t] = v;  // n * slices <= max(n, kJoinThreads) <= the array
+    }
+    for (int x = threadIdx.x; x < n; x += kJoinThreads) where[x] = map[x];
+    __syncthreads();
+    for (int x = threadIdx.x; x < n; x += kJoinThreads) {
+        double v = sums[x];
+        for (int s = 1; s < slices; ++s) v += sums[s * n + x];
+        sums[x] = v;  // read and written by this thread alone
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < n_buckets; b += kJoinThreads) {
+        double v = 0.0;
+        for (int x = 0; x < n; ++x)
+            if (where[x] == b) v += sums[x];
+        float* to = dtable + (int64_t)b * H + h;
+        *to = accumulate ? (float)((double)*to + v) : (float)v;
+    }
+}
+
+template <typename T, int W>
+void grad_w(const void* ds, float* partials, const BiasGradPlan& plan, int32_t B, int32_t H,
+            int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos, hipStream_t st) {
+    const dim3 grid((unsigned)plan.parts(), (unsigned)H);
+    const size_t lds = 4 * (2 * (size_t)radius + 1) * sizeof(float);
+    hipLaunchKernelGGL((bias_grad_kernel<T, W>), grid, dim3(kThreads), lds, st, (const T*)ds,
+                       partials, plan, B, H, radius, Tq, Tk, q_pos);
+}
+
+// Lanes that span the columns of a row: the smallest power of two that does.
+int32_t grad_lanes(int32_t Tk) {
+    int32_t w = 8;
+    while (w < 64 && 8 * w < Tk) w *= 2;
+    return w;
+}
+
+template <typename T>
+void grad_t(const void* ds, float* partials, const BiasGradPlan& plan, int32_t B, int32_t H,
+            int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos, hipStream_t st) {
+    switch (grad_lanes(Tk)) {
+        case 8: return grad_w<T, 8>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
+        case 16: return grad_w<T, 16>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
+        case 32: return grad_w<T, 32>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
+        default: return grad_w<T, 64>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t Tq, int32_t Tk,
+                           int32_t q_pos, hipStream_t st) {
+    const uint32_t per_row = ((uint32_t)Tk + 7) / 8;
+    const uint32_t groups = per_row * (uint32_t)Tq;
+    const uint32_t span = kThreads * kExpandGroups;
+    const dim3 grid((groups + span - 1) / span, (unsigned)b.H);
+    const FastDiv div(per_row);
+    switch (dtype) {
+        case ONEBIT_F32:
+            hipLaunchKernelGGL((rel_bias_kernel<float>), grid, dim3(kThreads), 0, st, b,
+                               (float*)out, groups, div, Tq, Tk, q_pos);
+            break;
+        case ONEBIT_BF16:
+            hipLaunchKernelGGL((rel_bias_kernel<bf16>), grid, dim3(kThreads), 0, st, b,
+                               (bf16*)out, groups, div, Tq, Tk, q_pos);
+            break;
+        case ONEBIT_F16:
+            hipLaunchKernelGGL((rel_bias_kernel<f16>), grid, dim3(kThreads), 0, st, b, (f16*)out,
+                               groups, div, Tq, Tk, q_pos);
+            break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+// Few, large parts once there are workgroups enough to fill the card.
+BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
+    constexpr int64_t kWant = 2048;
+    BiasGradPlan p;
+    const int32_t lanes = grad_lanes(Tk);
+    p.col_blocks = (Tk + 8 * lanes - 1) / (8 * lanes);
+    p.rows = 32;
+    const auto blocks = [&] { return (int64_t)((Tq + p.rows - 1) / p.rows) * p.col_blocks * H; };
+    while (blocks() > 2 * kWant && p.rows < 1024) p.rows *= 2;
+    p.row_blocks = (Tq + p.rows - 1) / p.rows;
+    int64_t split = (kWant + blocks() - 1) / blocks();
+    if (split > B) split = B;
+    p.batches = (int32_t)((B + split - 1) / split);
+    p.batch_blocks = (B + p.batches - 1) / p.batches;
+    return p;
+}
+
+hipError_t launch_bias_join(const float* partials, const int32_t* map, float* dtable, int32_t H,
+                            int64_t parts, int32_t n_buckets, int32_t radius, bool accumulate,
+                            hipStream_t st) {
+    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)H), dim3(kJoinThreads), 0, st, partials,
+                       map, dtable, H, parts, n_buckets, radius, accumulate ? 1 : 0);
+    return hipGetLastError();
+}
+
+hipError_t launch_rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtable,
+                                int32_t B, int32_t H, int32_t n_buckets, int32_t radius,
+                                int32_t Tq, int32_t Tk, int32_t q_pos, bool accumulate,
+                                float* partials, hipStream_t st) {
+    const BiasGradPlan plan = bias_grad_plan(B, H, Tq, Tk);
+    switch (dtype) {
+        case ONEBIT_F32: grad_t<float>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st); break;
+        case ONEBIT_BF16: grad_t<bf16>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st); break;
+        case ONEBIT_F16: grad_t<f16>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st); break;
+        default: return hipErrorInvalidValue;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_bias_join(partials, map, dtable, H, plan.parts(), n_buckets, radius, accumulate,
+                            st);
+}
+
+}  // namespace onebit

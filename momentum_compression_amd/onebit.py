@@ -28,6 +28,9 @@ ONEBIT_E_ARG = -5
 ONEBIT_E_HIP = -6
 ONEBIT_UNIT_SCALE = 1
 ONEBIT_KEEP_PREV = 2
+ONEBIT_F32 = 0
+ONEBIT_BF16 = 1
+ONEBIT_F16 = 2
 
 _c_i32, _c_i64, _c_u32, _c_u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 _c_f, _c_p, _c_sz = ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -79,6 +82,13 @@ _SIGNATURES = {
                                   _c_f, _c_f, _c_i32, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "lamb_momentum_scale": (_c_i32, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_sz, _c_p]),
     "warmup_workspace_bytes": (_c_sz, [_c_i64, _c_i32]),
+    "dropout_apply": (_c_i32, [_c_p, _c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                               _c_f, _c_u64, _c_u32, _c_p, _c_i64, _c_p]),
+    "rel_bias_expand": (_c_i32, [_c_p, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                 _c_i32, _c_p]),
+    "rel_bias_grad": (_c_i32, [_c_p, _c_i32, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                               _c_i32, _c_i32, _c_i32, _c_p, _c_sz, _c_p]),
+    "rel_bias_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
     "onebit_strerror": (ctypes.c_char_p, [_c_i32]),
 }
 
@@ -144,7 +154,12 @@ def _on_gpu(t) -> bool:
 
 # element kinds of the C ABI's buffers and the tensor dtypes that carry them
 _KINDS = {"f32": ("float32",), "u32": ("int32", "uint32"), "i64": ("int64",),
-          "i8": ("int8",), "u8": ("uint8",)}
+          "i8": ("int8",), "u8": ("uint8",), "i32": ("int32",),
+          "bf16": ("bfloat16",), "f16": ("float16",)}
+
+# element types of the training operators
+_DTYPES = {"float32": ("f32", ONEBIT_F32), "bfloat16": ("bf16", ONEBIT_BF16),
+           "float16": ("f16", ONEBIT_F16)}
 
 
 def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
@@ -356,3 +371,94 @@ def lamb_momentum_scale(m, N: int, seg_off, n_seg: int, k, ws, stream=None) -> N
     _check("lamb_momentum_scale", load().lamb_momentum_scale(
         _buf(m, N, "f32", "m"), N, _buf(seg_off, n_seg + 1, "i64", "seg_off"), n_seg,
         _buf(k, n_seg, "f32", "k"), _buf(ws, 0, "u8", "ws"), _nbytes(ws), _stream(stream)))
+
+
+# ---------------------------------------------------------------- training operators
+
+
+def _dtype(t, name: str):
+    """(element kind, C ABI type) of a training operator's tensor."""
+    found = _DTYPES.get(str(t.dtype).replace("torch.", ""))
+    if found is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    return found
+
+
+def _rows(x, rows: int, cols: int, kind: str, name: str):
+    """(device pointer, elements between rows) of a matrix argument: a
+    contiguous buffer of at least rows * cols elements, or a 2-D view of that
+    shape whose rows are contiguous."""
+    if x is None:
+        return None, cols
+    if x.is_contiguous() or x.dim() != 2 or rows <= 1:
+        return _buf(x, rows * cols, kind, name), cols
+    if tuple(x.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {(rows, cols)}")
+    if x.stride(1) != 1 or x.stride(0) < cols:
+        raise ValueError(f"{name} must have contiguous, disjoint rows")
+    if not _on_gpu(x):
+        raise ValueError(f"{name} must be a device tensor (got {x.device})")
+    if str(x.dtype).replace("torch.", "") not in _KINDS[kind]:
+        raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
+    return x.data_ptr(), x.stride(0)
+
+
+def dropout_apply(x, y, rows: int, cols: int, p: float, seed: int, step: int, residual=None,
+                  row0: int = 0, step_dev=None, stream=None) -> None:
+    """y = [residual +] dropout(x); on the gradient, its backward pass."""
+    kind, code = _dtype(x, "x")
+    xp, ld_x = _rows(x, rows, cols, kind, "x")
+    rp, ld_r = _rows(residual, rows, cols, kind, "residual")
+    yp, ld_y = _rows(y, rows, cols, kind, "y")
+    _check("dropout_apply", load().dropout_apply(
+        xp, rp, yp, code, rows, cols, ld_x, ld_r, ld_y, p, seed & 0xFFFFFFFFFFFFFFFF,
+        step & 0xFFFFFFFF, _buf(step_dev, 1, "u32", "step_dev"), row0, _stream(stream)))
+
+
+def _shape(t, dims: int, name: str):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions (got {t.dim()})")
+    return tuple(t.shape)
+
+
+def _radius(bucket_map) -> int:
+    """Largest distance of a bucket map of 2 radius + 1 entries."""
+    if bucket_map.dim() != 1 or bucket_map.numel() % 2 == 0:
+        raise ValueError("bucket_map must hold 2 * radius + 1 buckets")
+    return bucket_map.numel() // 2
+
+
+def rel_bias_expand(table, bucket_map, out, q_pos: int = 0, stream=None) -> None:
+    """out [H, Tq, Tk] from table [n_buckets, H]."""
+    n_buckets, H = _shape(table, 2, "table")
+    h, Tq, Tk = _shape(out, 3, "out")
+    if h != H:
+        raise ValueError(f"out has {h} heads, table has {H}")
+    kind, code = _dtype(out, "out")
+    radius = _radius(bucket_map)
+    _check("rel_bias_expand", load().rel_bias_expand(
+        _buf(table, n_buckets * H, "f32", "table"), _buf(bucket_map, 2 * radius + 1, "i32",
+                                                         "bucket_map"),
+        _buf(out, H * Tq * Tk, kind, "out"), code, H, n_buckets, radius, Tq, Tk, q_pos,
+        _stream(stream)))
+
+
+def rel_bias_workspace_bytes(B: int, H: int, Tq: int, Tk: int, radius: int) -> int:
+    return int(load().rel_bias_workspace_bytes(B, H, Tq, Tk, radius))
+
+
+def rel_bias_grad(ds, bucket_map, dtable, q_pos: int = 0, accumulate: bool = False, ws=None,
+                  stream=None) -> None:
+    """dtable [n_buckets, H] from the scores' gradient ds [B, H, Tq, Tk]."""
+    n_buckets, H = _shape(dtable, 2, "dtable")
+    B, h, Tq, Tk = _shape(ds, 4, "ds")
+    if h != H:
+        raise ValueError(f"ds has {h} heads, dtable has {H}")
+    kind, code = _dtype(ds, "ds")
+    radius = _radius(bucket_map)
+    _check("rel_bias_grad", load().rel_bias_grad(
+        _buf(ds, B * H * Tq * Tk, kind, "ds"), code, _buf(bucket_map, 2 * radius + 1, "i32",
+                                                          "bucket_map"),
+        _buf(dtable, n_buckets * H, "f32", "dtable"), B, H, n_buckets, radius, Tq, Tk, q_pos,
+        int(bool(accumulate)), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        _stream(stream)))
