@@ -6,7 +6,8 @@
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument is a DEVICE pointer owned by the caller, except
- *   the argument struct of frozen_v_step (host memory, read during the call).
+ *   the argument structs of frozen_v_step and rel_attention_* (host memory,
+ *   read during the call).
  *   The library never allocates, frees or synchronises; it validates
  *   arguments on the host (before any HIP call) and enqueues kernels on
  *   `stream` only.  Results are ready when the stream reaches them.
@@ -517,6 +518,85 @@ int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtab
 
 /* Workspace bytes of rel_bias_grad (0 if the sizes are invalid). */
 size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t radius);
+
+/*
+ * Attention whose scores carry the relative position bias and whose weights
+ * carry the dropout, forward and backward, scores never stored:
+ *   pos_b = q_pos_of ? q_pos_of[b] : q_pos    (query i stands at i + pos_b)
+ *   s_ij  = scale (q_i . k_j) + table[map[clamp(j - i - pos_b, +-radius)
+ *           + radius]][h], over the keys that query i sees: j < k_len[b]
+ *           (all Tk without k_len) and, if causal, j <= i + pos_b
+ *   P     = softmax over the seen keys;  lse_i = log sum_j exp s_ij
+ *   keep_ij = 65536 / T or 0, the draw of dropout_apply for row
+ *           (b H + h) Tq + i and column j
+ *   o_i   = sum_j P_ij keep_ij v_j
+ * A query that sees no key has o = 0, lse = -inf and no gradient.  Query head
+ * h reads key head h / (H / Hkv).
+ *
+ * backward, from the forward's o and lse and the same other arguments:
+ *   dP_ij = keep_ij (do_i . v_j),  dS_ij = P_ij (dP_ij - sum_j P_ij dP_ij)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,
+ *   dv_j = sum_i P_ij keep_ij do_i (over the heads that share a key head),
+ *   dtable[b][h] = (accumulate ? dtable[b][h] : 0) + sum of dS over bucket b
+ * Every element of dq, dk and dv is written; without dtable the bias has no
+ * gradient computed.
+ *
+ * Element type BF16 or F16; products of elements are summed in binary32, and
+ * P and dS are rounded to the element type for the products they enter.
+ * dtable is summed in binary32 and binary64 from unrounded dS.  Sums run in
+ * an order fixed by the sizes: the same call gives the same bits.
+ * Keys and values from k_len[b] on are not read (dk and dv are 0 there); the
+ * values of keys that only the causal mask hides are multiplied by 0 and have
+ * to be finite.  k_len and q_pos_of are clamped to 0 ... Tk and +-2^29.
+ *
+ * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
+ * heads.  *_stride: elements between sequences, tokens and heads, multiples
+ * of 8; D a multiple of 8, 8 ... 128, its elements side by side; 16-byte
+ * aligned.  So a fused projection's output and a cache of either order serve
+ * as they are.  Sequences of a batch may share keys (stride 0); outputs must
+ * not overlap each other or themselves.  lse [B][H][Tq] float, optional in
+ * the forward pass.  table [n_buckets][H] float and map as rel_bias_expand,
+ * or NULL, NULL, 0, 0 without a bias.  0 <= p < 1.
+ * ws: at least rel_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ * scratch between calls (a forward call whose need is 256 takes NULL too).
+ */
+typedef struct rel_attention_args {
+    int32_t dtype;
+    int32_t B, H, Hkv, Tq, Tk, D;
+    int32_t causal;
+    int32_t q_pos;
+    int32_t n_buckets, radius;
+    float scale;
+    float p;
+    uint32_t step;
+    uint64_t seed;
+    const uint32_t* step_dev;  /* or NULL                                   */
+    const int32_t* q_pos_of;   /* [B] or NULL                               */
+    const int32_t* k_len;      /* [B] or NULL                               */
+    const float* table;
+    const int32_t* map;
+    const void *q, *k, *v;
+    void* o;                   /* out; read by the backward pass            */
+    float* lse;                /* out, or NULL; read by the backward pass   */
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    const void* d_o;           /* from here on: backward pass only          */
+    void *dq, *dk, *dv;
+    int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+    float* dtable;             /* or NULL                                   */
+    int32_t accumulate;
+} rel_attention_args;
+
+int rel_attention_forward(const rel_attention_args* a, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+
+int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* Workspace bytes of rel_attention_forward (backward 0) or of both calls one
+ * after the other (backward 1); radius 0 without a bias or its gradient.  0 if
+ * the sizes are invalid. */
+size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk,
+                                     int32_t D, int32_t radius, int32_t backward);
 
 /* Static description of a status code. */
 const char* onebit_strerror(int status);

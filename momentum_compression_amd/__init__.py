@@ -31,4 +31,7 @@ from .onebit import (  # noqa: F401
     rel_bias_expand,
     rel_bias_grad,
     rel_bias_workspace_bytes,
+    rel_attention_backward,
+    rel_attention_forward,
+    rel_attention_workspace_bytes,
 )

@@ -23,7 +23,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libonebit.so")
 
 SOURCES = ["api.hip", "compress.hip", "finalize.hip", "server.hip", "scale.hip", "step.hip",
-           "int8.hip", "warmup.hip", "dropout.hip", "relbias.hip"]
+           "int8.hip", "warmup.hip", "dropout.hip", "relbias.hip",
+           "attn_fwd.hip", "attn_bwd.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "attention.h"
 #include "common.h"
 #include "train.h"
 
@@ -602,6 +603,188 @@ int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtab
     return hip_status(launch_rel_bias_grad(ds, dtype, map, dtable, B, H, n_buckets, radius, Tq, Tk,
                                            q_pos, accumulate != 0, static_cast<float*>(ws),
                                            stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Strides of a tensor of T tokens of heads * D elements per sequence.  What is
+// written must not overlap itself.
+int check_heads(const void* p, const int64_t s[3], int32_t B, int32_t T, int32_t heads, int32_t D,
+                bool written) {
+    if (B == 0 || T == 0) return ONEBIT_OK;
+    if (!p) return ONEBIT_E_NULL;
+    const int64_t count[3] = {B, T, heads};
+    for (int k = 0; k < 3; ++k) {
+        if (s[k] < 0 || s[k] > kMaxLd || s[k] % 8) return ONEBIT_E_SIZE;
+        if (written && count[k] > 1 && s[k] < D) return ONEBIT_E_SIZE;
+    }
+    return aligned(p, 16) ? ONEBIT_OK : ONEBIT_E_ALIGN;
+}
+
+Strides strides_of(const int64_t s[3]) { return Strides{s[0], s[1], s[2]}; }
+
+int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk, int32_t D,
+                          int32_t radius) {
+    const int st = check_lengths(Tq, Tk);
+    if (st) return st;
+    if (B < 0 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv) return ONEBIT_E_SIZE;
+    if (D < 8 || D > 128 || D % 8 || radius < 0 || radius > kMaxRadius) return ONEBIT_E_SIZE;
+    const int64_t heads = (int64_t)B * H;  // below 2^47
+    // rows of a launch, and the workgroups of a split or unsplit grid
+    if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16) return ONEBIT_E_SIZE;
+    if (!groups_ok(heads * attn_tiles(Tq) * attn_splits(B, H, Tq, Tk) + 8) ||
+        !groups_ok(heads * attn_tiles(Tk) + 8) || !groups_ok(ceil_div(heads * Tq, 4)))
+        return ONEBIT_E_SIZE;
+    return ONEBIT_OK;
+}
+
+// Workspace of the two directions, in the order it is carved.
+struct AttnSizes {
+    size_t split_o, split_ml;              // forward
+    size_t delta, exact, far, partials;    // backward
+};
+
+AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t D, int32_t radius) {
+    AttnSizes z = {};
+    const size_t rows = (size_t)B * H * Tq;
+    const int32_t splits = attn_splits(B, H, Tq, Tk);
+    if (splits > 1) {
+        z.split_o = round_up(rows * splits * D * sizeof(float));
+        z.split_ml = round_up(rows * splits * sizeof(float2));
+    }
+    z.delta = round_up(rows * sizeof(float));
+    if (radius > 0) {
+        const size_t parts = (size_t)B * attn_tiles(Tq) * H;
+        z.exact = round_up(rows * sizeof(float));
+        z.far = round_up(parts * sizeof(float2));
+        z.partials = round_up(parts * (2 * (size_t)radius + 1) * sizeof(float));
+    }
+    return z;
+}
+
+int check_attention(const rel_attention_args* a) {
+    if (!a) return ONEBIT_E_NULL;
+    if (a->dtype != ONEBIT_BF16 && a->dtype != ONEBIT_F16) return ONEBIT_E_ARG;
+    const bool bias = a->radius != 0 || a->n_buckets != 0 || a->table || a->map;
+    int st = check_attention_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->radius);
+    if (st) return st;
+    if (bias) {
+        if (!a->table || !a->map) return ONEBIT_E_NULL;
+        if ((st = check_bias_sizes(a->H, a->n_buckets, a->radius))) return st;
+    }
+    if (!(a->p >= 0.0f && a->p < 1.0f) || !isfinite(a->scale) || !position_ok(a->q_pos) ||
+        (a->causal != 0 && a->causal != 1))
+        return ONEBIT_E_ARG;
+    if (!aligned(a->table, 4) || !aligned(a->map, 4) || !aligned(a->q_pos_of, 4) ||
+        !aligned(a->k_len, 4) || !aligned(a->step_dev, 4) || !aligned(a->lse, 4))
+        return ONEBIT_E_ALIGN;
+    if ((st = check_heads(a->q, a->q_stride, a->B, a->Tq, a->H, a->D, false)) ||
+        (st = check_heads(a->k, a->k_stride, a->B, a->Tk, a->Hkv, a->D, false)) ||
+        (st = check_heads(a->v, a->v_stride, a->B, a->Tk, a->Hkv, a->D, false)))
+        return st;
+    return check_heads(a->o, a->o_stride, a->B, a->Tq, a->H, a->D, true);
+}
+
+AttnArgs attn_args(const rel_attention_args* a) {
+    AttnArgs k = {};
+    k.q = a->q;
+    k.k = a->k;
+    k.v = a->v;
+    k.o = a->o;
+    k.o_in = a->o;
+    k.sq = strides_of(a->q_stride);
+    k.sk = strides_of(a->k_stride);
+    k.sv = strides_of(a->v_stride);
+    k.so = strides_of(a->o_stride);
+    k.lse = a->lse;
+    k.q_pos_dev = a->q_pos_of;
+    k.k_len = a->k_len;
+    k.bias = RelBias{a->table, a->map, a->n_buckets, a->radius, a->H};
+    k.drop = drop_args(a->p, a->seed, a->step, a->step_dev);
+    k.B = a->B;
+    k.H = a->H;
+    k.Hkv = a->Hkv;
+    k.Tq = a->Tq;
+    k.Tk = a->Tk;
+    k.D = a->D;
+    k.q_pos = a->q_pos;
+    k.causal = a->causal;
+    k.splits = 1;
+    k.scale = a->scale;
+    return k;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk,
+                                     int32_t D, int32_t radius, int32_t backward) {
+    if (check_attention_sizes(B, H, Hkv, Tq, Tk, D, radius)) return 0;
+    const AttnSizes z = attn_sizes(B, H, Tq, Tk, D, radius);
+    const size_t fwd = z.split_o + z.split_ml;
+    const size_t bwd = z.delta + z.exact + z.far + z.partials;
+    const size_t need = backward && bwd > fwd ? bwd : fwd;
+    return need ? need : 256;
+}
+
+int rel_attention_forward(const rel_attention_args* a, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+    const int st = check_attention(a);
+    if (st) return st;
+    if (a->B == 0 || a->Tq == 0) return ONEBIT_OK;
+    AttnArgs k = attn_args(a);
+    k.splits = attn_splits(a->B, a->H, a->Tq, a->Tk);
+    if (k.splits > 1) {
+        const AttnSizes z = attn_sizes(a->B, a->H, a->Tq, a->Tk, a->D, a->radius);
+        if (!ws || ws_bytes < z.split_o + z.split_ml) return ONEBIT_E_WORKSPACE;
+        if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+        const int32_t tiles = (a->Tk + kStep - 1) / kStep;
+        k.split_tiles = (tiles + k.splits - 1) / k.splits;
+        k.split_o = static_cast<float*>(ws);
+        k.split_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.split_o);
+    }
+    drop_stale_error();
+    return hip_status(launch_attn_forward(k, a->dtype, stream));
+}
+
+int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_bytes,
+                           hipStream_t stream) {
+    int st = check_attention(a);
+    if (st) return st;
+    if ((st = check_heads(a->d_o, a->do_stride, a->B, a->Tq, a->H, a->D, false)) ||
+        (st = check_heads(a->dq, a->dq_stride, a->B, a->Tq, a->H, a->D, true)) ||
+        (st = check_heads(a->dk, a->dk_stride, a->B, a->Tk, a->Hkv, a->D, true)) ||
+        (st = check_heads(a->dv, a->dv_stride, a->B, a->Tk, a->Hkv, a->D, true)))
+        return st;
+    if (!a->lse && a->B > 0 && a->Tq > 0) return ONEBIT_E_NULL;
+    if ((a->dtable && !a->table) || (a->accumulate != 0 && a->accumulate != 1))
+        return ONEBIT_E_ARG;
+    if (!aligned(a->dtable, 4)) return ONEBIT_E_ALIGN;
+    const AttnSizes z = attn_sizes(a->B, a->H, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
+    if (!ws || ws_bytes < z.delta + z.exact + z.far + z.partials) return ONEBIT_E_WORKSPACE;
+    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    AttnArgs k = attn_args(a);
+    k.d_o = a->d_o;
+    k.dq = a->dq;
+    k.dk = a->dk;
+    k.dv = a->dv;
+    k.sdo = strides_of(a->do_stride);
+    k.sdq = strides_of(a->dq_stride);
+    k.sdk = strides_of(a->dk_stride);
+    k.sdv = strides_of(a->dv_stride);
+    char* p = static_cast<char*>(ws);
+    k.delta = reinterpret_cast<float*>(p);
+    p += z.delta;
+    k.exact = reinterpret_cast<float*>(p);
+    p += z.exact;
+    k.far = reinterpret_cast<float2*>(p);
+    p += z.far;
+    k.partials = reinterpret_cast<float*>(p);
+    drop_stale_error();
+    return hip_status(launch_attn_backward(k, a->dtype, a->dtable, a->accumulate != 0, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,246 @@
+// What the attention kernels share: arguments, the tile layout in LDS, matrix
+// instruction wrappers, the bias window and the launchers.
+//
+// Layouts.  v_mfma_f32_32x32x16 takes A[row = lane & 31][k] and
+// B[k][col = lane & 31] with k = 8 (lane >> 5) + 0 ... 7, and leaves
+// C[row = 8 (r >> 2) + 4 (lane >> 5) + (r & 3)][col = lane & 31] in register r.
+// Reading the rows of A in the order perm_row() makes register r of a lane
+// hold row 16 (r >> 3) + 8 (lane >> 5) + (r & 7) instead: eight consecutive
+// rows to a lane, which is exactly the B operand of the next product (no
+// exchange between lanes) and exactly one group of eight dropout draws.
+#pragma once
+
+#include "philox.h"
+#include "train.h"
+
+namespace onebit {
+
+constexpr int kRows = 32;           // rows of a wave (columns of its products)
+constexpr int kWaves = 4;
+constexpr int kTileRows = kRows * kWaves;
+constexpr int kStep = 64;           // rows of the other side per staged tile
+constexpr int kPad = 96;            // distances past the radius that a wave's tile can reach
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+using f32x16 = float __attribute__((ext_vector_type(16)));
+
+struct Strides {
+    int64_t b, t, h;  // elements between sequences, tokens, heads
+};
+
+struct AttnArgs {
+    const void *q, *k, *v, *d_o;
+    const void* o_in;
+    void *o, *dq, *dk, *dv;
+    Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
+    float* lse;           // [B][H][Tq] natural logarithm, or nullptr
+    float* delta;         // [B][H][Tq] row sums of dO * O
+    float* exact;         // [B][H][Tq] row sums of P * dP
+    float2* far;          // [H][parts] sums of dS before and past the radius
+    float* partials;      // distance sums [H][parts][2 radius + 1]
+    float* split_o;       // [rows][splits][D] of a split forward
+    float2* split_ml;     // [rows][splits] maximum (base 2) and sum
+    const int32_t* q_pos_dev;
+    const int32_t* k_len;
+    RelBias bias;         // radius 0: none
+    DropArgs drop;
+    int32_t B, H, Hkv, Tq, Tk, D;
+    int32_t q_pos, causal;
+    int32_t splits, split_tiles;  // key tiles of one split
+    float scale;
+};
+
+// ---------------------------------------------------------------- element types
+template <typename T>
+struct Mma;
+
+template <>
+struct Mma<bf16> {
+    using x8 = __bf16 __attribute__((ext_vector_type(8)));
+    using x4 = __bf16 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ f32x16 mul(x8 a, x8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Mma<f16> {
+    using x8 = _Float16 __attribute__((ext_vector_type(8)));
+    using x4 = _Float16 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ f32x16 mul(x8 a, x8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// Transposing read: of each 16 lanes, lane i asks for 8 bytes at p (row i / 4,
+// four columns from 4 (i % 4)) and gets column i of the four rows.
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::x4 read_tr(const char* p) {
+    using s4 = short __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(typename Mma<T>::x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                       (__attribute__((address_space(3))) s4*)p));
+}
+
+// Matrix row that lane row m of the A operand reads (see the top).
+__device__ __forceinline__ int perm_row(int m) {
+    return (m & 16) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);
+}
+
+// A tile of kStep rows of DP elements in LDS: 16-byte chunks, the chunk number
+// xored with a function of the row that differs over the rows {0-3, 8-11} of
+// one phase of the row reads and, without its lowest bit, over the four
+// consecutive rows of a transposing read, so neither meets a bank twice.
+__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 3) & 1); }
+
+template <int DP>
+__device__ __forceinline__ int tile_at(int row, int chunk) {
+    return row * (DP * 2) + ((chunk ^ swizzle(row)) << 4);
+}
+
+template <int DP>
+constexpr int tile_bytes() {
+    return kStep * DP * 2;
+}
+
+// One tile's global rows on their way to LDS: every thread holds kStep * DP /
+// (8 kThreads) chunks of 16 bytes.
+template <typename T, int DP>
+struct Stage {
+    static constexpr int kChunks = DP / 8;
+    static constexpr int kPer = kStep * kChunks / kThreads;
+    typename Mma<T>::x8 v[kPer];
+
+    // rows first ... first + kStep - 1 of `base`; rows from `end` on and
+    // columns from D on are 0 and not read
+    __device__ __forceinline__ void load(const T* base, int64_t stride, int32_t first, int32_t end,
+                                         int32_t D) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int idx = i * kThreads + (int)threadIdx.x;
+            const int32_t row = first + idx / kChunks;
+            const int c = 8 * (idx % kChunks);
+            v[i] = typename Mma<T>::x8{};
+            if (row < end && c < D)
+                v[i] = *reinterpret_cast<const typename Mma<T>::x8*>(base + (int64_t)row * stride +
+                                                                     c);
+        }
+    }
+    __device__ __forceinline__ void store(char* tile) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int idx = i * kThreads + (int)threadIdx.x;
+            *reinterpret_cast<typename Mma<T>::x8*>(
+                tile + tile_at<DP>(idx / kChunks, idx % kChunks)) = v[i];
+        }
+    }
+};
+
+// A operand: 32 rows (in perm_row order) of the tile from `row0`, columns
+// 16 kc ... 16 kc + 15.
+template <typename T, int DP>
+__device__ __forceinline__ typename Mma<T>::x8 row_frag(const char* tile, int row0, int kc,
+                                                        int lane) {
+    const int row = row0 + perm_row(lane & 31);
+    return *reinterpret_cast<const typename Mma<T>::x8*>(tile +
+                                                         tile_at<DP>(row, 2 * kc + (lane >> 5)));
+}
+
+// A operand of the transposed tile: rows are the tile's columns 32 db ... + 31,
+// k its rows row0 ... row0 + 15.  Sixteen lanes read four rows of 16 elements
+// and lane i gets column i of them.
+template <typename T, int DP>
+__device__ __forceinline__ typename Mma<T>::x8 col_frag(const char* tile, int row0, int db,
+                                                        int lane) {
+    const int i = lane & 15;
+    const int row = row0 + 8 * (lane >> 5) + (i >> 2);
+    const int chunk = 4 * db + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+    const char* p = tile + tile_at<DP>(row, chunk) + 8 * (i & 1);
+    const auto lo = read_tr<T>(p);
+    const auto hi = read_tr<T>(p + 4 * (DP * 2));  // rows + 4: the same swizzle
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// B operand straight from memory: row `row` of `base` (0 where not ok),
+// columns 16 kc + 8 (lane >> 5) ... + 7.
+template <typename T, int DP>
+__device__ __forceinline__ void load_frags(typename Mma<T>::x8 (&f)[DP / 16], const T* base,
+                                           int64_t stride, int32_t row, bool ok, int32_t D,
+                                           int lane) {
+#pragma unroll
+    for (int kc = 0; kc < DP / 16; ++kc) {
+        const int c = 16 * kc + 8 * (lane >> 5);
+        f[kc] = typename Mma<T>::x8{};
+        if (ok && c < D)
+            f[kc] = *reinterpret_cast<const typename Mma<T>::x8*>(base + (int64_t)row * stride + c);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::x8 pack8(const float* p) {
+    typename Mma<T>::x8 r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = (T)p[e];
+    return r;
+}
+
+// The value the other half of the wave holds for the same column.
+__device__ __forceinline__ float other_half(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return __uint_as_float((lane_id() < 32) ? r[1] : r[0]);
+}
+
+// ---------------------------------------------------------------- bias window
+// One head's bias, times log2 e, over the distances -radius - kPad ...
+// radius + kPad, so that a tile that reaches past the radius needs no clamp.
+__device__ __forceinline__ int window_floats(int radius) { return 2 * radius + 1 + 2 * kPad; }
+
+__device__ __forceinline__ void fill_window(float* w, const RelBias& b, int h) {
+    const int R = b.radius;
+    for (int x = threadIdx.x; x < window_floats(R); x += kThreads) {
+        int i = x - kPad;
+        i = i < 0 ? 0 : (i > 2 * R ? 2 * R : i);
+        const int m = b.map[i];
+        w[x] = (uint32_t)m < (uint32_t)b.n_buckets ? b.table[(int64_t)m * b.H + h] * kLog2e : 0.0f;
+    }
+}
+
+// A row's normaliser in base 2; one that empties a row without keys.
+__device__ __forceinline__ float base2_lse(float lse) {
+    return lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
+// ---------------------------------------------------------------- per sequence
+__device__ __forceinline__ int32_t query_position(const AttnArgs& a, int b) {
+    if (!a.q_pos_dev) return a.q_pos;
+    constexpr int32_t far = 1 << 29;  // as the host checks the number
+    const int32_t p = a.q_pos_dev[b];
+    return p < -far ? -far : (p > far ? far : p);
+}
+
+__device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b) {
+    if (!a.k_len) return a.Tk;
+    const int32_t n = a.k_len[b];
+    return n < 0 ? 0 : (n > a.Tk ? a.Tk : n);
+}
+
+// Workgroups go to the 8 XCDs in turn; this gives each XCD a contiguous run of
+// the work, so that the workgroups that read the same keys share an L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t n) {
+    const int64_t run = (n + 7) / 8;
+    return (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
+}
+inline unsigned xcd_grid(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
+
+inline int32_t attn_tiles(int32_t T) { return (T + kTileRows - 1) / kTileRows; }
+
+// ---------------------------------------------------------------- launchers
+// Splits of the keys that a forward call uses (1: none).
+int32_t attn_splits(int32_t B, int32_t H, int32_t Tq, int32_t Tk);
+
+hipError_t launch_attn_forward(const AttnArgs& a, int32_t dtype, hipStream_t st);
+hipError_t launch_attn_backward(const AttnArgs& a, int32_t dtype, float* dtable, bool accumulate,
+                                hipStream_t st);
+
+}  // namespace onebit

@@ -1,0 +1,516 @@
+// Attention with a relative position bias and dropout, backward.  With keep_ij
+// (0 or 1 / kept share), P from the scores and the forward's lse:
+//
+//   dP_ij = keep_ij (dO_i . v_j),   delta_i = sum_j P_ij dP_ij = dO_i . o_i
+//   dS_ij = P_ij (dP_ij - delta_i)
+//   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i
+//   dv_j = sum_i keep_ij P_ij dO_i, dtable[b][h] = sum of dS over bucket b
+//
+// Two passes compute the scores again, one with the queries and one with the
+// keys as a wave's columns, so that each gradient is summed by one workgroup
+// in a fixed order: no atomics, the same bits on every run.
+#include "attention.h"
+
+namespace onebit {
+
+namespace {
+
+// delta from the rounded output: 16 lanes a row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_delta_kernel(AttnArgs a) {
+    using x8 = typename Mma<T>::x8;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    const int c = 8 * (threadIdx.x & 15);
+    float s = 0.0f;
+    if (row < rows && c < a.D) {
+        const int64_t i = row % a.Tq, bh = row / a.Tq, h = bh % a.H, b = bh / a.H;
+        const x8 g = *reinterpret_cast<const x8*>((const T*)a.d_o + b * a.sdo.b + i * a.sdo.t +
+                                                  h * a.sdo.h + c);
+        const x8 o = *reinterpret_cast<const x8*>((const T*)a.o_in + b * a.so.b + i * a.so.t +
+                                                  h * a.so.h + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = __builtin_fmaf((float)g[e], (float)o[e], s);
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor(s, off, 16);
+    if (row < rows && c == 0) a.delta[row] = s;
+}
+
+// Where the 32 x 32 scores of queries from i0 and keys from j0 lie against the
+// radius: -1 all at or before -radius, 1 all at or past it, 0 otherwise.
+__device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int32_t R) {
+    const int32_t d = j0 - i0 - pos;
+    return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
+}
+
+// Queries as columns.
+//   kDq       dq
+//   kDqExact  dq, and for the table the rows' exact delta and the sums of dS
+//             beyond the radius
+//   kTable    the sums of dS for each distance within the radius
+// dtable is held in binary32, where delta from the rounded output would show
+// (each row's error times the row's weight in a bucket); so kDqExact sums
+// P dP in binary32 as it goes, and kTable, which needs it finished, computes
+// the scores near the diagonal once more.
+enum DqMode { kDq, kDqExact, kTable };
+
+template <typename T, int DP, bool BIAS, bool DROP, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
+    extern __shared__ __align__(16) char lds[];
+    using x8 = typename Mma<T>::x8;
+    constexpr int kc_n = DP / 16, db_n = DP / 32;
+    const int tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
+    const int64_t work = (int64_t)a.B * a.H * tiles_q;
+    int64_t w = xcd_order(work);
+    if (w >= work) return;
+    const int qt = tiles_q - 1 - (int)(w % tiles_q);
+    w /= tiles_q;
+    const int h = (int)(w % a.H), b = (int)(w / a.H);
+    const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t iw = qt * kTileRows + wave * kRows;
+    const int32_t i = iw + (lane & 31);
+    const int R = a.bias.radius, bins_n = 2 * R + 1;
+
+    float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
+    float* skew = window + window_floats(R) + wave * 1024;  // [32 keys][32 queries] of the wave
+    float* all_bins = window + window_floats(R) + kWaves * 1024;
+    float* bins = all_bins + wave * bins_n;
+    if (BIAS) fill_window(window, a.bias, h);
+    if (MODE == kTable)
+        for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
+
+    const int hk = h / (a.H / a.Hkv);
+    const T* kp = (const T*)a.k + b * a.sk.b + hk * a.sk.h;
+    const T* vp = (const T*)a.v + b * a.sv.b + hk * a.sv.h;
+    x8 qf[kc_n], gf[kc_n];
+    load_frags<T, DP>(qf, (const T*)a.q + b * a.sq.b + h * a.sq.h, a.sq.t, i, i < a.Tq, a.D, lane);
+    load_frags<T, DP>(gf, (const T*)a.d_o + b * a.sdo.b + h * a.sdo.h, a.sdo.t, i, i < a.Tq, a.D,
+                      lane);
+    const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
+    const float lse2 = i < a.Tq ? base2_lse(a.lse[row]) : INFINITY;
+    const float delta = i < a.Tq ? (MODE == kTable ? a.exact[row] : a.delta[row]) : 0.0f;
+
+    int32_t j0 = 0, end = n_keys;
+    const int32_t last_q = (qt + 1) * kTileRows < a.Tq ? (qt + 1) * kTileRows - 1 : a.Tq - 1;
+    if (a.causal && last_q + pos + 1 < end) end = last_q + pos + 1;
+    if (MODE == kTable) {
+        // keys within the radius of some query of the tile (of all 128, which
+        // is what side_of() goes by)
+        const int32_t lo = qt * kTileRows + pos - R + 1;
+        const int32_t hi = qt * kTileRows + kTileRows - 1 + pos + R;
+        if (lo > 0) j0 = lo / kStep * kStep;
+        if (hi < end) end = hi;
+    }
+    const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
+    const int32_t limit_lo = a.causal && iw + pos < n_keys - 1 ? iw + pos : n_keys - 1;
+    const int32_t limit_hi = a.causal && iw + 31 + pos < n_keys - 1 ? iw + 31 + pos : n_keys - 1;
+
+    f32x16 acc[MODE == kTable ? 1 : db_n];
+#pragma unroll
+    for (int d = 0; d < (MODE == kTable ? 1 : db_n); ++d) acc[d] = f32x16{};
+    // row sums of P dP: all, and with the sum of P before and past the radius
+    float sum = 0.0f, lo_d = 0.0f, lo_w = 0.0f, hi_d = 0.0f, hi_w = 0.0f;
+    const float scale2 = a.scale * kLog2e;
+    const uint64_t drop_row = (uint64_t)row;
+    const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+
+    Stage<T, DP> ks, vs;
+    if (j0 < end) {
+        ks.load(kp, a.sk.t, j0, n_keys, a.D);
+        vs.load(vp, a.sv.t, j0, n_keys, a.D);
+    }
+    int buf = 0;
+    __syncthreads();  // the window and the bins
+    for (; j0 < end; j0 += kStep, buf ^= 1) {
+        char* kt = lds + buf * 2 * tile_bytes<DP>();
+        char* vt = kt + tile_bytes<DP>();
+        ks.store(kt);
+        vs.store(vt);
+        __syncthreads();  // one a tile, as in the forward pass
+        if (j0 + kStep < end) {
+            ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
+            vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t js = j0 + 32 * u;
+            if (js > limit_hi) continue;
+            const int side = BIAS ? side_of(js, iw, pos, R) : 0;
+            if (MODE == kTable && side != 0) continue;
+            f32x16 s = {}, dp = {};
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                s = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s);
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                dp = Mma<T>::mul(row_frag<T, DP>(vt, 32 * u, kc, lane), gf[kc], dp);
+            if (BIAS && side == 0) {
+                const float* at = window + (js + 8 * half - i - pos + R + kPad);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[r] = __builtin_fmaf(s[r], scale2, at[16 * (r >> 3) + (r & 7)]);
+            } else {
+                const float c = !BIAS ? 0.0f : window[side < 0 ? 0 : 2 * R + 2 * kPad];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], scale2, c);
+            }
+            const int32_t seen = limit - js - 8 * half;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r] - lse2);
+            if (js + 31 > limit_lo) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (16 * (r >> 3) + (r & 7) > seen) s[r] = 0.0f;
+            }
+            if (DROP) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t wd[4];
+                    drop_draws(wd, (uint32_t)(js + 16 * c + 8 * half) >> 3, drop_row, step,
+                               a.drop.k0, a.drop.k1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dp[8 * c + e] = drop_keep(wd, e, a.drop.threshold)
+                                            ? dp[8 * c + e] * a.drop.scale
+                                            : 0.0f;
+                }
+            }
+            if (MODE == kDqExact) {
+                float sd = 0.0f, sw = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    sd = __builtin_fmaf(s[r], dp[r], sd);
+                    sw += s[r];
+                }
+                sum += sd;
+                if (side < 0) {
+                    lo_d += sd;
+                    lo_w += sw;
+                } else if (side > 0) {
+                    hi_d += sd;
+                    hi_w += sw;
+                }
+            }
+            float ds[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - delta);
+            if (MODE != kTable) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const x8 db = pack8<T>(ds + 8 * c);
+#pragma unroll
+                    for (int d = 0; d < db_n; ++d)
+                        acc[d] = Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db,
+                                             acc[d]);
+                }
+            } else {
+                // down the 63 diagonals: the scores go through the wave's own
+                // square in LDS and lane x sums the diagonal x - 31, then adds
+                // it to the bin of its distance (no two lanes have the same)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    skew[(16 * (r >> 3) + 8 * half + (r & 7)) * 32 + (lane & 31)] = ds[r];
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                float v = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int q = j - lane + 31;
+                    const float x = skew[j * 32 + (q & 31)];
+                    v += (uint32_t)q < 32u ? x : 0.0f;
+                }
+                const int32_t d = js - iw - pos + lane - 31;
+                if (d <= -R) lo_d += v;
+                else if (d >= R) hi_d += v;
+                else bins[d + R] += v;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    }
+
+    const int64_t part = (int64_t)b * tiles_q + qt, parts = (int64_t)a.B * tiles_q;
+    if (MODE != kTable) {
+        const float all = sum + other_half(sum);
+        if (MODE == kDqExact && i < a.Tq && half == 0) a.exact[row] = all;
+        if (i < a.Tq) {
+            T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
+#pragma unroll
+            for (int d = 0; d < db_n; ++d)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c = 32 * d + 8 * g + 4 * half;
+                    if (c >= a.D) continue;
+                    typename Mma<T>::x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * a.scale);
+                    *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
+                }
+        }
+        if (MODE == kDq) return;
+        lo_d -= all * lo_w;
+        hi_d -= all * hi_w;
+    }
+    if (MODE != kDq) {
+        for (int off = 32; off > 0; off >>= 1) {
+            lo_d += __shfl_xor(lo_d, off, 64);
+            hi_d += __shfl_xor(hi_d, off, 64);
+        }
+        __syncthreads();  // the tiles are read; the bins complete
+        float2* sums = reinterpret_cast<float2*>(lds);
+        if (lane == 0) sums[wave] = float2{lo_d, hi_d};
+        __syncthreads();
+        if (MODE == kDqExact) {
+            if (threadIdx.x == 0) {
+                const float lo = (sums[0].x + sums[1].x) + (sums[2].x + sums[3].x);
+                const float hi = (sums[0].y + sums[1].y) + (sums[2].y + sums[3].y);
+                a.far[h * parts + part] = float2{lo, hi};
+            }
+        } else {
+            const float2 far = a.far[h * parts + part];
+            float* to = a.partials + (h * parts + part) * bins_n;
+            for (int x = threadIdx.x; x < bins_n; x += kThreads) {
+                float v = (all_bins[x] + all_bins[bins_n + x]) +
+                          (all_bins[2 * bins_n + x] + all_bins[3 * bins_n + x]);
+                if (x == 0) v = far.x + ((sums[0].x + sums[1].x) + (sums[2].x + sums[3].x));
+                if (x == 2 * R) v = far.y + ((sums[0].y + sums[1].y) + (sums[2].y + sums[3].y));
+                to[x] = v;
+            }
+        }
+    }
+}
+
+// Keys as columns: dk and dv of 128 keys of one key head, over every query of
+// the heads that share it, in order.
+template <typename T, int DP, bool BIAS, bool DROP>
+__global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
+    extern __shared__ __align__(16) char lds[];
+    using x8 = typename Mma<T>::x8;
+    constexpr int kc_n = DP / 16, db_n = DP / 32;
+    const int tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
+    const int64_t work = (int64_t)a.B * a.Hkv * tiles_k;
+    int64_t w = xcd_order(work);
+    if (w >= work) return;
+    // under a causal mask the first keys have the most queries: first
+    const int kt_i = (int)(w % tiles_k);
+    w /= tiles_k;
+    const int hk = (int)(w % a.Hkv), b = (int)(w / a.Hkv);
+    const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t jw = kt_i * kTileRows + wave * kRows;
+    const int32_t j = jw + (lane & 31);
+    const int R = a.bias.radius, group = a.H / a.Hkv;
+
+    float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
+    // lse and delta of a tile's queries, two buffers
+    float* rows_lds = window + (BIAS ? window_floats(R) : 0);
+
+    x8 kf[kc_n], vf[kc_n];
+    load_frags<T, DP>(kf, (const T*)a.k + b * a.sk.b + hk * a.sk.h, a.sk.t, j, j < n_keys, a.D,
+                      lane);
+    load_frags<T, DP>(vf, (const T*)a.v + b * a.sv.b + hk * a.sv.h, a.sv.t, j, j < n_keys, a.D,
+                      lane);
+    f32x16 dk[db_n], dv[db_n];
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) dk[d] = dv[d] = f32x16{};
+    const float scale2 = a.scale * kLog2e;
+    const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+
+    // queries that see a key of the tile, for each head of the group in turn
+    int32_t first = a.causal ? kt_i * kTileRows - pos : 0;
+    first = first < 0 ? 0 : first / kStep * kStep;
+    const int32_t per_head =
+        kt_i * kTileRows < n_keys && first < a.Tq ? (a.Tq - first + kStep - 1) / kStep : 0;
+    const int64_t total = (int64_t)per_head * group;
+
+    Stage<T, DP> qs, gs;
+    float row_value = 0.0f;
+    int32_t head = hk * group, i0 = first;  // of the tile to load next
+    const auto load = [&] {
+        qs.load((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, i0, a.Tq, a.D);
+        gs.load((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, i0, a.Tq, a.D);
+        const int32_t i = i0 + (int)(threadIdx.x & 63);
+        const int64_t row = ((int64_t)b * a.H + head) * a.Tq + i;
+        if (threadIdx.x < 64) row_value = i < a.Tq ? base2_lse(a.lse[row]) : INFINITY;
+        else if (threadIdx.x < 128) row_value = i < a.Tq ? a.delta[row] : 0.0f;
+    };
+    if (total > 0) load();
+    int buf = 0, filled = -1;
+    for (int64_t t = 0; t < total; ++t, buf ^= 1) {
+        const int32_t h = head, it = i0;  // this tile
+        char* qt = lds + buf * 2 * tile_bytes<DP>();
+        char* gt = qt + tile_bytes<DP>();
+        float* lse2 = rows_lds + buf * 128;
+        const float* delta = lse2 + 64;
+        if (BIAS && filled != h) {
+            __syncthreads();  // the other head's window is read
+            fill_window(window, a.bias, h);
+            filled = h;
+        }
+        qs.store(qt);
+        gs.store(gt);
+        if (threadIdx.x < 128) lse2[threadIdx.x] = row_value;
+        __syncthreads();
+        if (t + 1 < total) {
+            i0 += kStep;
+            if (i0 >= a.Tq) {
+                i0 = first;
+                ++head;
+            }
+            load();
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t is = it + 32 * u;
+            if (is >= a.Tq || (a.causal && is + 31 + pos < jw) || jw >= n_keys) continue;
+            f32x16 s = {}, dp = {};
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                s = Mma<T>::mul(row_frag<T, DP>(qt, 32 * u, kc, lane), kf[kc], s);
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                dp = Mma<T>::mul(row_frag<T, DP>(gt, 32 * u, kc, lane), vf[kc], dp);
+            const int side = BIAS ? side_of(jw, is, pos, R) : 0;
+            if (BIAS && side == 0) {
+                const float* at = window + (j - is - 8 * half - pos + R + kPad);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[r] = __builtin_fmaf(s[r], scale2, at[-16 * (r >> 3) - (r & 7)]);
+            } else {
+                const float c = !BIAS ? 0.0f : window[side < 0 ? 0 : 2 * R + 2 * kPad];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], scale2, c);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                s[r] = __builtin_amdgcn_exp2f(
+                    s[r] - lse2[32 * u + 16 * (r >> 3) + 8 * half + (r & 7)]);
+            if ((a.causal && is + pos < jw + 31) || jw + 31 >= n_keys) {
+                // a key past the sequence is seen by no query
+                const int32_t from = j >= n_keys ? 64 : (a.causal ? j - pos - is - 8 * half : 0);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (16 * (r >> 3) + (r & 7) < from) s[r] = 0.0f;
+            }
+            uint32_t kept = 0;
+            if (DROP) {
+                // lane (query q, half) draws the keys 16 half ... + 15 of its
+                // query; joined, a query's 32 decisions are the lane mask of
+                // the register that holds it
+                const uint64_t row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq +
+                                     (uint64_t)(is + (lane & 31));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t wd[4];
+                    drop_draws(wd, (uint32_t)(jw + 16 * half + 8 * c) >> 3, row, step, a.drop.k0,
+                               a.drop.k1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        kept |= (drop_keep(wd, e, a.drop.threshold) ? 1u : 0u) << (8 * c + e);
+                }
+                kept <<= 16 * half;
+                kept |= __float_as_uint(other_half(__uint_as_float(kept)));
+            }
+            float ds[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int q = 16 * (r >> 3) + (r & 7);
+                float p = s[r], g = dp[r];
+                if (DROP) {
+                    const uint64_t mask =
+                        (uint32_t)__builtin_amdgcn_readlane((int)kept, q) |
+                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)kept, q + 8) << 32);
+                    const bool keep = __builtin_amdgcn_inverse_ballot_w64(mask);
+                    g = keep ? g * a.drop.scale : 0.0f;
+                    s[r] = keep ? p * a.drop.scale : 0.0f;
+                }
+                ds[r] = p * (g - delta[32 * u + 8 * half + q]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = s[8 * c + e];
+                const x8 pb = pack8<T>(p), db = pack8<T>(ds + 8 * c);
+#pragma unroll
+                for (int d = 0; d < db_n; ++d) {
+                    dv[d] = Mma<T>::mul(col_frag<T, DP>(gt, 32 * u + 16 * c, d, lane), pb, dv[d]);
+                    dk[d] = Mma<T>::mul(col_frag<T, DP>(qt, 32 * u + 16 * c, d, lane), db, dk[d]);
+                }
+            }
+        }
+    }
+    if (j >= a.Tk) return;
+    T* to_k = (T*)a.dk + b * a.sdk.b + (int64_t)j * a.sdk.t + hk * a.sdk.h;
+    T* to_v = (T*)a.dv + b * a.sdv.b + (int64_t)j * a.sdv.t + hk * a.sdv.h;
+#pragma unroll
+    for (int d = 0; d < db_n; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * half;
+            if (c >= a.D) continue;
+            typename Mma<T>::x4 x, y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = (T)(dk[d][4 * g + e] * a.scale);
+                y[e] = (T)dv[d][4 * g + e];
+            }
+            *reinterpret_cast<typename Mma<T>::x4*>(to_k + c) = x;
+            *reinterpret_cast<typename Mma<T>::x4*>(to_v + c) = y;
+        }
+}
+
+template <typename T, int DP, bool BIAS, bool DROP>
+hipError_t run(const AttnArgs& a, bool table, hipStream_t st) {
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    const size_t window = BIAS ? (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float) : 0;
+    const size_t tiles = 4 * tile_bytes<DP>() + window;
+    if (rows > 0) {
+        hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((rows + 15) / 16)),
+                           dim3(kThreads), 0, st, a);
+        const dim3 grid(xcd_grid((int64_t)a.B * a.H * attn_tiles(a.Tq)));
+        if (BIAS && table) {
+            hipLaunchKernelGGL((attn_dq_kernel<T, DP, true, DROP, kDqExact>), grid, dim3(kThreads),
+                               tiles, st, a);
+            const size_t lds = tiles + kWaves * 1024 * sizeof(float) +
+                               kWaves * (2 * (size_t)a.bias.radius + 1) * sizeof(float);
+            hipLaunchKernelGGL((attn_dq_kernel<T, DP, true, DROP, kTable>), grid, dim3(kThreads),
+                               lds, st, a);
+        } else {
+            hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, DROP, kDq>), grid, dim3(kThreads),
+                               tiles, st, a);
+        }
+    }
+    if (a.B > 0 && a.Tk > 0)
+        hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP>),
+                           dim3(xcd_grid((int64_t)a.B * a.Hkv * attn_tiles(a.Tk))), dim3(kThreads),
+                           tiles + 256 * sizeof(float), st, a);
+    return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t run_d(const AttnArgs& a, bool table, hipStream_t st) {
+    const bool bias = a.bias.radius > 0, drop = a.drop.threshold != kDropAll;
+    if (bias) return drop ? run<T, DP, true, true>(a, table, st) : run<T, DP, true, false>(a, table, st);
+    return drop ? run<T, DP, false, true>(a, table, st) : run<T, DP, false, false>(a, table, st);
+}
+
+}  // namespace
+
+hipError_t launch_attn_backward(const AttnArgs& a, int32_t dtype, float* dtable, bool accumulate,
+                                hipStream_t st) {
+    hipError_t e;
+    if (dtype == ONEBIT_BF16)
+        e = a.D <= 64 ? run_d<bf16, 64>(a, dtable, st) : run_d<bf16, 128>(a, dtable, st);
+    else
+        e = a.D <= 64 ? run_d<f16, 64>(a, dtable, st) : run_d<f16, 128>(a, dtable, st);
+    if (e != hipSuccess || !dtable) return e;
+    const bool none = a.B == 0 || a.Tq == 0;
+    return launch_bias_join(a.partials, a.bias.map, dtable, a.H,
+                            none ? 0 : (int64_t)a.B * attn_tiles(a.Tq), a.bias.n_buckets,
+                            a.bias.radius, accumulate, st);
+}
+
+}  // namespace onebit

@@ -1,0 +1,292 @@
+// Attention with a relative position bias and dropout, forward:
+//
+//   s_ij = scale q_i . k_j + bias(j - i - pos),  P = softmax over the seen keys
+//   o_i  = sum_j P_ij keep_ij v_j / (kept share),   lse_i = log sum_j exp s_ij
+//
+// One pass over the keys with the running maximum and sum; scores and weights
+// stay in registers.  A wave has 32 queries as the columns of
+// S^T = K Q^T, so a query's whole softmax lies in one lane and its other half,
+// and the rounded weights are the B operand of O^T += V^T P^T as they are.
+#include "attention.h"
+
+namespace onebit {
+
+namespace {
+
+// Tile type of the bias for one wave: the whole tile before or past the
+// radius has one value.
+enum BiasKind { kNoBias, kBelow, kAbove, kWindow };
+
+template <typename T, int DP, bool BIAS, bool DROP, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
+    extern __shared__ __align__(16) char lds[];
+    using x8 = typename Mma<T>::x8;
+    constexpr int kc_n = DP / 16, db_n = DP / 32;
+    const int tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
+    const int64_t work = (int64_t)a.B * a.H * tiles_q * a.splits;
+    int64_t w = xcd_order(work);
+    if (w >= work) return;
+    const int split = (int)(w % a.splits);
+    w /= a.splits;
+    // under a causal mask the last queries have the most keys: first
+    const int qt = tiles_q - 1 - (int)(w % tiles_q);
+    w /= tiles_q;
+    const int h = (int)(w % a.H), b = (int)(w / a.H);
+    const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t iw = qt * kTileRows + wave * kRows;  // the wave's first query
+    const int32_t i = iw + (lane & 31);
+    const int R = a.bias.radius;
+
+    float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
+    if (BIAS) fill_window(window, a.bias, h);
+
+    const T* kp = (const T*)a.k + b * a.sk.b + (int64_t)(h / (a.H / a.Hkv)) * a.sk.h;
+    const T* vp = (const T*)a.v + b * a.sv.b + (int64_t)(h / (a.H / a.Hkv)) * a.sv.h;
+    x8 qf[kc_n];
+    load_frags<T, DP>(qf, (const T*)a.q + b * a.sq.b + h * a.sq.h, a.sq.t, i, i < a.Tq, a.D, lane);
+
+    // keys this workgroup goes over, and the last one each query sees
+    int32_t j0 = 0, end = n_keys;
+    const int32_t last_q = (qt + 1) * kTileRows < a.Tq ? (qt + 1) * kTileRows - 1 : a.Tq - 1;
+    if (a.causal && last_q + pos + 1 < end) end = last_q + pos + 1;
+    if (SPLIT) {
+        j0 = split * a.split_tiles * kStep;
+        const int32_t stop = j0 + a.split_tiles * kStep;
+        if (stop < end) end = stop;
+    }
+    const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
+    const int32_t limit_lo = a.causal && iw + pos < n_keys - 1 ? iw + pos : n_keys - 1;
+    const int32_t limit_hi = a.causal && iw + 31 + pos < n_keys - 1 ? iw + 31 + pos : n_keys - 1;
+
+    f32x16 acc[db_n];
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
+    float m = -INFINITY, l = 0.0f;
+    const float scale2 = a.scale * kLog2e;
+    const uint64_t drop_row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq + (uint64_t)i;
+    const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+
+    Stage<T, DP> ks, vs;
+    if (j0 < end) {
+        ks.load(kp, a.sk.t, j0, n_keys, a.D);
+        vs.load(vp, a.sv.t, j0, n_keys, a.D);
+    }
+    int buf = 0;
+    __syncthreads();  // the window
+    for (; j0 < end; j0 += kStep, buf ^= 1) {
+        char* kt = lds + buf * 2 * tile_bytes<DP>();
+        char* vt = kt + tile_bytes<DP>();
+        ks.store(kt);
+        vs.store(vt);
+        // one barrier a tile: the buffer written two tiles on was read before
+        // the barrier of the tile between
+        __syncthreads();
+        if (j0 + kStep < end) {
+            ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
+            vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
+        }
+        if (j0 > limit_hi) continue;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            s[u] = f32x16{};
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                s[u] = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s[u]);
+        }
+        // base-2 scores with their bias
+        int kind = kNoBias;
+        const int32_t d_lo = j0 - (iw + 31) - pos, d_hi = j0 + kStep - 1 - iw - pos;
+        if (BIAS) kind = d_hi <= -R ? kBelow : (d_lo >= R ? kAbove : kWindow);
+        if (BIAS && kind == kWindow) {
+            const float* at = window + (j0 + 8 * half - i - pos + R + kPad);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[u][r] = __builtin_fmaf(s[u][r], scale2, at[32 * u + 16 * (r >> 3) + (r & 7)]);
+        } else {
+            const float c = !BIAS ? 0.0f : window[kind == kBelow ? 0 : 2 * R + 2 * kPad];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] = __builtin_fmaf(s[u][r], scale2, c);
+        }
+        if (j0 + kStep - 1 > limit_lo) {
+            const int32_t seen = limit - j0 - 8 * half;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (32 * u + 16 * (r >> 3) + (r & 7) > seen) s[u][r] = -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+        mx = fmaxf(mx, other_half(mx));
+        const float m_new = fmaxf(m, mx);
+        const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // no key seen yet
+        if (__any(m_new > m)) {
+            const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < db_n; ++d) acc[d] *= alpha;
+            m = m_new;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(s[u][8 * c + e] - m_use);
+                    l += p[e];
+                }
+                if (DROP) {
+                    uint32_t wd[4];
+                    drop_draws(wd, (uint32_t)(j0 + 32 * u + 16 * c + 8 * half) >> 3, drop_row, step,
+                               a.drop.k0, a.drop.k1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!drop_keep(wd, e, a.drop.threshold)) p[e] = 0.0f;
+                }
+                // weights rounded to the element type for the product, as the
+                // values they meet are: relative to 1, half a step
+                const x8 pb = pack8<T>(p);
+#pragma unroll
+                for (int d = 0; d < db_n; ++d)
+                    acc[d] = Mma<T>::mul(col_frag<T, DP>(vt, 32 * u + 16 * c, d, lane), pb, acc[d]);
+            }
+        }
+    }
+
+    l += other_half(l);
+    if (i >= a.Tq) return;
+    const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
+    if (SPLIT) {
+        float* to = a.split_o + (row * a.splits + split) * a.D;
+#pragma unroll
+        for (int d = 0; d < db_n; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = 32 * d + 8 * g + 4 * half;
+                if (c < a.D)
+                    *reinterpret_cast<f4*>(to + c) = f4{acc[d][4 * g], acc[d][4 * g + 1],
+                                                        acc[d][4 * g + 2], acc[d][4 * g + 3]};
+            }
+        if (half == 0) a.split_ml[row * a.splits + split] = float2{m, l};
+        return;
+    }
+    // no key seen: l is 0 and so is the row (a NaN goes through)
+    const float inv = l == 0.0f ? 0.0f : (DROP ? a.drop.scale : 1.0f) / l;
+    T* to = (T*)a.o + b * a.so.b + i * a.so.t + h * a.so.h;
+#pragma unroll
+    for (int d = 0; d < db_n; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * half;
+            if (c >= a.D) continue;
+            typename Mma<T>::x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * inv);
+            *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
+        }
+    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+}
+
+// Joins the splits of a row: a wave per row, two columns a lane.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (row >= rows) return;
+    const int lane = lane_id();
+    const float2* ml = a.split_ml + row * a.splits;
+    float m = -INFINITY;
+    for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[s].x);
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float m_use = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    const int c = 2 * lane;
+    const float* from = a.split_o + row * a.splits * (int64_t)a.D + c;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 x = ml[s];
+        const float wgt = __builtin_amdgcn_exp2f(x.x - m_use);
+        l += wgt * x.y;
+        if (c < a.D) {
+            const float2 v = *reinterpret_cast<const float2*>(from + (int64_t)s * a.D);
+            o0 += wgt * v.x;
+            o1 += wgt * v.y;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : a.drop.scale / l;
+    const int i = (int)(row % a.Tq);
+    const int64_t bh = row / a.Tq;
+    T* to = (T*)a.o + (bh / a.H) * a.so.b + i * a.so.t + (bh % a.H) * a.so.h;
+    if (c < a.D) {
+        to[c] = (T)(o0 * inv);
+        to[c + 1] = (T)(o1 * inv);
+    }
+    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+}
+
+template <typename T, int DP, bool BIAS, bool DROP>
+void run(const AttnArgs& a, hipStream_t st) {
+    const int64_t work = (int64_t)a.B * a.H * attn_tiles(a.Tq) * a.splits;
+    const size_t lds = 4 * tile_bytes<DP>() +
+                       (BIAS ? (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float) : 0);
+    const dim3 grid(xcd_grid(work));
+    if (a.splits > 1)
+        hipLaunchKernelGGL((attn_fwd_kernel<T, DP, BIAS, DROP, true>), grid, dim3(kThreads), lds,
+                           st, a);
+    else
+        hipLaunchKernelGGL((attn_fwd_kernel<T, DP, BIAS, DROP, false>), grid, dim3(kThreads), lds,
+                           st, a);
+}
+
+template <typename T, int DP>
+void run_d(const AttnArgs& a, hipStream_t st) {
+    const bool bias = a.bias.radius > 0, drop = a.drop.threshold != kDropAll;
+    if (bias && drop) run<T, DP, true, true>(a, st);
+    else if (bias) run<T, DP, true, false>(a, st);
+    else if (drop) run<T, DP, false, true>(a, st);
+    else run<T, DP, false, false>(a, st);
+}
+
+template <typename T>
+hipError_t run_t(const AttnArgs& a, hipStream_t st) {
+    if (a.D <= 64) run_d<T, 64>(a, st);
+    else run_d<T, 128>(a, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                       dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// A workgroup has 128 queries of one head; where these are too few for the
+// card's 256 CUs the keys are split, at least four tiles to a part.
+int32_t attn_splits(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
+    const int64_t work = (int64_t)B * H * attn_tiles(Tq);
+    const int32_t tiles = (Tk + kStep - 1) / kStep;
+    if (work == 0) return 1;
+    int64_t n = (512 + work - 1) / work;
+    if (n > tiles / 4) n = tiles / 4;
+    if (n > 64) n = 64;
+    return n < 1 ? 1 : (int32_t)n;
+}
+
+hipError_t launch_attn_forward(const AttnArgs& a, int32_t dtype, hipStream_t st) {
+    return dtype == ONEBIT_BF16 ? run_t<bf16>(a, st) : run_t<f16>(a, st);
+}
+
+}  // namespace onebit

@@ -54,6 +54,23 @@ class FrozenVArgs(ctypes.Structure):
     ]
 
 
+class RelAttentionArgs(ctypes.Structure):
+    """Mirror of rel_attention_args."""
+
+    _fields_ = [
+        ("dtype", _c_i32), ("B", _c_i32), ("H", _c_i32), ("Hkv", _c_i32), ("Tq", _c_i32),
+        ("Tk", _c_i32), ("D", _c_i32), ("causal", _c_i32), ("q_pos", _c_i32),
+        ("n_buckets", _c_i32), ("radius", _c_i32), ("scale", _c_f), ("p", _c_f),
+        ("step", _c_u32), ("seed", _c_u64), ("step_dev", _c_p), ("q_pos_of", _c_p),
+        ("k_len", _c_p), ("table", _c_p), ("map", _c_p), ("q", _c_p), ("k", _c_p), ("v", _c_p),
+        ("o", _c_p), ("lse", _c_p), ("q_stride", _c_i64 * 3), ("k_stride", _c_i64 * 3),
+        ("v_stride", _c_i64 * 3), ("o_stride", _c_i64 * 3), ("d_o", _c_p), ("dq", _c_p),
+        ("dk", _c_p), ("dv", _c_p), ("do_stride", _c_i64 * 3), ("dq_stride", _c_i64 * 3),
+        ("dk_stride", _c_i64 * 3), ("dv_stride", _c_i64 * 3), ("dtable", _c_p),
+        ("accumulate", _c_i32),
+    ]
+
+
 _SIGNATURES = {
     "onebit_compress": (_c_i32, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_f, _c_i32, _c_p, _c_p,
                                  _c_i32, _c_p, _c_sz, _c_p]),
@@ -89,6 +106,9 @@ _SIGNATURES = {
     "rel_bias_grad": (_c_i32, [_c_p, _c_i32, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                _c_i32, _c_i32, _c_i32, _c_p, _c_sz, _c_p]),
     "rel_bias_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "rel_attention_forward": (_c_i32, [ctypes.POINTER(RelAttentionArgs), _c_p, _c_sz, _c_p]),
+    "rel_attention_backward": (_c_i32, [ctypes.POINTER(RelAttentionArgs), _c_p, _c_sz, _c_p]),
+    "rel_attention_workspace_bytes": (_c_sz, [_c_i32] * 8),
     "onebit_strerror": (ctypes.c_char_p, [_c_i32]),
 }
 
@@ -461,4 +481,95 @@ def rel_bias_grad(ds, bucket_map, dtable, q_pos: int = 0, accumulate: bool = Fal
                                                           "bucket_map"),
         _buf(dtable, n_buckets * H, "f32", "dtable"), B, H, n_buckets, radius, Tq, Tk, q_pos,
         int(bool(accumulate)), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        _stream(stream)))
+
+
+def rel_attention_workspace_bytes(B: int, H: int, Hkv: int, Tq: int, Tk: int, D: int,
+                                  radius: int = 0, backward: bool = False) -> int:
+    return int(load().rel_attention_workspace_bytes(B, H, Hkv, Tq, Tk, D, radius,
+                                                    int(bool(backward))))
+
+
+def _heads(a, field: str, x, shape, kind: str, name: str, stride: str = None) -> None:
+    """Puts a [B, T, heads, D] tensor (any strides, D side by side) into the
+    argument struct."""
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {tuple(shape)}")
+    if not _on_gpu(x):
+        raise ValueError(f"{name} must be a device tensor (got {x.device})")
+    if str(x.dtype).replace("torch.", "") not in _KINDS[kind]:
+        raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
+    if x.numel() and x.stride(3) != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: the elements of a head must lie side by side")
+    setattr(a, field, x.data_ptr())
+    # a dimension of one element has no stride of its own
+    setattr(a, stride or f"{field}_stride",
+            (_c_i64 * 3)(*[x.stride(d) if x.shape[d] > 1 else 0 for d in range(3)]))
+
+
+def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed, step,
+                    step_dev):
+    B, Tq, H, D = _shape(q, 4, "q")
+    _, Tk, Hkv, _ = _shape(k, 4, "k")
+    kind, code = _dtype(q, "q")
+    if kind == "f32":
+        raise ValueError("attention takes bfloat16 or float16 (got torch.float32)")
+    a = RelAttentionArgs(dtype=code, B=B, H=H, Hkv=Hkv, Tq=Tq, Tk=Tk, D=D,
+                         causal=int(bool(causal)), p=p, seed=seed & 0xFFFFFFFFFFFFFFFF,
+                         step=step & 0xFFFFFFFF, scale=D ** -0.5 if scale is None else scale)
+    _heads(a, "q", q, (B, Tq, H, D), kind, "q")
+    _heads(a, "k", k, (B, Tk, Hkv, D), kind, "k")
+    _heads(a, "v", v, (B, Tk, Hkv, D), kind, "v")
+    _heads(a, "o", o, (B, Tq, H, D), kind, "o")
+    a.lse = _buf(lse, B * H * Tq, "f32", "lse")
+    a.step_dev = _buf(step_dev, 1, "u32", "step_dev")
+    a.k_len = _buf(k_len, B, "i32", "k_len")
+    if isinstance(q_pos, int):
+        a.q_pos = q_pos
+    else:
+        a.q_pos_of = _buf(q_pos, B, "i32", "q_pos")
+    if (table is None) != (bucket_map is None):
+        raise ValueError("a bias needs its table and its bucket map")
+    if table is not None:
+        n_buckets, heads = _shape(table, 2, "table")
+        if heads != H:
+            raise ValueError(f"table has {heads} heads, q has {H}")
+        a.n_buckets, a.radius = n_buckets, _radius(bucket_map)
+        a.table = _buf(table, n_buckets * H, "f32", "table")
+        a.map = _buf(bucket_map, 2 * a.radius + 1, "i32", "bucket_map")
+    return a, kind
+
+
+def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
+                          causal: bool = False, q_pos=0, k_len=None, table=None, bucket_map=None,
+                          p: float = 0.0, seed: int = 0, step: int = 0, step_dev=None, ws=None,
+                          stream=None) -> None:
+    """o [B, Tq, H, D] (and lse [B, H, Tq]) from q [B, Tq, H, D] and k, v
+    [B, Tk, Hkv, D]; scale is D ** -0.5 unless given, q_pos a number or an
+    int32 tensor [B]."""
+    a, _ = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p,
+                           seed, step, step_dev)
+    _check("rel_attention_forward", load().rel_attention_forward(
+        ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        _stream(stream)))
+
+
+def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumulate: bool = False,
+                           scale: Optional[float] = None, causal: bool = False, q_pos=0,
+                           k_len=None, table=None, bucket_map=None, p: float = 0.0, seed: int = 0,
+                           step: int = 0, step_dev=None, ws=None, stream=None) -> None:
+    """dq, dk, dv (and dtable) from the forward call's arguments, its o and lse
+    and the gradient do."""
+    a, kind = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p,
+                              seed, step, step_dev)
+    _heads(a, "d_o", do, q.shape, kind, "do", "do_stride")
+    _heads(a, "dq", dq, q.shape, kind, "dq")
+    _heads(a, "dk", dk, k.shape, kind, "dk")
+    _heads(a, "dv", dv, k.shape, kind, "dv")
+    if dtable is not None and table is not None and tuple(dtable.shape) != tuple(table.shape):
+        raise ValueError(f"dtable has shape {tuple(dtable.shape)}, table {tuple(table.shape)}")
+    a.dtable = _buf(dtable, a.n_buckets * a.H, "f32", "dtable")
+    a.accumulate = int(bool(accumulate))
+    _check("rel_attention_backward", load().rel_attention_backward(
+        ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream(stream)))

@@ -1,0 +1,326 @@
+"""rel_attention_forward and rel_attention_backward against the 64-bit forms,
+element by element within derived bounds (tests/_attention.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+from momentum_compression_amd import onebit as ob
+from momentum_compression_amd.attention import rel_bucket_map
+from tests._attention import (SEED, TYPES, check, expected, half_step, host64, make, numbers,
+                              workspace)
+from tests._gpu import device, gen
+
+pytestmark = pytest.mark.gpu
+
+# name: B, H, Hkv, Tq, Tk, D, causal, q_pos, k_len, buckets, max_distance, two_sided, p
+FORWARD = {
+    "one": (1, 1, 1, 1, 1, 8, False, 0, None, 0, 0, False, 0.0),
+    "tiny": (2, 3, 3, 5, 7, 16, True, 2, None, 4, 8, False, 0.0),
+    "plain": (2, 2, 2, 64, 64, 64, False, 0, None, 0, 0, False, 0.0),
+    "bias": (1, 2, 2, 70, 129, 64, False, 0, None, 32, 40, True, 0.0),
+    "causal_grouped": (1, 6, 2, 150, 150, 128, True, 0, None, 32, 128, False, 0.0),
+    "odd_width": (2, 2, 1, 33, 200, 40, True, 167, None, 8, 20, True, 0.0),
+    "wide_odd": (1, 2, 2, 130, 97, 104, False, -5, None, 32, 64, True, 0.0),
+    "padded": (4, 2, 2, 90, 90, 64, False, 0, (90, 33, 1, 64), 32, 128, True, 0.0),
+    "empty_rows": (4, 2, 1, 40, 70, 80, True, (-8, 30, -100, 3), (70, 0, 20, 5), 8, 20, False, 0.0),
+    "dropout": (2, 2, 2, 75, 139, 64, False, 0, (139, 100), 32, 40, True, 0.2),
+    "dropout_causal": (1, 4, 2, 140, 140, 128, True, 0, None, 0, 0, False, 0.5),
+    "far_radius": (1, 1, 1, 300, 900, 64, True, 600, None, 64, 1024, False, 0.0),
+    "narrow_radius": (1, 2, 2, 260, 400, 32, False, 0, None, 4, 8, True, 0.0),
+    "one_token": (3, 4, 2, 1, 1000, 128, True, (999, 500, 0), (1000, 501, 1), 32, 128, False, 0.0),
+    "one_token_many_heads": (2, 16, 2, 1, 777, 64, True, 776, None, 32, 128, False, 0.0),
+    "few_tokens": (2, 4, 4, 5, 1500, 96, True, 1495, None, 32, 128, False, 0.0),
+    "few_tokens_dropout": (1, 2, 2, 3, 1100, 64, False, 0, (1050,), 8, 100, True, 0.3),
+    "long_cache": (1, 1, 1, 2, 9000, 64, True, 8998, None, 32, 128, False, 0.0),
+}
+
+
+def _setup(name, dtype, cases, fused=False):
+    B, H, Hkv, Tq, Tk, D, causal, q_pos, k_len, n, far, two, p = cases[name]
+    dev = device()
+    print(f"[attention] {name} {dtype} {cases[name]}", flush=True)
+    g = gen(sum(map(ord, name)), dev)
+    q, k, v = make(dtype, B, H, Hkv, Tq, Tk, D, g, dev, fused=fused)
+    if isinstance(q_pos, tuple):
+        q_pos = torch.tensor(q_pos, dtype=torch.int32, device=dev)
+    if k_len is not None:
+        k_len = torch.tensor(k_len, dtype=torch.int32, device=dev)
+    table = torch.randn((n, H), generator=g, device=dev) if n else None
+    bmap = rel_bucket_map(n, far, two, dev) if n else None
+    how = dict(scale=D ** -0.5, causal=causal, q_pos=q_pos, k_len=k_len, table=table,
+               bucket_map=bmap, p=p, seed=SEED, step=17)
+    return q, k, v, how, g
+
+
+def _oracle(q, k, v, do, how, dtype):
+    kl = host64(how["k_len"])
+    return expected(host64(q), host64(k), host64(v), host64(do), how["scale"], how["causal"],
+                    numbers(how["q_pos"]), None if kl is None else kl.astype(int),
+                    host64(how["table"]),
+                    None if how["bucket_map"] is None else how["bucket_map"].cpu().numpy(),
+                    how["p"], SEED, 17, half_step(dtype))
+
+
+def _poison_past(k_len, *tensors):
+    """NaN in every key and value that no query may read."""
+    if k_len is not None:
+        for x in tensors:
+            for b, n in enumerate(k_len.tolist()):
+                x[b, max(0, n):] = float("nan")
+
+
+def _tiny(dtype):
+    # half the smallest step of the type, and as much again for each rounded
+    # operand of fp16's narrow range
+    return 2.0 ** -133 if dtype == "bf16" else 2.0 ** -22
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name", FORWARD)
+def test_forward(name, dtype):
+    q, k, v, how, _ = _setup(name, dtype, FORWARD)
+    want, tol = _oracle(q, k, v, None, how, dtype)
+    _poison_past(how["k_len"], k, v)
+    o = torch.full_like(q, 9.0)
+    lse = torch.full((q.shape[0], q.shape[2], q.shape[1]), 9.0, device=q.device)
+    ws = workspace(q, k)
+    ob.rel_attention_forward(q, k, v, o, lse=lse, ws=ws, **how)
+    check(dict(o=o, lse=lse), want, tol, ("o", "lse"), _tiny(dtype))
+    again = torch.empty_like(o)
+    ob.rel_attention_forward(q, k, v, again, ws=ws, **how)
+    assert torch.equal(again, o)
+
+
+BACKWARD = {
+    "one": (1, 1, 1, 1, 1, 8, False, 0, None, 0, 0, False, 0.0),
+    "tiny": (2, 3, 3, 5, 7, 16, True, 2, None, 4, 8, False, 0.0),
+    "plain": (2, 2, 2, 64, 64, 64, False, 0, None, 0, 0, False, 0.0),
+    "bias": (1, 2, 2, 70, 129, 64, False, 0, None, 32, 40, True, 0.0),
+    "causal_grouped": (2, 6, 2, 150, 150, 128, True, 0, None, 32, 128, False, 0.0),
+    "odd_width": (2, 2, 1, 33, 200, 40, True, 167, None, 8, 20, True, 0.1),
+    "wide_odd": (1, 2, 2, 130, 97, 104, False, -5, None, 32, 64, True, 0.3),
+    "padded_dropout": (4, 2, 2, 90, 90, 64, False, 0, (90, 33, 1, 64), 32, 128, True, 0.1),
+    "empty_rows": (4, 2, 1, 40, 70, 80, True, (-8, 30, -100, 3), (70, 0, 20, 5), 8, 20, False, 0.0),
+    "dropout_causal": (1, 4, 2, 140, 140, 128, True, 0, None, 0, 0, False, 0.5),
+    "dropout_plain": (1, 2, 2, 100, 170, 64, False, 0, None, 0, 0, False, 0.25),
+    "far_radius": (1, 1, 1, 300, 500, 64, True, 200, None, 64, 1024, False, 0.0),
+    "narrow_radius": (1, 2, 2, 260, 400, 32, False, 0, None, 4, 8, True, 0.0),
+    "ragged_tile": (1, 1, 1, 129, 385, 64, False, 100, None, 8, 24, True, 0.0),
+    "one_token": (2, 4, 4, 1, 300, 128, True, 299, None, 32, 128, False, 0.2),
+}
+
+
+def _backward(q, k, v, how, do, dtable=None, ws=None, fused=False, accumulate=False):
+    o = torch.full_like(do, 9.0)
+    lse = torch.full((q.shape[0], q.shape[2], q.shape[1]), 9.0, device=q.device)
+    radius = 0 if dtable is None else how["bucket_map"].numel() // 2
+    if ws is None:
+        ws = workspace(q, k, radius, True)
+    if fused:
+        H, Hkv = q.shape[2], k.shape[2]
+        d = torch.full((*q.shape[:2], H + 2 * Hkv, q.shape[3]), 9.0, dtype=q.dtype,
+                       device=q.device)
+        dq, dk, dv = d[:, :, :H], d[:, :, H:H + Hkv], d[:, :, H + Hkv:]
+    else:
+        dq, dk, dv = (torch.full(x.shape, 9.0, dtype=x.dtype, device=x.device) for x in (q, k, v))
+    ob.rel_attention_forward(q, k, v, o, lse=lse, ws=ws, **how)
+    ob.rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=dtable,
+                              accumulate=accumulate, ws=ws, **how)
+    return dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv, dtable=dtable)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name", BACKWARD)
+def test_backward(name, dtype):
+    fused = BACKWARD[name][3] == BACKWARD[name][4]
+    q, k, v, how, g = _setup(name, dtype, BACKWARD, fused=fused)
+    do = torch.randn(q.shape, generator=g, device=q.device).to(TYPES[dtype])
+    want, tol = _oracle(q, k, v, do, how, dtype)
+    if not fused:
+        _poison_past(how["k_len"], k, v)
+    dtable = None if how["table"] is None else torch.full_like(how["table"], 9.0)
+    got = _backward(q, k, v, how, do, dtable, fused=fused)
+    names = ["o", "lse", "dq", "dk", "dv"] + (["dtable"] if dtable is not None else [])
+    check(got, want, tol, names, _tiny(dtype))
+    if dtable is None:
+        return
+    # the same bits again, without the table's gradient too, and added to it
+    twice = _backward(q, k, v, how, do, dtable.clone(), fused=fused)
+    for n in names:
+        assert torch.equal(twice[n], got[n]), n
+    bare = _backward(q, k, v, how, do, None, fused=fused)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(bare[n], got[n]), n
+    more = _backward(q, k, v, how, do, dtable.clone(), fused=fused, accumulate=True)
+    assert torch.allclose(more["dtable"], 2 * dtable, rtol=2 ** -22, atol=0)
+
+
+def test_gradients_by_differences():
+    """The gradients against differences of the oracle's forward map at the
+    rounded inputs, along random directions."""
+    from oracle import training as ref
+
+    name = "padded_dropout"
+    q, k, v, how, g = _setup(name, "bf16", BACKWARD)
+    do = torch.randn(q.shape, generator=g, device=q.device).to(torch.bfloat16)
+    dtable = torch.empty_like(how["table"])
+    got = _backward(q, k, v, how, do, dtable)
+    x = {n: host64(t) for n, t in (("q", q), ("k", k), ("v", v), ("table", how["table"]))}
+    m = how["bucket_map"].cpu().numpy()
+    kl = how["k_len"].cpu().numpy()
+
+    def loss(y):
+        o = ref.attention(y["q"], y["k"], y["v"], how["scale"], how["causal"], 0, kl, y["table"],
+                          m, how["p"], SEED, 17)["o"]
+        return (o * host64(do)).sum()
+
+    rng = np.random.default_rng(1)
+    for n, d in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("table", "dtable")):
+        e = rng.standard_normal(x[n].shape)
+        h = 1e-5
+        by = (loss({**x, n: x[n] + h * e}) - loss({**x, n: x[n] - h * e})) / (2 * h)
+        grad = host64(got[d])
+        # random signs: the roundings of the terms add like their squares
+        spread = np.sqrt(((grad * e) ** 2).sum())
+        assert abs((grad * e).sum() - by) < 6 * 2.0 ** -8 * spread + 1e-6, n
+
+
+def test_dropout_mask_is_dropout_applys():
+    """Equal scores and one-hot values show the weights: each is kept where
+    dropout_apply keeps it on the score map's rows."""
+    dev = device()
+    B, H, Tq, Tk, p = 2, 2, 70, 64, 0.3
+    q = torch.zeros((B, Tq, H, 64), dtype=torch.bfloat16, device=dev)
+    k = torch.zeros((B, Tk, H, 64), dtype=torch.bfloat16, device=dev)
+    v = torch.eye(64, dtype=torch.bfloat16, device=dev)[None, :, None].expand(B, Tk, H, 64)
+    v = v.contiguous()
+    o = torch.empty_like(q)
+    ob.rel_attention_forward(q, k, v, o, p=p, seed=SEED, step=3)
+    ones = torch.ones((B * H * Tq, Tk), device=dev)
+    kept = torch.empty_like(ones)
+    ob.dropout_apply(ones, kept, B * H * Tq, Tk, p, SEED, 3)
+    assert torch.equal(o.permute(0, 2, 1, 3).reshape(B * H * Tq, Tk) != 0, kept != 0)
+
+
+def test_caches_and_orders_of_other_strides():
+    """[B, H, T, D] caches, one cache for all sequences (stride 0), and rows
+    further apart than they are wide give what contiguous copies give."""
+    dev = device()
+    g = gen(3, dev)
+    B, H, Hkv, Tq, Tk, D = 3, 4, 2, 60, 200, 64
+    q = torch.randn((B, H, Tq, D), generator=g, device=dev).bfloat16().transpose(1, 2)
+    kv = torch.randn((1, Hkv, Tk, 2 * D + 24), generator=g, device=dev).bfloat16()
+    k = kv[..., 8:8 + D].transpose(1, 2).expand(B, Tk, Hkv, D)
+    v = kv[..., D + 16:2 * D + 16].transpose(1, 2).expand(B, Tk, Hkv, D)
+    o = torch.full((B, H, Tq, D + 8), 5.0, dtype=torch.bfloat16, device=dev)
+    ov = o[..., :D].transpose(1, 2)
+    plain = torch.empty((B, Tq, H, D), dtype=torch.bfloat16, device=dev)
+    how = dict(causal=True, q_pos=140)
+    ob.rel_attention_forward(q, k, v, ov, ws=workspace(q, k), **how)
+    ob.rel_attention_forward(q.contiguous(), k.contiguous(), v.contiguous(), plain,
+                             ws=workspace(q, k), **how)
+    assert torch.equal(ov, plain) and bool((o[..., D:] == 5).all())
+
+
+def test_values_past_the_length_and_nan_inputs():
+    """NaN in a query reaches its own row alone."""
+    dev = device()
+    g = gen(9, dev)
+    q, k, v = make("bf16", 1, 1, 1, 40, 100, 64, g, dev)
+    clean = torch.empty_like(q)
+    ob.rel_attention_forward(q, k, v, clean, ws=workspace(q, k))
+    q[0, 7] = float("nan")
+    o = torch.empty_like(q)
+    ob.rel_attention_forward(q, k, v, o, ws=workspace(q, k))
+    assert bool(o[0, 7].isnan().all())
+    rest = [i for i in range(40) if i != 7]
+    assert torch.equal(o[0, rest], clean[0, rest])
+
+
+def test_lowest_bias_values():
+    """A table holding the type's lowest number, or -inf, hides its distances
+    without NaN."""
+    dev = device()
+    g = gen(2, dev)
+    q, k, v = make("f16", 1, 2, 2, 50, 80, 64, g, dev)
+    bmap = rel_bucket_map(8, 20, True, dev)
+    for low in (torch.finfo(torch.float32).min, float("-inf")):
+        table = torch.randn((8, 2), generator=g, device=dev)
+        table[5:] = low                       # every key after the query
+        o, lse = torch.empty_like(q), torch.empty((1, 2, 50), device=dev)
+        ob.rel_attention_forward(q, k, v, o, lse=lse, table=table, bucket_map=bmap,
+                                 ws=workspace(q, k))
+        want = torch.empty_like(q)
+        safe = torch.where(table == low, torch.zeros_like(table), table)
+        ob.rel_attention_forward(q, k, v, want, table=safe, bucket_map=bmap, causal=True,
+                                 ws=workspace(q, k))
+        assert torch.equal(o, want) and bool(lse.isfinite().all())
+
+
+def test_nothing_to_attend_or_ask():
+    dev = device()
+    q = torch.randn((2, 5, 2, 16), device=dev).bfloat16()
+    k = torch.empty((2, 0, 2, 16), device=dev).bfloat16()
+    o, lse = torch.full_like(q, 7), torch.full((2, 2, 5), 7.0, device=dev)
+    ob.rel_attention_forward(q, k, k, o, lse=lse)
+    assert bool((o == 0).all()) and bool((lse == float("-inf")).all())
+    dq, dk = torch.full_like(q, 7), torch.empty_like(k)
+    bmap = rel_bucket_map(8, 20, True, dev)
+    table = torch.randn((8, 2), device=dev)
+    dtable = torch.full_like(table, 7)
+    ob.rel_attention_backward(q, k, k, o, lse, q, dq, dk, dk, table=table, bucket_map=bmap,
+                              dtable=dtable, ws=workspace(q, k, 20, True))
+    assert bool((dq == 0).all()) and bool((dtable == 0).all())
+    # no queries: the keys' gradients are zeros
+    dkv = [torch.full_like(q, 7) for _ in range(2)]
+    e, el = q[:, :0], lse[:, :, :0]
+    dtable.fill_(7)
+    ob.rel_attention_forward(e, q, q, e, lse=el.contiguous())
+    ob.rel_attention_backward(e, q, q, e, el.contiguous(), e, e, *dkv, table=table,
+                              bucket_map=bmap, dtable=dtable, ws=workspace(e, q, 20, True))
+    assert all(bool((x == 0).all()) for x in dkv) and bool((dtable == 0).all())
+
+
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_replayed_graph_matches_eager(p):
+    """Forward and backward captured together; every replay, with eager work
+    between, equals the eager calls, and the mask follows the device step."""
+    dev = device()
+    g = gen(12, dev)
+    q, k, v = make("bf16", 2, 2, 2, 100, 100, 64, g, dev)
+    do = torch.randn(q.shape, generator=g, device=dev).bfloat16()
+    bmap = rel_bucket_map(32, 40, True, dev)
+    table = torch.randn((32, 2), generator=g, device=dev)
+    step = torch.zeros(1, dtype=torch.int32, device=dev)
+    how = dict(table=table, bucket_map=bmap, p=p, seed=SEED)
+
+    def both(out, ws, **more):
+        ob.rel_attention_forward(q, k, v, out["o"], lse=out["lse"], ws=ws, **how, **more)
+        ob.rel_attention_backward(q, k, v, out["o"], out["lse"], do, out["dq"], out["dk"],
+                                  out["dv"], dtable=out["dtable"], ws=ws, **how, **more)
+
+    def buffers():
+        return dict(o=torch.empty_like(q), lse=torch.empty((2, 2, 100), device=dev),
+                    dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                    dtable=torch.empty_like(table))
+
+    mine, theirs = buffers(), buffers()
+    ws, ws2 = workspace(q, k, 40, True), workspace(q, k, 40, True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both(mine, ws, step=5, step_dev=step)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(mine, ws, step=5, step_dev=step)
+    for t in range(4):
+        step.fill_(t)
+        q.copy_(torch.randn(q.shape, generator=g, device=dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        both(theirs, ws2, step=5 + t)
+        torch.cuda.synchronize()
+        for n in mine:
+            assert torch.equal(mine[n], theirs[n]), (t, n)

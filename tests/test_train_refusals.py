@@ -136,3 +136,113 @@ def test_bucket_map_borders_are_whole():
         rel_bucket_map(1, 10, True)
     with pytest.raises(ValueError):
         rel_bucket_map(32, 16, False)
+
+
+def _args(**kw):
+    a = ob.RelAttentionArgs(dtype=1, B=1, H=4, Hkv=2, Tq=8, Tk=8, D=64, scale=0.125, q=P, k=P, v=P,
+                            o=P, lse=P, d_o=P, dq=P, dk=P, dv=P)
+    for n, heads in (("q", 4), ("k", 2), ("v", 2), ("o", 4), ("do", 4), ("dq", 4), ("dk", 2),
+                     ("dv", 2)):
+        setattr(a, n + "_stride", (8 * heads * 64, heads * 64, 64))
+    for n, x in kw.items():
+        setattr(a, n, x)
+    return a
+
+
+def test_attention_refusals(lib):
+    import ctypes
+
+    def both(ws=P, wsb=1 << 30, **kw):
+        a = _args(**kw)
+        f = lib.rel_attention_forward(ctypes.byref(a), ws, wsb, None)
+        b = lib.rel_attention_backward(ctypes.byref(a), ws, wsb, None)
+        assert f == b, (kw, f, b)
+        return f
+
+    assert lib.rel_attention_forward(None, P, 1, None) == ob.ONEBIT_E_NULL
+    assert lib.rel_attention_backward(None, P, 1, None) == ob.ONEBIT_E_NULL
+    for bad in (dict(dtype=0), dict(dtype=3), dict(p=1.0), dict(p=-1.0), dict(p=NAN),
+                dict(scale=NAN), dict(scale=float("inf")), dict(causal=2), dict(q_pos=1 << 30),
+                dict(q_pos=-(1 << 30))):
+        assert both(**bad) == ob.ONEBIT_E_ARG, bad
+    for bad in (dict(B=-1), dict(H=0), dict(H=5), dict(Hkv=0), dict(Hkv=3), dict(Tq=-1),
+                dict(Tk=(1 << 29) + 1), dict(D=0), dict(D=12), dict(D=136), dict(radius=-1),
+                dict(radius=1025, n_buckets=4, table=P, map=P),
+                dict(radius=8, n_buckets=0, table=P, map=P), dict(B=1 << 30, H=8, Hkv=8),
+                dict(q_stride=(2048, 252, 64)), dict(k_stride=(1024, -128, 64)),
+                dict(v_stride=(1 << 41, 128, 64)), dict(o_stride=(2048, 0, 64)),
+                dict(o_stride=(2048, 256, 32))):
+        assert both(**bad) == ob.ONEBIT_E_SIZE, bad
+    for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(table=P),
+                dict(map=P, table=None), dict(radius=8, n_buckets=4)):
+        assert both(**bad) == ob.ONEBIT_E_NULL, bad
+    for bad in (dict(q=P + 8), dict(k=P + 2), dict(v=P + 4), dict(o=P + 8), dict(lse=P + 2),
+                dict(k_len=P + 1), dict(q_pos_of=P + 2), dict(step_dev=P + 1),
+                dict(table=P + 1, map=P, radius=4, n_buckets=4)):
+        assert both(**bad) == ob.ONEBIT_E_ALIGN, bad
+
+    def bwd(ws=P, wsb=1 << 30, **kw):
+        return lib.rel_attention_backward(ctypes.byref(_args(**kw)), ws, wsb, None)
+
+    for n in ("d_o", "dq", "dk", "dv", "lse"):
+        assert bwd(**{n: None}) == ob.ONEBIT_E_NULL, n
+    for n in ("d_o", "dq", "dk", "dv"):
+        assert bwd(**{n: P + 8}) == ob.ONEBIT_E_ALIGN, n
+    assert bwd(dk_stride=(1024, 0, 64)) == ob.ONEBIT_E_SIZE
+    assert bwd(dtable=P) == ob.ONEBIT_E_ARG
+    assert bwd(accumulate=2) == ob.ONEBIT_E_ARG
+    assert bwd(table=P, map=P, radius=4, n_buckets=4, dtable=P + 2) == ob.ONEBIT_E_ALIGN
+    assert bwd(ws=None) == bwd(wsb=8) == ob.ONEBIT_E_WORKSPACE
+    assert bwd(ws=P + 64) == ob.ONEBIT_E_ALIGN
+    # few rows over many keys: the forward call needs its workspace too
+    a = _args(Tq=1, Tk=1 << 14)
+    assert lib.rel_attention_forward(ctypes.byref(a), None, 0, None) == ob.ONEBIT_E_WORKSPACE
+    assert lib.rel_attention_forward(ctypes.byref(_args(Tq=0, q=None, o=None)), None, 0,
+                                     None) == ob.ONEBIT_OK
+
+
+def test_attention_workspace(lib):
+    f = ob.rel_attention_workspace_bytes
+    assert f(1, 4, 2, 8, 8, 64) == 256
+    assert f(1, 4, 2, 8, 8, 64, backward=True) == 256
+    assert f(1, 4, 2, 1, 1 << 14, 64) > 256
+    assert f(1, 4, 2, 8, 8, 64, radius=16, backward=True) > f(1, 4, 2, 8, 8, 64, backward=True)
+    assert f(1, 4, 3, 8, 8, 64) == f(1, 4, 2, 8, 8, 65) == f(-1, 4, 2, 8, 8, 64) == 0
+    assert f(0, 4, 2, 0, 8, 64) == 256
+
+
+def test_attention_struct_matches_header():
+    """Offsets that the C declaration implies (LP64)."""
+    import ctypes
+
+    A = ob.RelAttentionArgs
+    assert A.seed.offset == 56 and A.step_dev.offset == 64 and A.table.offset == 88
+    assert A.q.offset == 104 and A.lse.offset == 136 and A.q_stride.offset == 144
+    assert A.d_o.offset == 240 and A.do_stride.offset == 272 and A.dtable.offset == 368
+    assert A.accumulate.offset == 376 and ctypes.sizeof(A) == 384
+
+
+def test_attention_binding_refuses(monkeypatch):
+    monkeypatch.setattr(ob, "_on_gpu", lambda t: True)
+    q = torch.zeros((1, 4, 2, 16), dtype=torch.bfloat16)
+    f = ob.rel_attention_forward
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        f(q.float(), q.float(), q.float(), q.float())
+    with pytest.raises(ValueError, match="shape"):
+        f(q, q, q[:, :3], q)
+    with pytest.raises(ValueError, match="must be bfloat16"):
+        f(q, q.half(), q, q)
+    with pytest.raises(ValueError, match="side by side"):
+        f(q, q, q, torch.zeros((1, 4, 2, 32), dtype=torch.bfloat16)[..., ::2])
+    with pytest.raises(ValueError, match="its bucket map"):
+        f(q, q, q, q, table=torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="heads"):
+        f(q, q, q, q, table=torch.zeros(4, 3), bucket_map=torch.zeros(9, dtype=torch.int32))
+    with pytest.raises(ValueError, match="needs"):
+        f(q, q, q, q, lse=torch.zeros(7))
+    with pytest.raises(ValueError, match="int32"):
+        f(q, q, q, q, k_len=torch.zeros(1, dtype=torch.int64))
+    t, m = torch.zeros(4, 2), torch.zeros(9, dtype=torch.int32)
+    with pytest.raises(ValueError, match="dtable has shape"):
+        ob.rel_attention_backward(q, q, q, q, torch.zeros(1, 2, 4), q, q, q, q, table=t,
+                                  bucket_map=m, dtable=torch.zeros(2, 4))
