@@ -64,13 +64,16 @@ __global__ __launch_bounds__(kThreads) void rel_bias_kernel(RelBias b, T* __rest
 // lane, added to the wave's own bins in LDS without atomics (no two lanes own
 // the same distance), so the result does not depend on timing.  Narrow maps
 // give the other 64 / W parts of the wave other sequences.
+constexpr int kGradWaves = 8;
+constexpr int kGradThreads = 64 * kGradWaves;
+
 template <typename T, int W>
-__global__ __launch_bounds__(kThreads) void bias_grad_kernel(const T* __restrict__ ds,
+__global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __restrict__ ds,
                                                             float* __restrict__ partials,
                                                             BiasGradPlan plan, int32_t B, int32_t H,
                                                             int32_t radius, int32_t Tq, int32_t Tk,
                                                             int32_t q_pos) {
-    extern __shared__ float lds[];  // [4][2 radius + 1]
+    extern __shared__ float lds[];  // [waves][2 radius + 1]
     const int R = radius, bins_n = 2 * R + 1;
     const int wave = threadIdx.x >> 6, lane = lane_id();
     const int col = lane % W, sub = lane / W;
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void bias_grad_kernel(const T* __restrict
     const int32_t b1 = (bb + 1) * plan.batches < B ? (bb + 1) * plan.batches : B;
     const bool whole = c0 + 8 <= Tk;
     float far_lo = 0.0f, far_hi = 0.0f;
-    for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows; i0 += 32) {
+    for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows; i0 += 8 * kGradWaves) {
         float acc[15];
 #pragma unroll
         for (int k = 0; k < 15; ++k) acc[k] = 0.0f;
@@ -146,45 +149,71 @@ __global__ __launch_bounds__(kThreads) void bias_grad_kernel(const T* __restrict
     }
     __syncthreads();
     float* to = partials + ((int64_t)h * gridDim.x + blockIdx.x) * bins_n;
-    for (int x = threadIdx.x; x < bins_n; x += kThreads)
-        to[x] = (lds[x] + lds[bins_n + x]) + (lds[2 * bins_n + x] + lds[3 * bins_n + x]);
+    for (int x = threadIdx.x; x < bins_n; x += kGradThreads) {
+        float v = lds[x];
+#pragma unroll
+        for (int w = 1; w < kGradWaves; ++w) v += lds[w * bins_n + x];
+        to[x] = v;
+    }
 }
 
 constexpr int kJoinThreads = 1024;
 
-// One workgroup per head: each distance's sum over the parts in binary64 (as
-// many threads a distance as the workgroup has room for), then each bucket's
-// over its distances, in the order of the distances.
+// One workgroup per (bucket, head): the bucket's distances are listed in
+// order, then its threads take (part, distance) pairs in turn, neighbouring
+// threads neighbouring distances, and their binary64 sums are added in a fixed
+// order.
 __global__ __launch_bounds__(kJoinThreads) void bias_join_kernel(const float* __restrict__ partials,
-                                                                const int32_t* __restrict__ map,
-                                                                float* __restrict__ dtable,
-                                                                int32_t H, int64_t parts,
-                                                                int32_t n_buckets, int32_t radius,
-                                                                int32_t accumulate) {
-    __shared__ double sums[2 * kMaxRadius + 1];
-    __shared__ int32_t where[2 * kMaxRadius + 1];
-    const int h = blockIdx.x, n = 2 * radius + 1;
+                                                            const int32_t* __restrict__ map,
+                                                            float* __restrict__ dtable, int32_t H,
+                                                            int32_t parts, int32_t radius,
+                                                            int32_t accumulate) {
+    __shared__ double sums[kJoinThreads / 64];
+    __shared__ int16_t list[2 * kMaxRadius + 1];
+    __shared__ int32_t found[kJoinThreads / 64];
+    const int b = blockIdx.x, h = blockIdx.y, n = 2 * radius + 1;
+    const int wave = threadIdx.x >> 6, lane = lane_id();
+    int m = 0;
+    for (int x0 = 0; x0 < n; x0 += kJoinThreads) {
+        const int x = x0 + (int)threadIdx.x;
+        const bool mine = x < n && map[x] == b;
+        const uint64_t lanes = __ballot(mine);
+        if (lane == 0) found[wave] = __builtin_popcountll(lanes);
+        __syncthreads();
+        int at = m + __builtin_popcountll(lanes & (((uint64_t)1 << lane) - 1));
+        for (int w = 0; w < kJoinThreads / 64; ++w) {
+            if (w < wave) at += found[w];
+            m += found[w];
+        }
+        if (mine) list[at] = (int16_t)x;
+        __syncthreads();
+    }
     const float* from = partials + (int64_t)h * parts * n;
-    const int slices = n <= kJoinThreads ? kJoinThreads / n : 1;
-    for (int t = threadIdx.x; t < n * slices; t += kJoinThreads) {
-        const int x = t % n, s = t / n;
-        double v = 0.0;
-#pragma unroll 8
-        for (int64_t q = s; q < parts; q += slices) v += (double)from[q * n + x];
-        sums[t] = v;  // n * slices <= max(n, kJoinThreads) <= the array
+    double v = 0.0;
+    if (m > 0) {
+        const int dq = kJoinThreads / m, de = kJoinThreads % m;  // a thread's next pair
+        int q = (int)threadIdx.x / m, e = (int)threadIdx.x % m;
+        while (q < parts) {
+            float x[8];  // eight loads in flight
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                x[k] = q < parts ? from[(int64_t)q * n + list[e]] : 0.0f;
+                q += dq;
+                e += de;
+                if (e >= m) {
+                    e -= m;
+                    ++q;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += (double)x[k];
+        }
     }
-    for (int x = threadIdx.x; x < n; x += kJoinThreads) where[x] = map[x];
+    v = wave_sum(v);
+    if (lane == 0) sums[wave] = v;
     __syncthreads();
-    for (int x = threadIdx.x; x < n; x += kJoinThreads) {
-        double v = sums[x];
-        for (int s = 1; s < slices; ++s) v += sums[s * n + x];
-        sums[x] = v;  // read and written by this thread alone
-    }
-    __syncthreads();
-    for (int b = threadIdx.x; b < n_buckets; b += kJoinThreads) {
-        double v = 0.0;
-        for (int x = 0; x < n; ++x)
-            if (where[x] == b) v += sums[x];
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kJoinThreads / 64; ++w) v += sums[w];
         float* to = dtable + (int64_t)b * H + h;
         *to = accumulate ? (float)((double)*to + v) : (float)v;
     }
@@ -194,8 +223,8 @@ template <typename T, int W>
 void grad_w(const void* ds, float* partials, const BiasGradPlan& plan, int32_t B, int32_t H,
             int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos, hipStream_t st) {
     const dim3 grid((unsigned)plan.parts(), (unsigned)H);
-    const size_t lds = 4 * (2 * (size_t)radius + 1) * sizeof(float);
-    hipLaunchKernelGGL((bias_grad_kernel<T, W>), grid, dim3(kThreads), lds, st, (const T*)ds,
+    const size_t lds = kGradWaves * (2 * (size_t)radius + 1) * sizeof(float);
+    hipLaunchKernelGGL((bias_grad_kernel<T, W>), grid, dim3(kGradThreads), lds, st, (const T*)ds,
                        partials, plan, B, H, radius, Tq, Tk, q_pos);
 }
 
@@ -246,13 +275,13 @@ hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t T
 
 // Few, large parts once there are workgroups enough to fill the card.
 BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
-    constexpr int64_t kWant = 2048;
+    constexpr int64_t kWant = 1024;
     BiasGradPlan p;
     const int32_t lanes = grad_lanes(Tk);
     p.col_blocks = (Tk + 8 * lanes - 1) / (8 * lanes);
-    p.rows = 32;
+    p.rows = 8 * kGradWaves;
     const auto blocks = [&] { return (int64_t)((Tq + p.rows - 1) / p.rows) * p.col_blocks * H; };
-    while (blocks() > 2 * kWant && p.rows < 1024) p.rows *= 2;
+    while (blocks() > kWant && p.rows < 1024) p.rows *= 2;
     p.row_blocks = (Tq + p.rows - 1) / p.rows;
     int64_t split = (kWant + blocks() - 1) / blocks();
     if (split > B) split = B;
@@ -264,8 +293,9 @@ BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
 hipError_t launch_bias_join(const float* partials, const int32_t* map, float* dtable, int32_t H,
                             int64_t parts, int32_t n_buckets, int32_t radius, bool accumulate,
                             hipStream_t st) {
-    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)H), dim3(kJoinThreads), 0, st, partials,
-                       map, dtable, H, parts, n_buckets, radius, accumulate ? 1 : 0);
+    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)n_buckets, (unsigned)H),
+                       dim3(kJoinThreads), 0,
+                       st, partials, map, dtable, H, (int32_t)parts, radius, accumulate ? 1 : 0);
     return hipGetLastError();
 }
 

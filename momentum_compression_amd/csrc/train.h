@@ -81,7 +81,7 @@ hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t T
 // Bias gradient: workgroups of a head (their partial sums are the workspace).
 struct BiasGradPlan {
     int32_t row_blocks;   // blocks of rows of the score map
-    int32_t rows;         // rows of a block, a multiple of 8
+    int32_t rows;         // rows of a block
     int32_t col_blocks;   // segments of columns
     int32_t batches;      // sequences of one workgroup
     int32_t batch_blocks;

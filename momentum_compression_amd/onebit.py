@@ -169,7 +169,7 @@ def _ptr(x) -> Optional[int]:
 
 
 def _on_gpu(t) -> bool:
-    return t.device.type == "cuda"
+    return t.is_cuda
 
 
 # element kinds of the C ABI's buffers and the tensor dtypes that carry them
@@ -202,7 +202,8 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: building a Stream object around it costs 2.7 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -398,10 +399,27 @@ def lamb_momentum_scale(m, N: int, seg_off, n_seg: int, k, ws, stream=None) -> N
 
 def _dtype(t, name: str):
     """(element kind, C ABI type) of a training operator's tensor."""
-    found = _DTYPES.get(str(t.dtype).replace("torch.", ""))
+    found = _BY_DTYPE.get(t.dtype)
     if found is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+        found = _DTYPES.get(str(t.dtype).replace("torch.", ""))
+        if found is None:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+        _BY_DTYPE[t.dtype] = found
     return found
+
+
+_BY_DTYPE = {}  # _DTYPES by the dtype object, as calls meet them
+
+
+def _stream_of(x, stream) -> Optional[int]:
+    """The call's stream; the tensors must live on the device that the call
+    launches on."""
+    import torch
+
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
 
 
 def _rows(x, rows: int, cols: int, kind: str, name: str):
@@ -410,17 +428,22 @@ def _rows(x, rows: int, cols: int, kind: str, name: str):
     shape whose rows are contiguous."""
     if x is None:
         return None, cols
-    if x.is_contiguous() or x.dim() != 2 or rows <= 1:
+    if x.is_contiguous():
+        found = _BY_DTYPE.get(x.dtype)
+        if found is not None and found[0] == kind and x.numel() >= rows * cols and _on_gpu(x):
+            return x.data_ptr(), cols
+        return _buf(x, rows * cols, kind, name), cols
+    if x.dim() != 2 or rows <= 1 and x.shape != (rows, cols):
         return _buf(x, rows * cols, kind, name), cols
     if tuple(x.shape) != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {(rows, cols)}")
-    if x.stride(1) != 1 or x.stride(0) < cols:
+    if (x.stride(1) != 1 and cols > 1) or (x.stride(0) < cols and rows > 1):
         raise ValueError(f"{name} must have contiguous, disjoint rows")
     if not _on_gpu(x):
         raise ValueError(f"{name} must be a device tensor (got {x.device})")
     if str(x.dtype).replace("torch.", "") not in _KINDS[kind]:
         raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
-    return x.data_ptr(), x.stride(0)
+    return x.data_ptr(), x.stride(0) if rows > 1 else cols
 
 
 def dropout_apply(x, y, rows: int, cols: int, p: float, seed: int, step: int, residual=None,
@@ -432,7 +455,7 @@ def dropout_apply(x, y, rows: int, cols: int, p: float, seed: int, step: int, re
     yp, ld_y = _rows(y, rows, cols, kind, "y")
     _check("dropout_apply", load().dropout_apply(
         xp, rp, yp, code, rows, cols, ld_x, ld_r, ld_y, p, seed & 0xFFFFFFFFFFFFFFFF,
-        step & 0xFFFFFFFF, _buf(step_dev, 1, "u32", "step_dev"), row0, _stream(stream)))
+        step & 0xFFFFFFFF, _buf(step_dev, 1, "u32", "step_dev"), row0, _stream_of(x, stream)))
 
 
 def _shape(t, dims: int, name: str):
@@ -460,7 +483,7 @@ def rel_bias_expand(table, bucket_map, out, q_pos: int = 0, stream=None) -> None
         _buf(table, n_buckets * H, "f32", "table"), _buf(bucket_map, 2 * radius + 1, "i32",
                                                          "bucket_map"),
         _buf(out, H * Tq * Tk, kind, "out"), code, H, n_buckets, radius, Tq, Tk, q_pos,
-        _stream(stream)))
+        _stream_of(out, stream)))
 
 
 def rel_bias_workspace_bytes(B: int, H: int, Tq: int, Tk: int, radius: int) -> int:
@@ -481,7 +504,7 @@ def rel_bias_grad(ds, bucket_map, dtable, q_pos: int = 0, accumulate: bool = Fal
                                                           "bucket_map"),
         _buf(dtable, n_buckets * H, "f32", "dtable"), B, H, n_buckets, radius, Tq, Tk, q_pos,
         int(bool(accumulate)), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream(stream)))
+        _stream_of(ds, stream)))
 
 
 def rel_attention_workspace_bytes(B: int, H: int, Hkv: int, Tq: int, Tk: int, D: int,
@@ -551,7 +574,7 @@ def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
                            seed, step, step_dev)
     _check("rel_attention_forward", load().rel_attention_forward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream(stream)))
+        _stream_of(q, stream)))
 
 
 def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumulate: bool = False,
@@ -572,4 +595,4 @@ def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumul
     a.accumulate = int(bool(accumulate))
     _check("rel_attention_backward", load().rel_attention_backward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream(stream)))
+        _stream_of(q, stream)))
