@@ -634,8 +634,8 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
     const int64_t heads = (int64_t)B * H;  // below 2^47
     // rows of a launch, and the workgroups of a split or unsplit grid
     if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16) return ONEBIT_E_SIZE;
-    if (!groups_ok(heads * attn_tiles(Tq) * attn_splits(B, H, Tq, Tk) + 8) ||
-        !groups_ok(heads * attn_tiles(Tk) + 8) || !groups_ok(ceil_div(heads * Tq, 4)))
+    if (!groups_ok((heads + 7) * attn_tiles(Tq) * attn_splits(B, H, Tq, Tk)) ||
+        !groups_ok((heads + 7) * attn_tiles(Tk)) || !groups_ok(ceil_div(heads * Tq, 4)))
         return ONEBIT_E_SIZE;
     return ONEBIT_OK;
 }

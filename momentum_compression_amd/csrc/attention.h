@@ -225,13 +225,20 @@ __device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b) {
     return n < 0 ? 0 : (n > a.Tk ? a.Tk : n);
 }
 
-// Workgroups go to the 8 XCDs in turn; this gives each XCD a contiguous run of
-// the work, so that the workgroups that read the same keys share an L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t n) {
-    const int64_t run = (n + 7) / 8;
-    return (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
+// Workgroups go to the 8 XCDs in turn.  The workgroups of one group (a
+// sequence's head) read the same rows, so they get numbers of one XCD and share
+// its L2; successive groups go to successive XCDs, which spreads sequences of
+// different lengths.  False for a number past the work.
+__device__ __forceinline__ bool xcd_work(uint32_t groups, uint32_t per_group, uint32_t& group,
+                                         uint32_t& item) {
+    const uint32_t slot = blockIdx.x >> 3;
+    group = (slot / per_group) * 8 + (blockIdx.x & 7);
+    item = slot % per_group;
+    return group < groups;
 }
-inline unsigned xcd_grid(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
+inline unsigned xcd_grid(int64_t groups, int64_t per_group) {
+    return (unsigned)((groups + 7) / 8 * 8 * per_group);
+}
 
 inline int32_t attn_tiles(int32_t T) { return (T + kTileRows - 1) / kTileRows; }
 

@@ -60,13 +60,11 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
-    const int tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
-    const int64_t work = (int64_t)a.B * a.H * tiles_q;
-    int64_t w = xcd_order(work);
-    if (w >= work) return;
-    const int qt = tiles_q - 1 - (int)(w % tiles_q);
-    w /= tiles_q;
-    const int h = (int)(w % a.H), b = (int)(w / a.H);
+    const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
+    uint32_t bh, item;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, bh, item)) return;
+    const int qt = (int)(tiles_q - 1 - item);
+    const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t iw = qt * kTileRows + wave * kRows;
@@ -289,14 +287,12 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
-    const int tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
-    const int64_t work = (int64_t)a.B * a.Hkv * tiles_k;
-    int64_t w = xcd_order(work);
-    if (w >= work) return;
+    const uint32_t tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
+    uint32_t bh, item;
+    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, bh, item)) return;
     // under a causal mask the first keys have the most queries: first
-    const int kt_i = (int)(w % tiles_k);
-    w /= tiles_k;
-    const int hk = (int)(w % a.Hkv), b = (int)(w / a.Hkv);
+    const int kt_i = (int)item;
+    const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
     const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t jw = kt_i * kTileRows + wave * kRows;
@@ -470,7 +466,7 @@ hipError_t run(const AttnArgs& a, bool table, hipStream_t st) {
     if (rows > 0) {
         hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((rows + 15) / 16)),
                            dim3(kThreads), 0, st, a);
-        const dim3 grid(xcd_grid((int64_t)a.B * a.H * attn_tiles(a.Tq)));
+        const dim3 grid(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq)));
         if (BIAS && table) {
             hipLaunchKernelGGL((attn_dq_kernel<T, DP, true, DROP, kDqExact>), grid, dim3(kThreads),
                                tiles, st, a);
@@ -485,7 +481,7 @@ hipError_t run(const AttnArgs& a, bool table, hipStream_t st) {
     }
     if (a.B > 0 && a.Tk > 0)
         hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP>),
-                           dim3(xcd_grid((int64_t)a.B * a.Hkv * attn_tiles(a.Tk))), dim3(kThreads),
+                           dim3(xcd_grid((int64_t)a.B * a.Hkv, attn_tiles(a.Tk))), dim3(kThreads),
                            tiles + 256 * sizeof(float), st, a);
     return hipGetLastError();
 }

@@ -22,16 +22,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
-    const int tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
-    const int64_t work = (int64_t)a.B * a.H * tiles_q * a.splits;
-    int64_t w = xcd_order(work);
-    if (w >= work) return;
-    const int split = (int)(w % a.splits);
-    w /= a.splits;
+    const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
+    uint32_t bh, item;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q * a.splits, bh, item)) return;
     // under a causal mask the last queries have the most keys: first
-    const int qt = tiles_q - 1 - (int)(w % tiles_q);
-    w /= tiles_q;
-    const int h = (int)(w % a.H), b = (int)(w / a.H);
+    const int qt = (int)(tiles_q - 1 - item / a.splits);
+    const int split = (int)(item % a.splits);
+    const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t iw = qt * kTileRows + wave * kRows;  // the wave's first query
@@ -39,7 +36,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     const int R = a.bias.radius;
 
     float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
-    if (BIAS) fill_window(window, a.bias, h);
 
     const T* kp = (const T*)a.k + b * a.sk.b + (int64_t)(h / (a.H / a.Hkv)) * a.sk.h;
     const T* vp = (const T*)a.v + b * a.sv.b + (int64_t)(h / (a.H / a.Hkv)) * a.sv.h;
@@ -72,6 +68,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
         ks.load(kp, a.sk.t, j0, n_keys, a.D);
         vs.load(vp, a.sv.t, j0, n_keys, a.D);
     }
+    if (BIAS) fill_window(window, a.bias, h);
     int buf = 0;
     __syncthreads();  // the window
     for (; j0 < end; j0 += kStep, buf ^= 1) {
@@ -96,10 +93,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
             for (int kc = 0; kc < kc_n; ++kc)
                 s[u] = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s[u]);
         }
-        // base-2 scores with their bias
+        // scores in base 2 are mul * s + add: where the tile has one bias value
+        // it stays in `add` and goes into the exponential's argument
         int kind = kNoBias;
         const int32_t d_lo = j0 - (iw + 31) - pos, d_hi = j0 + kStep - 1 - iw - pos;
         if (BIAS) kind = d_hi <= -R ? kBelow : (d_lo >= R ? kAbove : kWindow);
+        float mul = scale2, add = 0.0f;
         if (BIAS && kind == kWindow) {
             const float* at = window + (j0 + 8 * half - i - pos + R + kPad);
 #pragma unroll
@@ -107,12 +106,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     s[u][r] = __builtin_fmaf(s[u][r], scale2, at[32 * u + 16 * (r >> 3) + (r & 7)]);
-        } else {
-            const float c = !BIAS ? 0.0f : window[kind == kBelow ? 0 : 2 * R + 2 * kPad];
+            mul = 1.0f;
+        } else if (BIAS) {
+            add = window[kind == kBelow ? 0 : 2 * R + 2 * kPad];
+        }
+        if (!(scale2 > 0.0f) && mul != 1.0f) {  // the order of the scores is not s's
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[u][r] = __builtin_fmaf(s[u][r], scale2, c);
+            for (int u = 0; u < 2; ++u) s[u] *= scale2;
+            mul = 1.0f;
         }
         if (j0 + kStep - 1 > limit_lo) {
             const int32_t seen = limit - j0 - 8 * half;
@@ -127,16 +128,19 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
         for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-        mx = fmaxf(mx, other_half(mx));
-        const float m_new = fmaxf(m, mx);
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // no key seen yet
-        if (__any(m_new > m)) {
-            const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+        mx = __builtin_fmaf(fmaxf(mx, other_half(mx)), mul, add);
+        // The reference value m follows the maximum only when that is more
+        // than 2^8 above it: weights up to 256 lose nothing, and most tiles
+        // leave the sums as they are.
+        if (__any(mx > m + 8.0f)) {
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - m_new);
             l *= alpha;
 #pragma unroll
             for (int d = 0; d < db_n; ++d) acc[d] *= alpha;
             m = m_new;
         }
+        add -= m == -INFINITY ? 0.0f : m;  // no key seen yet
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -144,9 +148,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(s[u][8 * c + e] - m_use);
-                    l += p[e];
+                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * c + e], mul, add));
                 }
+                l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
                 if (DROP) {
                     uint32_t wd[4];
                     drop_draws(wd, (uint32_t)(j0 + 32 * u + 16 * c + 8 * half) >> 3, drop_row, step,
@@ -238,10 +242,9 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
 
 template <typename T, int DP, bool BIAS, bool DROP>
 void run(const AttnArgs& a, hipStream_t st) {
-    const int64_t work = (int64_t)a.B * a.H * attn_tiles(a.Tq) * a.splits;
     const size_t lds = 4 * tile_bytes<DP>() +
                        (BIAS ? (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float) : 0);
-    const dim3 grid(xcd_grid(work));
+    const dim3 grid(xcd_grid((int64_t)a.B * a.H, (int64_t)attn_tiles(a.Tq) * a.splits));
     if (a.splits > 1)
         hipLaunchKernelGGL((attn_fwd_kernel<T, DP, BIAS, DROP, true>), grid, dim3(kThreads), lds,
                            st, a);
