@@ -556,7 +556,7 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * as they are.  Sequences of a batch may share keys (stride 0); outputs must
  * not overlap each other or themselves.  lse [B][H][Tq] float, optional in
  * the forward pass.  table [n_buckets][H] float and map as rel_bias_expand,
- * or NULL, NULL, 0, 0 without a bias.  0 <= p < 1.
+ * or NULL, NULL, 0, 0 without a bias.  0 <= p < 1; scale positive and finite.
  * ws: at least rel_attention_workspace_bytes(...) bytes, 256-byte aligned,
  * scratch between calls (a forward call whose need is 256 takes NULL too).
  */

@@ -674,7 +674,7 @@ int check_attention(const rel_attention_args* a) {
         if (!a->table || !a->map) return ONEBIT_E_NULL;
         if ((st = check_bias_sizes(a->H, a->n_buckets, a->radius))) return st;
     }
-    if (!(a->p >= 0.0f && a->p < 1.0f) || !isfinite(a->scale) || !position_ok(a->q_pos) ||
+    if (!(a->p >= 0.0f && a->p < 1.0f) || !(a->scale > 0.0f && isfinite(a->scale)) || !position_ok(a->q_pos) ||
         (a->causal != 0 && a->causal != 1))
         return ONEBIT_E_ARG;
     if (!aligned(a->table, 4) || !aligned(a->map, 4) || !aligned(a->q_pos_of, 4) ||

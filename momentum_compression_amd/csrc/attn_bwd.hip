@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal != 0, bh, item)) return;
     const int qt = (int)(tiles_q - 1 - item);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
     float* skew = window + window_floats(R) + wave * 1024;  // [32 keys][32 queries] of the wave
     float* all_bins = window + window_floats(R) + kWaves * 1024;
     float* bins = all_bins + wave * bins_n;
-    if (BIAS) fill_window(window, a.bias, h);
+    if (BIAS) fill_window(window, a.bias, h, a.scale);
     if (MODE == kTable)
         for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
 
@@ -138,25 +138,24 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
             const int side = BIAS ? side_of(js, iw, pos, R) : 0;
             if (MODE == kTable && side != 0) continue;
             f32x16 s = {}, dp = {};
+            float add = -lse2;
+            if (BIAS && side == 0) {
+                const float* at = window + (js + 8 * half - i - pos + R + kPad);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = at[16 * (r >> 3) + (r & 7)];
+            } else if (BIAS) {
+                add = __builtin_fmaf(window[side < 0 ? 0 : 2 * R + 2 * kPad], scale2, -lse2);
+            }
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 s = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s);
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(vt, 32 * u, kc, lane), gf[kc], dp);
-            if (BIAS && side == 0) {
-                const float* at = window + (js + 8 * half - i - pos + R + kPad);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] = __builtin_fmaf(s[r], scale2, at[16 * (r >> 3) + (r & 7)]);
-            } else {
-                const float c = !BIAS ? 0.0f : window[side < 0 ? 0 : 2 * R + 2 * kPad];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], scale2, c);
-            }
             const int32_t seen = limit - js - 8 * half;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r] - lse2);
+            for (int r = 0; r < 16; ++r)
+                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, add));
             if (js + 31 > limit_lo) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -289,7 +288,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, a.causal != 0, bh, item)) return;
     // under a causal mask the first keys have the most queries: first
     const int kt_i = (int)item;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
@@ -342,7 +341,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         const float* delta = lse2 + 64;
         if (BIAS && filled != h) {
             __syncthreads();  // the other head's window is read
-            fill_window(window, a.bias, h);
+            fill_window(window, a.bias, h, a.scale);
             filled = h;
         }
         qs.store(qt);
@@ -362,27 +361,25 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             const int32_t is = it + 32 * u;
             if (is >= a.Tq || (a.causal && is + 31 + pos < jw) || jw >= n_keys) continue;
             f32x16 s = {}, dp = {};
+            const int side = BIAS ? side_of(jw, is, pos, R) : 0;
+            float add = 0.0f;
+            if (BIAS && side == 0) {
+                const float* at = window + (j - is - 8 * half - pos + R + kPad);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = at[-16 * (r >> 3) - (r & 7)];
+            } else if (BIAS) {
+                add = window[side < 0 ? 0 : 2 * R + 2 * kPad] * scale2;
+            }
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 s = Mma<T>::mul(row_frag<T, DP>(qt, 32 * u, kc, lane), kf[kc], s);
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(gt, 32 * u, kc, lane), vf[kc], dp);
-            const int side = BIAS ? side_of(jw, is, pos, R) : 0;
-            if (BIAS && side == 0) {
-                const float* at = window + (j - is - 8 * half - pos + R + kPad);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] = __builtin_fmaf(s[r], scale2, at[-16 * (r >> 3) - (r & 7)]);
-            } else {
-                const float c = !BIAS ? 0.0f : window[side < 0 ? 0 : 2 * R + 2 * kPad];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], scale2, c);
-            }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(
-                    s[r] - lse2[32 * u + 16 * (r >> 3) + 8 * half + (r & 7)]);
+                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(
+                    s[r], scale2, add - lse2[32 * u + 16 * (r >> 3) + 8 * half + (r & 7)]));
             if ((a.causal && is + pos < jw + 31) || jw + 31 >= n_keys) {
                 // a key past the sequence is seen by no query
                 const int32_t from = j >= n_keys ? 64 : (a.causal ? j - pos - is - 8 * half : 0);

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.H, tiles_q * a.splits, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q * a.splits, a.causal != 0, bh, item)) return;
     // under a causal mask the last queries have the most keys: first
     const int qt = (int)(tiles_q - 1 - item / a.splits);
     const int split = (int)(item % a.splits);
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
         ks.load(kp, a.sk.t, j0, n_keys, a.D);
         vs.load(vp, a.sv.t, j0, n_keys, a.D);
     }
-    if (BIAS) fill_window(window, a.bias, h);
+    if (BIAS) fill_window(window, a.bias, h, a.scale);
     int buf = 0;
     __syncthreads();  // the window
     for (; j0 < end; j0 += kStep, buf ^= 1) {
@@ -85,35 +85,27 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
         }
         if (j0 > limit_hi) continue;
 
-        f32x16 s[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = f32x16{};
-#pragma unroll
-            for (int kc = 0; kc < kc_n; ++kc)
-                s[u] = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s[u]);
-        }
-        // scores in base 2 are mul * s + add: where the tile has one bias value
-        // it stays in `add` and goes into the exponential's argument
+        // the products start from the bias; where the tile has one value of it
+        // that is added in the exponential's argument
         int kind = kNoBias;
         const int32_t d_lo = j0 - (iw + 31) - pos, d_hi = j0 + kStep - 1 - iw - pos;
         if (BIAS) kind = d_hi <= -R ? kBelow : (d_lo >= R ? kAbove : kWindow);
-        float mul = scale2, add = 0.0f;
+        f32x16 s[2] = {};
+        float add = 0.0f;
         if (BIAS && kind == kWindow) {
             const float* at = window + (j0 + 8 * half - i - pos + R + kPad);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[u][r] = __builtin_fmaf(s[u][r], scale2, at[32 * u + 16 * (r >> 3) + (r & 7)]);
-            mul = 1.0f;
+                for (int r = 0; r < 16; ++r) s[u][r] = at[32 * u + 16 * (r >> 3) + (r & 7)];
         } else if (BIAS) {
-            add = window[kind == kBelow ? 0 : 2 * R + 2 * kPad];
+            add = window[kind == kBelow ? 0 : 2 * R + 2 * kPad] * scale2;
         }
-        if (!(scale2 > 0.0f) && mul != 1.0f) {  // the order of the scores is not s's
 #pragma unroll
-            for (int u = 0; u < 2; ++u) s[u] *= scale2;
-            mul = 1.0f;
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                s[u] = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s[u]);
         }
         if (j0 + kStep - 1 > limit_lo) {
             const int32_t seen = limit - j0 - 8 * half;
@@ -128,7 +120,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
         for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-        mx = __builtin_fmaf(fmaxf(mx, other_half(mx)), mul, add);
+        mx = __builtin_fmaf(fmaxf(mx, other_half(mx)), scale2, add);
         // The reference value m follows the maximum only when that is more
         // than 2^8 above it: weights up to 256 lose nothing, and most tiles
         // leave the sums as they are.
@@ -148,7 +140,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * c + e], mul, add));
+                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * c + e], scale2, add));
                 }
                 l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
                 if (DROP) {

@@ -162,7 +162,7 @@ def test_attention_refusals(lib):
     assert lib.rel_attention_forward(None, P, 1, None) == ob.ONEBIT_E_NULL
     assert lib.rel_attention_backward(None, P, 1, None) == ob.ONEBIT_E_NULL
     for bad in (dict(dtype=0), dict(dtype=3), dict(p=1.0), dict(p=-1.0), dict(p=NAN),
-                dict(scale=NAN), dict(scale=float("inf")), dict(causal=2), dict(q_pos=1 << 30),
+                dict(scale=NAN), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(causal=2), dict(q_pos=1 << 30),
                 dict(q_pos=-(1 << 30))):
         assert both(**bad) == ob.ONEBIT_E_ARG, bad
     for bad in (dict(B=-1), dict(H=0), dict(H=5), dict(Hkv=0), dict(Hkv=3), dict(Tq=-1),
