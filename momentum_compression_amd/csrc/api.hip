@@ -642,8 +642,8 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
 
 // Workspace of the two directions, in the order it is carved.
 struct AttnSizes {
-    size_t split_o, split_ml;              // forward
-    size_t delta, exact, far, partials;    // backward
+    size_t split_o, split_ml;   // forward
+    size_t delta, partials;     // backward
 };
 
 AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t D, int32_t radius) {
@@ -655,12 +655,9 @@ AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t D, in
         z.split_ml = round_up(rows * splits * sizeof(float2));
     }
     z.delta = round_up(rows * sizeof(float));
-    if (radius > 0) {
-        const size_t parts = (size_t)B * attn_tiles(Tq) * H;
-        z.exact = round_up(rows * sizeof(float));
-        z.far = round_up(parts * sizeof(float2));
-        z.partials = round_up(parts * (2 * (size_t)radius + 1) * sizeof(float));
-    }
+    if (radius > 0)
+        z.partials = round_up((size_t)B * attn_tiles(Tk) * H * (2 * (size_t)radius + 1) *
+                              sizeof(float));
     return z;
 }
 
@@ -725,7 +722,7 @@ size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t 
     if (check_attention_sizes(B, H, Hkv, Tq, Tk, D, radius)) return 0;
     const AttnSizes z = attn_sizes(B, H, Tq, Tk, D, radius);
     const size_t fwd = z.split_o + z.split_ml;
-    const size_t bwd = z.delta + z.exact + z.far + z.partials;
+    const size_t bwd = z.delta + z.partials;
     const size_t need = backward && bwd > fwd ? bwd : fwd;
     return need ? need : 256;
 }
@@ -764,7 +761,7 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
         return ONEBIT_E_ARG;
     if (!aligned(a->dtable, 4)) return ONEBIT_E_ALIGN;
     const AttnSizes z = attn_sizes(a->B, a->H, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
-    if (!ws || ws_bytes < z.delta + z.exact + z.far + z.partials) return ONEBIT_E_WORKSPACE;
+    if (!ws || ws_bytes < z.delta + z.partials) return ONEBIT_E_WORKSPACE;
     if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     AttnArgs k = attn_args(a);
     k.d_o = a->d_o;
@@ -775,14 +772,8 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
     k.sdq = strides_of(a->dq_stride);
     k.sdk = strides_of(a->dk_stride);
     k.sdv = strides_of(a->dv_stride);
-    char* p = static_cast<char*>(ws);
-    k.delta = reinterpret_cast<float*>(p);
-    p += z.delta;
-    k.exact = reinterpret_cast<float*>(p);
-    p += z.exact;
-    k.far = reinterpret_cast<float2*>(p);
-    p += z.far;
-    k.partials = reinterpret_cast<float*>(p);
+    k.delta = static_cast<float*>(ws);
+    k.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + z.delta);
     drop_stale_error();
     return hip_status(launch_attn_backward(k, a->dtype, a->dtable, a->accumulate != 0, stream));
 }

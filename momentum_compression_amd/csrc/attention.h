@@ -35,9 +35,7 @@ struct AttnArgs {
     void *o, *dq, *dk, *dv;
     Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
     float* lse;           // [B][H][Tq] natural logarithm, or nullptr
-    float* delta;         // [B][H][Tq] row sums of dO * O
-    float* exact;         // [B][H][Tq] row sums of P * dP
-    float2* far;          // [H][parts] sums of dS before and past the radius
+    float* delta;         // [B][H][Tq] row sums of P * dP
     float* partials;      // distance sums [H][parts][2 radius + 1]
     float* split_o;       // [rows][splits][D] of a split forward
     float2* split_ml;     // [rows][splits] maximum (base 2) and sum

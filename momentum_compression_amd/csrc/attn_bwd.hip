@@ -15,28 +15,6 @@ namespace onebit {
 
 namespace {
 
-// delta from the rounded output: 16 lanes a row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void attn_delta_kernel(AttnArgs a) {
-    using x8 = typename Mma<T>::x8;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    const int c = 8 * (threadIdx.x & 15);
-    float s = 0.0f;
-    if (row < rows && c < a.D) {
-        const int64_t i = row % a.Tq, bh = row / a.Tq, h = bh % a.H, b = bh / a.H;
-        const x8 g = *reinterpret_cast<const x8*>((const T*)a.d_o + b * a.sdo.b + i * a.sdo.t +
-                                                  h * a.sdo.h + c);
-        const x8 o = *reinterpret_cast<const x8*>((const T*)a.o_in + b * a.so.b + i * a.so.t +
-                                                  h * a.so.h + c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = __builtin_fmaf((float)g[e], (float)o[e], s);
-    }
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor(s, off, 16);
-    if (row < rows && c == 0) a.delta[row] = s;
-}
-
 // Where the 32 x 32 scores of queries from i0 and keys from j0 lie against the
 // radius: -1 all at or before -radius, 1 all at or past it, 0 otherwise.
 __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int32_t R) {
@@ -44,19 +22,15 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
     return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
 }
 
-// Queries as columns.
-//   kDq       dq
-//   kDqExact  dq, and for the table the rows' exact delta and the sums of dS
-//             beyond the radius
-//   kTable    the sums of dS for each distance within the radius
-// dtable is held in binary32, where delta from the rounded output would show
-// (each row's error times the row's weight in a bucket); so kDqExact sums
-// P dP in binary32 as it goes, and kTable, which needs it finished, computes
-// the scores near the diagonal once more.
-enum DqMode { kDq, kDqExact, kTable };
-
-template <typename T, int DP, bool BIAS, bool DROP, int MODE>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
+// Queries as columns: dq and, for the second pass, delta.  dq takes delta from
+// the rounded output.  dtable is held in binary32, where that would show (each
+// row's error times the row's weight in a bucket), so with EXACT the row sums
+// of P dP are formed in binary32 on the way and handed on instead.
+//
+// The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
+// with dP' and delta' before it, and it enters once, with the result's scale.
+template <typename T, int DP, bool BIAS, bool DROP, bool EXACT>
+__global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
@@ -69,15 +43,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t iw = qt * kTileRows + wave * kRows;
     const int32_t i = iw + (lane & 31);
-    const int R = a.bias.radius, bins_n = 2 * R + 1;
+    const int R = a.bias.radius;
 
     float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
-    float* skew = window + window_floats(R) + wave * 1024;  // [32 keys][32 queries] of the wave
-    float* all_bins = window + window_floats(R) + kWaves * 1024;
-    float* bins = all_bins + wave * bins_n;
-    if (BIAS) fill_window(window, a.bias, h, a.scale);
-    if (MODE == kTable)
-        for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
 
     const int hk = h / (a.H / a.Hkv);
     const T* kp = (const T*)a.k + b * a.sk.b + hk * a.sk.h;
@@ -88,28 +56,32 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
                       lane);
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
     const float lse2 = i < a.Tq ? base2_lse(a.lse[row]) : INFINITY;
-    const float delta = i < a.Tq ? (MODE == kTable ? a.exact[row] : a.delta[row]) : 0.0f;
+    float delta = 0.0f;
+    {
+        x8 of[kc_n];
+        load_frags<T, DP>(of, (const T*)a.o_in + b * a.so.b + h * a.so.h, a.so.t, i, i < a.Tq, a.D,
+                          lane);
+#pragma unroll
+        for (int kc = 0; kc < kc_n; ++kc)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                delta = __builtin_fmaf((float)of[kc][e], (float)gf[kc][e], delta);
+    }
+    delta += other_half(delta);
+    if (!EXACT && i < a.Tq && half == 0) a.delta[row] = delta;
+    if (DROP) delta /= a.drop.scale;
 
     int32_t j0 = 0, end = n_keys;
     const int32_t last_q = (qt + 1) * kTileRows < a.Tq ? (qt + 1) * kTileRows - 1 : a.Tq - 1;
     if (a.causal && last_q + pos + 1 < end) end = last_q + pos + 1;
-    if (MODE == kTable) {
-        // keys within the radius of some query of the tile (of all 128, which
-        // is what side_of() goes by)
-        const int32_t lo = qt * kTileRows + pos - R + 1;
-        const int32_t hi = qt * kTileRows + kTileRows - 1 + pos + R;
-        if (lo > 0) j0 = lo / kStep * kStep;
-        if (hi < end) end = hi;
-    }
     const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
     const int32_t limit_lo = a.causal && iw + pos < n_keys - 1 ? iw + pos : n_keys - 1;
     const int32_t limit_hi = a.causal && iw + 31 + pos < n_keys - 1 ? iw + 31 + pos : n_keys - 1;
 
-    f32x16 acc[MODE == kTable ? 1 : db_n];
+    f32x16 acc[db_n];
 #pragma unroll
-    for (int d = 0; d < (MODE == kTable ? 1 : db_n); ++d) acc[d] = f32x16{};
-    // row sums of P dP: all, and with the sum of P before and past the radius
-    float sum = 0.0f, lo_d = 0.0f, lo_w = 0.0f, hi_d = 0.0f, hi_w = 0.0f;
+    for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
+    float sum = 0.0f;
     const float scale2 = a.scale * kLog2e;
     const uint64_t drop_row = (uint64_t)row;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
@@ -119,8 +91,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
         ks.load(kp, a.sk.t, j0, n_keys, a.D);
         vs.load(vp, a.sv.t, j0, n_keys, a.D);
     }
+    if (BIAS) fill_window(window, a.bias, h, a.scale);
     int buf = 0;
-    __syncthreads();  // the window and the bins
+    __syncthreads();  // the window
     for (; j0 < end; j0 += kStep, buf ^= 1) {
         char* kt = lds + buf * 2 * tile_bytes<DP>();
         char* vt = kt + tile_bytes<DP>();
@@ -136,7 +109,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
             const int32_t js = j0 + 32 * u;
             if (js > limit_hi) continue;
             const int side = BIAS ? side_of(js, iw, pos, R) : 0;
-            if (MODE == kTable && side != 0) continue;
             f32x16 s = {}, dp = {};
             float add = -lse2;
             if (BIAS && side == 0) {
@@ -169,119 +141,86 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(AttnArgs a) {
                                a.drop.k0, a.drop.k1);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        dp[8 * c + e] = drop_keep(wd, e, a.drop.threshold)
-                                            ? dp[8 * c + e] * a.drop.scale
-                                            : 0.0f;
+                        if (!drop_keep(wd, e, a.drop.threshold)) dp[8 * c + e] = 0.0f;
                 }
             }
-            if (MODE == kDqExact) {
-                float sd = 0.0f, sw = 0.0f;
+            if (EXACT) {
+                float part = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    sd = __builtin_fmaf(s[r], dp[r], sd);
-                    sw += s[r];
-                }
-                sum += sd;
-                if (side < 0) {
-                    lo_d += sd;
-                    lo_w += sw;
-                } else if (side > 0) {
-                    hi_d += sd;
-                    hi_w += sw;
-                }
+                for (int r = 0; r < 16; ++r) part = __builtin_fmaf(s[r], dp[r], part);
+                sum += part;
             }
             float ds[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - delta);
-            if (MODE != kTable) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const x8 db = pack8<T>(ds + 8 * c);
+            for (int c = 0; c < 2; ++c) {
+                const x8 db = pack8<T>(ds + 8 * c);
 #pragma unroll
-                    for (int d = 0; d < db_n; ++d)
-                        acc[d] = Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db,
-                                             acc[d]);
-                }
-            } else {
-                // down the 63 diagonals: the scores go through the wave's own
-                // square in LDS and lane x sums the diagonal x - 31, then adds
-                // it to the bin of its distance (no two lanes have the same)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    skew[(16 * (r >> 3) + 8 * half + (r & 7)) * 32 + (lane & 31)] = ds[r];
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                float v = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int q = j - lane + 31;
-                    const float x = skew[j * 32 + (q & 31)];
-                    v += (uint32_t)q < 32u ? x : 0.0f;
-                }
-                const int32_t d = js - iw - pos + lane - 31;
-                if (d <= -R) lo_d += v;
-                else if (d >= R) hi_d += v;
-                else bins[d + R] += v;
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
+                for (int d = 0; d < db_n; ++d)
+                    acc[d] =
+                        Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db, acc[d]);
             }
         }
     }
 
-    const int64_t part = (int64_t)b * tiles_q + qt, parts = (int64_t)a.B * tiles_q;
-    if (MODE != kTable) {
-        const float all = sum + other_half(sum);
-        if (MODE == kDqExact && i < a.Tq && half == 0) a.exact[row] = all;
-        if (i < a.Tq) {
-            T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
+    if (EXACT) sum += other_half(sum);
+    if (i >= a.Tq) return;
+    if (EXACT && half == 0) a.delta[row] = DROP ? sum * a.drop.scale : sum;
+    const float out = DROP ? a.scale * a.drop.scale : a.scale;
+    T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
 #pragma unroll
-            for (int d = 0; d < db_n; ++d)
+    for (int d = 0; d < db_n; ++d)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int c = 32 * d + 8 * g + 4 * half;
-                    if (c >= a.D) continue;
-                    typename Mma<T>::x4 v;
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * half;
+            if (c >= a.D) continue;
+            typename Mma<T>::x4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * a.scale);
-                    *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
-                }
+            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * out);
+            *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
         }
-        if (MODE == kDq) return;
-        lo_d -= all * lo_w;
-        hi_d -= all * hi_w;
+}
+
+// Sums down the diagonals of the 32 x 32 scores' gradients of a wave (queries
+// as rows, eight consecutive ones to a lane) and adds them to the wave's bins.
+// The values go through the wave's own square in LDS.  Lane x + 32 g reads, of
+// the queries 16 g ... 16 g + 15, the key (q + x + 1) mod 32: those before the
+// wrap lie on the diagonal x + 1, the others on x - 31, so 16 reads a lane
+// serve all 63 diagonals.  No two lanes own the same one: no atomics.
+// first: the distance of diagonal 0.
+__device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* square, float* bins,
+                                              int32_t first, int R, float& below, float& above,
+                                              int lane) {
+    const int x = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        square[(16 * (r >> 3) + 8 * half + (r & 7)) * 32 + x] = ds[r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float all = 0.0f, up = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+        const int q = 16 * half + t;
+        const float v = square[q * 32 + ((q + x + 1) & 31)];
+        all += v;
+        up += q + x + 1 < 32 ? v : 0.0f;
     }
-    if (MODE != kDq) {
-        for (int off = 32; off > 0; off >>= 1) {
-            lo_d += __shfl_xor(lo_d, off, 64);
-            hi_d += __shfl_xor(hi_d, off, 64);
-        }
-        __syncthreads();  // the tiles are read; the bins complete
-        float2* sums = reinterpret_cast<float2*>(lds);
-        if (lane == 0) sums[wave] = float2{lo_d, hi_d};
-        __syncthreads();
-        if (MODE == kDqExact) {
-            if (threadIdx.x == 0) {
-                const float lo = (sums[0].x + sums[1].x) + (sums[2].x + sums[3].x);
-                const float hi = (sums[0].y + sums[1].y) + (sums[2].y + sums[3].y);
-                a.far[h * parts + part] = float2{lo, hi};
-            }
-        } else {
-            const float2 far = a.far[h * parts + part];
-            float* to = a.partials + (h * parts + part) * bins_n;
-            for (int x = threadIdx.x; x < bins_n; x += kThreads) {
-                float v = (all_bins[x] + all_bins[bins_n + x]) +
-                          (all_bins[2 * bins_n + x] + all_bins[3 * bins_n + x]);
-                if (x == 0) v = far.x + ((sums[0].x + sums[1].x) + (sums[2].x + sums[3].x));
-                if (x == 2 * R) v = far.y + ((sums[0].y + sums[1].y) + (sums[2].y + sums[3].y));
-                to[x] = v;
-            }
-        }
-    }
+    const float down = (all - up) + other_half(all - up);
+    up += other_half(up);
+    const float v = half ? up : down;
+    const int32_t d = first + x + (half ? 1 : -31);
+    if (d <= -R) below += v;
+    else if (d >= R) above += v;
+    else if (half == 0 || x < 31) bins[d + R] += v;  // lane 63 owns none
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Keys as columns: dk and dv of 128 keys of one key head, over every query of
-// the heads that share it, in order.
-template <typename T, int DP, bool BIAS, bool DROP>
+// the heads that share it, in order; with TABLE the sums of dS (from the exact
+// delta, unrounded) for each distance, one part a workgroup and head.
+template <typename T, int DP, bool BIAS, bool DROP, bool TABLE>
 __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
@@ -296,11 +235,15 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t jw = kt_i * kTileRows + wave * kRows;
     const int32_t j = jw + (lane & 31);
-    const int R = a.bias.radius, group = a.H / a.Hkv;
+    const int R = a.bias.radius, group = a.H / a.Hkv, bins_n = 2 * R + 1;
 
-    float* window = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
     // lse and delta of a tile's queries, two buffers
-    float* rows_lds = window + (BIAS ? window_floats(R) : 0);
+    float* rows_lds = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
+    float* square = rows_lds + 256 + (TABLE ? wave * 1024 : 0);
+    float* window = rows_lds + 256 + (TABLE ? kWaves * 1024 : 0);
+    float* all_bins = window + window_floats(R);
+    float* bins = all_bins + wave * bins_n;
+    float below = 0.0f, above = 0.0f;  // dS at or past the radius
 
     x8 kf[kc_n], vf[kc_n];
     load_frags<T, DP>(kf, (const T*)a.k + b * a.sk.b + hk * a.sk.h, a.sk.t, j, j < n_keys, a.D,
@@ -312,6 +255,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     for (int d = 0; d < db_n; ++d) dk[d] = dv[d] = f32x16{};
     const float scale2 = a.scale * kLog2e;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+    const float drop_inv = DROP ? 1.0f / a.drop.scale : 1.0f;
 
     // queries that see a key of the tile, for each head of the group in turn
     int32_t first = a.causal ? kt_i * kTileRows - pos : 0;
@@ -328,19 +272,44 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         gs.load((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, i0, a.Tq, a.D);
         const int32_t i = i0 + (int)(threadIdx.x & 63);
         const int64_t row = ((int64_t)b * a.H + head) * a.Tq + i;
-        if (threadIdx.x < 64) row_value = i < a.Tq ? base2_lse(a.lse[row]) : INFINITY;
-        else if (threadIdx.x < 128) row_value = i < a.Tq ? a.delta[row] : 0.0f;
+        if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
+        else if (threadIdx.x < 128) row_value = i < a.Tq ? a.delta[row] * drop_inv : 0.0f;
     };
+    // one head's sums to its part; its bins are complete
+    const auto flush = [&](int h) {
+        for (int off = 32; off > 0; off >>= 1) {
+            below += __shfl_xor(below, off, 64);
+            above += __shfl_xor(above, off, 64);
+        }
+        if (lane == 0) {
+            bins[0] = below;
+            bins[2 * R] = above;
+        }
+        below = above = 0.0f;
+        __syncthreads();
+        const int64_t part = (int64_t)b * tiles_k + kt_i, parts = (int64_t)a.B * tiles_k;
+        float* to = a.partials + ((int64_t)h * parts + part) * bins_n;
+        for (int x = threadIdx.x; x < bins_n; x += kThreads) {
+            const float v = (all_bins[x] + all_bins[bins_n + x]) +
+                            (all_bins[2 * bins_n + x] + all_bins[3 * bins_n + x]);
+            to[x] = DROP ? v * a.drop.scale : v;
+        }
+        __syncthreads();
+        for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
+    };
+    if (TABLE)
+        for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
     if (total > 0) load();
     int buf = 0, filled = -1;
     for (int64_t t = 0; t < total; ++t, buf ^= 1) {
         const int32_t h = head, it = i0;  // this tile
         char* qt = lds + buf * 2 * tile_bytes<DP>();
         char* gt = qt + tile_bytes<DP>();
-        float* lse2 = rows_lds + buf * 128;
+        float* lse2 = rows_lds + buf * 128;  // negative
         const float* delta = lse2 + 64;
         if (BIAS && filled != h) {
             __syncthreads();  // the other head's window is read
+            if (TABLE && filled >= 0) flush(filled);
             fill_window(window, a.bias, h, a.scale);
             filled = h;
         }
@@ -376,10 +345,13 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(gt, 32 * u, kc, lane), vf[kc], dp);
+            const float* lse_at = lse2 + 32 * u + 8 * half;
+            const float* delta_at = delta + 32 * u + 8 * half;
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(
-                    s[r], scale2, add - lse2[32 * u + 16 * (r >> 3) + 8 * half + (r & 7)]));
+            for (int r = 0; r < 16; ++r) {
+                const float l = lse_at[16 * (r >> 3) + (r & 7)];
+                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, BIAS ? add + l : l));
+            }
             if ((a.causal && is + pos < jw + 31) || jw + 31 >= n_keys) {
                 // a key past the sequence is seen by no query
                 const int32_t from = j >= n_keys ? 64 : (a.causal ? j - pos - is - 8 * half : 0);
@@ -406,36 +378,52 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                 kept <<= 16 * half;
                 kept |= __float_as_uint(other_half(__uint_as_float(kept)));
             }
-            float ds[16];
+            float ds[16], p[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int q = 16 * (r >> 3) + (r & 7);
-                float p = s[r], g = dp[r];
+                float g = dp[r];
+                p[r] = s[r];
                 if (DROP) {
                     const uint64_t mask =
                         (uint32_t)__builtin_amdgcn_readlane((int)kept, q) |
                         ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)kept, q + 8) << 32);
                     const bool keep = __builtin_amdgcn_inverse_ballot_w64(mask);
-                    g = keep ? g * a.drop.scale : 0.0f;
-                    s[r] = keep ? p * a.drop.scale : 0.0f;
+                    if (!keep) p[r] = g = 0.0f;
                 }
-                ds[r] = p * (g - delta[32 * u + 8 * half + q]);
+                ds[r] = s[r] * (g - delta_at[q]);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = s[8 * c + e];
-                const x8 pb = pack8<T>(p), db = pack8<T>(ds + 8 * c);
+                const x8 pb = pack8<T>(p + 8 * c), db = pack8<T>(ds + 8 * c);
 #pragma unroll
                 for (int d = 0; d < db_n; ++d) {
                     dv[d] = Mma<T>::mul(col_frag<T, DP>(gt, 32 * u + 16 * c, d, lane), pb, dv[d]);
                     dk[d] = Mma<T>::mul(col_frag<T, DP>(qt, 32 * u + 16 * c, d, lane), db, dk[d]);
                 }
             }
+            if (TABLE) {
+                if (side == 0) {
+                    add_diagonals(ds, square, bins, jw - is - pos, R, below, above, lane);
+                } else {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) v += ds[r];
+                    if (side < 0) below += v;
+                    else above += v;
+                }
+            }
         }
     }
+    if (TABLE) {
+        // the last head's part, and those of a group that saw no query
+        __syncthreads();
+        if (filled >= 0) flush(filled);
+        else
+            for (int h = hk * group; h < (hk + 1) * group; ++h) flush(h);
+    }
     if (j >= a.Tk) return;
+    const float out_v = DROP ? a.drop.scale : 1.0f, out_k = a.scale * out_v;
     T* to_k = (T*)a.dk + b * a.sdk.b + (int64_t)j * a.sdk.t + hk * a.sdk.h;
     T* to_v = (T*)a.dv + b * a.sdv.b + (int64_t)j * a.sdv.t + hk * a.sdv.h;
 #pragma unroll
@@ -447,47 +435,39 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             typename Mma<T>::x4 x, y;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[e] = (T)(dk[d][4 * g + e] * a.scale);
-                y[e] = (T)dv[d][4 * g + e];
+                x[e] = (T)(dk[d][4 * g + e] * out_k);
+                y[e] = (T)(dv[d][4 * g + e] * out_v);
             }
             *reinterpret_cast<typename Mma<T>::x4*>(to_k + c) = x;
             *reinterpret_cast<typename Mma<T>::x4*>(to_v + c) = y;
         }
 }
 
-template <typename T, int DP, bool BIAS, bool DROP>
-hipError_t run(const AttnArgs& a, bool table, hipStream_t st) {
-    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    const size_t window = BIAS ? (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float) : 0;
-    const size_t tiles = 4 * tile_bytes<DP>() + window;
-    if (rows > 0) {
-        hipLaunchKernelGGL((attn_delta_kernel<T>), dim3((unsigned)((rows + 15) / 16)),
-                           dim3(kThreads), 0, st, a);
-        const dim3 grid(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq)));
-        if (BIAS && table) {
-            hipLaunchKernelGGL((attn_dq_kernel<T, DP, true, DROP, kDqExact>), grid, dim3(kThreads),
-                               tiles, st, a);
-            const size_t lds = tiles + kWaves * 1024 * sizeof(float) +
-                               kWaves * (2 * (size_t)a.bias.radius + 1) * sizeof(float);
-            hipLaunchKernelGGL((attn_dq_kernel<T, DP, true, DROP, kTable>), grid, dim3(kThreads),
-                               lds, st, a);
-        } else {
-            hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, DROP, kDq>), grid, dim3(kThreads),
-                               tiles, st, a);
-        }
-    }
-    if (a.B > 0 && a.Tk > 0)
-        hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP>),
+template <typename T, int DP, bool BIAS, bool DROP, bool TABLE>
+hipError_t run(const AttnArgs& a, hipStream_t st) {
+    const size_t window = (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float);
+    const size_t tiles = 4 * tile_bytes<DP>();
+    if ((int64_t)a.B * a.Tq > 0)
+        hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, DROP, TABLE>),
+                           dim3(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq))), dim3(kThreads),
+                           tiles + (BIAS ? window : 0), st, a);
+    if ((int64_t)a.B * a.Tk > 0) {
+        size_t lds = tiles + 256 * sizeof(float) + (BIAS ? window : 0);
+        if (TABLE)
+            lds += kWaves * (1024 + 2 * (size_t)a.bias.radius + 1) * sizeof(float);
+        hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP, TABLE>),
                            dim3(xcd_grid((int64_t)a.B * a.Hkv, attn_tiles(a.Tk))), dim3(kThreads),
-                           tiles + 256 * sizeof(float), st, a);
+                           lds, st, a);
+    }
     return hipGetLastError();
 }
 
 template <typename T, int DP>
 hipError_t run_d(const AttnArgs& a, bool table, hipStream_t st) {
     const bool bias = a.bias.radius > 0, drop = a.drop.threshold != kDropAll;
-    if (bias) return drop ? run<T, DP, true, true>(a, table, st) : run<T, DP, true, false>(a, table, st);
-    return drop ? run<T, DP, false, true>(a, table, st) : run<T, DP, false, false>(a, table, st);
+    if (table) return drop ? run<T, DP, true, true, true>(a, st) : run<T, DP, true, false, true>(a, st);
+    if (bias) return drop ? run<T, DP, true, true, false>(a, st) : run<T, DP, true, false, false>(a, st);
+    return drop ? run<T, DP, false, true, false>(a, st) : run<T, DP, false, false, false>(a, st);
 }
 
 }  // namespace
@@ -500,10 +480,9 @@ hipError_t launch_attn_backward(const AttnArgs& a, int32_t dtype, float* dtable,
     else
         e = a.D <= 64 ? run_d<f16, 64>(a, dtable, st) : run_d<f16, 128>(a, dtable, st);
     if (e != hipSuccess || !dtable) return e;
-    const bool none = a.B == 0 || a.Tq == 0;
     return launch_bias_join(a.partials, a.bias.map, dtable, a.H,
-                            none ? 0 : (int64_t)a.B * attn_tiles(a.Tq), a.bias.n_buckets,
-                            a.bias.radius, accumulate, st);
+                            (int64_t)a.B * attn_tiles(a.Tk), a.bias.n_buckets, a.bias.radius,
+                            accumulate, st);
 }
 
 }  // namespace onebit
