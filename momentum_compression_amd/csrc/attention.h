@@ -189,6 +189,11 @@ __device__ __forceinline__ typename Mma<T>::x8 pack8(const float* p) {
     return r;
 }
 
+// The wave's number as a scalar, so that what follows from it branches as one.
+__device__ __forceinline__ int wave_id() {
+    return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
 // The value the other half of the wave holds for the same column.
 __device__ __forceinline__ float other_half(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,

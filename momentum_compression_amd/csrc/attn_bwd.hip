@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
     if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal != 0, bh, item)) return;
     const int qt = (int)(tiles_q - 1 - item);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
-    const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
+    const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t iw = qt * kTileRows + wave * kRows;
     const int32_t i = iw + (lane & 31);
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
             ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
             vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
         }
-#pragma unroll
+#pragma nounroll
         for (int u = 0; u < 2; ++u) {
             const int32_t js = j0 + 32 * u;
             if (js > limit_hi) continue;
@@ -192,7 +192,11 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
 __device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* square, float* bins,
                                               int32_t first, int R, float& below, float& above,
                                               int lane) {
-    const int x = lane & 31, half = lane >> 5;
+    int x = lane & 31;
+    const int half = lane >> 5;
+    // sixteen comparisons with x kept over the loop would take 32 scalar
+    // registers; they are made where they are used
+    asm volatile("" : "+v"(x));
 #pragma unroll
     for (int r = 0; r < 16; ++r)
         square[(16 * (r >> 3) + 8 * half + (r & 7)) * 32 + x] = ds[r];
@@ -231,16 +235,17 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     // under a causal mask the first keys have the most queries: first
     const int kt_i = (int)item;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
-    const int lane = lane_id(), wave = threadIdx.x >> 6, half = lane >> 5;
+    const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
     const int32_t jw = kt_i * kTileRows + wave * kRows;
     const int32_t j = jw + (lane & 31);
     const int R = a.bias.radius, group = a.H / a.Hkv, bins_n = 2 * R + 1;
 
-    // lse and delta of a tile's queries, two buffers
+    // negative lse and delta of a tile's queries, two buffers
     float* rows_lds = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
-    float* square = rows_lds + 256 + (TABLE ? wave * 1024 : 0);
-    float* window = rows_lds + 256 + (TABLE ? kWaves * 1024 : 0);
+    uint32_t* kept_lds = reinterpret_cast<uint32_t*>(rows_lds + 256) + wave * 32;
+    float* square = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? wave * 1024 : 0);
+    float* window = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? kWaves * 1024 : 0);
     float* all_bins = window + window_floats(R);
     float* bins = all_bins + wave * bins_n;
     float below = 0.0f, above = 0.0f;  // dS at or past the radius
@@ -255,6 +260,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     for (int d = 0; d < db_n; ++d) dk[d] = dv[d] = f32x16{};
     const float scale2 = a.scale * kLog2e;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+    const int key_bit = drop_bit(lane & 31);
     const float drop_inv = DROP ? 1.0f / a.drop.scale : 1.0f;
 
     // queries that see a key of the tile, for each head of the group in turn
@@ -273,7 +279,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         const int32_t i = i0 + (int)(threadIdx.x & 63);
         const int64_t row = ((int64_t)b * a.H + head) * a.Tq + i;
         if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
-        else if (threadIdx.x < 128) row_value = i < a.Tq ? a.delta[row] * drop_inv : 0.0f;
+        else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] * drop_inv : 0.0f;
     };
     // one head's sums to its part; its bins are complete
     const auto flush = [&](int h) {
@@ -305,7 +311,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         const int32_t h = head, it = i0;  // this tile
         char* qt = lds + buf * 2 * tile_bytes<DP>();
         char* gt = qt + tile_bytes<DP>();
-        float* lse2 = rows_lds + buf * 128;  // negative
+        float* lse2 = rows_lds + buf * 128;
         const float* delta = lse2 + 64;
         if (BIAS && filled != h) {
             __syncthreads();  // the other head's window is read
@@ -325,33 +331,36 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             }
             load();
         }
-#pragma unroll
+#pragma nounroll
         for (int u = 0; u < 2; ++u) {
             const int32_t is = it + 32 * u;
             if (is >= a.Tq || (a.causal && is + 31 + pos < jw) || jw >= n_keys) continue;
-            f32x16 s = {}, dp = {};
+            const float* lse_at = lse2 + 32 * u + 8 * half;
+            const float* delta_at = delta + 32 * u + 8 * half;
+            // the scores start from the bias, dP from -delta
+            f32x16 s = {}, dp;
             const int side = BIAS ? side_of(jw, is, pos, R) : 0;
-            float add = 0.0f;
             if (BIAS && side == 0) {
                 const float* at = window + (j - is - 8 * half - pos + R + kPad);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = at[-16 * (r >> 3) - (r & 7)];
             } else if (BIAS) {
-                add = window[side < 0 ? 0 : 2 * R + 2 * kPad] * scale2;
+                const float c = window[side < 0 ? 0 : 2 * R + 2 * kPad];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = c;
             }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] = delta_at[16 * (r >> 3) + (r & 7)];
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 s = Mma<T>::mul(row_frag<T, DP>(qt, 32 * u, kc, lane), kf[kc], s);
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(gt, 32 * u, kc, lane), vf[kc], dp);
-            const float* lse_at = lse2 + 32 * u + 8 * half;
-            const float* delta_at = delta + 32 * u + 8 * half;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float l = lse_at[16 * (r >> 3) + (r & 7)];
-                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, BIAS ? add + l : l));
-            }
+            for (int r = 0; r < 16; ++r)
+                s[r] = __builtin_amdgcn_exp2f(
+                    __builtin_fmaf(s[r], scale2, lse_at[16 * (r >> 3) + (r & 7)]));
             if ((a.causal && is + pos < jw + 31) || jw + 31 >= n_keys) {
                 // a key past the sequence is seen by no query
                 const int32_t from = j >= n_keys ? 64 : (a.causal ? j - pos - is - 8 * half : 0);
@@ -359,39 +368,41 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                 for (int r = 0; r < 16; ++r)
                     if (16 * (r >> 3) + (r & 7) < from) s[r] = 0.0f;
             }
-            uint32_t kept = 0;
             if (DROP) {
                 // lane (query q, half) draws the keys 16 half ... + 15 of its
-                // query; joined, a query's 32 decisions are the lane mask of
-                // the register that holds it
+                // query; a query's 32 decisions go to LDS as a word, bit
+                // drop_bit(key)
                 const uint64_t row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq +
                                      (uint64_t)(is + (lane & 31));
+                uint32_t dropped = 0;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t wd[4];
                     drop_draws(wd, (uint32_t)(jw + 16 * half + 8 * c) >> 3, row, step, a.drop.k0,
                                a.drop.k1);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        kept |= (drop_keep(wd, e, a.drop.threshold) ? 1u : 0u) << (8 * c + e);
+                    for (int k = 0; k < 4; ++k)
+                        dropped |= drop_pair(wd[k], a.drop.threshold) << (4 * c + k);
                 }
-                kept <<= 16 * half;
-                kept |= __float_as_uint(other_half(__uint_as_float(kept)));
+                dropped <<= 8 * half;
+                dropped |= __float_as_uint(other_half(__uint_as_float(dropped)));
+                if (half == 0) kept_lds[lane] = ~dropped;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
             }
             float ds[16], p[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int q = 16 * (r >> 3) + (r & 7);
-                float g = dp[r];
                 p[r] = s[r];
+                float g = dp[r];
                 if (DROP) {
-                    const uint64_t mask =
-                        (uint32_t)__builtin_amdgcn_readlane((int)kept, q) |
-                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)kept, q + 8) << 32);
-                    const bool keep = __builtin_amdgcn_inverse_ballot_w64(mask);
-                    if (!keep) p[r] = g = 0.0f;
+                    const int m = __builtin_amdgcn_sbfe((int)kept_lds[q + 8 * half], key_bit, 1);
+                    p[r] = __int_as_float(__float_as_int(p[r]) & m);
+                    g = __int_as_float((__float_as_int(g) & m) |
+                                       (__float_as_int(delta_at[q]) & ~m));
                 }
-                ds[r] = s[r] * (g - delta_at[q]);
+                ds[r] = s[r] * g;
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -401,6 +412,10 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                     dv[d] = Mma<T>::mul(col_frag<T, DP>(gt, 32 * u + 16 * c, d, lane), pb, dv[d]);
                     dk[d] = Mma<T>::mul(col_frag<T, DP>(qt, 32 * u + 16 * c, d, lane), db, dk[d]);
                 }
+            }
+            if (DROP) {  // the words are read before the next ones are written
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
             }
             if (TABLE) {
                 if (side == 0) {
@@ -452,7 +467,7 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
                            dim3(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq))), dim3(kThreads),
                            tiles + (BIAS ? window : 0), st, a);
     if ((int64_t)a.B * a.Tk > 0) {
-        size_t lds = tiles + 256 * sizeof(float) + (BIAS ? window : 0);
+        size_t lds = tiles + (256 + (DROP ? kWaves * 32 : 0)) * sizeof(float) + (BIAS ? window : 0);
         if (TABLE)
             lds += kWaves * (1024 + 2 * (size_t)a.bias.radius + 1) * sizeof(float);
         hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP, TABLE>),

@@ -81,4 +81,20 @@ __device__ __forceinline__ bool drop_keep(const uint32_t w[4], int e, uint32_t t
     return u < threshold;
 }
 
+// The two decisions of one word at once: bit 0 and bit 16 set where the low
+// and the high draw drop their element (saturating 16-bit arithmetic).
+__device__ __forceinline__ uint32_t drop_pair(uint32_t w, uint32_t threshold) {
+    using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+    const uint16_t t = (uint16_t)(threshold - 1);
+    const u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w), u16x2{t, t});
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(over, u16x2{1, 1}));
+}
+
+// Where 32 columns' decisions lie when drop_pair's words of their four groups
+// are gathered, word k of group g shifted by 4 g + k: even columns in the low
+// half, odd ones in the high half.
+__device__ __forceinline__ int drop_bit(int column) {
+    return 16 * (column & 1) + 4 * (column >> 3) + ((column >> 1) & 3);
+}
+
 }  // namespace onebit
