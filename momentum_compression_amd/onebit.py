@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -182,6 +183,16 @@ _DTYPES = {"float32": ("f32", ONEBIT_F32), "bfloat16": ("bf16", ONEBIT_BF16),
            "float16": ("f16", ONEBIT_F16)}
 
 
+_NAMES = {}  # dtype objects' names, as calls meet them
+
+
+def _name(dtype) -> str:
+    found = _NAMES.get(dtype)
+    if found is None:
+        found = _NAMES[dtype] = str(dtype).replace("torch.", "")
+    return found
+
+
 def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
     """Device pointer of a tensor argument that must hold at least ``count``
     elements of ``kind``.  Plain integers (raw device addresses) pass as they
@@ -191,7 +202,7 @@ def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
         return x
     if not _on_gpu(x):
         raise ValueError(f"{name} must be a device tensor (got {x.device})")
-    if str(x.dtype).replace("torch.", "") not in _KINDS[kind]:
+    if _name(x.dtype) not in _KINDS[kind]:
         raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
     if x.numel() < count:
         raise ValueError(f"{name} holds {x.numel()} elements, the call needs {count}")
@@ -513,54 +524,70 @@ def rel_attention_workspace_bytes(B: int, H: int, Hkv: int, Tq: int, Tk: int, D:
                                                     int(bool(backward))))
 
 
-def _heads(a, field: str, x, shape, kind: str, name: str, stride: str = None) -> None:
-    """Puts a [B, T, heads, D] tensor (any strides, D side by side) into the
-    argument struct."""
-    if tuple(x.shape) != tuple(shape):
+def _heads(x, shape, dtype, name: str):
+    """(device pointer, strides of sequences, tokens and heads) of a
+    [B, T, heads, D] tensor of any strides, D side by side."""
+    st = x.stride()
+    if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {tuple(shape)}")
     if not _on_gpu(x):
         raise ValueError(f"{name} must be a device tensor (got {x.device})")
-    if str(x.dtype).replace("torch.", "") not in _KINDS[kind]:
-        raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
-    if x.numel() and x.stride(3) != 1 and shape[3] > 1:
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} (got {x.dtype})")
+    if st[3] != 1 and shape[3] > 1 and x.numel():
         raise ValueError(f"{name}: the elements of a head must lie side by side")
-    setattr(a, field, x.data_ptr())
     # a dimension of one element has no stride of its own
-    setattr(a, stride or f"{field}_stride",
-            (_c_i64 * 3)(*[x.stride(d) if x.shape[d] > 1 else 0 for d in range(3)]))
+    return (x.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0,
+            st[2] if shape[2] > 1 else 0)
+
+
+# rel_attention_args as one packing: the struct's fields in order (its size and
+# offsets are checked against the declaration by the tests)
+_ATTENTION = struct.Struct("<11i2fIQ10q12q4q12qqi4x")
+_NONE = (0, 0, 0, 0)
 
 
 def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed, step,
-                    step_dev):
+                    step_dev, do=None, dq=None, dk=None, dv=None, dtable=None, accumulate=False):
+    q_shape, k_shape = q.shape, k.shape
     B, Tq, H, D = _shape(q, 4, "q")
     _, Tk, Hkv, _ = _shape(k, 4, "k")
     kind, code = _dtype(q, "q")
     if kind == "f32":
         raise ValueError("attention takes bfloat16 or float16 (got torch.float32)")
-    a = RelAttentionArgs(dtype=code, B=B, H=H, Hkv=Hkv, Tq=Tq, Tk=Tk, D=D,
-                         causal=int(bool(causal)), p=p, seed=seed & 0xFFFFFFFFFFFFFFFF,
-                         step=step & 0xFFFFFFFF, scale=D ** -0.5 if scale is None else scale)
-    _heads(a, "q", q, (B, Tq, H, D), kind, "q")
-    _heads(a, "k", k, (B, Tk, Hkv, D), kind, "k")
-    _heads(a, "v", v, (B, Tk, Hkv, D), kind, "v")
-    _heads(a, "o", o, (B, Tq, H, D), kind, "o")
-    a.lse = _buf(lse, B * H * Tq, "f32", "lse")
-    a.step_dev = _buf(step_dev, 1, "u32", "step_dev")
-    a.k_len = _buf(k_len, B, "i32", "k_len")
+    dt = q.dtype
+    kv_shape = (B, Tk, Hkv, D)
+    qp, kp = _heads(q, q_shape, dt, "q"), _heads(k, kv_shape, dt, "k")
+    vp, op = _heads(v, kv_shape, dt, "v"), _heads(o, q_shape, dt, "o")
+    n_buckets = radius = tp = mp = pos = 0
+    pos_of = None
     if isinstance(q_pos, int):
-        a.q_pos = q_pos
+        pos = q_pos
     else:
-        a.q_pos_of = _buf(q_pos, B, "i32", "q_pos")
+        pos_of = _buf(q_pos, B, "i32", "q_pos")
     if (table is None) != (bucket_map is None):
         raise ValueError("a bias needs its table and its bucket map")
     if table is not None:
         n_buckets, heads = _shape(table, 2, "table")
         if heads != H:
             raise ValueError(f"table has {heads} heads, q has {H}")
-        a.n_buckets, a.radius = n_buckets, _radius(bucket_map)
-        a.table = _buf(table, n_buckets * H, "f32", "table")
-        a.map = _buf(bucket_map, 2 * a.radius + 1, "i32", "bucket_map")
-    return a, kind
+        radius = _radius(bucket_map)
+        tp = _buf(table, n_buckets * H, "f32", "table")
+        mp = _buf(bucket_map, 2 * radius + 1, "i32", "bucket_map")
+    gp = dqp = dkp = dvp = _NONE
+    if do is not None:
+        gp, dqp = _heads(do, q_shape, dt, "do"), _heads(dq, q_shape, dt, "dq")
+        dkp, dvp = _heads(dk, k_shape, dt, "dk"), _heads(dv, k_shape, dt, "dv")
+        if dtable is not None and table is not None and dtable.shape != table.shape:
+            raise ValueError(f"dtable has shape {tuple(dtable.shape)}, table {tuple(table.shape)}")
+    return RelAttentionArgs.from_buffer_copy(_ATTENTION.pack(
+        code, B, H, Hkv, Tq, Tk, D, 1 if causal else 0, pos, n_buckets, radius,
+        D ** -0.5 if scale is None else scale, p, step & 0xFFFFFFFF, seed & 0xFFFFFFFFFFFFFFFF,
+        _buf(step_dev, 1, "u32", "step_dev") or 0, pos_of or 0, _buf(k_len, B, "i32", "k_len") or 0,
+        tp, mp, qp[0], kp[0], vp[0], op[0], _buf(lse, B * H * Tq, "f32", "lse") or 0,
+        *qp[1:], *kp[1:], *vp[1:], *op[1:], gp[0], dqp[0], dkp[0], dvp[0],
+        *gp[1:], *dqp[1:], *dkp[1:], *dvp[1:], _buf(dtable, n_buckets * H, "f32", "dtable") or 0,
+        1 if accumulate else 0))
 
 
 def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
@@ -570,8 +597,8 @@ def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
     """o [B, Tq, H, D] (and lse [B, H, Tq]) from q [B, Tq, H, D] and k, v
     [B, Tk, Hkv, D]; scale is D ** -0.5 unless given, q_pos a number or an
     int32 tensor [B]."""
-    a, _ = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p,
-                           seed, step, step_dev)
+    a = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed,
+                        step, step_dev)
     _check("rel_attention_forward", load().rel_attention_forward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(q, stream)))
@@ -583,16 +610,8 @@ def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumul
                            step: int = 0, step_dev=None, ws=None, stream=None) -> None:
     """dq, dk, dv (and dtable) from the forward call's arguments, its o and lse
     and the gradient do."""
-    a, kind = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p,
-                              seed, step, step_dev)
-    _heads(a, "d_o", do, q.shape, kind, "do", "do_stride")
-    _heads(a, "dq", dq, q.shape, kind, "dq")
-    _heads(a, "dk", dk, k.shape, kind, "dk")
-    _heads(a, "dv", dv, k.shape, kind, "dv")
-    if dtable is not None and table is not None and tuple(dtable.shape) != tuple(table.shape):
-        raise ValueError(f"dtable has shape {tuple(dtable.shape)}, table {tuple(table.shape)}")
-    a.dtable = _buf(dtable, a.n_buckets * a.H, "f32", "dtable")
-    a.accumulate = int(bool(accumulate))
+    a = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed,
+                        step, step_dev, do, dq, dk, dv, dtable, accumulate)
     _check("rel_attention_backward", load().rel_attention_backward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(q, stream)))

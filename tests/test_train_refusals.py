@@ -246,3 +246,19 @@ def test_attention_binding_refuses(monkeypatch):
     with pytest.raises(ValueError, match="dtable has shape"):
         ob.rel_attention_backward(q, q, q, q, torch.zeros(1, 2, 4), q, q, q, q, table=t,
                                   bucket_map=m, dtable=torch.zeros(2, 4))
+
+
+def test_attention_packing_matches_the_struct():
+    """The binding packs the struct's fields in one go; each lands where the
+    declaration has it."""
+    import ctypes
+
+    n = 11 + 2 + 1 + 1 + 10 + 12 + 4 + 12 + 1 + 1
+    packed = ob._ATTENTION.pack(*range(1, n + 1))
+    assert len(packed) == ctypes.sizeof(ob.RelAttentionArgs)
+    a = ob.RelAttentionArgs.from_buffer_copy(packed)
+    got = []
+    for name, kind in a._fields_:
+        x = getattr(a, name)
+        got += list(x) if kind is ctypes.c_int64 * 3 else [x]
+    assert [float(x) for x in got] == [float(x) for x in range(1, n + 1)]
