@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libonebit.so")
 
 SOURCES = ["api.hip", "compress.hip", "finalize.hip", "server.hip", "scale.hip", "step.hip",
            "int8.hip", "warmup.hip", "dropout.hip", "relbias.hip",
-           "attn_fwd.hip", "attn_bwd.hip"]
+           "attn_fwd.hip", "attn_few.hip", "attn_bwd.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

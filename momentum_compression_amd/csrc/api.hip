@@ -634,7 +634,7 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
     const int64_t heads = (int64_t)B * H;  // below 2^47
     // rows of a launch, and the workgroups of a split or unsplit grid
     if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16) return ONEBIT_E_SIZE;
-    if (!groups_ok((heads + 7) * attn_tiles(Tq) * attn_splits(B, H, Tq, Tk)) ||
+    if (!groups_ok((heads + 7) * attn_tiles(Tq) * attn_splits(B, H, Hkv, Tq, Tk).splits) ||
         !groups_ok((heads + 7) * attn_tiles(Tk)) || !groups_ok(ceil_div(heads * Tq, 4)))
         return ONEBIT_E_SIZE;
     return ONEBIT_OK;
@@ -646,10 +646,11 @@ struct AttnSizes {
     size_t delta, partials;     // backward
 };
 
-AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t D, int32_t radius) {
+AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk, int32_t D,
+                     int32_t radius) {
     AttnSizes z = {};
     const size_t rows = (size_t)B * H * Tq;
-    const int32_t splits = attn_splits(B, H, Tq, Tk);
+    const int32_t splits = attn_splits(B, H, Hkv, Tq, Tk).splits;
     if (splits > 1) {
         z.split_o = round_up(rows * splits * D * sizeof(float));
         z.split_ml = round_up(rows * splits * sizeof(float2));
@@ -720,7 +721,7 @@ extern "C" {
 size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk,
                                      int32_t D, int32_t radius, int32_t backward) {
     if (check_attention_sizes(B, H, Hkv, Tq, Tk, D, radius)) return 0;
-    const AttnSizes z = attn_sizes(B, H, Tq, Tk, D, radius);
+    const AttnSizes z = attn_sizes(B, H, Hkv, Tq, Tk, D, radius);
     const size_t fwd = z.split_o + z.split_ml;
     const size_t bwd = z.delta + z.partials;
     const size_t need = backward && bwd > fwd ? bwd : fwd;
@@ -733,9 +734,11 @@ int rel_attention_forward(const rel_attention_args* a, void* ws, size_t ws_bytes
     if (st) return st;
     if (a->B == 0 || a->Tq == 0) return ONEBIT_OK;
     AttnArgs k = attn_args(a);
-    k.splits = attn_splits(a->B, a->H, a->Tq, a->Tk);
+    const AttnSplits plan = attn_splits(a->B, a->H, a->Hkv, a->Tq, a->Tk);
+    k.few = plan.few;
+    k.splits = plan.splits;
     if (k.splits > 1) {
-        const AttnSizes z = attn_sizes(a->B, a->H, a->Tq, a->Tk, a->D, a->radius);
+        const AttnSizes z = attn_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->radius);
         if (!ws || ws_bytes < z.split_o + z.split_ml) return ONEBIT_E_WORKSPACE;
         if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
         const int32_t tiles = (a->Tk + kStep - 1) / kStep;
@@ -760,7 +763,7 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
     if ((a->dtable && !a->table) || (a->accumulate != 0 && a->accumulate != 1))
         return ONEBIT_E_ARG;
     if (!aligned(a->dtable, 4)) return ONEBIT_E_ALIGN;
-    const AttnSizes z = attn_sizes(a->B, a->H, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
+    const AttnSizes z = attn_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
     if (!ws || ws_bytes < z.delta + z.partials) return ONEBIT_E_WORKSPACE;
     if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     AttnArgs k = attn_args(a);

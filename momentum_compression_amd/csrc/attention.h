@@ -45,6 +45,7 @@ struct AttnArgs {
     DropArgs drop;
     int32_t B, H, Hkv, Tq, Tk, D;
     int32_t q_pos, causal;
+    bool few;                     // attn_few_kernel
     int32_t splits, split_tiles;  // key tiles of one split
     float scale;
 };
@@ -266,10 +267,57 @@ inline unsigned xcd_grid(int64_t groups, int64_t per_group) {
 
 inline int32_t attn_tiles(int32_t T) { return (T + kTileRows - 1) / kTileRows; }
 
-// ---------------------------------------------------------------- launchers
-// Splits of the keys that a forward call uses (1: none).
-int32_t attn_splits(int32_t B, int32_t H, int32_t Tq, int32_t Tk);
+// ---------------------------------------------------------------- results
+// A query's row from the accumulators (column 32 d + 8 (r >> 2) + 4 half +
+// (r & 3) in register r of block d), its maximum m (base 2) and sum l.
+template <typename T, int DP>
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const f32x16 (&acc)[DP / 32], int b,
+                                           int h, int32_t i, int64_t row, float m, float l,
+                                           int half) {
+    // no key seen: l is 0 and so is the row (a NaN goes through)
+    const float inv = l == 0.0f ? 0.0f : a.drop.scale / l;
+    T* to = (T*)a.o + b * a.so.b + i * a.so.t + h * a.so.h;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * half;
+            if (c >= a.D) continue;
+            typename Mma<T>::x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * inv);
+            *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
+        }
+    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+}
 
+// The same of one split, to be joined.
+template <int DP>
+__device__ __forceinline__ void write_split(const AttnArgs& a, const f32x16 (&acc)[DP / 32],
+                                            int64_t row, int split, float m, float l, int half) {
+    float* to = a.split_o + (row * a.splits + split) * a.D;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * half;
+            if (c < a.D)
+                *reinterpret_cast<f4*>(to + c) = f4{acc[d][4 * g], acc[d][4 * g + 1],
+                                                    acc[d][4 * g + 2], acc[d][4 * g + 3]};
+        }
+    if (half == 0) a.split_ml[row * a.splits + split] = float2{m, l};
+}
+
+// ---------------------------------------------------------------- launchers
+// How a forward call divides its work: by the kernel for few queries or the one
+// for many, and the keys over this many workgroups.
+struct AttnSplits {
+    bool few;
+    int32_t splits;
+};
+AttnSplits attn_splits(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk);
+
+hipError_t launch_attn_few(const AttnArgs& a, int32_t dtype, hipStream_t st);
 hipError_t launch_attn_forward(const AttnArgs& a, int32_t dtype, hipStream_t st);
 hipError_t launch_attn_backward(const AttnArgs& a, int32_t dtype, float* dtable, bool accumulate,
                                 hipStream_t st);

@@ -1,0 +1,229 @@
+// Attention forward for few queries over many keys: single tokens over a
+// cache, where all that counts is to read the keys and values once.
+//
+// The queries of all heads that share a key head (at most 32 together) are the
+// columns of the products, so a key is read once for all of them.  The keys of
+// a sequence are split over workgroups and over their waves; a wave goes
+// through its part alone, 32 keys at a time, without barriers: keys straight
+// into the operand registers, values through LDS of its own for the transpose,
+// the next 32 on their way while these are used.  The waves of a workgroup are
+// joined in LDS, the workgroups by attn_join.
+//
+// Bound by memory: at 32 sequences of up to 8192 keys, 4 key heads of 128 and
+// 16 query heads, the matrix instructions (mostly on empty columns) take a
+// tenth of the time that the bytes take.
+#include "attention.h"
+
+namespace onebit {
+
+namespace {
+
+template <typename T, int DP, bool BIAS, bool DROP>
+__global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
+    using x8 = typename Mma<T>::x8;
+    constexpr int kc_n = DP / 16, db_n = DP / 32;
+    constexpr int chunks = DP / 8, v_n = kRows * chunks / 64;  // 16-byte pieces a lane
+    // the waves' value tiles; afterwards the joined rows of two waves
+    __shared__ __align__(16) char tiles[kWaves * kRows * DP * 2];
+    __shared__ float2 stats[kWaves][kRows];
+
+    uint32_t bh, part;
+    if (!xcd_work((uint32_t)a.B * a.Hkv, (uint32_t)a.splits, false, bh, part)) return;
+    const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
+    const int lane = lane_id(), wave = wave_id(), half = lane >> 5, col = lane & 31;
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int group = a.H / a.Hkv, R = a.bias.radius;
+    const bool mine = col < group * a.Tq;
+    const int h = hk * group + (mine ? col % group : 0);
+    const int32_t i = mine ? col / group : 0;
+
+    const T* kp = (const T*)a.k + b * a.sk.b + hk * a.sk.h;
+    const T* vp = (const T*)a.v + b * a.sv.b + hk * a.sv.h;
+    x8 qf[kc_n];
+    load_frags<T, DP>(qf, (const T*)a.q + b * a.sq.b + h * a.sq.h, a.sq.t, i, mine, a.D, lane);
+
+    int32_t end = n_keys;
+    if (a.causal && a.Tq + pos < end) end = a.Tq + pos;
+    const int32_t n_tiles = end > 0 ? (end + kRows - 1) / kRows : 0;
+    const int32_t waves = a.splits * kWaves;
+    const int32_t per = (n_tiles + waves - 1) / waves;
+    int32_t t = ((int)part * kWaves + wave) * per;
+    const int32_t stop = t + per < n_tiles ? t + per : n_tiles;
+    const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
+    const int32_t limit_lo = a.causal && pos < n_keys - 1 ? pos : n_keys - 1;
+
+    const float scale2 = a.scale * kLog2e;
+    const auto bias_at = [&](int32_t d) {  // of this lane's head
+        d = d < -R ? -R : (d > R ? R : d);
+        const int m = a.bias.map[d + R];
+        return (uint32_t)m < (uint32_t)a.bias.n_buckets ? a.bias.table[(int64_t)m * a.H + h] : 0.0f;
+    };
+    const float below = BIAS ? bias_at(-R) * kLog2e : 0.0f;
+    const float above = BIAS ? bias_at(R) * kLog2e : 0.0f;
+    const uint64_t drop_row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq + (uint64_t)i;
+    const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
+
+    char* vt = tiles + wave * (kRows * DP * 2);
+    x8 kf[kc_n], vr[v_n];
+    const auto load_k = [&](int32_t tile) {
+        const int32_t j = tile * kRows + perm_row(col);
+        load_frags<T, DP>(kf, kp, a.sk.t, j, j < n_keys, a.D, lane);
+    };
+    const auto load_v = [&](int32_t tile) {
+#pragma unroll
+        for (int x = 0; x < v_n; ++x) {
+            const int32_t j = tile * kRows + (x * 64 + lane) / chunks;
+            const int c = 8 * (lane % chunks);
+            vr[x] = x8{};
+            if (j < n_keys && c < a.D)
+                vr[x] = *reinterpret_cast<const x8*>(vp + (int64_t)j * a.sv.t + c);
+        }
+    };
+
+    f32x16 acc[db_n];
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
+    float m = -INFINITY, l = 0.0f;
+    if (t < stop) {
+        load_k(t);
+        load_v(t);
+    }
+    for (; t < stop; ++t) {
+        const int32_t j0 = t * kRows;
+#pragma unroll
+        for (int x = 0; x < v_n; ++x)
+            *reinterpret_cast<x8*>(vt + tile_at<DP>((x * 64 + lane) / chunks, lane % chunks)) =
+                vr[x];
+        if (t + 1 < stop) load_v(t + 1);
+        f32x16 s = {};
+#pragma unroll
+        for (int kc = 0; kc < kc_n; ++kc) s = Mma<T>::mul(kf[kc], qf[kc], s);
+        if (t + 1 < stop) load_k(t + 1);
+        // base-2 scores; the queries of the columns stand at pos ... pos + Tq - 1
+        if (BIAS && j0 + 31 - pos > -R && j0 - (pos + a.Tq - 1) < R) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                s[r] = __builtin_fmaf(
+                    s[r], scale2,
+                    bias_at(j0 + 16 * (r >> 3) + 8 * half + (r & 7) - i - pos) * kLog2e);
+        } else {
+            const float c = !BIAS ? 0.0f : (j0 < pos ? below : above);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], scale2, c);
+        }
+        if (j0 + 31 > limit_lo) {
+            const int32_t seen = limit - j0 - 8 * half;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (16 * (r >> 3) + (r & 7) > seen) s[r] = -INFINITY;
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
+        mx = fmaxf(mx, other_half(mx));
+        if (__any(mx > m + 8.0f)) {  // as in the forward pass for many queries
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - m_new);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < db_n; ++d) acc[d] *= alpha;
+            m = m_new;
+        }
+        const float m_use = m == -INFINITY ? 0.0f : m;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the value tile is written
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(s[8 * c + e] - m_use);
+            l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            if (DROP) {
+                uint32_t wd[4];
+                drop_draws(wd, (uint32_t)(j0 + 16 * c + 8 * half) >> 3, drop_row, step, a.drop.k0,
+                           a.drop.k1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!drop_keep(wd, e, a.drop.threshold)) p[e] = 0.0f;
+            }
+            const x8 pb = pack8<T>(p);
+#pragma unroll
+            for (int d = 0; d < db_n; ++d)
+                acc[d] = Mma<T>::mul(col_frag<T, DP>(vt, 16 * c, d, lane), pb, acc[d]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // ... and read
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    // the waves' maxima and sums, then their rows, two waves at a time
+    l += other_half(l);
+    if (half == 0) stats[wave][col] = float2{m, l};
+    __syncthreads();
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, stats[w][col].x);
+    const float m_use = m == -INFINITY ? 0.0f : m;
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        l += __builtin_amdgcn_exp2f(stats[w][col].x - m_use) * stats[w][col].y;
+    const float weight = __builtin_amdgcn_exp2f(stats[wave][col].x - m_use);
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) acc[d] *= weight;
+    float* rows = reinterpret_cast<float*>(tiles);
+#pragma unroll
+    for (int left = 2; left >= 1; left >>= 1) {  // waves that take in another's
+        float* at = rows + (wave % left) * (kRows * DP) + half * 4 * kRows + col;
+        if (wave >= left && wave < 2 * left) {
+#pragma unroll
+            for (int d = 0; d < db_n; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    at[(32 * d + 8 * (r >> 2) + (r & 3)) * kRows] = acc[d][r];
+        }
+        __syncthreads();
+        if (wave < left) {
+#pragma unroll
+            for (int d = 0; d < db_n; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[d][r] += at[(32 * d + 8 * (r >> 2) + (r & 3)) * kRows];
+        }
+        __syncthreads();
+    }
+    if (wave != 0 || !mine) return;
+    const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
+    if (a.splits > 1)
+        write_split<DP>(a, acc, row, (int)part, m, l, half);
+    else
+        write_rows<T, DP>(a, acc, b, h, i, row, m, l, half);
+}
+
+template <typename T, int DP>
+void run_d(const AttnArgs& a, hipStream_t st) {
+    const bool bias = a.bias.radius > 0, drop = a.drop.threshold != kDropAll;
+    const dim3 grid(xcd_grid((int64_t)a.B * a.Hkv, a.splits));
+    if (bias && drop)
+        hipLaunchKernelGGL((attn_few_kernel<T, DP, true, true>), grid, dim3(kThreads), 0, st, a);
+    else if (bias)
+        hipLaunchKernelGGL((attn_few_kernel<T, DP, true, false>), grid, dim3(kThreads), 0, st, a);
+    else if (drop)
+        hipLaunchKernelGGL((attn_few_kernel<T, DP, false, true>), grid, dim3(kThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_few_kernel<T, DP, false, false>), grid, dim3(kThreads), 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_attn_few(const AttnArgs& a, int32_t dtype, hipStream_t st) {
+    if (dtype == ONEBIT_BF16) {
+        if (a.D <= 64) run_d<bf16, 64>(a, st);
+        else run_d<bf16, 128>(a, st);
+    } else {
+        if (a.D <= 64) run_d<f16, 64>(a, st);
+        else run_d<f16, 128>(a, st);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace onebit

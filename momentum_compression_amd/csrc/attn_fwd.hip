@@ -164,35 +164,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     l += other_half(l);
     if (i >= a.Tq) return;
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
-    if (SPLIT) {
-        float* to = a.split_o + (row * a.splits + split) * a.D;
-#pragma unroll
-        for (int d = 0; d < db_n; ++d)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int c = 32 * d + 8 * g + 4 * half;
-                if (c < a.D)
-                    *reinterpret_cast<f4*>(to + c) = f4{acc[d][4 * g], acc[d][4 * g + 1],
-                                                        acc[d][4 * g + 2], acc[d][4 * g + 3]};
-            }
-        if (half == 0) a.split_ml[row * a.splits + split] = float2{m, l};
-        return;
-    }
-    // no key seen: l is 0 and so is the row (a NaN goes through)
-    const float inv = l == 0.0f ? 0.0f : (DROP ? a.drop.scale : 1.0f) / l;
-    T* to = (T*)a.o + b * a.so.b + i * a.so.t + h * a.so.h;
-#pragma unroll
-    for (int d = 0; d < db_n; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int c = 32 * d + 8 * g + 4 * half;
-            if (c >= a.D) continue;
-            typename Mma<T>::x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * inv);
-            *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
-        }
-    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+    if (SPLIT) write_split<DP>(a, acc, row, split, m, l, half);
+    else write_rows<T, DP>(a, acc, b, h, i, row, m, l, half);
 }
 
 // Joins the splits of a row: a wave per row, two columns a lane.
@@ -255,10 +228,15 @@ void run_d(const AttnArgs& a, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t run_t(const AttnArgs& a, hipStream_t st) {
-    if (a.D <= 64) run_d<T, 64>(a, st);
-    else run_d<T, 128>(a, st);
-    const hipError_t e = hipGetLastError();
+hipError_t run_t(const AttnArgs& a, int32_t dtype, hipStream_t st) {
+    hipError_t e;
+    if (a.few) {
+        e = launch_attn_few(a, dtype, st);
+    } else {
+        if (a.D <= 64) run_d<T, 64>(a, st);
+        else run_d<T, 128>(a, st);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = (int64_t)a.B * a.H * a.Tq;
     hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
@@ -268,20 +246,27 @@ hipError_t run_t(const AttnArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// A workgroup has 128 queries of one head; where these are too few for the
-// card's 256 CUs the keys are split, at least four tiles to a part.
-int32_t attn_splits(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
-    const int64_t work = (int64_t)B * H * attn_tiles(Tq);
-    const int32_t tiles = (Tk + kStep - 1) / kStep;
-    if (work == 0) return 1;
-    int64_t n = (512 + work - 1) / work;
-    if (n > tiles / 4) n = tiles / 4;
+AttnSplits attn_splits(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk) {
+    AttnSplits p = {false, 1};
+    if (B == 0 || Tq == 0) return p;
+    // all queries of a key head in one wave's columns
+    p.few = (int64_t)Tq * (H / Hkv) <= kRows;
+    const int64_t work = p.few ? (int64_t)B * Hkv : (int64_t)B * H * attn_tiles(Tq);
+    // few: two workgroups a CU at a time and as many again to even out lengths,
+    // a wave with four tiles of 32 keys at least; otherwise two a CU, four
+    // tiles of 64 at least
+    const int64_t want = p.few ? 1024 : 512;
+    const int64_t most = (Tk + (p.few ? 4 * kWaves * kRows : 4 * kStep) - 1) /
+                         (p.few ? 4 * kWaves * kRows : 4 * kStep);
+    int64_t n = (want + work - 1) / work;
+    if (n > most) n = most;
     if (n > 64) n = 64;
-    return n < 1 ? 1 : (int32_t)n;
+    p.splits = n < 1 ? 1 : (int32_t)n;
+    return p;
 }
 
 hipError_t launch_attn_forward(const AttnArgs& a, int32_t dtype, hipStream_t st) {
-    return dtype == ONEBIT_BF16 ? run_t<bf16>(a, st) : run_t<f16>(a, st);
+    return dtype == ONEBIT_BF16 ? run_t<bf16>(a, dtype, st) : run_t<f16>(a, dtype, st);
 }
 
 }  // namespace onebit
