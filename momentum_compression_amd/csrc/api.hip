@@ -635,7 +635,7 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
     // rows of a launch, and the workgroups of a split or unsplit grid
     if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16) return ONEBIT_E_SIZE;
     if (!groups_ok((heads + 7) * attn_tiles(Tq) * attn_splits(B, H, Hkv, Tq, Tk).splits) ||
-        !groups_ok((heads + 7) * attn_tiles(Tk)) || !groups_ok(ceil_div(heads * Tq, 4)))
+        !groups_ok((heads + 7) * attn_tiles(Tk)) || !groups_ok(heads * Tq))
         return ONEBIT_E_SIZE;
     return ONEBIT_OK;
 }

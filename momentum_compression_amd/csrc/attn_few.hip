@@ -4,9 +4,9 @@
 // The queries of all heads that share a key head (at most 32 together) are the
 // columns of the products, so a key is read once for all of them.  The keys of
 // a sequence are split over workgroups and over their waves; a wave goes
-// through its part alone, 32 keys at a time, without barriers: keys straight
-// into the operand registers, values through LDS of its own for the transpose,
-// the next 32 on their way while these are used.  The waves of a workgroup are
+// through its part alone, 32 keys at a time, without barriers: whole rows come
+// in, through LDS of its own they become operands, the next 32 on their way
+// while these are used.  The waves of a workgroup are
 // joined in LDS, the workgroups by attn_join.
 //
 // Bound by memory: at 32 sequences of up to 8192 keys, 4 key heads of 128 and
@@ -23,8 +23,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     constexpr int chunks = DP / 8, v_n = kRows * chunks / 64;  // 16-byte pieces a lane
-    // the waves' value tiles; afterwards the joined rows of two waves
-    __shared__ __align__(16) char tiles[kWaves * kRows * DP * 2];
+    // the waves' key and value tiles; afterwards the joined rows of two waves
+    __shared__ __align__(16) char tiles[2 * kWaves * kRows * DP * 2];
     __shared__ float2 stats[kWaves][kRows];
 
     uint32_t bh, part;
@@ -45,10 +45,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     int32_t end = n_keys;
     if (a.causal && a.Tq + pos < end) end = a.Tq + pos;
     const int32_t n_tiles = end > 0 ? (end + kRows - 1) / kRows : 0;
+    // every waves-th tile: neighbouring waves read neighbouring rows, and the
+    // few tiles near the queries, whose bias is gathered, go to different waves
     const int32_t waves = a.splits * kWaves;
-    const int32_t per = (n_tiles + waves - 1) / waves;
-    int32_t t = ((int)part * kWaves + wave) * per;
-    const int32_t stop = t + per < n_tiles ? t + per : n_tiles;
+    int32_t t = (int)part * kWaves + wave;
     const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
     const int32_t limit_lo = a.causal && pos < n_keys - 1 ? pos : n_keys - 1;
 
@@ -63,42 +63,46 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     const uint64_t drop_row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq + (uint64_t)i;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
-    char* vt = tiles + wave * (kRows * DP * 2);
-    x8 kf[kc_n], vr[v_n];
-    const auto load_k = [&](int32_t tile) {
-        const int32_t j = tile * kRows + perm_row(col);
-        load_frags<T, DP>(kf, kp, a.sk.t, j, j < n_keys, a.D, lane);
-    };
-    const auto load_v = [&](int32_t tile) {
+    char* kt = tiles + 2 * wave * (kRows * DP * 2);
+    char* vt = kt + kRows * DP * 2;
+    x8 kr[v_n], vr[v_n];
+    const auto load = [&](x8 (&to)[v_n], const T* base, int64_t stride, int32_t tile) {
 #pragma unroll
         for (int x = 0; x < v_n; ++x) {
             const int32_t j = tile * kRows + (x * 64 + lane) / chunks;
             const int c = 8 * (lane % chunks);
-            vr[x] = x8{};
+            to[x] = x8{};
             if (j < n_keys && c < a.D)
-                vr[x] = *reinterpret_cast<const x8*>(vp + (int64_t)j * a.sv.t + c);
+                to[x] = *reinterpret_cast<const x8*>(base + (int64_t)j * stride + c);
         }
+    };
+    const auto store = [&](char* tile, const x8 (&from)[v_n]) {
+#pragma unroll
+        for (int x = 0; x < v_n; ++x)
+            *reinterpret_cast<x8*>(tile + tile_at<DP>((x * 64 + lane) / chunks, lane % chunks)) =
+                from[x];
     };
 
     f32x16 acc[db_n];
 #pragma unroll
     for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
     float m = -INFINITY, l = 0.0f;
-    if (t < stop) {
-        load_k(t);
-        load_v(t);
+    if (t < n_tiles) {
+        load(kr, kp, a.sk.t, t);
+        load(vr, vp, a.sv.t, t);
     }
-    for (; t < stop; ++t) {
+    for (; t < n_tiles; t += waves) {
         const int32_t j0 = t * kRows;
-#pragma unroll
-        for (int x = 0; x < v_n; ++x)
-            *reinterpret_cast<x8*>(vt + tile_at<DP>((x * 64 + lane) / chunks, lane % chunks)) =
-                vr[x];
-        if (t + 1 < stop) load_v(t + 1);
+        store(kt, kr);
+        if (t + waves < n_tiles) load(kr, kp, a.sk.t, t + waves);
+        store(vt, vr);
+        if (t + waves < n_tiles) load(vr, vp, a.sv.t, t + waves);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the tiles are written
+        __builtin_amdgcn_wave_barrier();
         f32x16 s = {};
 #pragma unroll
-        for (int kc = 0; kc < kc_n; ++kc) s = Mma<T>::mul(kf[kc], qf[kc], s);
-        if (t + 1 < stop) load_k(t + 1);
+        for (int kc = 0; kc < kc_n; ++kc)
+            s = Mma<T>::mul(row_frag<T, DP>(kt, 0, kc, lane), qf[kc], s);
         // base-2 scores; the queries of the columns stand at pos ... pos + Tq - 1
         if (BIAS && j0 + 31 - pos > -R && j0 - (pos + a.Tq - 1) < R) {
 #pragma unroll
@@ -130,8 +134,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
             m = m_new;
         }
         const float m_use = m == -INFINITY ? 0.0f : m;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the value tile is written
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float p[8];

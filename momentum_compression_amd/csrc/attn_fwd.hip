@@ -168,41 +168,68 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     else write_rows<T, DP>(a, acc, b, h, i, row, m, l, half);
 }
 
-// Joins the splits of a row: a wave per row, two columns a lane.
-template <typename T>
+// Joins the splits of a row (at most 64, one a lane for their weights), two
+// columns a lane.  WAVES waves share a row's splits where there are many: one
+// wave would take 14 us for 32 of them, a load after the other.
+template <typename T, int WAVES>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+    __shared__ float2 sums[kWaves][64];
     const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    if (row >= rows) return;
-    const int lane = lane_id();
-    const float2* ml = a.split_ml + row * a.splits;
-    float m = -INFINITY;
-    for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[s].x);
-    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    const float m_use = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    const int wave = wave_id(), lane = lane_id();
+    const int64_t row = (int64_t)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
+    const bool ok = row < rows;
+    float m = -INFINITY, l = 0.0f;
+    if (ok && lane < a.splits) {
+        const float2 x = a.split_ml[row * a.splits + lane];
+        m = x.x;
+        l = x.y;
+    }
+    float top = m;
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    const float weight = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+    l *= weight;
+    for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
     const int c = 2 * lane;
-    const float* from = a.split_o + row * a.splits * (int64_t)a.D + c;
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 x = ml[s];
-        const float wgt = __builtin_amdgcn_exp2f(x.x - m_use);
-        l += wgt * x.y;
-        if (c < a.D) {
-            const float2 v = *reinterpret_cast<const float2*>(from + (int64_t)s * a.D);
-            o0 += wgt * v.x;
-            o1 += wgt * v.y;
+    float2 o = {0.0f, 0.0f};
+    if (ok && c < a.D) {
+        const float* from = a.split_o + row * a.splits * (int64_t)a.D + c;
+        for (int s0 = wave % WAVES; s0 < a.splits; s0 += 8 * WAVES) {
+            float2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int s = s0 + k * WAVES;
+                v[k] = s < a.splits ? *reinterpret_cast<const float2*>(from + (int64_t)s * a.D)
+                                    : float2{0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = __uint_as_float(__builtin_amdgcn_readlane(
+                    __float_as_uint(weight), (s0 + k * WAVES) & 63));
+                o.x = __builtin_fmaf(w, v[k].x, o.x);
+                o.y = __builtin_fmaf(w, v[k].y, o.y);
+            }
         }
     }
+    if (WAVES > 1) {
+        sums[wave][lane] = o;
+        __syncthreads();
+        if (wave % WAVES) return;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            o.x += sums[wave + w][lane].x;
+            o.y += sums[wave + w][lane].y;
+        }
+    }
+    if (!ok) return;
     const float inv = l == 0.0f ? 0.0f : a.drop.scale / l;
     const int i = (int)(row % a.Tq);
     const int64_t bh = row / a.Tq;
     T* to = (T*)a.o + (bh / a.H) * a.so.b + i * a.so.t + (bh % a.H) * a.so.h;
     if (c < a.D) {
-        to[c] = (T)(o0 * inv);
-        to[c + 1] = (T)(o1 * inv);
+        to[c] = (T)(o.x * inv);
+        to[c + 1] = (T)(o.y * inv);
     }
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : top * kLn2 + __logf(l);
 }
 
 template <typename T, int DP, bool BIAS, bool DROP>
@@ -239,8 +266,12 @@ hipError_t run_t(const AttnArgs& a, int32_t dtype, hipStream_t st) {
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, st, a);
+    if (a.splits > 8)
+        hipLaunchKernelGGL((attn_join_kernel<T, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0,
+                           st, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<T, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -253,11 +284,11 @@ AttnSplits attn_splits(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk
     p.few = (int64_t)Tq * (H / Hkv) <= kRows;
     const int64_t work = p.few ? (int64_t)B * Hkv : (int64_t)B * H * attn_tiles(Tq);
     // few: two workgroups a CU at a time and as many again to even out lengths,
-    // a wave with four tiles of 32 keys at least; otherwise two a CU, four
+    // a wave with two tiles of 32 keys at least; otherwise two a CU, four
     // tiles of 64 at least
     const int64_t want = p.few ? 1024 : 512;
-    const int64_t most = (Tk + (p.few ? 4 * kWaves * kRows : 4 * kStep) - 1) /
-                         (p.few ? 4 * kWaves * kRows : 4 * kStep);
+    const int64_t most = (Tk + (p.few ? 2 * kWaves * kRows : 4 * kStep) - 1) /
+                         (p.few ? 2 * kWaves * kRows : 4 * kStep);
     int64_t n = (want + work - 1) / work;
     if (n > most) n = most;
     if (n > 64) n = 64;
