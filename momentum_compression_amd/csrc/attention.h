@@ -240,23 +240,28 @@ __device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b) {
 // Workgroups go to the 8 XCDs in turn.  The workgroups of one group (a
 // sequence's head) read the same rows, so they get numbers of one XCD and share
 // its L2; successive groups go to successive XCDs, which spreads sequences of
-// different lengths.  Items of one size go group by group.  Items of falling
-// size (a causal mask) go size by size, every second 32 (an XCD's CUs) in
-// reverse, so that a CU that got a large one gets a small one with it: a
-// prompt of 4093 tokens and 16 heads took 162 us group by group.  False for a
-// number past the work.
-__device__ __forceinline__ bool xcd_work(uint32_t groups, uint32_t per_group, bool falling,
+// different lengths.  Items of one size go group by group; items of falling
+// size (a causal mask) go size by size, the largest first.
+enum WorkOrder {
+    kEven,       // one size
+    kFalling,    // one workgroup a CU at a time: who is done takes the next size
+    kFallingTwo  // two or more at a time: every second 32 (an XCD's CUs) in
+                 // reverse, so that a large one has a small one beside it (a
+                 // prompt of 4093 tokens and 16 heads: 162 -> 123 us)
+};
+// False for a number past the work.
+__device__ __forceinline__ bool xcd_work(uint32_t groups, uint32_t per_group, WorkOrder order,
                                          uint32_t& group, uint32_t& item) {
     const uint32_t x = blockIdx.x & 7;
     uint32_t s = blockIdx.x >> 3;
-    if (!falling) {
+    if (order == kEven) {
         group = (s / per_group) * 8 + x;
         item = s % per_group;
         return group < groups;
     }
     const uint32_t mine = (groups + 7 - x) / 8;  // groups of this XCD
     if (s >= mine * per_group) return false;
-    if ((s & 32) && (s | 31) < mine * per_group) s ^= 31;
+    if (order == kFallingTwo && (s & 32) && (s | 31) < mine * per_group) s ^= 31;
     item = s / mine;
     group = (s % mine) * 8 + x;
     return true;

@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal != 0, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal ? (DP == 64 ? kFallingTwo : kFalling) : kEven, bh, item)) return;
     const int qt = (int)(tiles_q - 1 - item);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
             ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
             vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
         }
-#pragma nounroll
+#pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int32_t js = j0 + 32 * u;
             if (js > limit_hi) continue;
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, a.causal != 0, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, a.causal ? (DP == 64 ? kFallingTwo : kFalling) : kEven, bh, item)) return;
     // under a causal mask the first keys have the most queries: first
     const int kt_i = (int)item;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);

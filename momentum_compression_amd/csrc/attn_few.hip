@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     __shared__ float2 stats[kWaves][kRows];
 
     uint32_t bh, part;
-    if (!xcd_work((uint32_t)a.B * a.Hkv, (uint32_t)a.splits, false, bh, part)) return;
+    if (!xcd_work((uint32_t)a.B * a.Hkv, (uint32_t)a.splits, kEven, bh, part)) return;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5, col = lane & 31;
     const int32_t pos = query_position(a, b), n_keys = key_count(a, b);

@@ -24,7 +24,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.H, tiles_q * a.splits, a.causal != 0, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q * a.splits, a.causal ? kFallingTwo : kEven, bh,
+                  item)) return;
     // under a causal mask the last queries have the most keys: first
     const int qt = (int)(tiles_q - 1 - item / a.splits);
     const int split = (int)(item % a.splits);
