@@ -551,7 +551,7 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  *
  * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
  * heads.  *_stride: elements between sequences, tokens and heads, multiples
- * of 8; D a multiple of 8, 8 ... 128, its elements side by side; 16-byte
+ * of 8, between tokens at most 2^23; D a multiple of 8, 8 ... 128, its elements side by side; 16-byte
  * aligned.  So a fused projection's output and a cache of either order serve
  * as they are.  Sequences of a batch may share keys (stride 0); outputs must
  * not overlap each other or themselves.  lse [B][H][Tq] float, optional in

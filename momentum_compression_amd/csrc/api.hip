@@ -505,6 +505,7 @@ namespace {
 
 constexpr int64_t kMaxPositions = (int64_t)1 << 29;  // lengths and positions: 32-bit differences
 constexpr int64_t kMaxLd = (int64_t)1 << 40;         // strides: 64-bit offsets stay in range
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 23;  // 64 rows: a buffer below 2^31 bytes
 
 // bytes of an element, 0 for an unknown type
 size_t type_size(int32_t dtype) {
@@ -617,7 +618,8 @@ int check_heads(const void* p, const int64_t s[3], int32_t B, int32_t T, int32_t
     if (!p) return ONEBIT_E_NULL;
     const int64_t count[3] = {B, T, heads};
     for (int k = 0; k < 3; ++k) {
-        if (s[k] < 0 || s[k] > kMaxLd || s[k] % 8) return ONEBIT_E_SIZE;
+        if (s[k] < 0 || s[k] > (k == 1 ? kMaxTokenStride : kMaxLd) || s[k] % 8)
+            return ONEBIT_E_SIZE;
         if (written && count[k] > 1 && s[k] < D) return ONEBIT_E_SIZE;
     }
     return aligned(p, 16) ? ONEBIT_OK : ONEBIT_E_ALIGN;

@@ -110,36 +110,37 @@ constexpr int tile_bytes() {
     return kStep * DP * 2;
 }
 
-// One tile's global rows on their way to LDS: every thread holds kStep * DP /
-// (8 kThreads) chunks of 16 bytes.
+// Fills tiles with global rows, memory to LDS without registers between: a
+// lane's 16 bytes land beside its neighbours', so the lane asks for the chunk
+// that the swizzle puts there.  Rows past the last one and columns from D on
+// lie past the buffer's end, which reads as 0.  What is under way is done when
+// the issuing wave has passed a __syncthreads().
 template <typename T, int DP>
-struct Stage {
+struct Feed {
     static constexpr int kChunks = DP / 8;
-    static constexpr int kPer = kStep * kChunks / kThreads;
-    typename Mma<T>::x8 v[kPer];
+    static constexpr int kPer = kStep * kChunks / kThreads;  // loads a lane and tile
+    const T* base;
+    uint32_t stride, row_bytes, at;  // in bytes
 
-    // rows first ... first + kStep - 1 of `base`; rows from `end` on and
-    // columns from D on are 0 and not read
-    __device__ __forceinline__ void load(const T* base, int64_t stride, int32_t first, int32_t end,
-                                         int32_t D) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = i * kThreads + (int)threadIdx.x;
-            const int32_t row = first + idx / kChunks;
-            const int c = 8 * (idx % kChunks);
-            v[i] = typename Mma<T>::x8{};
-            if (row < end && c < D)
-                v[i] = *reinterpret_cast<const typename Mma<T>::x8*>(base + (int64_t)row * stride +
-                                                                     c);
-        }
+    __device__ __forceinline__ Feed(const T* from, int64_t token_stride, int32_t D, int wave,
+                                    int lane)
+        : base(from), stride((uint32_t)token_stride * 2), row_bytes((uint32_t)D * 2) {
+        const int row = wave * (64 / kChunks) + lane / kChunks;
+        const int chunk = (lane % kChunks) ^ swizzle<DP>(row);  // the same kStep / kPer rows on
+        at = 8 * chunk < D ? (uint32_t)row * stride + 16 * chunk : 0x80000000u;
     }
-    __device__ __forceinline__ void store(char* tile) const {
+    // rows first ... first + kStep - 1, those below `end`
+    __device__ __forceinline__ void load(char* tile, int32_t first, int32_t end, int wave) const {
+        const int32_t rows = end - first < kStep ? end - first : kStep;
+        const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * stride + row_bytes : 0u;
+        const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)((const char*)base + (int64_t)first * stride), 0, (int)bytes, 0x00027000);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = i * kThreads + (int)threadIdx.x;
-            *reinterpret_cast<typename Mma<T>::x8*>(
-                tile + tile_at<DP>(idx / kChunks, idx % kChunks)) = v[i];
-        }
+        for (int x = 0; x < kPer; ++x)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                from,
+                (__attribute__((address_space(3))) void*)(tile + (x * kWaves + wave) * 1024), 16,
+                (int)(at + (uint32_t)x * (kStep / kPer) * stride), 0, 0, 0);
     }
 };
 
@@ -227,13 +228,13 @@ __device__ __forceinline__ float base2_lse(float lse) {
 __device__ __forceinline__ int32_t query_position(const AttnArgs& a, int b) {
     if (!a.q_pos_dev) return a.q_pos;
     constexpr int32_t far = 1 << 29;  // as the host checks the number
-    const int32_t p = a.q_pos_dev[b];
+    const int32_t p = __builtin_amdgcn_readfirstlane(a.q_pos_dev[b]);
     return p < -far ? -far : (p > far ? far : p);
 }
 
 __device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b) {
     if (!a.k_len) return a.Tk;
-    const int32_t n = a.k_len[b];
+    const int32_t n = __builtin_amdgcn_readfirstlane(a.k_len[b]);
     return n < 0 ? 0 : (n > a.Tk ? a.Tk : n);
 }
 

@@ -86,23 +86,22 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
     const uint64_t drop_row = (uint64_t)row;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
-    Stage<T, DP> ks, vs;
+    const Feed<T, DP> ks(kp, a.sk.t, a.D, wave, lane), vs(vp, a.sv.t, a.D, wave, lane);
     if (j0 < end) {
-        ks.load(kp, a.sk.t, j0, n_keys, a.D);
-        vs.load(vp, a.sv.t, j0, n_keys, a.D);
+        ks.load(lds, j0, n_keys, wave);
+        vs.load(lds + tile_bytes<DP>(), j0, n_keys, wave);
     }
     if (BIAS) fill_window(window, a.bias, h, a.scale);
     int buf = 0;
-    __syncthreads();  // the window
     for (; j0 < end; j0 += kStep, buf ^= 1) {
         char* kt = lds + buf * 2 * tile_bytes<DP>();
         char* vt = kt + tile_bytes<DP>();
-        ks.store(kt);
-        vs.store(vt);
-        __syncthreads();  // one a tile, as in the forward pass
+        // this tile (and the window) is there, and the other buffer is read
+        __syncthreads();
         if (j0 + kStep < end) {
-            ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
-            vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
+            char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
+            ks.load(next, j0 + kStep, n_keys, wave);
+            vs.load(next + tile_bytes<DP>(), j0 + kStep, n_keys, wave);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -270,16 +269,22 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         kt_i * kTileRows < n_keys && first < a.Tq ? (a.Tq - first + kStep - 1) / kStep : 0;
     const int64_t total = (int64_t)per_head * group;
 
-    Stage<T, DP> qs, gs;
     float row_value = 0.0f;
     int32_t head = hk * group, i0 = first;  // of the tile to load next
-    const auto load = [&] {
-        qs.load((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, i0, a.Tq, a.D);
-        gs.load((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, i0, a.Tq, a.D);
+    const auto load = [&](int to) {
         const int32_t i = i0 + (int)(threadIdx.x & 63);
         const int64_t row = ((int64_t)b * a.H + head) * a.Tq + i;
         if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
         else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] * drop_inv : 0.0f;
+        char* tile = lds + to * 2 * tile_bytes<DP>();
+        const Feed<T, DP> qs((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, a.D, wave, lane);
+        const Feed<T, DP> gs((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, a.D, wave,
+                             lane);
+        qs.load(tile, i0, a.Tq, wave);
+        gs.load(tile + tile_bytes<DP>(), i0, a.Tq, wave);
+    };
+    const auto keep_rows = [&](int to) {
+        if (threadIdx.x < 128) rows_lds[to * 128 + threadIdx.x] = row_value;
     };
     // one head's sums to its part; its bins are complete
     const auto flush = [&](int h) {
@@ -305,13 +310,16 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     };
     if (TABLE)
         for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
-    if (total > 0) load();
+    if (total > 0) {
+        load(0);
+        keep_rows(0);
+    }
     int buf = 0, filled = -1;
     for (int64_t t = 0; t < total; ++t, buf ^= 1) {
         const int32_t h = head, it = i0;  // this tile
         char* qt = lds + buf * 2 * tile_bytes<DP>();
         char* gt = qt + tile_bytes<DP>();
-        float* lse2 = rows_lds + buf * 128;
+        const float* lse2 = rows_lds + buf * 128;
         const float* delta = lse2 + 64;
         if (BIAS && filled != h) {
             __syncthreads();  // the other head's window is read
@@ -319,17 +327,15 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             fill_window(window, a.bias, h, a.scale);
             filled = h;
         }
-        qs.store(qt);
-        gs.store(gt);
-        if (threadIdx.x < 128) lse2[threadIdx.x] = row_value;
-        __syncthreads();
-        if (t + 1 < total) {
+        __syncthreads();  // this tile is there, and the other buffer is read
+        const bool more = t + 1 < total;
+        if (more) {
             i0 += kStep;
             if (i0 >= a.Tq) {
                 i0 = first;
                 ++head;
             }
-            load();
+            load(buf ^ 1);
         }
 #pragma nounroll
         for (int u = 0; u < 2; ++u) {
@@ -429,6 +435,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                 }
             }
         }
+        if (more) keep_rows(buf ^ 1);
     }
     if (TABLE) {
         // the last head's part, and those of a group that saw no query

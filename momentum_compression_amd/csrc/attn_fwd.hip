@@ -64,25 +64,22 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
     const uint64_t drop_row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq + (uint64_t)i;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
-    Stage<T, DP> ks, vs;
+    const Feed<T, DP> ks(kp, a.sk.t, a.D, wave, lane), vs(vp, a.sv.t, a.D, wave, lane);
     if (j0 < end) {
-        ks.load(kp, a.sk.t, j0, n_keys, a.D);
-        vs.load(vp, a.sv.t, j0, n_keys, a.D);
+        ks.load(lds, j0, n_keys, wave);
+        vs.load(lds + tile_bytes<DP>(), j0, n_keys, wave);
     }
     if (BIAS) fill_window(window, a.bias, h, a.scale);
     int buf = 0;
-    __syncthreads();  // the window
     for (; j0 < end; j0 += kStep, buf ^= 1) {
         char* kt = lds + buf * 2 * tile_bytes<DP>();
         char* vt = kt + tile_bytes<DP>();
-        ks.store(kt);
-        vs.store(vt);
-        // one barrier a tile: the buffer written two tiles on was read before
-        // the barrier of the tile between
+        // this tile (and the window) is there, and the other buffer is read
         __syncthreads();
         if (j0 + kStep < end) {
-            ks.load(kp, a.sk.t, j0 + kStep, n_keys, a.D);
-            vs.load(vp, a.sv.t, j0 + kStep, n_keys, a.D);
+            char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
+            ks.load(next, j0 + kStep, n_keys, wave);
+            vs.load(next + tile_bytes<DP>(), j0 + kStep, n_keys, wave);
         }
         if (j0 > limit_hi) continue;
 

@@ -170,7 +170,7 @@ def test_attention_refusals(lib):
                 dict(radius=1025, n_buckets=4, table=P, map=P),
                 dict(radius=8, n_buckets=0, table=P, map=P), dict(B=1 << 30, H=8, Hkv=8),
                 dict(q_stride=(2048, 252, 64)), dict(k_stride=(1024, -128, 64)),
-                dict(v_stride=(1 << 41, 128, 64)), dict(o_stride=(2048, 0, 64)),
+                dict(v_stride=(1 << 41, 128, 64)), dict(k_stride=(1 << 30, (1 << 23) + 8, 64)), dict(o_stride=(2048, 0, 64)),
                 dict(o_stride=(2048, 256, 32))):
         assert both(**bad) == ob.ONEBIT_E_SIZE, bad
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(table=P),
