@@ -634,8 +634,10 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
     if (B < 0 || H < 1 || H > 65535 || Hkv < 1 || H % Hkv) return ONEBIT_E_SIZE;
     if (D < 8 || D > 128 || D % 8 || radius < 0 || radius > kMaxRadius) return ONEBIT_E_SIZE;
     const int64_t heads = (int64_t)B * H;  // below 2^47
-    // rows of a launch, and the workgroups of a split or unsplit grid
-    if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16) return ONEBIT_E_SIZE;
+    // rows of a launch, and query tiles that one key head goes through
+    if (heads > INT32_MAX || heads * Tq > (int64_t)INT32_MAX * 16 ||
+        (int64_t)(Tq / kStep + 1) * (H / Hkv) > INT32_MAX)
+        return ONEBIT_E_SIZE;
     if (!groups_ok((heads + 7) * attn_tiles(Tq) * attn_splits(B, H, Hkv, Tq, Tk).splits) ||
         !groups_ok((heads + 7) * attn_tiles(Tk)) || !groups_ok(heads * Tq))
         return ONEBIT_E_SIZE;

@@ -168,6 +168,24 @@ __device__ __forceinline__ typename Mma<T>::x8 col_frag(const char* tile, int ro
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Order of the LDS reads and matrix instructions of a block: AHEAD reads first,
+// then after each matrix instruction the reads of a later one.  Left alone they
+// come one or two instructions before their use, and a wave that has its SIMD
+// to itself waits out the LDS latency at every one.
+template <int READS_PER_MMA, int MMAS, int AHEAD>
+__device__ __forceinline__ void read_ahead() {
+    constexpr int kRead = 0x100, kMma = 0x8;
+    constexpr int later = (READS_PER_MMA * MMAS - AHEAD) / READS_PER_MMA;
+    static_assert(AHEAD % READS_PER_MMA == 0 && later >= 0, "whole instructions");
+    __builtin_amdgcn_sched_group_barrier(kRead, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < later; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, READS_PER_MMA, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMma, MMAS - later, 0);
+}
+
 // B operand straight from memory: row `row` of `base` (0 where not ok),
 // columns 16 kc + 8 (lane >> 5) ... + 7.
 template <typename T, int DP>

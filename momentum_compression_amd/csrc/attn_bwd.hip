@@ -30,13 +30,13 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.
 template <typename T, int DP, bool BIAS, bool DROP, bool EXACT>
-__global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_q = (a.Tq + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal ? (DP == 64 ? kFallingTwo : kFalling) : kEven, bh, item)) return;
+    if (!xcd_work((uint32_t)a.B * a.H, tiles_q, a.causal ? kFallingTwo : kEven, bh, item)) return;
     const int qt = (int)(tiles_q - 1 - item);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
@@ -182,40 +182,34 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dq_kernel(Att
 }
 
 // Sums down the diagonals of the 32 x 32 scores' gradients of a wave (queries
-// as rows, eight consecutive ones to a lane) and adds them to the wave's bins.
-// The values go through the wave's own square in LDS.  Lane x + 32 g reads, of
-// the queries 16 g ... 16 g + 15, the key (q + x + 1) mod 32: those before the
-// wrap lie on the diagonal x + 1, the others on x - 31, so 16 reads a lane
-// serve all 63 diagonals.  No two lanes own the same one: no atomics.
+// as rows, eight consecutive ones to a lane), added to the wave's bins.  The
+// values go through LDS of the wave's own: a query's 32 keys, then 32 zeros
+// that stay.  Lane x sums the diagonal x - 31: it reads word q + x - 31 of each
+// query's row, which past either end of the keys lies among zeros (its own
+// row's or the one's before), so there is nothing to select.  No two lanes own
+// the same diagonal: no atomics.
 // first: the distance of diagonal 0.
-__device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* square, float* bins,
+constexpr int kSkewRow = 64;
+constexpr int kSkewFloats = 32 + 32 * kSkewRow;  // zeros before the first row
+
+__device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* skew, float* bins,
                                               int32_t first, int R, float& below, float& above,
                                               int lane) {
-    int x = lane & 31;
     const int half = lane >> 5;
-    // sixteen comparisons with x kept over the loop would take 32 scalar
-    // registers; they are made where they are used
-    asm volatile("" : "+v"(x));
+    float* to = skew + 32 + 8 * half * kSkewRow + (lane & 31);
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-        square[(16 * (r >> 3) + 8 * half + (r & 7)) * 32 + x] = ds[r];
+    for (int r = 0; r < 16; ++r) to[(16 * (r >> 3) + (r & 7)) * kSkewRow] = ds[r];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    float all = 0.0f, up = 0.0f;
+    const float* from = skew + 1 + lane;  // 32 + q (kSkewRow + 1) + lane - 31
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-        const int q = 16 * half + t;
-        const float v = square[q * 32 + ((q + x + 1) & 31)];
-        all += v;
-        up += q + x + 1 < 32 ? v : 0.0f;
-    }
-    const float down = (all - up) + other_half(all - up);
-    up += other_half(up);
-    const float v = half ? up : down;
-    const int32_t d = first + x + (half ? 1 : -31);
-    if (d <= -R) below += v;
-    else if (d >= R) above += v;
-    else if (half == 0 || x < 31) bins[d + R] += v;  // lane 63 owns none
+    for (int q = 0; q < 32; ++q) v[q & 3] += from[q * (kSkewRow + 1)];
+    const float sum = (v[0] + v[1]) + (v[2] + v[3]);
+    const int32_t d = first + lane - 31;
+    if (d <= -R) below += sum;
+    else if (d >= R) above += sum;
+    else if (lane < 63) bins[d + R] += sum;  // lane 63's diagonal is empty
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
@@ -243,8 +237,8 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     // negative lse and delta of a tile's queries, two buffers
     float* rows_lds = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
     uint32_t* kept_lds = reinterpret_cast<uint32_t*>(rows_lds + 256) + wave * 32;
-    float* square = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? wave * 1024 : 0);
-    float* window = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? kWaves * 1024 : 0);
+    float* skew = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? wave * kSkewFloats : 0);
+    float* window = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? kWaves * kSkewFloats : 0);
     float* all_bins = window + window_floats(R);
     float* bins = all_bins + wave * bins_n;
     float below = 0.0f, above = 0.0f;  // dS at or past the radius
@@ -267,19 +261,19 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     first = first < 0 ? 0 : first / kStep * kStep;
     const int32_t per_head =
         kt_i * kTileRows < n_keys && first < a.Tq ? (a.Tq - first + kStep - 1) / kStep : 0;
-    const int64_t total = (int64_t)per_head * group;
+    const uint32_t total = (uint32_t)per_head * (uint32_t)group;
 
     float row_value = 0.0f;
     int32_t head = hk * group, i0 = first;  // of the tile to load next
+    Feed<T, DP> qs((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, a.D, wave, lane);
+    Feed<T, DP> gs((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, a.D, wave, lane);
+    int64_t head_row = ((int64_t)b * a.H + head) * a.Tq;
     const auto load = [&](int to) {
         const int32_t i = i0 + (int)(threadIdx.x & 63);
-        const int64_t row = ((int64_t)b * a.H + head) * a.Tq + i;
+        const int64_t row = head_row + i;
         if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
         else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] * drop_inv : 0.0f;
         char* tile = lds + to * 2 * tile_bytes<DP>();
-        const Feed<T, DP> qs((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, a.D, wave, lane);
-        const Feed<T, DP> gs((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, a.D, wave,
-                             lane);
         qs.load(tile, i0, a.Tq, wave);
         gs.load(tile + tile_bytes<DP>(), i0, a.Tq, wave);
     };
@@ -308,14 +302,16 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         __syncthreads();
         for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
     };
-    if (TABLE)
+    if (TABLE) {
         for (int x = lane; x < bins_n; x += 64) bins[x] = 0.0f;
+        for (int x = lane; x < kSkewFloats; x += 64) skew[x] = 0.0f;
+    }
     if (total > 0) {
         load(0);
         keep_rows(0);
     }
     int buf = 0, filled = -1;
-    for (int64_t t = 0; t < total; ++t, buf ^= 1) {
+    for (uint32_t t = 0; t < total; ++t, buf ^= 1) {
         const int32_t h = head, it = i0;  // this tile
         char* qt = lds + buf * 2 * tile_bytes<DP>();
         char* gt = qt + tile_bytes<DP>();
@@ -334,6 +330,9 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             if (i0 >= a.Tq) {
                 i0 = first;
                 ++head;
+                qs.base += a.sq.h;
+                gs.base += a.sdo.h;
+                head_row += a.Tq;
             }
             load(buf ^ 1);
         }
@@ -363,6 +362,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(gt, 32 * u, kc, lane), vf[kc], dp);
+            read_ahead<1, 2 * kc_n, 6>();
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 s[r] = __builtin_amdgcn_exp2f(
@@ -419,13 +419,14 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                     dk[d] = Mma<T>::mul(col_frag<T, DP>(qt, 32 * u + 16 * c, d, lane), db, dk[d]);
                 }
             }
+            read_ahead<2, 4 * db_n, 8>();
             if (DROP) {  // the words are read before the next ones are written
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
             }
             if (TABLE) {
                 if (side == 0) {
-                    add_diagonals(ds, square, bins, jw - is - pos, R, below, above, lane);
+                    add_diagonals(ds, skew, bins, jw - is - pos, R, below, above, lane);
                 } else {
                     float v = 0.0f;
 #pragma unroll
@@ -476,7 +477,7 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
     if ((int64_t)a.B * a.Tk > 0) {
         size_t lds = tiles + (256 + (DROP ? kWaves * 32 : 0)) * sizeof(float) + (BIAS ? window : 0);
         if (TABLE)
-            lds += kWaves * (1024 + 2 * (size_t)a.bias.radius + 1) * sizeof(float);
+            lds += kWaves * (kSkewFloats + 2 * (size_t)a.bias.radius + 1) * sizeof(float);
         hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP, TABLE>),
                            dim3(xcd_grid((int64_t)a.B * a.Hkv, attn_tiles(a.Tk))), dim3(kThreads),
                            lds, st, a);
