@@ -123,6 +123,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 dp = Mma<T>::mul(row_frag<T, DP>(vt, 32 * u, kc, lane), gf[kc], dp);
+            read_ahead<1, 2 * kc_n, 4>();
             const int32_t seen = limit - js - 8 * half;
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -160,6 +161,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
                     acc[d] =
                         Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db, acc[d]);
             }
+            read_ahead<2, 2 * db_n, 4>();
         }
     }
 
