@@ -22,14 +22,24 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
     return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
 }
 
-// Queries as columns: dq and, for the second pass, delta.  dq takes delta from
-// the rounded output.  dtable is held in binary32, where that would show (each
-// row's error times the row's weight in a bucket), so with EXACT the row sums
-// of P dP are formed in binary32 on the way and handed on instead.
+// Queries as columns: dq and, for the second pass, delta as the row's sums of
+// P dP over those of P, in binary32.  dq itself takes delta from the rounded
+// output, which is there before the pass: off by half a step of the element
+// type times the row's output.  That is small beside what dS is rounded by
+// where many keys share the weight, but not where few do (a query that sees one
+// key has dS = 0), so workgroups with at most kTwice keys make the pass twice,
+// the first time for the sums alone.  Measured error of dq against 64 bits, in
+// units of the output's own rounding, with one pass and with two: 37 keys 1.51
+// and 1.41, 256 keys 1.47 and 1.43, fp16 rows of at most 5 keys 2.9 and 1.4;
+// with one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would
+// take 74 instead of 53 us for 16 sequences of up to 512 keys and 16 heads of
+// 64; one pass always, 50.
+constexpr int kTwice = 256;
+
 //
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.
-template <typename T, int DP, bool BIAS, bool DROP, bool EXACT>
+template <typename T, int DP, bool BIAS, bool DROP>
 __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
@@ -68,10 +78,9 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
                 delta = __builtin_fmaf((float)of[kc][e], (float)gf[kc][e], delta);
     }
     delta += other_half(delta);
-    if (!EXACT && i < a.Tq && half == 0) a.delta[row] = delta;
     if (DROP) delta /= a.drop.scale;
 
-    int32_t j0 = 0, end = n_keys;
+    int32_t end = n_keys;
     const int32_t last_q = (qt + 1) * kTileRows < a.Tq ? (qt + 1) * kTileRows - 1 : a.Tq - 1;
     if (a.causal && last_q + pos + 1 < end) end = last_q + pos + 1;
     const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
@@ -81,93 +90,105 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
     f32x16 acc[db_n];
 #pragma unroll
     for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
-    float sum = 0.0f;
+    float sum = 0.0f, weight = 0.0f;  // row sums of P dP and P
     const float scale2 = a.scale * kLog2e;
     const uint64_t drop_row = (uint64_t)row;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
     const Feed<T, DP> ks(kp, a.sk.t, a.D, wave, lane), vs(vp, a.sv.t, a.D, wave, lane);
-    if (j0 < end) {
-        ks.load(lds, j0, n_keys, wave);
-        vs.load(lds + tile_bytes<DP>(), j0, n_keys, wave);
-    }
     if (BIAS) fill_window(window, a.bias, h, a.scale);
-    int buf = 0;
-    for (; j0 < end; j0 += kStep, buf ^= 1) {
-        char* kt = lds + buf * 2 * tile_bytes<DP>();
-        char* vt = kt + tile_bytes<DP>();
-        // this tile (and the window) is there, and the other buffer is read
-        __syncthreads();
-        if (j0 + kStep < end) {
-            char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
-            ks.load(next, j0 + kStep, n_keys, wave);
-            vs.load(next + tile_bytes<DP>(), j0 + kStep, n_keys, wave);
+    for (int pass = end <= kTwice ? 0 : 1; pass < 2; ++pass) {
+        if (end > 0) {
+            ks.load(lds, 0, n_keys, wave);
+            vs.load(lds + tile_bytes<DP>(), 0, n_keys, wave);
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t js = j0 + 32 * u;
-            if (js > limit_hi) continue;
-            const int side = BIAS ? side_of(js, iw, pos, R) : 0;
-            f32x16 s = {}, dp = {};
-            float add = -lse2;
-            if (BIAS && side == 0) {
-                const float* at = window + (js + 8 * half - i - pos + R + kPad);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = at[16 * (r >> 3) + (r & 7)];
-            } else if (BIAS) {
-                add = __builtin_fmaf(window[side < 0 ? 0 : 2 * R + 2 * kPad], scale2, -lse2);
+        int buf = 0;
+        for (int32_t j0 = 0; j0 < end; j0 += kStep, buf ^= 1) {
+            char* kt = lds + buf * 2 * tile_bytes<DP>();
+            char* vt = kt + tile_bytes<DP>();
+            // this tile (and the window) is there, and the other buffer is read
+            __syncthreads();
+            if (j0 + kStep < end) {
+                char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
+                ks.load(next, j0 + kStep, n_keys, wave);
+                vs.load(next + tile_bytes<DP>(), j0 + kStep, n_keys, wave);
             }
 #pragma unroll
-            for (int kc = 0; kc < kc_n; ++kc)
-                s = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s);
+            for (int u = 0; u < 2; ++u) {
+                const int32_t js = j0 + 32 * u;
+                if (js > limit_hi) continue;
+                const int side = BIAS ? side_of(js, iw, pos, R) : 0;
+                f32x16 s = {}, dp = {};
+                float add = -lse2;
+                if (BIAS && side == 0) {
+                    const float* at = window + (js + 8 * half - i - pos + R + kPad);
 #pragma unroll
-            for (int kc = 0; kc < kc_n; ++kc)
-                dp = Mma<T>::mul(row_frag<T, DP>(vt, 32 * u, kc, lane), gf[kc], dp);
-            read_ahead<1, 2 * kc_n, 4>();
-            const int32_t seen = limit - js - 8 * half;
+                    for (int r = 0; r < 16; ++r) s[r] = at[16 * (r >> 3) + (r & 7)];
+                } else if (BIAS) {
+                    add = __builtin_fmaf(window[side < 0 ? 0 : 2 * R + 2 * kPad], scale2, -lse2);
+                }
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, add));
-            if (js + 31 > limit_lo) {
+                for (int kc = 0; kc < kc_n; ++kc)
+                    s = Mma<T>::mul(row_frag<T, DP>(kt, 32 * u, kc, lane), qf[kc], s);
+#pragma unroll
+                for (int kc = 0; kc < kc_n; ++kc)
+                    dp = Mma<T>::mul(row_frag<T, DP>(vt, 32 * u, kc, lane), gf[kc], dp);
+                read_ahead<1, 2 * kc_n, 4>();
+                const int32_t seen = limit - js - 8 * half;
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (16 * (r >> 3) + (r & 7) > seen) s[r] = 0.0f;
-            }
-            if (DROP) {
+                    s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, add));
+                if (js + 31 > limit_lo) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (16 * (r >> 3) + (r & 7) > seen) s[r] = 0.0f;
+                }
+                if (DROP) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t wd[4];
+                        drop_draws(wd, (uint32_t)(js + 16 * c + 8 * half) >> 3, drop_row, step,
+                                   a.drop.k0, a.drop.k1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!drop_keep(wd, e, a.drop.threshold)) dp[8 * c + e] = 0.0f;
+                    }
+                }
+                float part[2] = {0.0f, 0.0f}, part_w[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    part[r & 1] = __builtin_fmaf(s[r], dp[r], part[r & 1]);
+                    part_w[r & 1] += s[r];
+                }
+                sum += part[0] + part[1];
+                weight += part_w[0] + part_w[1];
+                if (pass == 0) continue;
+                float ds[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - delta);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t wd[4];
-                    drop_draws(wd, (uint32_t)(js + 16 * c + 8 * half) >> 3, drop_row, step,
-                               a.drop.k0, a.drop.k1);
+                    const x8 db = pack8<T>(ds + 8 * c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!drop_keep(wd, e, a.drop.threshold)) dp[8 * c + e] = 0.0f;
+                    for (int d = 0; d < db_n; ++d)
+                        acc[d] =
+                            Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db, acc[d]);
                 }
+                read_ahead<2, 2 * db_n, 4>();
             }
-            if (EXACT) {
-                float part = 0.0f;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) part = __builtin_fmaf(s[r], dp[r], part);
-                sum += part;
-            }
-            float ds[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - delta);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const x8 db = pack8<T>(ds + 8 * c);
-#pragma unroll
-                for (int d = 0; d < db_n; ++d)
-                    acc[d] =
-                        Mma<T>::mul(col_frag<T, DP>(kt, 32 * u + 16 * c, d, lane), db, acc[d]);
-            }
-            read_ahead<2, 2 * db_n, 4>();
+        }
+        sum += other_half(sum);
+        weight += other_half(weight);
+        sum = weight == 0.0f ? 0.0f : sum / weight;  // no key seen: 0
+        if (pass == 0) {
+            delta = sum;
+            sum = weight = 0.0f;
+            __syncthreads();  // the tiles are read
         }
     }
 
-    if (EXACT) sum += other_half(sum);
     if (i >= a.Tq) return;
-    if (EXACT && half == 0) a.delta[row] = DROP ? sum * a.drop.scale : sum;
+    if (half == 0) a.delta[row] = DROP ? sum * a.drop.scale : sum;
     const float out = DROP ? a.scale * a.drop.scale : a.scale;
     T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
 #pragma unroll
@@ -344,8 +365,12 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             if (is >= a.Tq || (a.causal && is + 31 + pos < jw) || jw >= n_keys) continue;
             const float* lse_at = lse2 + 32 * u + 8 * half;
             const float* delta_at = delta + 32 * u + 8 * half;
-            // the scores start from the bias, dP from -delta
-            f32x16 s = {}, dp;
+            // the scores start from the bias.  dP starts from 0 as in the query
+            // pass, so that both have the same bits and dS sums to 0 over a
+            // row: started from -delta, the matrix instructions' rounding
+            // showed in the far buckets of dtable (1.7e-6 of the table, at
+            // 1000 keys)
+            f32x16 s = {}, dp = {};
             const int side = BIAS ? side_of(jw, is, pos, R) : 0;
             if (BIAS && side == 0) {
                 const float* at = window + (j - is - 8 * half - pos + R + kPad);
@@ -356,8 +381,6 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = c;
             }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] = delta_at[16 * (r >> 3) + (r & 7)];
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
                 s = Mma<T>::mul(row_frag<T, DP>(qt, 32 * u, kc, lane), kf[kc], s);
@@ -407,10 +430,9 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                 if (DROP) {
                     const int m = __builtin_amdgcn_sbfe((int)kept_lds[q + 8 * half], key_bit, 1);
                     p[r] = __int_as_float(__float_as_int(p[r]) & m);
-                    g = __int_as_float((__float_as_int(g) & m) |
-                                       (__float_as_int(delta_at[q]) & ~m));
+                    g = __int_as_float(__float_as_int(g) & m);
                 }
-                ds[r] = s[r] * g;
+                ds[r] = s[r] * (g + delta_at[q]);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -473,7 +495,7 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
     const size_t window = (2 * (size_t)a.bias.radius + 1 + 2 * kPad) * sizeof(float);
     const size_t tiles = 4 * tile_bytes<DP>();
     if ((int64_t)a.B * a.Tq > 0)
-        hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, DROP, TABLE>),
+        hipLaunchKernelGGL((attn_dq_kernel<T, DP, BIAS, DROP>),
                            dim3(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq))), dim3(kThreads),
                            tiles + (BIAS ? window : 0), st, a);
     if ((int64_t)a.B * a.Tk > 0) {
