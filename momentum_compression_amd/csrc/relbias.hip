@@ -273,21 +273,37 @@ hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t T
     return hipGetLastError();
 }
 
-// Few, large parts once there are workgroups enough to fill the card.
+// Rows and sequences of a workgroup: the split whose rounds of 512 workgroups
+// (two a CU at a time) take the fewest row visits, each workgroup's bins and
+// its part of the join counted as 24 rows.  A map of 16 x 16 heads and 512 x 512
+// took 28 us with 512 workgroups, 31 with 1024, 36 with 2048; an odd one of
+// 3 x 7 and 1021 x 2053 50, 47 and 47, and 45 with the 840 that this picks.
 BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
-    constexpr int64_t kWant = 1024;
-    BiasGradPlan p;
+    constexpr int64_t kResident = 512;
+    BiasGradPlan best = {};
     const int32_t lanes = grad_lanes(Tk);
-    p.col_blocks = (Tk + 8 * lanes - 1) / (8 * lanes);
-    p.rows = 8 * kGradWaves;
-    const auto blocks = [&] { return (int64_t)((Tq + p.rows - 1) / p.rows) * p.col_blocks * H; };
-    while (blocks() > kWant && p.rows < 1024) p.rows *= 2;
-    p.row_blocks = (Tq + p.rows - 1) / p.rows;
-    int64_t split = (kWant + blocks() - 1) / blocks();
-    if (split > B) split = B;
-    p.batches = (int32_t)((B + split - 1) / split);
-    p.batch_blocks = (B + p.batches - 1) / p.batches;
-    return p;
+    const int32_t col_blocks = (Tk + 8 * lanes - 1) / (8 * lanes);
+    int64_t least = INT64_MAX;
+    for (int32_t rows = 8 * kGradWaves; rows <= 1024; rows *= 2) {
+        const int32_t row_blocks = (Tq + rows - 1) / rows;
+        for (int64_t split = 1; split <= B; split = split < 4 ? split + 1 : split + split / 2) {
+            BiasGradPlan p;
+            p.rows = rows;
+            p.row_blocks = row_blocks;
+            p.col_blocks = col_blocks;
+            p.batches = (int32_t)((B + split - 1) / split);
+            p.batch_blocks = (B + p.batches - 1) / p.batches;
+            const int64_t groups = p.parts() * H;
+            const int64_t visits = (int64_t)(rows < Tq ? rows : Tq) * p.batches + 24;
+            const int64_t cost = (groups + kResident - 1) / kResident * visits;
+            if (cost < least || (cost == least && groups < best.parts() * H)) {
+                least = cost;
+                best = p;
+            }
+        }
+        if (row_blocks == 1) break;
+    }
+    return best;
 }
 
 hipError_t launch_bias_join(const float* partials, const int32_t* map, float* dtable, int32_t H,
