@@ -32,7 +32,9 @@ __device__ __forceinline__ Vec8<T> load_tail(const T* p, int64_t n) {
 }
 
 // Whole 32-bit words go out: stores of single elements would be merged with
-// those of a partial group and split the access.
+// those of a partial group and split the access.  Past the caches: what a pass
+// over a tensor writes is not read by it (dropout with a residual over 16384 x
+// 4096 bf16: 74 -> 57 us; loads stay cached, past the caches 65).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float in[8]) {
     constexpr int words = 8 * sizeof(T) / 4;
@@ -40,7 +42,7 @@ __device__ __forceinline__ void store8(T* p, const float in[8]) {
     T x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = (T)in[e];
-    *reinterpret_cast<Words*>(p) = __builtin_bit_cast(Words, x);
+    __builtin_nontemporal_store(__builtin_bit_cast(Words, x), reinterpret_cast<Words*>(p));
 }
 
 // Division of a 32-bit number by one fixed divisor: a multiplication's high
