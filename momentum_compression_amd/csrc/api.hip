@@ -580,7 +580,10 @@ int rel_bias_expand(const float* table, const int32_t* map, void* out, int32_t d
 size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t radius) {
     if (B < 0 || check_lengths(Tq, Tk) || check_bias_sizes(H, 1, radius)) return 0;
     if (B == 0 || Tq == 0 || Tk == 0) return 256;
-    return bias_grad_ws_bytes(bias_grad_plan(B, H, Tq, Tk).parts(), H, radius);
+    // of either width of element
+    const int64_t wide = bias_grad_plan(B, H, Tq, Tk, ONEBIT_F32).parts();
+    const int64_t narrow = bias_grad_plan(B, H, Tq, Tk, ONEBIT_BF16).parts();
+    return bias_grad_ws_bytes(wide > narrow ? wide : narrow, H, radius);
 }
 
 int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtable, int32_t B,
@@ -594,7 +597,7 @@ int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtab
     const bool empty = B == 0 || Tq == 0 || Tk == 0;
     if (!map || !dtable || (!ds && !empty)) return ONEBIT_E_NULL;
     if (!aligned(ds, size) || !aligned(map, 4) || !aligned(dtable, 4)) return ONEBIT_E_ALIGN;
-    if (!empty && !groups_ok(bias_grad_plan(B, H, Tq, Tk).parts())) return ONEBIT_E_SIZE;
+    if (!empty && !groups_ok(2 * bias_grad_plan(B, H, Tq, Tk, dtype).parts())) return ONEBIT_E_SIZE;
     if (!ws || ws_bytes < rel_bias_workspace_bytes(B, H, Tq, Tk, radius)) return ONEBIT_E_WORKSPACE;
     if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     drop_stale_error();

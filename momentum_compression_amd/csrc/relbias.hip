@@ -57,15 +57,32 @@ __global__ __launch_bounds__(kThreads) void rel_bias_kernel(RelBias b, T* __rest
     }
 }
 
-// Gradient.  One pass over ds.  A wave holds 8 rows of 8 * W columns: a lane
-// has 8 columns of each row, whose 64 values fall on 15 diagonals, so it keeps
-// 15 sums in registers over all its sequences.  Neighbouring lanes' diagonals
-// overlap and are joined by one shuffle each; what is left are 8 distances a
-// lane, added to the wave's own bins in LDS without atomics (no two lanes own
-// the same distance), so the result does not depend on timing.  Narrow maps
-// give the other 64 / W parts of the wave other sequences.
+// Gradient.  One pass over ds.  A wave holds 8 rows of C * W columns: a lane has
+// C columns (16 bytes) of each row, whose values fall on C + 7 diagonals, so it
+// keeps that many sums in registers over all its sequences.  Neighbouring
+// lanes' diagonals overlap by 7 and are joined by 7 shuffles; what is left are
+// C distances a lane, added to the wave's own bins in LDS without atomics (no
+// two lanes own the same distance), so the result does not depend on timing.
+// Narrow maps give the other 64 / W parts of the wave other sequences.
 constexpr int kGradWaves = 8;
 constexpr int kGradThreads = 64 * kGradWaves;
+
+// 16 bytes of consecutive elements, and the first n of them (the others 0).
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Piece {
+    static constexpr int kCols = 16 / sizeof(T);
+    T v[kCols];
+    __device__ __forceinline__ static Piece load(const T* p) {
+        return *reinterpret_cast<const Piece*>(p);
+    }
+    __device__ __forceinline__ static Piece tail(const T* p, int n) {
+        Piece x = {};
+#pragma unroll
+        for (int e = 0; e < kCols - 1; ++e)
+            if (e < n) x.v[e] = p[e];
+        return x;
+    }
+};
 
 template <typename T, int W>
 __global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __restrict__ ds,
@@ -74,6 +91,7 @@ __global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __rest
                                                             int32_t radius, int32_t Tq, int32_t Tk,
                                                             int32_t q_pos) {
     extern __shared__ float lds[];  // [waves][2 radius + 1]
+    constexpr int C = Piece<T>::kCols;
     const int R = radius, bins_n = 2 * R + 1;
     const int wave = threadIdx.x >> 6, lane = lane_id();
     const int col = lane % W, sub = lane / W;
@@ -86,48 +104,51 @@ __global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __rest
     part /= plan.batch_blocks;
     const int cb = (int)(part % plan.col_blocks);
     const int rb = (int)(part / plan.col_blocks);
-    const int32_t c0 = cb * (8 * W) + 8 * col;
+    const int32_t c0 = cb * (C * W) + C * col;
     const int32_t b1 = (bb + 1) * plan.batches < B ? (bb + 1) * plan.batches : B;
-    const bool whole = c0 + 8 <= Tk;
+    const bool whole = c0 + C <= Tk;
     float far_lo = 0.0f, far_hi = 0.0f;
-    for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows; i0 += 8 * kGradWaves) {
-        float acc[15];
+    for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows;
+         i0 += 8 * kGradWaves) {
+        float acc[C + 7];
 #pragma unroll
-        for (int k = 0; k < 15; ++k) acc[k] = 0.0f;
+        for (int k = 0; k < C + 7; ++k) acc[k] = 0.0f;
         for (int32_t b = bb * plan.batches + sub; b < b1; b += subs) {
             const T* p = ds + (((int64_t)b * H + h) * Tq + i0) * (int64_t)Tk + c0;
-            Vec8<T> v[8];
+            Piece<T> v[8];
             if (whole && i0 + 8 <= Tq) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) v[r] = load8(p + (int64_t)r * Tk);
+                for (int r = 0; r < 8; ++r) v[r] = Piece<T>::load(p + (int64_t)r * Tk);
             } else {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    v[r] = Vec8<T>{};
+                    v[r] = Piece<T>{};
                     if (i0 + r >= Tq) continue;
-                    v[r] = whole ? load8(p + (int64_t)r * Tk)
-                                 : load_tail(p + (int64_t)r * Tk, Tk - c0);
+                    v[r] = whole ? Piece<T>::load(p + (int64_t)r * Tk)
+                                 : Piece<T>::tail(p + (int64_t)r * Tk, Tk - c0);
                 }
             }
 #pragma unroll
             for (int r = 0; r < 8; ++r)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e - r + 7] += (float)v[r].v[e];
+                for (int e = 0; e < C; ++e) acc[e - r + 7] += (float)v[r].v[e];
         }
 #pragma unroll
         for (int off = W; off < 64; off <<= 1)
 #pragma unroll
-            for (int k = 0; k < 15; ++k) acc[k] += __shfl_xor(acc[k], off, 64);
+            for (int k = 0; k < C + 7; ++k) acc[k] += __shfl_xor(acc[k], off, 64);
+        // the next lane's sum k is this lane's k + C; ascending, so that what a
+        // sum takes in is passed on with it where C < 7
 #pragma unroll
         for (int k = 0; k < 7; ++k) {
             const float next = __shfl_down(acc[k], 1, 64);
-            if (col + 1 < W) acc[k + 8] += next;
+            if (col + 1 < W) acc[k + C] += next;
         }
         // acc[k] is the sum of distance d0 + k
         const int32_t d0 = c0 - i0 - q_pos - 7;
         if (sub == 0) {
 #pragma unroll
-            for (int k = 0; k < 15; ++k) {
+            for (int k = 0; k < C + 7; ++k) {
                 if (k < 7 && col != 0) continue;
                 const int32_t d = d0 + k;
                 if (d <= -R) far_lo += acc[k];
@@ -229,16 +250,16 @@ void grad_w(const void* ds, float* partials, const BiasGradPlan& plan, int32_t B
 }
 
 // Lanes that span the columns of a row: the smallest power of two that does.
-int32_t grad_lanes(int32_t Tk) {
+int32_t grad_lanes(int32_t Tk, int32_t cols) {
     int32_t w = 8;
-    while (w < 64 && 8 * w < Tk) w *= 2;
+    while (w < 64 && cols * w < Tk) w *= 2;
     return w;
 }
 
 template <typename T>
 void grad_t(const void* ds, float* partials, const BiasGradPlan& plan, int32_t B, int32_t H,
             int32_t radius, int32_t Tq, int32_t Tk, int32_t q_pos, hipStream_t st) {
-    switch (grad_lanes(Tk)) {
+    switch (grad_lanes(Tk, Piece<T>::kCols)) {
         case 8: return grad_w<T, 8>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
         case 16: return grad_w<T, 16>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
         case 32: return grad_w<T, 32>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st);
@@ -278,11 +299,12 @@ hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t T
 // its part of the join counted as 24 rows.  A map of 16 x 16 heads and 512 x 512
 // took 28 us with 512 workgroups, 31 with 1024, 36 with 2048; an odd one of
 // 3 x 7 and 1021 x 2053 50, 47 and 47, and 45 with the 840 that this picks.
-BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk) {
+BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t dtype) {
     constexpr int64_t kResident = 512;
     BiasGradPlan best = {};
-    const int32_t lanes = grad_lanes(Tk);
-    const int32_t col_blocks = (Tk + 8 * lanes - 1) / (8 * lanes);
+    const int32_t cols = dtype == ONEBIT_F32 ? 4 : 8;
+    const int32_t wide = cols * grad_lanes(Tk, cols);
+    const int32_t col_blocks = (Tk + wide - 1) / wide;
     int64_t least = INT64_MAX;
     for (int32_t rows = 8 * kGradWaves; rows <= 1024; rows *= 2) {
         const int32_t row_blocks = (Tq + rows - 1) / rows;
@@ -319,7 +341,7 @@ hipError_t launch_rel_bias_grad(const void* ds, int32_t dtype, const int32_t* ma
                                 int32_t B, int32_t H, int32_t n_buckets, int32_t radius,
                                 int32_t Tq, int32_t Tk, int32_t q_pos, bool accumulate,
                                 float* partials, hipStream_t st) {
-    const BiasGradPlan plan = bias_grad_plan(B, H, Tq, Tk);
+    const BiasGradPlan plan = bias_grad_plan(B, H, Tq, Tk, dtype);
     switch (dtype) {
         case ONEBIT_F32: grad_t<float>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st); break;
         case ONEBIT_BF16: grad_t<bf16>(ds, partials, plan, B, H, radius, Tq, Tk, q_pos, st); break;

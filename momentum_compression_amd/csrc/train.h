@@ -89,7 +89,7 @@ struct BiasGradPlan {
     int32_t batch_blocks;
     int64_t parts() const { return (int64_t)row_blocks * col_blocks * batch_blocks; }
 };
-BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk);
+BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t dtype);
 
 hipError_t launch_rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtable,
                                 int32_t B, int32_t H, int32_t n_buckets, int32_t radius,
