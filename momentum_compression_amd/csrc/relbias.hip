@@ -297,8 +297,8 @@ hipError_t launch_rel_bias(const RelBias& b, void* out, int32_t dtype, int32_t T
 // Rows and sequences of a workgroup: the split whose rounds of 512 workgroups
 // (two a CU at a time) take the fewest row visits, each workgroup's bins and
 // its part of the join counted as 24 rows.  A map of 16 x 16 heads and 512 x 512
-// took 28 us with 512 workgroups, 31 with 1024, 36 with 2048; an odd one of
-// 3 x 7 and 1021 x 2053 50, 47 and 47, and 45 with the 840 that this picks.
+// takes 28 us with 512 workgroups, against 31 with 1024 and 36 with 2048; an odd
+// binary32 one of 3 x 7 and 1021 x 2053 34 us with the 504 that this picks.
 BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_t dtype) {
     constexpr int64_t kResident = 512;
     BiasGradPlan best = {};
