@@ -549,14 +549,19 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * values of keys that only the causal mask hides are multiplied by 0 and have
  * to be finite.  k_len and q_pos_of are clamped to 0 ... Tk and +-2^29.
  *
+ * A table value so low that it leaves binary32 when divided by the scale or
+ * multiplied by log2 e counts as -infinity: its keys have no weight.
+ *
  * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
- * heads.  *_stride: elements between sequences, tokens and heads, multiples
- * of 8, between tokens at most 2^23; D a multiple of 8, 8 ... 128, its elements side by side; 16-byte
- * aligned.  So a fused projection's output and a cache of either order serve
- * as they are.  Sequences of a batch may share keys (stride 0); outputs must
- * not overlap each other or themselves.  lse [B][H][Tq] float, optional in
- * the forward pass.  table [n_buckets][H] float and map as rel_bias_expand,
- * or NULL, NULL, 0, 0 without a bias.  0 <= p < 1; scale positive and finite.
+ * heads; D a multiple of 8, 8 ... 128, its elements side by side, 16-byte
+ * aligned.  *_stride: elements between sequences, tokens and heads, multiples
+ * of 8, between tokens at most 2^23.  So a fused projection's output and a
+ * cache of either order serve as they are.  Sequences of a batch may share
+ * keys (stride 0); an output's dimensions must lie one within the other, and
+ * outputs must not overlap each other or an input.
+ * lse [B][H][Tq] float, optional in the forward pass.  table [n_buckets][H]
+ * float and map as rel_bias_expand, or NULL, NULL, 0, 0 without a bias.
+ * 0 <= p < 1; 2^-64 <= scale <= 2^64.
  * ws: at least rel_attention_workspace_bytes(...) bytes, 256-byte aligned,
  * scratch between calls (a forward call whose need is 256 takes NULL too).
  */

@@ -229,11 +229,13 @@ __device__ __forceinline__ int window_floats(int radius) { return 2 * radius + 1
 
 __device__ __forceinline__ void fill_window(float* w, const RelBias& b, int h, float scale) {
     const int R = b.radius;
+    const float inv_scale = 1.0f / scale;
     for (int x = threadIdx.x; x < window_floats(R); x += kThreads) {
         int i = x - kPad;
         i = i < 0 ? 0 : (i > 2 * R ? 2 * R : i);
         const int m = b.map[i];
-        w[x] = (uint32_t)m < (uint32_t)b.n_buckets ? b.table[(int64_t)m * b.H + h] / scale : 0.0f;
+        w[x] = (uint32_t)m < (uint32_t)b.n_buckets ? b.table[(int64_t)m * b.H + h] * inv_scale
+                                             : 0.0f;
     }
 }
 

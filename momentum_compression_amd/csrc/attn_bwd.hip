@@ -34,11 +34,11 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
 // with one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would
 // take 74 instead of 53 us for 16 sequences of up to 512 keys and 16 heads of
 // 64; one pass always, 50.
-constexpr int kTwice = 256;
-
 //
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.
+constexpr int kTwice = 256;
+
 template <typename T, int DP, bool BIAS, bool DROP>
 __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
@@ -210,8 +210,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
 // that stay.  Lane x sums the diagonal x - 31: it reads word q + x - 31 of each
 // query's row, which past either end of the keys lies among zeros (its own
 // row's or the one's before), so there is nothing to select.  No two lanes own
-// the same diagonal: no atomics.
-// first: the distance of diagonal 0.
+// the same diagonal: no atomics.  `first` is the distance of lane 31's.
 constexpr int kSkewRow = 64;
 constexpr int kSkewFloats = 32 + 32 * kSkewRow;  // zeros before the first row
 
@@ -247,7 +246,8 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     constexpr int kc_n = DP / 16, db_n = DP / 32;
     const uint32_t tiles_k = (a.Tk + kTileRows - 1) / kTileRows;
     uint32_t bh, item;
-    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, a.causal ? (DP == 64 ? kFallingTwo : kFalling) : kEven, bh, item)) return;
+    const WorkOrder order = !a.causal ? kEven : (DP == 64 ? kFallingTwo : kFalling);
+    if (!xcd_work((uint32_t)a.B * a.Hkv, tiles_k, order, bh, item)) return;
     // under a causal mask the first keys have the most queries: first
     const int kt_i = (int)item;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
@@ -512,8 +512,10 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 template <typename T, int DP>
 hipError_t run_d(const AttnArgs& a, bool table, hipStream_t st) {
     const bool bias = a.bias.radius > 0, drop = a.drop.threshold != kDropAll;
-    if (table) return drop ? run<T, DP, true, true, true>(a, st) : run<T, DP, true, false, true>(a, st);
-    if (bias) return drop ? run<T, DP, true, true, false>(a, st) : run<T, DP, true, false, false>(a, st);
+    if (table)
+        return drop ? run<T, DP, true, true, true>(a, st) : run<T, DP, true, false, true>(a, st);
+    if (bias)
+        return drop ? run<T, DP, true, true, false>(a, st) : run<T, DP, true, false, false>(a, st);
     return drop ? run<T, DP, false, true, false>(a, st) : run<T, DP, false, false, false>(a, st);
 }
 

@@ -52,14 +52,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
     const int32_t limit_lo = a.causal && pos < n_keys - 1 ? pos : n_keys - 1;
 
-    const float scale2 = a.scale * kLog2e;
+    const float scale2 = a.scale * kLog2e, inv_scale = 1.0f / a.scale;
     const auto bias_at = [&](int32_t d) {  // of this lane's head
         d = d < -R ? -R : (d > R ? R : d);
         const int m = a.bias.map[d + R];
-        return (uint32_t)m < (uint32_t)a.bias.n_buckets ? a.bias.table[(int64_t)m * a.H + h] : 0.0f;
+        // divided by the scale and multiplied again, so that the values too low
+        // for the other kernels' windows are too low here
+        return (uint32_t)m < (uint32_t)a.bias.n_buckets
+                   ? a.bias.table[(int64_t)m * a.H + h] * inv_scale * scale2
+                   : 0.0f;
     };
-    const float below = BIAS ? bias_at(-R) * kLog2e : 0.0f;
-    const float above = BIAS ? bias_at(R) * kLog2e : 0.0f;
+    const float below = BIAS ? bias_at(-R) : 0.0f;
+    const float above = BIAS ? bias_at(R) : 0.0f;
     const uint64_t drop_row = ((uint64_t)b * a.H + h) * (uint64_t)a.Tq + (uint64_t)i;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
@@ -107,9 +111,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
         if (BIAS && j0 + 31 - pos > -R && j0 - (pos + a.Tq - 1) < R) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_fmaf(
-                    s[r], scale2,
-                    bias_at(j0 + 16 * (r >> 3) + 8 * half + (r & 7) - i - pos) * kLog2e);
+                s[r] = __builtin_fmaf(s[r], scale2,
+                                      bias_at(j0 + 16 * (r >> 3) + 8 * half + (r & 7) - i - pos));
         } else {
             const float c = !BIAS ? 0.0f : (j0 < pos ? below : above);
 #pragma unroll

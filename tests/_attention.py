@@ -17,6 +17,9 @@ e = 2^-24 (binary32), to first order and per element:
             where it is rounded for a product
   dq, dk    scale times the product of that bound with |k| or |q|, (n + 8) e
             of the sum's own terms, u of the result; dv as o
+  below     a weight or dS below the type's normal range is rounded by up to half
+            its smallest step instead (`sub`); weights are at least as large
+            against their row's sum as they are alone
   dtable    the unrounded dS's bounds summed, and the additions' e: fewer than
             8 roundings a tile of 32 and one a tile on the way
 """
@@ -38,12 +41,18 @@ def half_step(dtype):
     return torch.finfo(TYPES[dtype]).eps / 2
 
 
+def below_normal(u):
+    """Half the smallest step of the type with half step u."""
+    return 2.0 ** -25 if u == 2.0 ** -11 else 2.0 ** -134
+
+
 def expected(q, k, v, do, scale, causal, q_pos, k_len, table, bmap, p, seed, step, u):
     """(oracle results, bounds), both dicts of numpy arrays."""
     want = ref.attention(q, k, v, scale, causal, q_pos, k_len, table, bmap, p, seed, step, do=do)
     B, Tq, H, D = q.shape
     Tk, Hkv = k.shape[1], k.shape[2]
     G = H // Hkv
+    sub = below_normal(u)
     tol = {n: np.zeros_like(x) for n, x in want.items()}
     for b in range(B):
         pos = int(q_pos[b]) if np.ndim(q_pos) else int(q_pos)
@@ -67,7 +76,7 @@ def expected(q, k, v, do, scale, causal, q_pos, k_len, table, bmap, p, seed, ste
             tol["lse"][b, h] = (worst + (Tk + 24) * E + 4 * E * ln)[:, 0]
             f = ref.keep_factor(Tq, Tk, p, seed, step, (b * H + h) * Tq) if p > 0 else 1.0
             o = want["o"][b, :, h]
-            to = u * np.abs(o) + (u + ep) * ((prob * f) @ np.abs(vh))
+            to = u * np.abs(o) + ((u + ep) * prob * f + sub * seen * f) @ np.abs(vh)
             tol["o"][b, :, h] = to
             if do is None:
                 continue
@@ -81,11 +90,12 @@ def expected(q, k, v, do, scale, causal, q_pos, k_len, table, bmap, p, seed, ste
                        + Tk * E * (prob * np.abs(dp)).sum(1, keepdims=True))
             ds = prob * (dp - delta)
             t_ds = prob * (ep * (np.abs(dp) + np.abs(delta)) + tdp)
-            t_round = t_ds + prob * t_delta + u * np.abs(ds)
+            t_round = t_ds + prob * t_delta + u * np.abs(ds) + sub * seen * np.max(f)
             tol["dq"][b, :, h] = scale * ((t_round + (Tk + 8) * E * np.abs(ds)) @ np.abs(kh))
             tol["dk"][b, :, h // G] += scale * ((t_round + (G * Tq + 8) * E * np.abs(ds)).T
                                                 @ np.abs(qh))
-            tol["dv"][b, :, h // G] += ((u + ep + (G * Tq + 8) * E) * prob * f).T @ np.abs(g)
+            tol["dv"][b, :, h // G] += ((u + ep + (G * Tq + 8) * E) * prob * f
+                                        + sub * seen * f).T @ np.abs(g)
             if table is not None:
                 adds = 8 * (Tq + Tk) / 32 + Tk / 8 + 64
                 both = t_ds + prob * t_exact + adds * E * np.abs(ds)

@@ -71,9 +71,8 @@ def _poison_past(k_len, *tensors):
 
 
 def _tiny(dtype):
-    # half the smallest step of the type, and as much again for each rounded
-    # operand of fp16's narrow range
-    return 2.0 ** -133 if dtype == "bf16" else 2.0 ** -22
+    # the smallest step of the type, for results below its normal range
+    return 2.0 ** -133 if dtype == "bf16" else 2.0 ** -24
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -256,6 +255,116 @@ def test_lowest_bias_values():
         ob.rel_attention_forward(q, k, v, want, table=safe, bucket_map=bmap, causal=True,
                                  ws=workspace(q, k))
         assert torch.equal(o, want) and bool(lse.isfinite().all())
+
+
+@pytest.mark.parametrize("Tq", [1, 50])
+def test_lowest_bias_values_backward(Tq):
+    """... nor in the gradients: those of the keys it hides are 0, and so are
+    all of a row that it hides whole.  One query goes through the kernel for
+    few, whose bias comes another way."""
+    dev = device()
+    g = gen(4, dev)
+    q, k, v = make("bf16", 1, 2, 2, Tq, 80, 64, g, dev)
+    do = torch.randn(q.shape, generator=g, device=dev).bfloat16()
+    bmap = rel_bucket_map(8, 20, True, dev)
+    for low in (torch.finfo(torch.float32).min, -1e38, float("-inf")):
+        table = torch.randn((8, 2), generator=g, device=dev)
+        table[5:, 0] = low                    # every key after the query
+        table[:, 1] = low                     # every key of the second head
+        dtable = torch.full_like(table, 9)
+        got = _backward(q, k, v, dict(table=table, bucket_map=bmap), do, dtable)
+        for n in ("o", "dq", "dk", "dv"):
+            assert bool(got[n].isfinite().all()) and bool((got[n][:, :, 1] == 0).all()), n
+        assert bool((dtable[5:] == 0).all()) and bool((dtable[:, 1] == 0).all())
+        assert bool(dtable.isfinite().all())
+        assert bool((got["lse"][:, 1] == float("-inf")).all())
+        assert bool((got["dk"][:, Tq:, 0] == 0).all()) and bool((got["dv"][:, Tq:, 0] == 0).all())
+        safe = torch.where(table == low, torch.zeros_like(table), table)
+        want = _backward(q, k, v, dict(table=safe, bucket_map=bmap, causal=True), do,
+                         torch.empty_like(table))
+        for n in ("o", "dq", "dk", "dv"):
+            assert torch.equal(got[n][:, :, 0], want[n][:, :, 0]), n
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at once, each with its own workspace (split keys,
+    and a backward pass with the table's gradient), equal the same calls one
+    after the other."""
+    dev = device()
+    g = gen(21, dev)
+    bmap = rel_bucket_map(32, 64, True, dev)
+    work = []
+    for Tq, Tk in ((1, 9000), (300, 900)):
+        q, k, v = make("bf16", 2, 4, 2, Tq, Tk, 64, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).bfloat16()
+        table = torch.randn((32, 4), generator=g, device=dev)
+        how = dict(table=table, bucket_map=bmap, p=0.1, seed=SEED, step=2, q_pos=Tk - Tq)
+        work.append((q, k, v, how, do, [workspace(q, k, 64, True) for _ in range(2)]))
+    alone = [_backward(q, k, v, how, do, torch.empty_like(how["table"]), ws=ws[0])
+             for q, k, v, how, do, ws in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    both = [[], []]
+    for _ in range(5):
+        for n, (q, k, v, how, do, ws) in enumerate(work):
+            with torch.cuda.stream(streams[n]):
+                both[n].append(_backward(q, k, v, how, do, torch.empty_like(how["table"]),
+                                         ws=ws[1]))
+    torch.cuda.synchronize()
+    for want, gots in zip(alone, both):
+        for got in gots:
+            for n in want:
+                assert torch.equal(got[n], want[n]), n
+
+
+def test_two_graphs_share_a_workspace():
+    """The workspace holds nothing between calls: two graphs captured with the
+    same one, replayed in turn, give the eager results."""
+    dev = device()
+    g = gen(22, dev)
+    bmap = rel_bucket_map(32, 64, True, dev)
+    graphs, results, inputs = [], [], []
+    q0, k0, _ = make("bf16", 2, 4, 4, 1, 6000, 64, g, dev)
+    ws = torch.full((max(workspace(q0, k0, 64, True).numel(), 1 << 22),), 0xFF, dtype=torch.uint8,
+                    device=dev)
+    for Tq, Tk in ((1, 6000), (129, 130)):
+        q, k, v = make("bf16", 2, 4, 4, Tq, Tk, 64, g, dev)
+        table = torch.randn((32, 4), generator=g, device=dev)
+        do = torch.randn(q.shape, generator=g, device=dev).bfloat16()
+        inputs.append((q, k, v, dict(table=table, bucket_map=bmap), do))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            _backward(*inputs[-1], torch.empty_like(table), ws=ws)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results.append(_backward(*inputs[-1], torch.empty_like(table), ws=ws))
+        graphs.append(graph)
+    for t in range(4):
+        for n, (q, k, v, how, do) in enumerate(inputs):
+            q.copy_(torch.randn(q.shape, generator=g, device=dev))
+            graphs[n].replay()
+            torch.cuda.synchronize()
+            want = _backward(q, k, v, how, do, torch.empty_like(how["table"]))
+            torch.cuda.synchronize()
+            for x in want:
+                assert torch.equal(results[n][x], want[x]), (t, n, x)
+
+
+def test_largest_token_strides_and_a_long_cache():
+    """Tokens 2^23 elements apart, and rows past the 32-bit offsets of a cache."""
+    dev = device()
+    g = gen(23, dev)
+    store = torch.zeros(300 * (1 << 23), dtype=torch.bfloat16, device=dev)  # 5 GB
+    apart = store.as_strided((1, 300, 2, 64), (0, 1 << 23, 64, 1))
+    for Tq in (1, 40):
+        q, k, v = make("bf16", 1, 2, 2, Tq, 300, 64, g, dev)
+        apart.copy_(k)
+        o, want = torch.empty_like(q), torch.empty_like(q)
+        ob.rel_attention_forward(q, apart, v, o, ws=workspace(q, k))
+        ob.rel_attention_forward(q, k, v, want, ws=workspace(q, k))
+        assert torch.equal(o, want)
 
 
 def test_nothing_to_attend_or_ask():
