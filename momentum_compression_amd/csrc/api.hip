@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <mutex>
+#include <utility>
 
 #include "attention.h"
 #include "common.h"
@@ -504,7 +505,7 @@ int lamb_momentum_scale(const float* m, int64_t N, const int64_t* seg_off, int32
 namespace {
 
 constexpr int64_t kMaxPositions = (int64_t)1 << 29;  // lengths and positions: 32-bit differences
-constexpr int64_t kMaxLd = (int64_t)1 << 40;         // strides: 64-bit offsets stay in range
+constexpr int64_t kMaxLd = (int64_t)1 << 40;         // strides: more than any memory spans
 constexpr int64_t kMaxTokenStride = (int64_t)1 << 23;  // 64 rows: a buffer below 2^31 bytes
 
 // bytes of an element, 0 for an unknown type
@@ -614,16 +615,28 @@ int rel_bias_grad(const void* ds, int32_t dtype, const int32_t* map, float* dtab
 namespace {
 
 // Strides of a tensor of T tokens of heads * D elements per sequence.  What is
-// written must not overlap itself.
+// written must not overlap itself: each dimension steps over all that the ones
+// of smaller strides span, as every slice or reordering of a whole tensor does.
 int check_heads(const void* p, const int64_t s[3], int32_t B, int32_t T, int32_t heads, int32_t D,
                 bool written) {
     if (B == 0 || T == 0) return ONEBIT_OK;
     if (!p) return ONEBIT_E_NULL;
-    const int64_t count[3] = {B, T, heads};
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 3; ++k)
         if (s[k] < 0 || s[k] > (k == 1 ? kMaxTokenStride : kMaxLd) || s[k] % 8)
             return ONEBIT_E_SIZE;
-        if (written && count[k] > 1 && s[k] < D) return ONEBIT_E_SIZE;
+    int64_t dim[3][2] = {{s[0], B}, {s[1], T}, {s[2], heads}};  // stride, count
+    for (int k = 0; k < 3; ++k)
+        for (int m = 0; m + 1 < 3; ++m)
+            if (dim[m][0] > dim[m + 1][0]) {
+                std::swap(dim[m][0], dim[m + 1][0]);
+                std::swap(dim[m][1], dim[m + 1][1]);
+            }
+    int64_t span = D;
+    for (int k = 0; k < 3 && written; ++k) {
+        if (dim[k][1] == 1) continue;
+        if (dim[k][0] < span) return ONEBIT_E_SIZE;
+        if (dim[k][0] > (INT64_MAX - span) / dim[k][1]) return ONEBIT_E_SIZE;  // past any memory
+        span += dim[k][0] * (dim[k][1] - 1);
     }
     return aligned(p, 16) ? ONEBIT_OK : ONEBIT_E_ALIGN;
 }
@@ -679,7 +692,9 @@ int check_attention(const rel_attention_args* a) {
         if (!a->table || !a->map) return ONEBIT_E_NULL;
         if ((st = check_bias_sizes(a->H, a->n_buckets, a->radius))) return st;
     }
-    if (!(a->p >= 0.0f && a->p < 1.0f) || !(a->scale > 0.0f && isfinite(a->scale)) || !position_ok(a->q_pos) ||
+    // the bias divided by the scale, and the scale times log2 e, stay in range
+    if (!(a->scale >= 0x1p-64f && a->scale <= 0x1p64f)) return ONEBIT_E_ARG;
+    if (!(a->p >= 0.0f && a->p < 1.0f) || !position_ok(a->q_pos) ||
         (a->causal != 0 && a->causal != 1))
         return ONEBIT_E_ARG;
     if (!aligned(a->table, 4) || !aligned(a->map, 4) || !aligned(a->q_pos_of, 4) ||
@@ -770,7 +785,8 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
     if ((a->dtable && !a->table) || (a->accumulate != 0 && a->accumulate != 1))
         return ONEBIT_E_ARG;
     if (!aligned(a->dtable, 4)) return ONEBIT_E_ALIGN;
-    const AttnSizes z = attn_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
+    const AttnSizes z =
+        attn_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
     if (!ws || ws_bytes < z.delta + z.partials) return ONEBIT_E_WORKSPACE;
     if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     AttnArgs k = attn_args(a);

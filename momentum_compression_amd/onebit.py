@@ -206,7 +206,9 @@ def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
         raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
     if x.numel() < count:
         raise ValueError(f"{name} holds {x.numel()} elements, the call needs {count}")
-    return _ptr(x)
+    if not x.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return x.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
@@ -422,15 +424,26 @@ def _dtype(t, name: str):
 _BY_DTYPE = {}  # _DTYPES by the dtype object, as calls meet them
 
 
-def _stream_of(x, stream) -> Optional[int]:
-    """The call's stream; the tensors must live on the device that the call
-    launches on."""
+def _stream_of(stream, *tensors) -> Optional[int]:
+    """The call's stream; its tensors must live on the device that it launches
+    on (None and raw addresses are passed over)."""
     import torch
 
-    if x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {x.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    current = torch.cuda.current_device()
+    for x in tensors:
+        if x is not None and not isinstance(x, int) and x.get_device() != current:
+            raise ValueError(f"a tensor is on {x.device}, the current device is cuda:{current}")
+    if stream is None:
+        # the raw handle: building a Stream object around it costs 2.7 us
+        return torch._C._cuda_getCurrentRawStream(current)
     return _stream(stream)
+
+
+def _i32(x, name: str) -> int:
+    """A number that the C ABI takes in 32 bits, which would wrap silently."""
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name} = {x} does not fit in 32 bits")
+    return x
 
 
 def _rows(x, rows: int, cols: int, kind: str, name: str):
@@ -466,7 +479,8 @@ def dropout_apply(x, y, rows: int, cols: int, p: float, seed: int, step: int, re
     yp, ld_y = _rows(y, rows, cols, kind, "y")
     _check("dropout_apply", load().dropout_apply(
         xp, rp, yp, code, rows, cols, ld_x, ld_r, ld_y, p, seed & 0xFFFFFFFFFFFFFFFF,
-        step & 0xFFFFFFFF, _buf(step_dev, 1, "u32", "step_dev"), row0, _stream_of(x, stream)))
+        step & 0xFFFFFFFF, _buf(step_dev, 1, "u32", "step_dev"), row0,
+        _stream_of(stream, x, y, residual, step_dev)))
 
 
 def _shape(t, dims: int, name: str):
@@ -493,12 +507,14 @@ def rel_bias_expand(table, bucket_map, out, q_pos: int = 0, stream=None) -> None
     _check("rel_bias_expand", load().rel_bias_expand(
         _buf(table, n_buckets * H, "f32", "table"), _buf(bucket_map, 2 * radius + 1, "i32",
                                                          "bucket_map"),
-        _buf(out, H * Tq * Tk, kind, "out"), code, H, n_buckets, radius, Tq, Tk, q_pos,
-        _stream_of(out, stream)))
+        _buf(out, H * Tq * Tk, kind, "out"), code, _i32(H, "H"), _i32(n_buckets, "n_buckets"),
+        _i32(radius, "radius"), _i32(Tq, "Tq"), _i32(Tk, "Tk"), _i32(q_pos, "q_pos"),
+        _stream_of(stream, table, bucket_map, out)))
 
 
 def rel_bias_workspace_bytes(B: int, H: int, Tq: int, Tk: int, radius: int) -> int:
-    return int(load().rel_bias_workspace_bytes(B, H, Tq, Tk, radius))
+    return int(load().rel_bias_workspace_bytes(_i32(B, "B"), _i32(H, "H"), _i32(Tq, "Tq"),
+                                               _i32(Tk, "Tk"), _i32(radius, "radius")))
 
 
 def rel_bias_grad(ds, bucket_map, dtable, q_pos: int = 0, accumulate: bool = False, ws=None,
@@ -513,25 +529,28 @@ def rel_bias_grad(ds, bucket_map, dtable, q_pos: int = 0, accumulate: bool = Fal
     _check("rel_bias_grad", load().rel_bias_grad(
         _buf(ds, B * H * Tq * Tk, kind, "ds"), code, _buf(bucket_map, 2 * radius + 1, "i32",
                                                           "bucket_map"),
-        _buf(dtable, n_buckets * H, "f32", "dtable"), B, H, n_buckets, radius, Tq, Tk, q_pos,
-        int(bool(accumulate)), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream_of(ds, stream)))
+        _buf(dtable, n_buckets * H, "f32", "dtable"), _i32(B, "B"), _i32(H, "H"),
+        _i32(n_buckets, "n_buckets"), _i32(radius, "radius"), _i32(Tq, "Tq"), _i32(Tk, "Tk"),
+        _i32(q_pos, "q_pos"), int(bool(accumulate)), _buf(ws, 0, "u8", "ws"),
+        _nbytes(ws) if ws is not None else 0, _stream_of(stream, ds, bucket_map, dtable, ws)))
 
 
 def rel_attention_workspace_bytes(B: int, H: int, Hkv: int, Tq: int, Tk: int, D: int,
                                   radius: int = 0, backward: bool = False) -> int:
-    return int(load().rel_attention_workspace_bytes(B, H, Hkv, Tq, Tk, D, radius,
-                                                    int(bool(backward))))
+    return int(load().rel_attention_workspace_bytes(
+        _i32(B, "B"), _i32(H, "H"), _i32(Hkv, "Hkv"), _i32(Tq, "Tq"), _i32(Tk, "Tk"), _i32(D, "D"),
+        _i32(radius, "radius"), int(bool(backward))))
 
 
-def _heads(x, shape, dtype, name: str):
+def _heads(x, shape, dtype, device: int, name: str):
     """(device pointer, strides of sequences, tokens and heads) of a
-    [B, T, heads, D] tensor of any strides, D side by side."""
+    [B, T, heads, D] tensor of any strides, D side by side, on the device of
+    the call's others."""
     st = x.stride()
     if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {tuple(shape)}")
-    if not _on_gpu(x):
-        raise ValueError(f"{name} must be a device tensor (got {x.device})")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, not with q")
     if x.dtype != dtype:
         raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} (got {x.dtype})")
     if st[3] != 1 and shape[3] > 1 and x.numel():
@@ -555,10 +574,12 @@ def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_
     kind, code = _dtype(q, "q")
     if kind == "f32":
         raise ValueError("attention takes bfloat16 or float16 (got torch.float32)")
-    dt = q.dtype
+    if not _on_gpu(q):
+        raise ValueError(f"q must be a device tensor (got {q.device})")
+    dt, dev = q.dtype, q.get_device()
     kv_shape = (B, Tk, Hkv, D)
-    qp, kp = _heads(q, q_shape, dt, "q"), _heads(k, kv_shape, dt, "k")
-    vp, op = _heads(v, kv_shape, dt, "v"), _heads(o, q_shape, dt, "o")
+    qp, kp = _heads(q, q_shape, dt, dev, "q"), _heads(k, kv_shape, dt, dev, "k")
+    vp, op = _heads(v, kv_shape, dt, dev, "v"), _heads(o, q_shape, dt, dev, "o")
     n_buckets = radius = tp = mp = pos = 0
     pos_of = None
     if isinstance(q_pos, int):
@@ -576,18 +597,24 @@ def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_
         mp = _buf(bucket_map, 2 * radius + 1, "i32", "bucket_map")
     gp = dqp = dkp = dvp = _NONE
     if do is not None:
-        gp, dqp = _heads(do, q_shape, dt, "do"), _heads(dq, q_shape, dt, "dq")
-        dkp, dvp = _heads(dk, k_shape, dt, "dk"), _heads(dv, k_shape, dt, "dv")
+        gp, dqp = _heads(do, q_shape, dt, dev, "do"), _heads(dq, q_shape, dt, dev, "dq")
+        dkp, dvp = _heads(dk, k_shape, dt, dev, "dk"), _heads(dv, k_shape, dt, dev, "dv")
         if dtable is not None and table is not None and dtable.shape != table.shape:
             raise ValueError(f"dtable has shape {tuple(dtable.shape)}, table {tuple(table.shape)}")
-    return RelAttentionArgs.from_buffer_copy(_ATTENTION.pack(
-        code, B, H, Hkv, Tq, Tk, D, 1 if causal else 0, pos, n_buckets, radius,
-        D ** -0.5 if scale is None else scale, p, step & 0xFFFFFFFF, seed & 0xFFFFFFFFFFFFFFFF,
-        _buf(step_dev, 1, "u32", "step_dev") or 0, pos_of or 0, _buf(k_len, B, "i32", "k_len") or 0,
-        tp, mp, qp[0], kp[0], vp[0], op[0], _buf(lse, B * H * Tq, "f32", "lse") or 0,
-        *qp[1:], *kp[1:], *vp[1:], *op[1:], gp[0], dqp[0], dkp[0], dvp[0],
-        *gp[1:], *dqp[1:], *dkp[1:], *dvp[1:], _buf(dtable, n_buckets * H, "f32", "dtable") or 0,
-        1 if accumulate else 0))
+    lens = _buf(k_len, B, "i32", "k_len") or 0
+    lse_p = _buf(lse, B * H * Tq, "f32", "lse") or 0
+    dtp = _buf(dtable, n_buckets * H, "f32", "dtable") or 0
+    step_p = _buf(step_dev, 1, "u32", "step_dev") or 0
+    try:
+        packed = _ATTENTION.pack(
+            code, B, H, Hkv, Tq, Tk, D, 1 if causal else 0, pos, n_buckets, radius,
+            D ** -0.5 if scale is None else scale, p, step & 0xFFFFFFFF, seed & 0xFFFFFFFFFFFFFFFF,
+            step_p, pos_of or 0, lens, tp, mp, qp[0], kp[0], vp[0], op[0], lse_p,
+            *qp[1:], *kp[1:], *vp[1:], *op[1:], gp[0], dqp[0], dkp[0], dvp[0],
+            *gp[1:], *dqp[1:], *dkp[1:], *dvp[1:], dtp, 1 if accumulate else 0)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"a size, position, scale or p is not a number of 32 bits: {e}") from None
+    return RelAttentionArgs.from_buffer_copy(packed)
 
 
 def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
@@ -601,7 +628,7 @@ def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
                         step, step_dev)
     _check("rel_attention_forward", load().rel_attention_forward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream_of(q, stream)))
+        _stream_of(stream, q, lse, q_pos, k_len, table, bucket_map, step_dev, ws)))
 
 
 def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumulate: bool = False,
@@ -614,4 +641,4 @@ def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumul
                         step, step_dev, do, dq, dk, dv, dtable, accumulate)
     _check("rel_attention_backward", load().rel_attention_backward(
         ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
-        _stream_of(q, stream)))
+        _stream_of(stream, q, lse, dtable, q_pos, k_len, table, bucket_map, step_dev, ws)))

@@ -162,7 +162,8 @@ def test_attention_refusals(lib):
     assert lib.rel_attention_forward(None, P, 1, None) == ob.ONEBIT_E_NULL
     assert lib.rel_attention_backward(None, P, 1, None) == ob.ONEBIT_E_NULL
     for bad in (dict(dtype=0), dict(dtype=3), dict(p=1.0), dict(p=-1.0), dict(p=NAN),
-                dict(scale=NAN), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(causal=2), dict(q_pos=1 << 30),
+                dict(scale=NAN), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1),
+                dict(scale=2.0 ** -65), dict(scale=2.0 ** 65), dict(causal=2), dict(q_pos=1 << 30),
                 dict(q_pos=-(1 << 30))):
         assert both(**bad) == ob.ONEBIT_E_ARG, bad
     for bad in (dict(B=-1), dict(H=0), dict(H=5), dict(Hkv=0), dict(Hkv=3), dict(Tq=-1),
@@ -170,8 +171,11 @@ def test_attention_refusals(lib):
                 dict(radius=1025, n_buckets=4, table=P, map=P),
                 dict(radius=8, n_buckets=0, table=P, map=P), dict(B=1 << 30, H=8, Hkv=8),
                 dict(q_stride=(2048, 252, 64)), dict(k_stride=(1024, -128, 64)),
-                dict(v_stride=(1 << 41, 128, 64)), dict(k_stride=(1 << 30, (1 << 23) + 8, 64)), dict(o_stride=(2048, 0, 64)),
-                dict(o_stride=(2048, 256, 32))):
+                dict(v_stride=(1 << 41, 128, 64)), dict(k_stride=(1 << 30, (1 << 23) + 8, 64)),
+                dict(o_stride=(2048, 0, 64)), dict(o_stride=(2048, 256, 32)),
+                dict(o_stride=(2048, 64, 64)), dict(o_stride=(2048, 248, 64)),
+                dict(B=2, o_stride=(1024, 256, 64)), dict(B=2, o_stride=(128, 256, 64)),
+                dict(B=1 << 24, o_stride=(1 << 40, 256, 64))):
         assert both(**bad) == ob.ONEBIT_E_SIZE, bad
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(table=P),
                 dict(map=P, table=None), dict(radius=8, n_buckets=4)):
@@ -194,6 +198,9 @@ def test_attention_refusals(lib):
     assert bwd(table=P, map=P, radius=4, n_buckets=4, dtable=P + 2) == ob.ONEBIT_E_ALIGN
     assert bwd(ws=None) == bwd(wsb=8) == ob.ONEBIT_E_WORKSPACE
     assert bwd(ws=P + 64) == ob.ONEBIT_E_ALIGN
+    # outputs of other orders: heads outermost, sequences inmost, gaps
+    for order in ((2048, 64, 512), (64, 512, 128), (4096, 512, 72)):
+        assert bwd(B=2, o_stride=order, dq_stride=order, ws=None) == ob.ONEBIT_E_WORKSPACE, order
     # few rows over many keys: the forward call needs its workspace too
     a = _args(Tq=1, Tk=1 << 14)
     assert lib.rel_attention_forward(ctypes.byref(a), None, 0, None) == ob.ONEBIT_E_WORKSPACE
@@ -246,6 +253,39 @@ def test_attention_binding_refuses(monkeypatch):
     with pytest.raises(ValueError, match="dtable has shape"):
         ob.rel_attention_backward(q, q, q, q, torch.zeros(1, 2, 4), q, q, q, q, table=t,
                                   bucket_map=m, dtable=torch.zeros(2, 4))
+
+
+def test_binding_refuses_numbers_past_32_bits(monkeypatch):
+    monkeypatch.setattr(ob, "_on_gpu", lambda t: True)
+    q = torch.zeros((1, 4, 2, 16), dtype=torch.bfloat16)
+    t, m = torch.zeros(4, 2), torch.zeros(9, dtype=torch.int32)
+    for far in (1 << 31, 1 << 32, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="32 bits"):
+            ob.rel_attention_forward(q, q, q, q, q_pos=far)
+        with pytest.raises(ValueError, match="32 bits"):
+            ob.rel_bias_expand(t, m, torch.zeros(2, 3, 3), q_pos=far)
+        with pytest.raises(ValueError, match="32 bits"):
+            ob.rel_bias_grad(torch.zeros(1, 2, 3, 3), m, t, q_pos=far)
+        with pytest.raises(ValueError, match="32 bits"):
+            ob.rel_bias_workspace_bytes(1, 2, 3, far, 4)
+        with pytest.raises(ValueError, match="32 bits"):
+            ob.rel_attention_workspace_bytes(1, 2, 2, 3, far, 64)
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    """Host tensors stand for another device's."""
+    monkeypatch.setattr(ob, "_on_gpu", lambda t: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q = torch.zeros((1, 4, 2, 16), dtype=torch.bfloat16)
+    t, m = torch.zeros(4, 2), torch.zeros(9, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    for call in (lambda: ob.dropout_apply(q, q, 4, 32, 0.1, 1, 2),
+                 lambda: ob.rel_bias_expand(t, m, torch.zeros(2, 3, 3)),
+                 lambda: ob.rel_bias_grad(torch.zeros(1, 2, 3, 3), m, t, ws=ws),
+                 lambda: ob.rel_attention_forward(q, q, q, q),
+                 lambda: ob.rel_attention_backward(q, q, q, q, torch.zeros(1, 2, 4), q, q, q, q)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
 
 
 def test_attention_packing_matches_the_struct():
