@@ -352,8 +352,8 @@ def test_two_graphs_share_a_workspace():
                 assert torch.equal(results[n][x], want[x]), (t, n, x)
 
 
-def test_largest_token_strides_and_a_long_cache():
-    """Tokens 2^23 elements apart, and rows past the 32-bit offsets of a cache."""
+def test_largest_token_strides():
+    """Tokens 2^23 elements apart, the last of them past 32-bit offsets."""
     dev = device()
     g = gen(23, dev)
     store = torch.zeros(300 * (1 << 23), dtype=torch.bfloat16, device=dev)  # 5 GB
@@ -433,3 +433,34 @@ def test_replayed_graph_matches_eager(p):
         torch.cuda.synchronize()
         for n in mine:
             assert torch.equal(mine[n], theirs[n]), (t, n)
+
+
+@pytest.mark.parametrize("Tq", [1, 40])
+def test_a_long_cache(Tq):
+    """200 001 keys: a token's row and a few more against 64 bits."""
+    dev = device()
+    g = gen(24, dev)
+    Tk, H, D = 200_001, 2, 128
+    q, k, v = make("bf16", 1, H, 1, Tq, Tk, D, g, dev)
+    bmap = rel_bucket_map(32, 128, False, dev)
+    table = torch.randn((32, H), generator=g, device=dev)
+    o, lse = torch.empty_like(q), torch.empty((1, H, Tq), device=dev)
+    pos = Tk - Tq
+    ob.rel_attention_forward(q, k, v, o, lse=lse, causal=True, q_pos=pos, table=table,
+                             bucket_map=bmap, ws=workspace(q, k))
+    kd, vd = k[0, :, 0].double(), v[0, :, 0].double()
+    j = torch.arange(Tk, device=dev)
+    for i in {0, Tq // 2, Tq - 1}:
+        d = (j - i - pos).clamp(-128, 128) + 128
+        for h in range(H):
+            qd = q[0, i, h].double()
+            s = kd @ qd * D ** -0.5 + table[bmap[d].long(), h].double()
+            s[j > i + pos] = float("-inf")
+            want = torch.softmax(s, 0)[None] @ vd
+            # the row's scores are off by (D + 8) e (|scores| + |terms|) < 2^-15
+            # in all, its sum by the additions of a split, a wave and a lane
+            # (fewer than 2^10), so weights by 2^-12 beside their rounding
+            bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * (
+                torch.softmax(s, 0)[None] @ vd.abs())
+            assert bool(((o[0, i, h].double() - want[0]).abs() <= bound[0]).all()), (i, h)
+            assert abs(float(lse[0, h, i]) - float(torch.logsumexp(s, 0))) < 2.0 ** -12

@@ -146,3 +146,16 @@ def test_replayed_graph_takes_the_device_step():
         assert torch.equal(y, want), t
         seen.append(want)
     assert not torch.equal(seen[0], seen[1])
+
+
+def test_more_elements_than_32_bits_count():
+    """The last rows of a tensor of 2^31 elements and more, in place, are what
+    a call on them alone gives."""
+    dev = device()
+    rows, cols, tail = 262_147, 8200, 5
+    x = torch.full((rows, cols), 1.5, dtype=torch.bfloat16, device=dev)
+    want = torch.empty((tail, cols), dtype=torch.bfloat16, device=dev)
+    ob.dropout_apply(x[-tail:], want, tail, cols, 0.3, SEED, 4, row0=rows - tail)
+    ob.dropout_apply(x, x, rows, cols, 0.3, SEED, 4)
+    assert torch.equal(x[-tail:], want)
+    assert bool((want == 0).any()) and bool((want != 0).any())

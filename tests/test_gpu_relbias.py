@@ -8,7 +8,7 @@ import torch
 from momentum_compression_amd import onebit as ob
 from momentum_compression_amd.attention import rel_bucket_map
 from oracle import training as ref
-from tests._gpu import device, gen
+from tests._gpu import device, gen, host
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,22 @@ def test_grad_of_nothing_is_zero():
     assert bool((got == 5).all())
     ob.rel_bias_grad(torch.empty((2, 3, 4, 0), device=dev), bmap, got, ws=ws)
     assert bool((got == 0).all())
+
+
+def test_more_scores_than_32_bits_count():
+    """Ones over 2^31 scores and more: every bucket's sum is its count.  Counts
+    of a workgroup stay below 2^24, so binary32 has them exactly."""
+    dev = device()
+    B, H, Tq, Tk, far = 9, 16, 4100, 3700, 128
+    ds = torch.ones((B, H, Tq, Tk), dtype=torch.bfloat16, device=dev)
+    assert ds.numel() > 2 ** 31
+    bmap = rel_bucket_map(32, far, True, dev)
+    dtable = torch.empty((32, H), device=dev)
+    ws = torch.empty(ob.rel_bias_workspace_bytes(B, H, Tq, Tk, far), dtype=torch.uint8, device=dev)
+    ob.rel_bias_grad(ds, bmap, dtable, ws=ws)
+    d = np.arange(-Tq + 1, Tk)
+    times = np.minimum.reduce([d + Tq, Tk - d, np.full(d.size, min(Tq, Tk))])
+    count = np.bincount(bmap.cpu().numpy()[np.clip(d, -far, far) + far], weights=times,
+                        minlength=32) * B
+    assert count.sum() == B * Tq * Tk
+    assert np.array_equal(host(dtable), np.repeat(count.astype(np.float32)[:, None], H, 1))
