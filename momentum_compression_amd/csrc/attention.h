@@ -35,7 +35,7 @@ struct AttnArgs {
     void *o, *dq, *dk, *dv;
     Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
     float* lse;           // [B][H][Tq] natural logarithm, or nullptr
-    float* delta;         // [B][H][Tq] row sums of P * dP
+    float* delta;         // [B][H][Tq] row sums of P dP, without the kept share's scale
     float* partials;      // distance sums [H][parts][2 radius + 1]
     float* split_o;       // [rows][splits][D] of a split forward
     float2* split_ml;     // [rows][splits] maximum (base 2) and sum

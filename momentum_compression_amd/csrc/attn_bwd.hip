@@ -22,18 +22,20 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
     return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
 }
 
-// Queries as columns: dq and, for the second pass, delta as the row's sums of
-// P dP over those of P, in binary32.  dq itself takes delta from the rounded
-// output, which is there before the pass: off by half a step of the element
-// type times the row's output.  That is small beside what dS is rounded by
-// where many keys share the weight, but not where few do (a query that sees one
-// key has dS = 0), so workgroups with at most kTwice keys make the pass twice,
-// the first time for the sums alone.  Measured error of dq against 64 bits, in
-// units of the output's own rounding, with one pass and with two: 37 keys 1.51
-// and 1.41, 256 keys 1.47 and 1.43, fp16 rows of at most 5 keys 2.9 and 1.4;
-// with one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would
-// take 74 instead of 53 us for 16 sequences of up to 512 keys and 16 heads of
-// 64; one pass always, 50.
+// Queries as columns: dq and, for the second pass, delta in binary32.  With any
+// value delta' near it, delta = delta' + sum P (dP - delta') / sum P, which the
+// pass sums beside dS.  dq itself takes delta' = dO . o of the rounded output,
+// which is there before the pass: off by half a step of the element type times
+// the row's output.  That is small beside what dS is rounded by where many keys
+// share the weight, but not where few do, so workgroups with at most kTwice keys
+// make the pass twice, the first time for the sums alone and from the first key's
+// dP: a query that sees one key then has delta = dP to the bit, and dS = 0 in
+// both passes over the scores.  Measured error of dq against 64 bits, in units
+// of the output's own rounding, with one pass and with two: 37 keys 1.51 and
+// 1.41, 256 keys 1.47 and 1.43, fp16 rows of at most 5 keys 2.9 and 1.4; with
+// one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would take
+// 74 instead of 53 us for 16 sequences of up to 512 keys and 16 heads of 64; one
+// pass always, 50.
 //
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.
@@ -90,7 +92,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
     f32x16 acc[db_n];
 #pragma unroll
     for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
-    float sum = 0.0f, weight = 0.0f;  // row sums of P dP and P
+    float sum = 0.0f, weight = 0.0f;  // row sums of P (dP - delta) and P
     const float scale2 = a.scale * kLog2e;
     const uint64_t drop_row = (uint64_t)row;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
@@ -154,18 +156,20 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
                             if (!drop_keep(wd, e, a.drop.threshold)) dp[8 * c + e] = 0.0f;
                     }
                 }
-                float part[2] = {0.0f, 0.0f}, part_w[2] = {0.0f, 0.0f};
+                if (pass == 0 && js == 0) {  // the first key's dP, whichever half has it
+                    const float other = other_half(dp[0]);
+                    delta = half ? other : dp[0];
+                }
+                float ds[16], part[2] = {0.0f, 0.0f}, part_w[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    part[r & 1] = __builtin_fmaf(s[r], dp[r], part[r & 1]);
+                    ds[r] = s[r] * (dp[r] - delta);
+                    part[r & 1] += ds[r];
                     part_w[r & 1] += s[r];
                 }
                 sum += part[0] + part[1];
                 weight += part_w[0] + part_w[1];
                 if (pass == 0) continue;
-                float ds[16];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - delta);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const x8 db = pack8<T>(ds + 8 * c);
@@ -179,16 +183,13 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
         }
         sum += other_half(sum);
         weight += other_half(weight);
-        sum = weight == 0.0f ? 0.0f : sum / weight;  // no key seen: 0
-        if (pass == 0) {
-            delta = sum;
-            sum = weight = 0.0f;
-            __syncthreads();  // the tiles are read
-        }
+        if (weight != 0.0f) delta += sum / weight;  // (0: no key seen)
+        sum = weight = 0.0f;
+        if (pass == 0) __syncthreads();  // the tiles are read
     }
 
     if (i >= a.Tq) return;
-    if (half == 0) a.delta[row] = DROP ? sum * a.drop.scale : sum;
+    if (half == 0) a.delta[row] = delta;
     const float out = DROP ? a.scale * a.drop.scale : a.scale;
     T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
 #pragma unroll
@@ -277,7 +278,6 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     const float scale2 = a.scale * kLog2e;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
     const int key_bit = drop_bit(lane & 31);
-    const float drop_inv = DROP ? 1.0f / a.drop.scale : 1.0f;
 
     // queries that see a key of the tile, for each head of the group in turn
     int32_t first = a.causal ? kt_i * kTileRows - pos : 0;
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         const int32_t i = i0 + (int)(threadIdx.x & 63);
         const int64_t row = head_row + i;
         if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
-        else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] * drop_inv : 0.0f;
+        else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] : 0.0f;
         char* tile = lds + to * 2 * tile_bytes<DP>();
         qs.load(tile, i0, a.Tq, wave);
         gs.load(tile + tile_bytes<DP>(), i0, a.Tq, wave);

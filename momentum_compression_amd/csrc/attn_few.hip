@@ -9,9 +9,11 @@
 // while these are used.  The waves of a workgroup are
 // joined in LDS, the workgroups by attn_join.
 //
-// Bound by memory: at 32 sequences of up to 8192 keys, 4 key heads of 128 and
-// 16 query heads, the matrix instructions (mostly on empty columns) take a
-// tenth of the time that the bytes take.
+// Bound by memory: 32 sequences of 8192 keys, 4 key heads of 128 and 16 query
+// heads take 107 us without a bias (5.0 TB/s, a large copy's rate) and 112 with
+// one; of 2048 ... 8192 keys 74 and 78 us (4.6 and 4.3 TB/s), where the short
+// sequences' workgroups end first.  One token of one sequence over 16384 keys
+// takes 25 us, most of it the latencies of two launches.
 #include "attention.h"
 
 namespace onebit {

@@ -107,8 +107,9 @@ _SIGNATURES = {
     "rel_bias_grad": (_c_i32, [_c_p, _c_i32, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                _c_i32, _c_i32, _c_i32, _c_p, _c_sz, _c_p]),
     "rel_bias_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
-    "rel_attention_forward": (_c_i32, [ctypes.POINTER(RelAttentionArgs), _c_p, _c_sz, _c_p]),
-    "rel_attention_backward": (_c_i32, [ctypes.POINTER(RelAttentionArgs), _c_p, _c_sz, _c_p]),
+    # the struct by reference, or its bytes as the binding packs them
+    "rel_attention_forward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
+    "rel_attention_backward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
     "rel_attention_workspace_bytes": (_c_sz, [_c_i32] * 8),
     "onebit_strerror": (ctypes.c_char_p, [_c_i32]),
 }
@@ -173,14 +174,11 @@ _DTYPES = {"float32": ("f32", ONEBIT_F32), "bfloat16": ("bf16", ONEBIT_BF16),
            "float16": ("f16", ONEBIT_F16)}
 
 
-_NAMES = {}  # dtype objects' names, as calls meet them
+_CARRIES = set()  # (dtype object, kind) that go together, as calls meet them
 
 
 def _name(dtype) -> str:
-    found = _NAMES.get(dtype)
-    if found is None:
-        found = _NAMES[dtype] = str(dtype).replace("torch.", "")
-    return found
+    return str(dtype).replace("torch.", "")
 
 
 def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
@@ -192,8 +190,10 @@ def _buf(x, count: int, kind: str, name: str) -> Optional[int]:
         return x
     if not _on_gpu(x):
         raise ValueError(f"{name} must be a device tensor (got {x.device})")
-    if _name(x.dtype) not in _KINDS[kind]:
-        raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
+    if (x.dtype, kind) not in _CARRIES:
+        if _name(x.dtype) not in _KINDS[kind]:
+            raise ValueError(f"{name} must be {' or '.join(_KINDS[kind])} (got {x.dtype})")
+        _CARRIES.add((x.dtype, kind))
     if x.numel() < count:
         raise ValueError(f"{name} holds {x.numel()} elements, the call needs {count}")
     if not x.is_contiguous():
@@ -421,7 +421,7 @@ def _stream_of(stream, *tensors) -> Optional[int]:
 
     current = torch.cuda.current_device()
     for x in tensors:
-        if x is not None and not isinstance(x, int) and x.get_device() != current:
+        if x is not None and type(x) is not int and x.get_device() != current:
             raise ValueError(f"a tensor is on {x.device}, the current device is cuda:{current}")
     if stream is None:
         # the raw handle: building a Stream object around it costs 2.7 us
@@ -559,8 +559,10 @@ _NONE = (0, 0, 0, 0)
 def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed, step,
                     step_dev, do=None, dq=None, dk=None, dv=None, dtable=None, accumulate=False):
     q_shape, k_shape = q.shape, k.shape
-    B, Tq, H, D = _shape(q, 4, "q")
-    _, Tk, Hkv, _ = _shape(k, 4, "k")
+    if len(q_shape) != 4 or len(k_shape) != 4:
+        raise ValueError("q and k must have 4 dimensions")
+    B, Tq, H, D = q_shape
+    _, Tk, Hkv, _ = k_shape
     kind, code = _dtype(q, "q")
     if kind == "f32":
         raise ValueError("attention takes bfloat16 or float16 (got torch.float32)")
@@ -596,7 +598,7 @@ def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_
     dtp = _buf(dtable, n_buckets * H, "f32", "dtable") or 0
     step_p = _buf(step_dev, 1, "u32", "step_dev") or 0
     try:
-        packed = _ATTENTION.pack(
+        return _ATTENTION.pack(
             code, B, H, Hkv, Tq, Tk, D, 1 if causal else 0, pos, n_buckets, radius,
             D ** -0.5 if scale is None else scale, p, step & 0xFFFFFFFF, seed & 0xFFFFFFFFFFFFFFFF,
             step_p, pos_of or 0, lens, tp, mp, qp[0], kp[0], vp[0], op[0], lse_p,
@@ -604,7 +606,6 @@ def _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_
             *gp[1:], *dqp[1:], *dkp[1:], *dvp[1:], dtp, 1 if accumulate else 0)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"a size, position, scale or p is not a number of 32 bits: {e}") from None
-    return RelAttentionArgs.from_buffer_copy(packed)
 
 
 def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
@@ -617,7 +618,7 @@ def rel_attention_forward(q, k, v, o, lse=None, scale: Optional[float] = None,
     a = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed,
                         step, step_dev)
     _check("rel_attention_forward", load().rel_attention_forward(
-        ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(stream, q, lse, q_pos, k_len, table, bucket_map, step_dev, ws)))
 
 
@@ -630,5 +631,5 @@ def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumul
     a = _attention_args(q, k, v, o, lse, scale, causal, q_pos, k_len, table, bucket_map, p, seed,
                         step, step_dev, do, dq, dk, dv, dtable, accumulate)
     _check("rel_attention_backward", load().rel_attention_backward(
-        ctypes.byref(a), _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(stream, q, lse, dtable, q_pos, k_len, table, bucket_map, step_dev, ws)))

@@ -286,6 +286,32 @@ def test_lowest_bias_values_backward(Tq):
             assert torch.equal(got[n][:, :, 0], want[n][:, :, 0]), n
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("p", [0.0, 0.4])
+def test_a_row_of_one_key_has_no_score_gradient(dtype, p):
+    """A softmax over one key is 1 whatever the score: dq and the row's parts of
+    dk and dtable are zeros, not what two roundings leave."""
+    dev = device()
+    g = gen(31, dev)
+    bmap = rel_bucket_map(32, 128, False, dev)
+    for B, H, Hkv, Tq, Tk, causal, k_len in ((3, 4, 2, 1, 1, False, None),
+                                             (2, 2, 2, 70, 70, True, None),
+                                             (2, 2, 1, 130, 300, False, (1, 1))):
+        q, k, v = make(dtype, B, H, Hkv, Tq, Tk, 64, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        table = torch.randn((32, H), generator=g, device=dev)
+        how = dict(table=table, bucket_map=bmap, p=p, seed=SEED, step=3, causal=causal)
+        if k_len is not None:
+            how["k_len"] = torch.tensor(k_len, dtype=torch.int32, device=dev)
+        if causal:  # a row of one key beside rows of more
+            do[:, 1:] = 0
+        dtable = torch.full_like(table, 9)
+        got = _backward(q, k, v, how, do, dtable)
+        for n in ("dq", "dk", "dtable"):
+            assert bool((got[n] == 0).all()), (Tq, Tk, n, float(got[n].abs().max()))
+        assert bool((got["dv"] != 0).any())
+
+
 def test_two_streams_at_once():
     """Calls on two streams at once, each with its own workspace (split keys,
     and a backward pass with the table's gradient), equal the same calls one
