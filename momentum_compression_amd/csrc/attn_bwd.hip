@@ -23,10 +23,12 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
 }
 
 // Queries as columns: dq and, for the second pass, delta in binary32.  With any
-// value delta' near it, delta = delta' + sum P (dP - delta') / sum P, which the
-// pass sums beside dS.  dq itself takes delta' = dO . o of the rounded output,
-// which is there before the pass: off by half a step of the element type times
-// the row's output.  That is small beside what dS is rounded by where many keys
+// value delta' near it, delta = delta' + sum P (dP - delta') / sum P; the sum of
+// dS comes beside dS, and the sum of P is 1 but for the roundings of lse, 2^-20
+// or so of a correction that is itself 2^-8 of delta (summed and divided by, it
+// took 3 % longer).  dq itself takes delta' = dO . o of the rounded output, which
+// is there before the pass: off by half a step of the element type times the
+// row's output.  That is small beside what dS is rounded by where many keys
 // share the weight, but not where few do, so workgroups with at most kTwice keys
 // make the pass twice, the first time for the sums alone and from the first key's
 // dP: a query that sees one key then has delta = dP to the bit, and dS = 0 in
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
     f32x16 acc[db_n];
 #pragma unroll
     for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
-    float sum = 0.0f, weight = 0.0f;  // row sums of P (dP - delta) and P
+    float sum = 0.0f;  // of P (dP - delta) over the row
     const float scale2 = a.scale * kLog2e;
     const uint64_t drop_row = (uint64_t)row;
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
@@ -160,15 +162,13 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
                     const float other = other_half(dp[0]);
                     delta = half ? other : dp[0];
                 }
-                float ds[16], part[2] = {0.0f, 0.0f}, part_w[2] = {0.0f, 0.0f};
+                float ds[16], part[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     ds[r] = s[r] * (dp[r] - delta);
                     part[r & 1] += ds[r];
-                    part_w[r & 1] += s[r];
                 }
                 sum += part[0] + part[1];
-                weight += part_w[0] + part_w[1];
                 if (pass == 0) continue;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -181,10 +181,8 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 3 : 2) void attn_dq_kernel(Att
                 read_ahead<2, 2 * db_n, 4>();
             }
         }
-        sum += other_half(sum);
-        weight += other_half(weight);
-        if (weight != 0.0f) delta += sum / weight;  // (0: no key seen)
-        sum = weight = 0.0f;
+        delta += sum + other_half(sum);
+        sum = 0.0f;
         if (pass == 0) __syncthreads();  // the tiles are read
     }
 
