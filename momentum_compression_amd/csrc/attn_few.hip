@@ -10,10 +10,11 @@
 // joined in LDS, the workgroups by attn_join.
 //
 // Bound by memory: 32 sequences of 8192 keys, 4 key heads of 128 and 16 query
-// heads take 107 us without a bias (5.0 TB/s, a large copy's rate) and 112 with
-// one; of 2048 ... 8192 keys 74 and 78 us (4.6 and 4.3 TB/s), where the short
-// sequences' workgroups end first.  One token of one sequence over 16384 keys
-// takes 25 us, most of it the latencies of two launches.
+// heads take 94 us without a bias (5.7 TB/s) and 97 with one, of 2048 ... 8192
+// keys 68 and 70 us (4.9 and 4.8 TB/s; the short sequences' workgroups end
+// first).  Loads past the caches, as each key is read once (113 and 79 us with a
+// bias through them).  One token of one sequence over 16384 keys takes 22 us,
+// most of it the latencies of two launches.
 #include "attention.h"
 
 namespace onebit {
@@ -79,7 +80,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
             const int c = 8 * (lane % chunks);
             to[x] = x8{};
             if (j < n_keys && c < a.D)
-                to[x] = *reinterpret_cast<const x8*>(base + (int64_t)j * stride + c);
+                to[x] = __builtin_nontemporal_load(
+                    reinterpret_cast<const x8*>(base + (int64_t)j * stride + c));
         }
     };
     const auto store = [&](char* tile, const x8 (&from)[v_n]) {

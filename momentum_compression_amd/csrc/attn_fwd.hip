@@ -283,10 +283,11 @@ AttnSplits attn_splits(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk
     // all queries of a key head in one wave's columns
     p.few = (int64_t)Tq * (H / Hkv) <= kRows;
     const int64_t work = p.few ? (int64_t)B * Hkv : (int64_t)B * H * attn_tiles(Tq);
-    // few: two workgroups a CU at a time and as many again to even out lengths,
-    // a wave with two tiles of 32 keys at least; otherwise two a CU, four
-    // tiles of 64 at least
-    const int64_t want = p.few ? 1024 : 512;
+    // two workgroups a CU; few: a wave with two tiles of 32 keys at least,
+    // otherwise four tiles of 64.  Twice as many workgroups even out lengths but
+    // start and end twice (few, 32 sequences and 4 key heads: 97 -> 100 us of
+    // 8192 keys, 70 -> 72 of a quarter to all; 64, 8 and 1024 keys 50 -> 60)
+    const int64_t want = 512;
     const int64_t most = (Tk + (p.few ? 2 * kWaves * kRows : 4 * kStep) - 1) /
                          (p.few ? 2 * kWaves * kRows : 4 * kStep);
     int64_t n = (want + work - 1) / work;
