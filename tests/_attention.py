@@ -17,6 +17,8 @@ e = 2^-24 (binary32), to first order and per element:
             where it is rounded for a product
   dq, dk    scale times the product of that bound with |k| or |q|, (n + 8) e
             of the sum's own terms, u of the result; dv as o
+  short     up to 64 queries and keys the gradients' products take P and dS as a
+            rounded part and a rounded rest (u^2), with the exact delta
   below     a weight or dS below the type's normal range is rounded by up to half
             its smallest step instead (`sub`); weights are at least as large
             against their row's sum as they are alone
@@ -53,6 +55,8 @@ def expected(q, k, v, do, scale, causal, q_pos, k_len, table, bmap, p, seed, ste
     Tk, Hkv = k.shape[1], k.shape[2]
     G = H // Hkv
     sub = below_normal(u)
+    short = max(Tq, Tk) <= 64
+    u_p = u * u if short else u
     tol = {n: np.zeros_like(x) for n, x in want.items()}
     for b in range(B):
         pos = int(q_pos[b]) if np.ndim(q_pos) else int(q_pos)
@@ -90,11 +94,12 @@ def expected(q, k, v, do, scale, causal, q_pos, k_len, table, bmap, p, seed, ste
                        + Tk * E * (prob * np.abs(dp)).sum(1, keepdims=True))
             ds = prob * (dp - delta)
             t_ds = prob * (ep * (np.abs(dp) + np.abs(delta)) + tdp)
-            t_round = t_ds + prob * t_delta + u * np.abs(ds) + sub * seen * np.max(f)
+            t_round = (t_ds + prob * (t_exact if short else t_delta) + u_p * np.abs(ds)
+                       + sub * seen * np.max(f))
             tol["dq"][b, :, h] = scale * ((t_round + (Tk + 8) * E * np.abs(ds)) @ np.abs(kh))
             tol["dk"][b, :, h // G] += scale * ((t_round + (G * Tq + 8) * E * np.abs(ds)).T
                                                 @ np.abs(qh))
-            tol["dv"][b, :, h // G] += ((u + ep + (G * Tq + 8) * E) * prob * f
+            tol["dv"][b, :, h // G] += ((u_p + ep + (G * Tq + 8) * E) * prob * f
                                         + sub * seen * f).T @ np.abs(g)
             if table is not None:
                 adds = 8 * (Tq + Tk) / 32 + Tk / 8 + 64
