@@ -542,7 +542,8 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * gradient computed.
  *
  * Element type BF16 or F16; products of elements are summed in binary32, and
- * P and dS are rounded to the element type for the products they enter.
+ * P and dS are rounded to the element type for the products they enter (the
+ * gradients' products of up to 64 queries and keys take the rest as well).
  * dtable is summed in binary32 and binary64 from unrounded dS.  Sums run in
  * an order fixed by the sizes: the same call gives the same bits.
  * Keys and values from k_len[b] on are not read (dk and dv are 0 there); the

@@ -145,7 +145,7 @@ def test_backward(name, dtype):
     if dtable is None:
         return
     # the same bits again, and the table's gradient added to itself; without it
-    # the other gradients come from another delta, within the same bounds
+    # another kernel computes dk and dv, within the same bounds
     twice = _backward(q, k, v, how, do, dtable.clone(), fused=fused)
     for n in names:
         assert torch.equal(twice[n], got[n]), n
