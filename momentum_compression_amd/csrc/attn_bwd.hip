@@ -20,8 +20,8 @@ namespace {
 // roundings as they are, where those of many average them out.  Measured error
 // of dq and dk over a plain form's that rounds only results, heads of 16 ... 128:
 // 2 tokens up to 4.1 times, 5 up to 1.9, 10 up to 1.7, 64 and more 1.4; with the
-// rest 1.0.  A few tokens are as fast with it (2 sequences of 37, bias and
-// dropout: 32 us a training step's two calls, 34 without).
+// rest 1.0.  A few sequences are as fast with it (2 of 37 tokens, backward 25.6
+// us, 25.4 without), many nearly (64 of 64 tokens, 16 heads of 64: 56.5 and 53.7).
 constexpr int kShort = 64;
 
 // What rounding left of eight values.
@@ -63,8 +63,7 @@ __device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int3
 constexpr int kTwice = 256;
 
 template <typename T, int DP, bool BIAS, bool DROP, bool SHORT>
-__global__ __launch_bounds__(kThreads, SHORT ? 1 : (DP == 64 ? 3 : 2)) void attn_dq_kernel(
-    AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32;
@@ -262,8 +261,7 @@ __device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* skew
 // the heads that share it, in order; with TABLE the sums of dS (from the exact
 // delta, unrounded) for each distance, one part a workgroup and head.
 template <typename T, int DP, bool BIAS, bool DROP, bool TABLE, bool SHORT>
-__global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 2 : 1) void attn_dkv_kernel(
-    AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     using x8 = typename Mma<T>::x8;
     constexpr int kc_n = DP / 16, db_n = DP / 32, kUnroll = TABLE && DP == 128 ? 1 : 2;
