@@ -113,8 +113,9 @@ constexpr int tile_bytes() {
 // Fills tiles with global rows, memory to LDS without registers between: a
 // lane's 16 bytes land beside its neighbours', so the lane asks for the chunk
 // that the swizzle puts there.  Rows past the last one and columns from D on
-// lie past the buffer's end, which reads as 0.  What is under way is done when
-// the issuing wave has passed a __syncthreads().
+// lie past the buffer's end, which reads as 0.  What is under way is there for
+// the workgroup when every wave that issued a part of it has passed
+// tiles_barrier(): a __syncthreads() alone does not wait for it.
 template <typename T, int DP>
 struct Feed {
     static constexpr int kChunks = DP / 8;
@@ -143,6 +144,13 @@ struct Feed {
                 (int)(at + (uint32_t)x * (kStep / kPer) * stride), 0, 0, 0);
     }
 };
+
+// A barrier that shows all waves the tiles whose loads they issued before it.
+// Each wave waits for its own loads first (vmcnt 0, the other counters left).
+__device__ __forceinline__ void tiles_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+}
 
 // A operand: 32 rows (in perm_row order) of the tile from `row0`, columns
 // 16 kc ... 16 kc + 15.

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_
             char* kt = lds + buf * 2 * tile_bytes<DP>();
             char* vt = kt + tile_bytes<DP>();
             // this tile (and the window) is there, and the other buffer is read
-            __syncthreads();
+            tiles_barrier();
             if (j0 + kStep < end) {
                 char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
                 ks.load(next, j0 + kStep, n_keys, wave);
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
             fill_window(window, a.bias, h, a.scale);
             filled = h;
         }
-        __syncthreads();  // this tile is there, and the other buffer is read
+        tiles_barrier();  // this tile is there, and the other buffer is read
         const bool more = t + 1 < total;
         if (more) {
             i0 += kStep;

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
         char* kt = lds + buf * 2 * tile_bytes<DP>();
         char* vt = kt + tile_bytes<DP>();
         // this tile (and the window) is there, and the other buffer is read
-        __syncthreads();
+        tiles_barrier();
         if (j0 + kStep < end) {
             char* next = lds + (buf ^ 1) * 2 * tile_bytes<DP>();
             ks.load(next, j0 + kStep, n_keys, wave);

@@ -155,6 +155,33 @@ def test_backward(name, dtype):
     assert torch.allclose(more["dtable"], 2 * dtable, rtol=2 ** -22, atol=0)
 
 
+# Causal prompts behind a cache.  From positions of 1 to 32 modulo 64 on, the
+# first waves of a tile of 97 queries or more are through with the keys while
+# the last ones still have a tile to come, of which they brought their part.
+BEHIND = {
+    f"behind_{pos}_{Tq}": (2, 4, 2, Tq, pos + Tq, D, True, pos, None, n, 64, False, p)
+    for pos, Tq, D, n, p in ((1, 97, 64, 0, 0.0), (20, 128, 64, 32, 0.0), (32, 129, 128, 0, 0.1),
+                             (33, 128, 64, 0, 0.0), (64 + 16, 300, 128, 32, 0.0),
+                             (256 + 1, 257, 64, 32, 0.1), (512 + 32, 99, 128, 32, 0.0))
+}
+BEHIND["behind_two"] = (2, 4, 4, 200, 700, 64, True, (500, 65), (700, 265), 32, 64, False, 0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name", BEHIND)
+def test_prompts_behind_a_cache(name, dtype):
+    q, k, v, how, g = _setup(name, dtype, BEHIND)
+    do = torch.randn(q.shape, generator=g, device=q.device).to(TYPES[dtype])
+    want, tol = _oracle(q, k, v, do, how, dtype)
+    dtable = None if how["table"] is None else torch.full_like(how["table"], 9.0)
+    names = ["o", "lse", "dq", "dk", "dv"] + (["dtable"] if dtable is not None else [])
+    got = _backward(q, k, v, how, do, dtable)
+    check(got, want, tol, names, _tiny(dtype))
+    again = _backward(q, k, v, how, do, dtable.clone() if dtable is not None else None)
+    for n in names:
+        assert torch.equal(again[n], got[n]), n
+
+
 def test_gradients_by_differences():
     """The gradients against differences of the oracle's forward map at the
     rounded inputs, along random directions."""
