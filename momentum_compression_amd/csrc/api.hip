@@ -43,7 +43,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // A dispatch counts its grid in work-items with 32 bits: a launch takes at
 // most 2^32 - 1 work-items along x, i.e. 16,777,215 workgroups of 256.
 // Larger requests would be cut short without an error, so they are refused.
-bool groups_ok(int64_t groups) { return groups <= (int64_t)(0xFFFFFFFFu / kThreads); }
+bool groups_ok(int64_t groups) {
+    return groups >= 0 && groups <= (int64_t)(0xFFFFFFFFu / kThreads);
+}
 
 // LAMB step: the layer keys, then one slot per workgroup of the pass
 size_t lamb_ws_bytes(int64_t N, int32_t n_seg) {

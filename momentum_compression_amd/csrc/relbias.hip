@@ -105,7 +105,10 @@ __global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __rest
     const int cb = (int)(part % plan.col_blocks);
     const int rb = (int)(part / plan.col_blocks);
     const int32_t c0 = cb * (C * W) + C * col;
-    const int32_t b1 = (bb + 1) * plan.batches < B ? (bb + 1) * plan.batches : B;
+    // unsigned: up to a part and a step past the last sequence, below 2^32
+    const uint32_t b0 = (uint32_t)bb * (uint32_t)plan.batches;
+    const uint32_t stop = b0 + (uint32_t)plan.batches;
+    const uint32_t b1 = stop < (uint32_t)B ? stop : (uint32_t)B;
     const bool whole = c0 + C <= Tk;
     float far_lo = 0.0f, far_hi = 0.0f;
     for (int32_t i0 = rb * plan.rows + 8 * wave; i0 < Tq && i0 < (rb + 1) * plan.rows;
@@ -113,7 +116,7 @@ __global__ __launch_bounds__(kGradThreads) void bias_grad_kernel(const T* __rest
         float acc[C + 7];
 #pragma unroll
         for (int k = 0; k < C + 7; ++k) acc[k] = 0.0f;
-        for (int32_t b = bb * plan.batches + sub; b < b1; b += subs) {
+        for (uint32_t b = b0 + sub; b < b1; b += subs) {
             const T* p = ds + (((int64_t)b * H + h) * Tq + i0) * (int64_t)Tk + c0;
             Piece<T> v[8];
             if (whole && i0 + 8 <= Tq) {
@@ -314,7 +317,7 @@ BiasGradPlan bias_grad_plan(int32_t B, int32_t H, int32_t Tq, int32_t Tk, int32_
             p.row_blocks = row_blocks;
             p.col_blocks = col_blocks;
             p.batches = (int32_t)((B + split - 1) / split);
-            p.batch_blocks = (B + p.batches - 1) / p.batches;
+            p.batch_blocks = (int32_t)(((int64_t)B + p.batches - 1) / p.batches);
             const int64_t groups = p.parts() * H;
             const int64_t visits = (int64_t)(rows < Tq ? rows : Tq) * p.batches + 24;
             const int64_t cost = (groups + kResident - 1) / kResident * visits;

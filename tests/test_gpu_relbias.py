@@ -115,3 +115,19 @@ def test_more_scores_than_32_bits_count():
                         minlength=32) * B
     assert count.sum() == B * Tq * Tk
     assert np.array_equal(host(dtable), np.repeat(count.astype(np.float32)[:, None], H, 1))
+
+
+@pytest.mark.parametrize("B", [(1 << 30) + 1, (1 << 31) - 1])
+def test_more_sequences_than_2_30(B):
+    """Scores of one query and key: one bucket, whose sum takes in the first
+    and the last sequence and those about the parts' middle (whole numbers, of
+    which a part's sums stay exact)."""
+    dev = device()
+    ds = torch.zeros((B, 1, 1, 1), dtype=torch.bfloat16, device=dev)
+    for at, x in ((0, 3.0), (1 << 28, 5.0), (B // 2, 7.0), (B - 2, 11.0), (B - 1, 13.0)):
+        ds[at] = x
+    bmap = rel_bucket_map(4, 8, True, dev)
+    dtable = torch.full((4, 1), 9.0, device=dev)
+    ws = torch.empty(ob.rel_bias_workspace_bytes(B, 1, 1, 1, 8), dtype=torch.uint8, device=dev)
+    ob.rel_bias_grad(ds, bmap, dtable, ws=ws)
+    assert dtable[:, 0].tolist() == [39.0, 0.0, 0.0, 0.0]

@@ -91,6 +91,19 @@ def test_rel_bias_workspace(lib):
         assert f(B, H, Tq, Tk, 128) % (257 * 4) < 256 and f(B, H, Tq, Tk, 128) > 0
 
 
+@pytest.mark.parametrize("B", [(1 << 30) - 1, (1 << 30) + 1, (1 << 31) - 1])
+def test_rel_bias_grad_of_the_most_sequences(lib, B):
+    """Sequences past 2^30 (2^30 + 1 scores of one query and key are 2 GiB): the
+    plan's numbers stay positive, its workspace takes less than the scores, and
+    a call without that workspace is refused."""
+    for Tq, Tk in ((1, 1), (3, 1), (70, 9)):
+        n = ob.rel_bias_workspace_bytes(B, 1, Tq, Tk, 16)
+        assert 33 * 4 <= n < 2 * B * Tq * Tk
+        for dt in (0, 1, 2):
+            assert lib.rel_bias_grad(P, dt, P, P, B, 1, 8, 16, Tq, Tk, 0, 0, P, n - 256,
+                                     None) == ob.ONEBIT_E_WORKSPACE
+
+
 def test_binding_refuses_shapes_and_types(monkeypatch):
     monkeypatch.setattr(ob, "_on_gpu", lambda t: True)
     x = torch.zeros(4, 16)
