@@ -191,23 +191,25 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
     for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off, 64);
     const int c = 2 * lane;
     float2 o = {0.0f, 0.0f};
-    if (ok && c < a.D) {
-        const float* from = a.split_o + row * a.splits * (int64_t)a.D + c;
-        for (int s0 = wave % WAVES; s0 < a.splits; s0 += 8 * WAVES) {
-            float2 v[8];
+    // Every lane goes through the loop, those without a column too: they hold
+    // splits' weights for the others.
+    const bool mine = ok && c < a.D;
+    const float* from = a.split_o + (mine ? row * a.splits * (int64_t)a.D + c : 0);
+    for (int s0 = wave % WAVES; s0 < a.splits; s0 += 8 * WAVES) {
+        float2 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int s = s0 + k * WAVES;
-                v[k] = s < a.splits ? *reinterpret_cast<const float2*>(from + (int64_t)s * a.D)
-                                    : float2{0.0f, 0.0f};
-            }
+        for (int k = 0; k < 8; ++k) {
+            const int s = s0 + k * WAVES;
+            v[k] = mine && s < a.splits
+                       ? *reinterpret_cast<const float2*>(from + (int64_t)s * a.D)
+                       : float2{0.0f, 0.0f};
+        }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float w = __uint_as_float(__builtin_amdgcn_readlane(
-                    __float_as_uint(weight), (s0 + k * WAVES) & 63));
-                o.x = __builtin_fmaf(w, v[k].x, o.x);
-                o.y = __builtin_fmaf(w, v[k].y, o.y);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float w = __uint_as_float(__builtin_amdgcn_readlane(
+                __float_as_uint(weight), (s0 + k * WAVES) & 63));
+            o.x = __builtin_fmaf(w, v[k].x, o.x);
+            o.y = __builtin_fmaf(w, v[k].y, o.y);
         }
     }
     if (WAVES > 1) {

@@ -91,6 +91,25 @@ def test_forward(name, dtype):
     assert torch.equal(again, o)
 
 
+# Narrow heads over many splits: fewer lanes of the join have a column than
+# have a split's weight.
+NARROW = {
+    f"narrow_{D}_{Tq}": (1, 2, 1, Tq, 9000, D, True, 9000 - Tq, None, 32, 128, False, p)
+    for D, Tq, p in ((8, 1, 0.0), (16, 1, 0.2), (16, 40, 0.0), (40, 3, 0.0), (8, 130, 0.1))
+}
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name", NARROW)
+def test_forward_of_narrow_heads_over_many_splits(name, dtype):
+    q, k, v, how, _ = _setup(name, dtype, NARROW)
+    want, tol = _oracle(q, k, v, None, how, dtype)
+    o = torch.full_like(q, 9.0)
+    lse = torch.full((q.shape[0], q.shape[2], q.shape[1]), 9.0, device=q.device)
+    ob.rel_attention_forward(q, k, v, o, lse=lse, ws=workspace(q, k), **how)
+    check(dict(o=o, lse=lse), want, tol, ("o", "lse"), _tiny(dtype))
+
+
 BACKWARD = {
     "one": (1, 1, 1, 1, 1, 8, False, 0, None, 0, 0, False, 0.0),
     "tiny": (2, 3, 3, 5, 7, 16, True, 2, None, 4, 8, False, 0.0),
