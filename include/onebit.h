@@ -550,8 +550,11 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * values of keys that only the causal mask hides are multiplied by 0 and have
  * to be finite.  k_len and q_pos_of are clamped to 0 ... Tk and +-2^29.
  *
- * A table value so low that it leaves binary32 when divided by the scale or
- * multiplied by log2 e counts as -infinity: its keys have no weight.
+ * A table value of -2^40 or less counts as -infinity, and so does one that
+ * leaves binary32 when divided by the scale or multiplied by log2 e: its keys
+ * have no weight.  Other large values are scores like any: a row whose seen
+ * keys all carry one has the weights that it has without it, but for an error
+ * of up to 2^-22 of the value in what the scores are rounded at.
  *
  * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
  * heads; D a multiple of 8, 8 ... 128, its elements side by side, 16-byte

@@ -665,7 +665,7 @@ int check_attention_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t
 // Workspace of the two directions, in the order it is carved.
 struct AttnSizes {
     size_t split_o, split_ml;   // forward
-    size_t delta, partials;     // backward
+    size_t delta, partials;     // backward; delta and norm together
 };
 
 AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk, int32_t D,
@@ -675,9 +675,9 @@ AttnSizes attn_sizes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk, 
     const int32_t splits = attn_splits(B, H, Hkv, Tq, Tk).splits;
     if (splits > 1) {
         z.split_o = round_up(rows * splits * D * sizeof(float));
-        z.split_ml = round_up(rows * splits * sizeof(float2));
+        z.split_ml = round_up(rows * splits * sizeof(f4));
     }
-    z.delta = round_up(rows * sizeof(float));
+    z.delta = round_up(2 * rows * sizeof(float));
     if (radius > 0)
         z.partials = round_up((size_t)B * attn_tiles(Tk) * H * (2 * (size_t)radius + 1) *
                               sizeof(float));
@@ -768,7 +768,7 @@ int rel_attention_forward(const rel_attention_args* a, void* ws, size_t ws_bytes
         const int32_t tiles = (a->Tk + kStep - 1) / kStep;
         k.split_tiles = (tiles + k.splits - 1) / k.splits;
         k.split_o = static_cast<float*>(ws);
-        k.split_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.split_o);
+        k.split_ml = reinterpret_cast<f4*>(static_cast<char*>(ws) + z.split_o);
     }
     drop_stale_error();
     return hip_status(launch_attn_forward(k, a->dtype, stream));
@@ -801,6 +801,7 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
     k.sdk = strides_of(a->dk_stride);
     k.sdv = strides_of(a->dv_stride);
     k.delta = static_cast<float*>(ws);
+    k.norm = k.delta + (size_t)a->B * a->H * a->Tq;
     k.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + z.delta);
     drop_stale_error();
     return hip_status(launch_attn_backward(k, a->dtype, a->dtable, a->accumulate != 0, stream));

@@ -36,9 +36,10 @@ struct AttnArgs {
     Strides sq, sk, sv, so, sdo, sdq, sdk, sdv;
     float* lse;           // [B][H][Tq] natural logarithm, or nullptr
     float* delta;         // [B][H][Tq] row sums of P dP, without the kept share's scale
+    float* norm;          // [B][H][Tq] rows with a base: log2 of the sum above it
     float* partials;      // distance sums [H][parts][2 radius + 1]
     float* split_o;       // [rows][splits][D] of a split forward
-    float2* split_ml;     // [rows][splits] maximum (base 2) and sum
+    f4* split_ml;         // [rows][splits] base, reference and sum
     const int32_t* q_pos_dev;
     const int32_t* k_len;
     RelBias bias;         // radius 0: none
@@ -235,6 +236,11 @@ __device__ __forceinline__ float other_half(float x) {
 // the products of a tile start from it, and one scale serves both.
 __device__ __forceinline__ int window_floats(int radius) { return 2 * radius + 1 + 2 * kPad; }
 
+//
+// A table value of -2^40 or less counts as -infinity, and so does one that
+// leaves binary32 here.
+__device__ __forceinline__ float low_value(float t) { return t <= -0x1p40f ? -INFINITY : t; }
+
 __device__ __forceinline__ void fill_window(float* w, const RelBias& b, int h, float scale) {
     const int R = b.radius;
     const float inv_scale = 1.0f / scale;
@@ -242,10 +248,31 @@ __device__ __forceinline__ void fill_window(float* w, const RelBias& b, int h, f
         int i = x - kPad;
         i = i < 0 ? 0 : (i > 2 * R ? 2 * R : i);
         const int m = b.map[i];
-        w[x] = (uint32_t)m < (uint32_t)b.n_buckets ? b.table[(int64_t)m * b.H + h] * inv_scale
-                                             : 0.0f;
+        w[x] = (uint32_t)m < (uint32_t)b.n_buckets
+                   ? low_value(b.table[(int64_t)m * b.H + h]) * inv_scale
+                   : 0.0f;
     }
 }
+
+// An exponential's argument is one fused multiplication and addition of the
+// score and the row's reference, which leaves up to half a step of the
+// reference in it: an exponent of 64 at 2^30.  From 2^13 on (base 2; half a step
+// of 2^-11) a row gets a base near its reference that is taken off its scores
+// before the products are added, so that scores and reference are small again.
+__device__ __forceinline__ bool is_large(float reference) {
+    const float r = __builtin_fabsf(reference);
+    return r >= 0x1p13f && r < INFINITY;
+}
+
+// Where the 32 x 32 scores of queries from i0 and keys from j0 lie against the
+// radius: -1 all at or before -radius, 1 all at or past it, 0 otherwise.
+__device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int32_t R) {
+    const int32_t d = j0 - i0 - pos;
+    return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
+}
+
+// The backward pass's base of a row of large lse.
+__device__ __forceinline__ float large_base(float lse, float scale) { return lse / scale; }
 
 // A row's normaliser in base 2; one that empties a row without keys.
 __device__ __forceinline__ float base2_lse(float lse) {
@@ -303,11 +330,13 @@ inline int32_t attn_tiles(int32_t T) { return (T + kTileRows - 1) / kTileRows; }
 
 // ---------------------------------------------------------------- results
 // A query's row from the accumulators (column 32 d + 8 (r >> 2) + 4 half +
-// (r & 3) in register r of block d), its maximum m (base 2) and sum l.
+// (r & 3) in register r of block d), its reference (the base, m above it in base
+// 2) and sum l.  Bases are scores before the scale; of the kernel for few
+// queries, base-2 ones.
 template <typename T, int DP>
 __device__ __forceinline__ void write_rows(const AttnArgs& a, const f32x16 (&acc)[DP / 32], int b,
-                                           int h, int32_t i, int64_t row, float m, float l,
-                                           int half) {
+                                           int h, int32_t i, int64_t row, float base, float m,
+                                           float l, int half) {
     // no key seen: l is 0 and so is the row (a NaN goes through)
     const float inv = l == 0.0f ? 0.0f : a.drop.scale / l;
     T* to = (T*)a.o + b * a.so.b + i * a.so.t + h * a.so.h;
@@ -322,13 +351,17 @@ __device__ __forceinline__ void write_rows(const AttnArgs& a, const f32x16 (&acc
             for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * inv);
             *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
         }
-    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+    if (a.lse && half == 0)
+        a.lse[row] = l == 0.0f
+                         ? -INFINITY
+                         : base * (a.few ? kLn2 : a.scale) + (m * kLn2 + __logf(l));
 }
 
 // The same of one split, to be joined.
 template <int DP>
 __device__ __forceinline__ void write_split(const AttnArgs& a, const f32x16 (&acc)[DP / 32],
-                                            int64_t row, int split, float m, float l, int half) {
+                                            int64_t row, int split, float base, float m, float l,
+                                            int half) {
     float* to = a.split_o + (row * a.splits + split) * a.D;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
@@ -339,7 +372,7 @@ __device__ __forceinline__ void write_split(const AttnArgs& a, const f32x16 (&ac
                 *reinterpret_cast<f4*>(to + c) = f4{acc[d][4 * g], acc[d][4 * g + 1],
                                                     acc[d][4 * g + 2], acc[d][4 * g + 3]};
         }
-    if (half == 0) a.split_ml[row * a.splits + split] = float2{m, l};
+    if (half == 0) a.split_ml[row * a.splits + split] = f4{base, m, l, 0.0f};
 }
 
 // ---------------------------------------------------------------- launchers

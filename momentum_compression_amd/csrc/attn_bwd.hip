@@ -9,6 +9,8 @@
 // Two passes compute the scores again, one with the queries and one with the
 // keys as a wave's columns, so that each gradient is summed by one workgroup
 // in a fixed order: no atomics, the same bits on every run.
+#include <type_traits>
+
 #include "attention.h"
 
 namespace onebit {
@@ -32,13 +34,6 @@ __device__ __forceinline__ typename Mma<T>::x8 pack_rest(const float* p,
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = (T)(p[e] - (float)rounded[e]);
     return r;
-}
-
-// Where the 32 x 32 scores of queries from i0 and keys from j0 lie against the
-// radius: -1 all at or before -radius, 1 all at or past it, 0 otherwise.
-__device__ __forceinline__ int side_of(int32_t j0, int32_t i0, int32_t pos, int32_t R) {
-    const int32_t d = j0 - i0 - pos;
-    return d + 31 <= -R ? -1 : (d - 31 >= R ? 1 : 0);
 }
 
 // Queries as columns: dq and, for the second pass, delta in binary32.  With any
@@ -208,21 +203,139 @@ __global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_
         if (pass == 0) __syncthreads();  // the tiles are read
     }
 
-    if (i >= a.Tq) return;
-    if (half == 0) a.delta[row] = delta;
-    const float out = DROP ? a.scale * a.drop.scale : a.scale;
-    T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
+    const auto write = [&]() __attribute__((always_inline)) {
+        if (half == 0) a.delta[row] = delta;
+        const float out = DROP ? a.scale * a.drop.scale : a.scale;
+        T* to = (T*)a.dq + b * a.sdq.b + i * a.sdq.t + h * a.sdq.h;
 #pragma unroll
-    for (int d = 0; d < db_n; ++d)
+        for (int d = 0; d < db_n; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int c = 32 * d + 8 * g + 4 * half;
-            if (c >= a.D) continue;
-            typename Mma<T>::x4 v;
+            for (int g = 0; g < 4; ++g) {
+                const int c = 32 * d + 8 * g + 4 * half;
+                if (c >= a.D) continue;
+                typename Mma<T>::x4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * out);
-            *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
+                for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * out);
+                *reinterpret_cast<typename Mma<T>::x4*>(to + c) = v;
+            }
+    };
+    const bool again = is_large(lse2);
+    if (i < a.Tq && !again) write();
+
+    // Rows of large references once more, from their bases and with the
+    // normaliser above the base, which lse has lost: it is summed first, then
+    // delta from the first key's dP, then dq.  32 keys at a time, a tile after
+    // the other.
+    __shared__ uint32_t waves_large[kWaves];
+    if (lane == 0) waves_large[wave] = __any(again);
+    __syncthreads();  // the tiles are read, too
+    const bool none = !(waves_large[0] | waves_large[1] | waves_large[2] | waves_large[3]);
+    if (__builtin_expect(none, 1)) return;
+    // The generator's keys, and below the lane's addresses, anew: kept through
+    // the first pass for this one they would go to memory (with that, launches
+    // take up to 5 us longer).
+    uint32_t k0 = a.drop.k0, k1 = a.drop.k1;
+    asm volatile("" : "+s"(k0), "+s"(k1));
+    const float base = again ? large_base(a.lse[i < a.Tq ? row : 0], a.scale) : 0.0f;
+    float m = -0x1p12f, l = 0.0f, norm = 0.0f;
+    delta = sum = 0.0f;
+    const auto sweep = [&](auto which) __attribute__((always_inline)) {
+        constexpr int pass = decltype(which)::value;
+        for (int32_t j0 = 0; j0 < end; j0 += kStep) {
+            char* vt = lds + tile_bytes<DP>();
+            ks.load(lds, j0, n_keys, wave);
+            vs.load(vt, j0, n_keys, wave);
+            tiles_barrier();
+#pragma unroll 1
+            for (int u = 0; u < kStep; u += 32) {
+                const int32_t js = j0 + u;
+                if (js > limit_hi) break;
+                int lane_now = lane;
+                asm volatile("" : "+v"(lane_now));
+                const int lane = lane_now, half = lane >> 5;
+                const int side = BIAS ? side_of(js, iw, pos, R) : 0;
+                f32x16 s = {}, dp = {};
+                if (BIAS && side == 0) {
+                    const float* at = window + (js + 8 * half - i - pos + R + kPad);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = at[16 * (r >> 3) + (r & 7)] - base;
+                } else {
+                    const float flat = BIAS ? window[side < 0 ? 0 : 2 * R + 2 * kPad] : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = flat - base;
+                }
+#pragma unroll
+                for (int kc = 0; kc < kc_n; ++kc)
+                    s = Mma<T>::mul(row_frag<T, DP>(lds, u, kc, lane), qf[kc], s);
+                read_ahead<1, kc_n, 2>();
+                const int32_t seen = limit - js - 8 * half;
+                if (pass == 0) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        s[r] = 16 * (r >> 3) + (r & 7) > seen ? -INFINITY : s[r] * scale2;
+                        mx = fmaxf(mx, s[r]);
+                    }
+                    const float m_new = fmaxf(m, fmaxf(mx, other_half(mx)));
+                    l *= __builtin_amdgcn_exp2f(m - m_new);
+                    m = m_new;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) l += __builtin_amdgcn_exp2f(s[r] - m);
+                    continue;
+                }
+#pragma unroll
+                for (int kc = 0; kc < kc_n; ++kc)
+                    dp = Mma<T>::mul(row_frag<T, DP>(vt, u, kc, lane), gf[kc], dp);
+                read_ahead<1, kc_n, 2>();
+                if (DROP) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t wd[4];
+                        drop_draws(wd, (uint32_t)(js + 16 * c + 8 * half) >> 3, drop_row, step,
+                                   k0, k1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!drop_keep(wd, e, a.drop.threshold)) dp[8 * c + e] = 0.0f;
+                    }
+                }
+                if (pass == 1 && js == 0) {
+                    const float other = other_half(dp[0]);
+                    delta = half ? other : dp[0];
+                }
+                float ds[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, -norm));
+                    ds[r] = 16 * (r >> 3) + (r & 7) > seen ? 0.0f : p * (dp[r] - delta);
+                    sum += ds[r];
+                }
+                if (pass == 1) continue;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const x8 db = pack8<T>(ds + 8 * c), dr = pack_rest<T>(ds + 8 * c, db);
+#pragma unroll
+                    for (int d = 0; d < db_n; ++d) {
+                        const x8 kd = col_frag<T, DP>(lds, u + 16 * c, d, lane);
+                        acc[d] = Mma<T>::mul(kd, db, acc[d]);
+                        acc[d] = Mma<T>::mul(kd, dr, acc[d]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+            __syncthreads();  // this tile is read
         }
+        if (pass == 0) norm = m + __log2f(l + other_half(l));
+        delta += sum + other_half(sum);
+        sum = 0.0f;
+    };
+    sweep(std::integral_constant<int, 0>());
+    sweep(std::integral_constant<int, 1>());
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
+    sweep(std::integral_constant<int, 2>());
+    if (i >= a.Tq || !again) return;
+    if (half == 0) a.norm[row] = norm;
+    write();
 }
 
 // Sums down the diagonals of the 32 x 32 scores' gradients of a wave (queries
@@ -257,6 +370,8 @@ __device__ __forceinline__ void add_diagonals(const float (&ds)[16], float* skew
     __builtin_amdgcn_wave_barrier();
 }
 
+constexpr int kRowFloats = 384;  // a query tile's rows in LDS, two buffers
+
 // Keys as columns: dk and dv of 128 keys of one key head, over every query of
 // the heads that share it, in order; with TABLE the sums of dS (from the exact
 // delta, unrounded) for each distance, one part a workgroup and head.
@@ -278,11 +393,14 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     const int32_t j = jw + (lane & 31);
     const int R = a.bias.radius, group = a.H / a.Hkv, bins_n = 2 * R + 1;
 
-    // negative lse and delta of a tile's queries, two buffers
+    // negative normaliser and delta of a tile's queries, and bases where one
+    // has any; two buffers
     float* rows_lds = reinterpret_cast<float*>(lds + 4 * tile_bytes<DP>());
-    uint32_t* kept_lds = reinterpret_cast<uint32_t*>(rows_lds + 256) + wave * 32;
-    float* skew = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? wave * kSkewFloats : 0);
-    float* window = rows_lds + 256 + (DROP ? kWaves * 32 : 0) + (TABLE ? kWaves * kSkewFloats : 0);
+    uint32_t* kept_lds = reinterpret_cast<uint32_t*>(rows_lds + kRowFloats) + wave * 32;
+    float* skew =
+        rows_lds + kRowFloats + (DROP ? kWaves * 32 : 0) + (TABLE ? wave * kSkewFloats : 0);
+    float* window =
+        rows_lds + kRowFloats + (DROP ? kWaves * 32 : 0) + (TABLE ? kWaves * kSkewFloats : 0);
     float* all_bins = window + window_floats(R);
     float* bins = all_bins + wave * bins_n;
     float below = 0.0f, above = 0.0f;  // dS at or past the radius
@@ -306,22 +424,34 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         kt_i * kTileRows < n_keys && first < a.Tq ? (a.Tq - first + kStep - 1) / kStep : 0;
     const uint32_t total = (uint32_t)per_head * (uint32_t)group;
 
-    float row_value = 0.0f;
+    float row_lse = 0.0f, row_delta = 0.0f;
+    bool large = false;  // the tile has a row with a base
     int32_t head = hk * group, i0 = first;  // of the tile to load next
     Feed<T, DP> qs((const T*)a.q + b * a.sq.b + head * a.sq.h, a.sq.t, a.D, wave, lane);
     Feed<T, DP> gs((const T*)a.d_o + b * a.sdo.b + head * a.sdo.h, a.sdo.t, a.D, wave, lane);
     int64_t head_row = ((int64_t)b * a.H + head) * a.Tq;
     const auto load = [&](int to) {
-        const int32_t i = i0 + (int)(threadIdx.x & 63);
+        const int32_t i = i0 + lane;
         const int64_t row = head_row + i;
-        if (threadIdx.x < 64) row_value = i < a.Tq ? -base2_lse(a.lse[row]) : -INFINITY;
-        else if (threadIdx.x < 128) row_value = i < a.Tq ? -a.delta[row] : 0.0f;
+        row_lse = i < a.Tq ? a.lse[row] : -INFINITY;
+        if (wave == 1) row_delta = i < a.Tq ? a.delta[row] : 0.0f;
         char* tile = lds + to * 2 * tile_bytes<DP>();
         qs.load(tile, i0, a.Tq, wave);
         gs.load(tile + tile_bytes<DP>(), i0, a.Tq, wave);
     };
     const auto keep_rows = [&](int to) {
-        if (threadIdx.x < 128) rows_lds[to * 128 + threadIdx.x] = row_value;
+        float value = -base2_lse(row_lse);
+        const bool far = is_large(value);
+        large = __any(far);
+        if (wave == 0) {
+            if (large) {
+                if (far) value = -a.norm[head_row + i0 + lane];
+                rows_lds[256 + to * 64 + lane] = far ? large_base(row_lse, a.scale) : 0.0f;
+            }
+            rows_lds[to * 128 + lane] = value;
+        } else if (wave == 1) {
+            rows_lds[to * 128 + 64 + lane] = -row_delta;
+        }
     };
     // one head's sums to its part; its bins are complete
     const auto flush = [&](int h) {
@@ -360,6 +490,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
         char* gt = qt + tile_bytes<DP>();
         const float* lse2 = rows_lds + buf * 128;
         const float* delta = lse2 + 64;
+        const float* bases = rows_lds + 256 + buf * 64;
         if (BIAS && filled != h) {
             __syncthreads();  // the other head's window is read
             if (TABLE && filled >= 0) flush(filled);
@@ -403,6 +534,11 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
                 const float c = window[side < 0 ? 0 : 2 * R + 2 * kPad];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = c;
+            }
+            if (large) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[r] -= bases[32 * u + 8 * half + 16 * (r >> 3) + (r & 7)];
             }
 #pragma unroll
             for (int kc = 0; kc < kc_n; ++kc)
@@ -528,7 +664,8 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
                            dim3(xcd_grid((int64_t)a.B * a.H, attn_tiles(a.Tq))), dim3(kThreads),
                            tiles + (BIAS ? window : 0), st, a);
     if ((int64_t)a.B * a.Tk > 0) {
-        size_t lds = tiles + (256 + (DROP ? kWaves * 32 : 0)) * sizeof(float) + (BIAS ? window : 0);
+        size_t lds =
+            tiles + (kRowFloats + (DROP ? kWaves * 32 : 0)) * sizeof(float) + (BIAS ? window : 0);
         if (TABLE)
             lds += kWaves * (kSkewFloats + 2 * (size_t)a.bias.radius + 1) * sizeof(float);
         hipLaunchKernelGGL((attn_dkv_kernel<T, DP, BIAS, DROP, TABLE, SHORT>),

@@ -46,12 +46,12 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
     load_frags<T, DP>(qf, (const T*)a.q + b * a.sq.b + h * a.sq.h, a.sq.t, i, i < a.Tq, a.D, lane);
 
     // keys this workgroup goes over, and the last one each query sees
-    int32_t j0 = 0, end = n_keys;
+    int32_t first = 0, end = n_keys;
     const int32_t last_q = (qt + 1) * kTileRows < a.Tq ? (qt + 1) * kTileRows - 1 : a.Tq - 1;
     if (a.causal && last_q + pos + 1 < end) end = last_q + pos + 1;
     if (SPLIT) {
-        j0 = split * a.split_tiles * kStep;
-        const int32_t stop = j0 + a.split_tiles * kStep;
+        first = split * a.split_tiles * kStep;
+        const int32_t stop = first + a.split_tiles * kStep;
         if (stop < end) end = stop;
     }
     const int32_t limit = a.causal && i + pos < n_keys - 1 ? i + pos : n_keys - 1;
@@ -67,13 +67,13 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
     const uint32_t step = DROP ? a.drop.step + (a.drop.step_dev ? *a.drop.step_dev : 0u) : 0u;
 
     const Feed<T, DP> ks(kp, a.sk.t, a.D, wave, lane), vs(vp, a.sv.t, a.D, wave, lane);
-    if (j0 < end) {
-        ks.load(lds, j0, n_keys, wave);
-        vs.load(lds + tile_bytes<DP>(), j0, n_keys, wave);
+    if (first < end) {
+        ks.load(lds, first, n_keys, wave);
+        vs.load(lds + tile_bytes<DP>(), first, n_keys, wave);
     }
     if (BIAS) fill_window(window, a.bias, h, a.scale);
     int buf = 0;
-    for (; j0 < end; j0 += kStep, buf ^= 1) {
+    for (int32_t j0 = first; j0 < end; j0 += kStep, buf ^= 1) {
         char* kt = lds + buf * 2 * tile_bytes<DP>();
         char* vt = kt + tile_bytes<DP>();
         // this tile (and the window) is there, and the other buffer is read
@@ -127,6 +127,16 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
         if (__any(mx > m + 8.0f)) {
             const float m_new = fmaxf(m, mx);
             const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - m_new);
+            // sums from a large reference far below may not be numbers: gone,
+            // not multiplied (a NaN of a score stays in l)
+            const bool gone = alpha == 0.0f && is_large(m);
+            if (__builtin_expect(__any(gone), 0)) {
+                if (gone && l == l) l = 0.0f;
+#pragma unroll
+                for (int d = 0; d < db_n; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[d][r] = gone ? 0.0f : acc[d][r];
+            }
             l *= alpha;
 #pragma unroll
             for (int d = 0; d < db_n; ++d) acc[d] *= alpha;
@@ -162,10 +172,98 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
     }
 
     l += other_half(l);
-    if (i >= a.Tq) return;
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
-    if (SPLIT) write_split<DP>(a, acc, row, split, m, l, half);
-    else write_rows<T, DP>(a, acc, b, h, i, row, m, l, half);
+    const bool again = is_large(m);
+    if (i < a.Tq && !again) {
+        if (SPLIT) write_split<DP>(a, acc, row, split, 0.0f, m, l, half);
+        else write_rows<T, DP>(a, acc, b, h, i, row, 0.0f, m, l, half);
+    }
+
+    // Rows of large references once more: the reference is what holds of them.
+    // It becomes the base, and m starts low, but above what far lower keys
+    // have.  32 keys at a time, a tile after the other.
+    __shared__ uint32_t waves_large[kWaves];
+    if (lane == 0) waves_large[wave] = __any(again);
+    __syncthreads();  // the tiles are read, too
+    const bool none = !(waves_large[0] | waves_large[1] | waves_large[2] | waves_large[3]);
+    if (__builtin_expect(none, 1)) return;
+    // The generator's keys, and below the lane's addresses, anew: kept through
+    // the first pass for this one they would go to memory (with that, launches
+    // take up to 5 us longer).
+    uint32_t k0 = a.drop.k0, k1 = a.drop.k1;
+    asm volatile("" : "+s"(k0), "+s"(k1));
+    const float base = again ? m / scale2 : 0.0f;
+    m = -0x1p12f;
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};
+    for (int32_t j0 = first; j0 < end; j0 += kStep) {
+        ks.load(lds, j0, n_keys, wave);
+        vs.load(lds + tile_bytes<DP>(), j0, n_keys, wave);
+        tiles_barrier();
+#pragma unroll 1
+        for (int u = 0; u < kStep; u += 32) {
+            const int32_t js = j0 + u;
+            if (js > limit_hi) break;
+            int lane_now = lane;
+            asm volatile("" : "+v"(lane_now));
+            const int lane = lane_now, half = lane >> 5;
+            const int side = BIAS ? side_of(js, iw, pos, R) : 0;
+            f32x16 s = {};
+            float flat = 0.0f;
+            if (BIAS && side == 0) {
+                const float* at = window + (js + 8 * half - i - pos + R + kPad);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = at[16 * (r >> 3) + (r & 7)] - base;
+            } else {
+                if (BIAS) flat = window[side < 0 ? 0 : 2 * R + 2 * kPad];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = flat - base;
+            }
+#pragma unroll
+            for (int kc = 0; kc < kc_n; ++kc)
+                s = Mma<T>::mul(row_frag<T, DP>(lds, u, kc, lane), qf[kc], s);
+            const int32_t seen = limit - js - 8 * half;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[r] = 16 * (r >> 3) + (r & 7) > seen ? -INFINITY : s[r] * scale2;
+                mx = fmaxf(mx, s[r]);
+            }
+            const float m_new = fmaxf(m, fmaxf(mx, other_half(mx)));
+            const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+            const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < db_n; ++d) acc[d] *= alpha;
+            m = m_new;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(s[8 * c + e] - m_use);
+                l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+                if (DROP) {
+                    uint32_t wd[4];
+                    drop_draws(wd, (uint32_t)(js + 16 * c + 8 * half) >> 3, drop_row, step,
+                               k0, k1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!drop_keep(wd, e, a.drop.threshold)) p[e] = 0.0f;
+                }
+                const x8 pb = pack8<T>(p);
+#pragma unroll
+                for (int d = 0; d < db_n; ++d)
+                    acc[d] = Mma<T>::mul(
+                        col_frag<T, DP>(lds + tile_bytes<DP>(), u + 16 * c, d, lane), pb, acc[d]);
+            }
+        }
+        __syncthreads();  // this tile is read
+    }
+    l += other_half(l);
+    if (i >= a.Tq || !again) return;
+    if (SPLIT) write_split<DP>(a, acc, row, split, base, m, l, half);
+    else write_rows<T, DP>(a, acc, b, h, i, row, base, m, l, half);
 }
 
 // Joins the splits of a row (at most 64, one a lane for their weights), two
@@ -178,13 +276,27 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
     const int wave = wave_id(), lane = lane_id();
     const int64_t row = (int64_t)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
     const bool ok = row < rows;
-    float m = -INFINITY, l = 0.0f;
+    float base = 0.0f, m = -INFINITY, l = 0.0f;
     if (ok && lane < a.splits) {
-        const float2 x = a.split_ml[row * a.splits + lane];
-        m = x.x;
-        l = x.y;
+        const f4 x = a.split_ml[row * a.splits + lane];
+        base = x[0];
+        m = x[1];
+        l = x[2];
     }
-    float top = m;
+    const float unit = a.few ? 1.0f : a.scale * kLog2e;  // of the bases
+    float origin = 0.0f, top = m;
+    if (__any(base != 0.0f)) {
+        // all to one split's base: the highest's, as far as a first one shows
+        for (int k = 0; k < 2; ++k) {
+            const float above = m == -INFINITY ? m : (base - origin) * unit + m;
+            float most = above;
+            for (int off = 32; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+            const uint64_t at = __ballot(above == most);
+            if (at) origin = __shfl(base, __builtin_ctzll(at), 64);
+        }
+        if (m != -INFINITY) m += (base - origin) * unit;
+        top = m;
+    }
     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
     const float weight = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
     l *= weight;
@@ -231,7 +343,10 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
         to[c] = (T)(o.x * inv);
         to[c + 1] = (T)(o.y * inv);
     }
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : top * kLn2 + __logf(l);
+    if (a.lse && lane == 0)
+        a.lse[row] = l == 0.0f
+                         ? -INFINITY
+                         : origin * (a.few ? kLn2 : a.scale) + (top * kLn2 + __logf(l));
 }
 
 template <typename T, int DP, bool BIAS, bool DROP>

@@ -358,6 +358,135 @@ def test_a_row_of_one_key_has_no_score_gradient(dtype, p):
         assert bool((got["dv"] != 0).any())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", [-1e4, -1e6, -1e9, 1e9])
+def test_rows_of_one_large_bias(low, dtype):
+    """A softmax does not change when all its scores do: a head whose table
+    holds one large number has the outputs and gradients of a head without a
+    bias, and an lse further by that number.  The references of such rows are
+    rounded, which leaves |low| 2^-22 of the number in the scores at most: the
+    oracle gets a table of that much, and its bounds with it.  Single queries
+    and many go through different kernels."""
+    dev = device()
+    rest = abs(low) * 2.0 ** -22
+    for Tq, Tk, D, p, k_len in ((1, 300, 64, 0.0, None), (3, 2000, 128, 0.2, (1500,)),
+                                (50, 80, 64, 0.2, None), (150, 400, 128, 0.0, (333,)),
+                                (40, 1100, 64, 0.0, None), (130, 64, 80, 0.1, None)):
+        g = gen(Tq + D, dev)
+        q, k, v = make(dtype, 1, 2, 1, Tq, Tk, D, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        table = torch.randn((32, 2), generator=g, device=dev)
+        how = dict(scale=D ** -0.5, causal=False, q_pos=Tk - Tq, k_len=None,
+                   bucket_map=rel_bucket_map(32, 40, True, dev), p=p, seed=SEED, step=17)
+        if k_len is not None:
+            how["k_len"] = torch.tensor(k_len, dtype=torch.int32, device=dev)
+        table[:, 1] = rest
+        want, tol = _oracle(q, k, v, do, dict(table=table, **how), dtype)
+        want["lse"][:, 1] += low - rest
+        tol["lse"][:, 1] += 4 * 2.0 ** -24 * abs(low)
+        table[:, 1] = low
+        dtable = torch.full_like(table, 9.0)
+        got = _backward(q, k, v, dict(table=table, **how), do, dtable)
+        print(f"[attention] {low} {dtype} {Tq}x{Tk}x{D}", flush=True)
+        check(got, want, tol, ("o", "lse", "dq", "dk", "dv", "dtable"), _tiny(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", [-2.0 ** 40, -1e15, -1e30])
+def test_rows_hidden_whole(low, dtype):
+    """From -2^40 on a bias counts as -inf: its keys have no weight, a row of
+    nothing else no output and no gradient, in every kernel."""
+    dev = device()
+    for Tq, Tk, D in ((1, 300, 64), (4, 1500, 128), (50, 80, 64), (150, 400, 128)):
+        g = gen(Tq + D, dev)
+        q, k, v = make(dtype, 1, 2, 2, Tq, Tk, D, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        table = torch.randn((8, 2), generator=g, device=dev)
+        table[5:, 0] = low                    # every key after the query
+        table[:, 1] = low
+        how = dict(q_pos=Tk // 2, bucket_map=rel_bucket_map(8, 20, True, dev))
+        dtable = torch.full_like(table, 9)
+        got = _backward(q, k, v, dict(table=table, **how), do, dtable)
+        for n in ("o", "dq", "dk", "dv"):
+            assert bool(got[n].isfinite().all()) and bool((got[n][:, :, 1] == 0).all()), n
+        assert bool((got["lse"][:, 1] == float("-inf")).all())
+        assert bool((dtable[5:] == 0).all()) and bool((dtable[:, 1] == 0).all())
+        table[table == low] = float("-inf")
+        want = _backward(q, k, v, dict(table=table, **how), do, torch.full_like(table, 9))
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", [-1e4, -1e9, -1e12])
+def test_large_biases_far_away(low, dtype):
+    """Keys that a low bias hides behind others of the row count as hidden ones,
+    wherever they come: first (the far keys of a decoder), last, or as all that
+    a part of a split row has."""
+    dev = device()
+    for Tq, Tk, D, two in ((1, 3000, 128, False), (3, 500, 64, False), (100, 700, 64, False),
+                           (150, 300, 128, True), (40, 1500, 64, True)):
+        g = gen(Tq + D, dev)
+        q, k, v = make(dtype, 1, 2, 2, Tq, Tk, D, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        bmap = rel_bucket_map(8, 20, two, dev)
+        table = torch.randn((8, 2), generator=g, device=dev)
+        table[bmap[0]] = low
+        table[bmap[-1] if two else bmap[0]] = low
+        how = dict(q_pos=Tk // 2 if two else Tk - Tq, causal=not two, bucket_map=bmap, p=0.1,
+                   seed=SEED, step=17)
+        dtable = torch.full_like(table, 9)
+        got = _backward(q, k, v, dict(table=table, **how), do, dtable)
+        table[table == low] = float("-inf")
+        want = _backward(q, k, v, dict(table=table, **how), do, torch.full_like(table, 9))
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("far", [3e2, 1e4])
+def test_large_products(far, dtype):
+    """Scores of up to 10^8 and more: each row's weight lies on one key to more
+    than binary32 shows (its margin is checked), so o is that key's value, dv
+    takes the rows' gradients whole, and no score has a gradient but for the
+    rounding of delta."""
+    dev = device()
+    e = 2.0 ** -24
+    for Tq, Tk, D in ((1, 200, 64), (2, 2000, 128), (50, 80, 64), (150, 300, 128)):
+        g = gen(Tq + D, dev)
+        q, k, v = make(dtype, 1, 2, 1, Tq, Tk, D, g, dev)
+        q, k = q * far, k * far
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        q64, k64, v64, do64 = (x[0].double().transpose(0, 1) for x in (q, k, v, do))
+        s = q64 @ k64.transpose(1, 2) * D ** -0.5
+        size = q64.abs() @ k64.abs().transpose(1, 2) * D ** -0.5
+        top = s.topk(2, 2)
+        off = (D + 8) * e * size.amax(2)
+        sure = top.values[..., 0] - top.values[..., 1] > 2 * off + 200
+        do64 = do64 * sure[..., None]
+        do = do64.to(do.dtype).transpose(0, 1)[None].contiguous()  # the other rows' count 0
+        got = _backward(q, k, v, {}, do, None)
+        best = top.indices[..., 0]
+        want = v64[0][best]
+        o = got["o"][0].double().transpose(0, 1)
+        assert bool(sure.any())
+        assert torch.equal(o[sure], want[sure])
+        lse = got["lse"][0].double()
+        assert bool(((lse - top.values[..., 0]).abs() <= off + 4 * e * lse.abs()).all())
+        dv = torch.zeros_like(v64[0]).index_add_(0, best[sure], do64[sure])
+        size_dv = torch.zeros_like(v64[0]).index_add_(0, best[sure], do64[sure].abs())
+        err = (got["dv"][0, :, 0].double() - dv).abs()
+        assert bool((err <= half_step(dtype) * dv.abs() + 2 * Tq * e * size_dv).all())
+        # dP is known to (D + 2) e of its terms, and delta adds one of a few
+        # roundings more: dS = dP - delta of that key alone
+        ds = ((D + 8) * e * (do64.abs() @ v64.abs().transpose(1, 2)).amax(2)) * 4
+        dq = got["dq"][0].double().transpose(0, 1)
+        bound = D ** -0.5 * ds[..., None] * k64.abs().amax((1, 2))
+        assert bool((dq.abs() <= bound + _tiny(dtype)).all())
+        bound = D ** -0.5 * (ds.sum() * q64.abs().max())
+        assert bool((got["dk"].double().abs() <= bound + _tiny(dtype)).all())
+
+
 def test_two_streams_at_once():
     """Calls on two streams at once, each with its own workspace (split keys,
     and a backward pass with the table's gradient), equal the same calls one
