@@ -546,9 +546,11 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * gradients' products of up to 64 queries and keys take the rest as well).
  * dtable is summed in binary32 and binary64 from unrounded dS.  Sums run in
  * an order fixed by the sizes: the same call gives the same bits.
- * Keys and values from k_len[b] on are not read (dk and dv are 0 there); the
- * values of keys that only the causal mask hides are multiplied by 0 and have
- * to be finite.  k_len and q_pos_of are clamped to 0 ... Tk and +-2^29.
+ * Keys and values that no query of the sequence sees, from k_len[b] on or, if
+ * causal, from pos_b + Tq on, are not read (dk and dv are 0 there); the values
+ * of the others are multiplied by 0 for queries that the causal mask hides them
+ * from, and have to be finite.  k_len and q_pos_of are clamped to 0 ... Tk and
+ * +-2^29.
  *
  * A table value of -2^40 or less counts as -infinity, and so does one that
  * leaves binary32 when divided by the scale or multiplied by log2 e: its keys

@@ -287,10 +287,15 @@ __device__ __forceinline__ int32_t query_position(const AttnArgs& a, int b) {
     return p < -far ? -far : (p > far ? far : p);
 }
 
-__device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b) {
-    if (!a.k_len) return a.Tk;
-    const int32_t n = __builtin_amdgcn_readfirstlane(a.k_len[b]);
-    return n < 0 ? 0 : (n > a.Tk ? a.Tk : n);
+// Keys that some query sees: the others are not read, whatever lies there.
+__device__ __forceinline__ int32_t key_count(const AttnArgs& a, int b, int32_t pos) {
+    int32_t n = a.Tk;
+    if (a.k_len) {
+        n = __builtin_amdgcn_readfirstlane(a.k_len[b]);
+        n = n > a.Tk ? a.Tk : n;
+    }
+    if (a.causal && a.Tq + pos < n) n = a.Tq + pos;
+    return n < 0 ? 0 : n;
 }
 
 // Workgroups go to the 8 XCDs in turn.  The workgroups of one group (a

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_
     const int qt = (int)(tiles_q - 1 - item);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b, pos);
     const int32_t iw = qt * kTileRows + wave * kRows;
     const int32_t i = iw + (lane & 31);
     const int R = a.bias.radius;
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 2 : 1) void attn_dkv_kernel(At
     const int kt_i = (int)item;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b, pos);
     const int32_t jw = kt_i * kTileRows + wave * kRows;
     const int32_t j = jw + (lane & 31);
     const int R = a.bias.radius, group = a.H / a.Hkv, bins_n = 2 * R + 1;

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     if (!xcd_work((uint32_t)a.B * a.Hkv, (uint32_t)a.splits, kEven, bh, part)) return;
     const int hk = (int)(bh % a.Hkv), b = (int)(bh / a.Hkv);
     const int lane = lane_id(), wave = wave_id();
-    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b, pos);
     const int group = a.H / a.Hkv, R = a.bias.radius;
     // The query of a lane's column.  The lane number comes anew for each use: what
     // follows from it, kept through the keys, would go to memory (with that a
@@ -57,9 +57,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
 
     const T* kp = (const T*)a.k + b * a.sk.b + hk * a.sk.h;
     const T* vp = (const T*)a.v + b * a.sv.b + hk * a.sv.h;
-    int32_t end = n_keys;
-    if (a.causal && a.Tq + pos < end) end = a.Tq + pos;
-    const int32_t n_tiles = end > 0 ? (end + kRows - 1) / kRows : 0;
+    const int32_t n_tiles = (n_keys + kRows - 1) / kRows;
     // every waves-th tile: neighbouring waves read neighbouring rows, and the
     // few tiles near the queries, whose bias is gathered, go to different waves
     const int32_t waves = a.splits * kWaves;

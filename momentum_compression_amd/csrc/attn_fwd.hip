@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
     const int split = (int)(item % a.splits);
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int lane = lane_id(), wave = wave_id(), half = lane >> 5;
-    const int32_t pos = query_position(a, b), n_keys = key_count(a, b);
+    const int32_t pos = query_position(a, b), n_keys = key_count(a, b, pos);
     const int32_t iw = qt * kTileRows + wave * kRows;  // the wave's first query
     const int32_t i = iw + (lane & 31);
     const int R = a.bias.radius;

@@ -283,6 +283,37 @@ def test_values_past_the_length_and_nan_inputs():
     assert torch.equal(o[0, rest], clean[0, rest])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cache_places_that_no_query_sees(dtype):
+    """Under the causal mask a cache may hold anything past the last query's
+    position: the results are those of a cache that ends there, and its keys'
+    gradients are 0."""
+    dev = device()
+    bmap = rel_bucket_map(32, 40, False, dev)
+    for Tq, Tk, D, pos, k_len in ((1, 1000, 64, (700, 0), None), (5, 500, 128, (300, 64), None),
+                                  (70, 400, 64, (200, -30), (400, 41)),
+                                  (130, 256, 80, (0, 17), None),
+                                  (40, 3000, 128, (1000, 2000), None)):
+        g = gen(Tq + D, dev)
+        q, k, v = make(dtype, 2, 4, 2, Tq, Tk, D, g, dev)
+        do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+        table = torch.randn((32, 4), generator=g, device=dev)
+        how = dict(causal=True, q_pos=torch.tensor(pos, dtype=torch.int32, device=dev),
+                   table=table, bucket_map=bmap, p=0.1, seed=SEED, step=5)
+        if k_len is not None:
+            how["k_len"] = torch.tensor(k_len, dtype=torch.int32, device=dev)
+        want = _backward(q, k, v, how, do, torch.empty_like(table))
+        for b, n in enumerate(pos):
+            for x in (k, v):
+                x[b, max(0, n + Tq):] = float("nan")
+        got = _backward(q, k, v, how, do, torch.empty_like(table))
+        for n in want:
+            assert torch.equal(got[n], want[n]), (Tq, Tk, n)
+        for b, n in enumerate(pos):
+            for x in ("dk", "dv"):
+                assert bool((got[x][b, max(0, n + Tq):] == 0).all())
+
+
 def test_lowest_bias_values():
     """A table holding the type's lowest number, or -inf, hides its distances
     without NaN."""
