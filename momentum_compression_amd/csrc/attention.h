@@ -256,12 +256,13 @@ __device__ __forceinline__ void fill_window(float* w, const RelBias& b, int h, f
 
 // An exponential's argument is one fused multiplication and addition of the
 // score and the row's reference, which leaves up to half a step of the
-// reference in it: an exponent of 64 at 2^30.  From 2^13 on (base 2; half a step
-// of 2^-11) a row gets a base near its reference that is taken off its scores
+// reference in it, in the backward pass a few (lse is a product and its base-2
+// form another): an exponent of 64 at 2^30.  From 2^10 on (base 2; half a step of
+// 2^-14) a row gets a base near its reference that is taken off its scores
 // before the products are added, so that scores and reference are small again.
 __device__ __forceinline__ bool is_large(float reference) {
     const float r = __builtin_fabsf(reference);
-    return r >= 0x1p13f && r < INFINITY;
+    return r >= 0x1p10f && r < INFINITY;
 }
 
 // Where the 32 x 32 scores of queries from i0 and keys from j0 lie against the

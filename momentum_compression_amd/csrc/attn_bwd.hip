@@ -17,13 +17,14 @@ namespace onebit {
 
 namespace {
 
-// Up to kShort queries and keys the products take P and dS as a rounded part and
-// the rounded rest, twice the products of these: sums of few terms leave the
-// roundings as they are, where those of many average them out.  Measured error
-// of dq and dk over a plain form's that rounds only results, heads of 16 ... 128:
-// 2 tokens up to 4.1 times, 5 up to 1.9, 10 up to 1.7, 64 and more 1.4; with the
-// rest 1.0.  A few sequences are as fast with it (2 of 37 tokens, backward 25.6
-// us, 25.4 without), many nearly (64 of 64 tokens, 16 heads of 64: 56.5 and 53.7).
+// Up to kShort queries and keys (the call's lengths, padding included) the
+// products take P and dS as a rounded part and the rounded rest, twice the
+// products of these.  The roundings of P and dS add to the result's own, each as
+// large: measured error of dq, dk and dv over a plain form's that rounds only
+// results 1.4 without the rest, whatever the lengths (heads of 8 ... 128, rows of
+// 2 ... 600 keys), and 1.0 with it.  A few short sequences are as fast with it
+// (2 of 37 tokens, backward 25.7 us, 25.1 without), many nearly (64 of 64
+// tokens, 16 heads of 64: 54.6 and 53.3); at longer ones the products count.
 constexpr int kShort = 64;
 
 // What rounding left of eight values.
@@ -38,20 +39,22 @@ __device__ __forceinline__ typename Mma<T>::x8 pack_rest(const float* p,
 
 // Queries as columns: dq and, for the second pass, delta in binary32.  With any
 // value delta' near it, delta = delta' + sum P (dP - delta') / sum P; the sum of
-// dS comes beside dS, and the sum of P is 1 but for the roundings of lse, 2^-20
-// or so of a correction that is itself 2^-8 of delta (summed and divided by, it
-// took 3 % longer).  dq itself takes delta' = dO . o of the rounded output, which
+// dS comes beside dS, and the sum of P is 1 but for the roundings of lse: 5 times
+// 2^-24 of it, 2^-12 at the largest that rows without a base have, of a correction
+// that is itself 2^-8 of delta (summed and divided by, it took 3 % longer).  dq itself takes delta' = dO . o of the rounded output, which
 // is there before the pass: off by half a step of the element type times the
 // row's output.  That is small beside what dS is rounded by where many keys
 // share the weight, but not where few do, so workgroups with at most kTwice keys
 // make the pass twice, the first time for the sums alone and from the first key's
 // dP: a query that sees one key then has delta = dP to the bit, and dS = 0 in
-// both passes over the scores.  Measured error of dq against 64 bits, in units
+// both passes over the scores.  (Over more keys a query whose weight lies on one
+// of them by its scores keeps the half step times that key in dq, where dk and
+// dtable have the exact delta.)  Measured error of dq against 64 bits, in units
 // of the output's own rounding, with one pass and with two: 37 keys 1.51 and
 // 1.41, 256 keys 1.47 and 1.43, fp16 rows of at most 5 keys 2.9 and 1.4; with
 // one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would take
-// 74 instead of 53 us for 16 sequences of up to 512 keys and 16 heads of 64; one
-// pass always, 50.
+// 69 instead of 50 us for 16 sequences of up to 512 keys and 16 heads of 64; one
+// pass always, 46.
 //
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.

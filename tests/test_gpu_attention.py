@@ -518,6 +518,39 @@ def test_large_products(far, dtype):
         assert bool((got["dk"].double().abs() <= bound + _tiny(dtype)).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Tk", [200, 300, 1100])
+def test_rows_of_one_heavy_key(Tk, dtype):
+    """A row whose weight lies on one key of many has next to no score gradient.
+    The query pass over more than 256 keys takes delta from the rounded output:
+    dq is off by half a step of the output times the gradient, times that key.
+    Over fewer keys, and in the key pass always, delta is binary32's.  The weight
+    is 1 but for what lse has rounded, less than 5 times 2^-24 |lse| (its
+    reference, two constants and two products), of the distance between that
+    key's dP and what delta starts from."""
+    dev = device()
+    e, Tq, D = 2.0 ** -24, 70, 64
+    g = gen(Tk, dev)
+    q, k, v = make(dtype, 1, 2, 1, Tq, Tk, D, g, dev)
+    q, k = q * 8, k * 8
+    do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+    q64, k64, v64, do64 = (x[0].double().transpose(0, 1) for x in (q, k, v, do))
+    top = (q64 @ k64.transpose(1, 2) * D ** -0.5).topk(2, 2).values
+    sure = top[..., 0] - top[..., 1] > 25  # the others weigh less than 2^-25 together
+    assert bool(sure.any())
+    do64 = do64 * sure[..., None]
+    do = do64.to(do.dtype).transpose(0, 1)[None].contiguous()
+    got = _backward(q, k, v, {}, do, None)
+    o64 = got["o"][0].double().transpose(0, 1)
+    exact = (4 * (D + 8) + 10 * top[..., 0].abs()) * e * (
+        do64.abs() @ v64.abs().transpose(1, 2)).amax(2)
+    rounded = exact + half_step(dtype) * (do64 * o64).abs().sum(2) * (1 if Tk > 256 else 0)
+    dq = got["dq"][0].double().transpose(0, 1).abs()
+    assert bool((dq <= D ** -0.5 * rounded[..., None] * k64.abs().amax() + _tiny(dtype)).all())
+    dk = got["dk"].double().abs()
+    assert bool((dk <= D ** -0.5 * exact.sum() * q64.abs().max() + _tiny(dtype)).all())
+
+
 def test_two_streams_at_once():
     """Calls on two streams at once, each with its own workspace (split keys,
     and a backward pass with the table's gradient), equal the same calls one
