@@ -478,7 +478,8 @@ typedef enum { ONEBIT_F32 = 0, ONEBIT_BF16 = 1, ONEBIT_F16 = 2 } onebit_dtype;
  * passes step_dev draws new masks on each replay as the caller changes it.
  *
  * x, residual, y: rows of `cols` elements, ld_* elements apart (ld >= cols);
- * aligned to their element.  y may be x or residual itself (same ld).
+ * aligned to their element.  y may be x or residual itself (same ld), and lie
+ * between their rows; where its rows lie over theirs the call is refused.
  * residual may be NULL (ld_r unread), step_dev too (device, 4-byte aligned).
  * 0 <= p < 1, row0 >= 0, rows * ceil(cols / 8) < 2^31.  No rows or columns:
  * a no-op.
@@ -564,7 +565,8 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * of 8, between tokens at most 2^23.  So a fused projection's output and a
  * cache of either order serve as they are.  Sequences of a batch may share
  * keys (stride 0); an output's dimensions must lie one within the other, and
- * outputs must not overlap each other or an input.
+ * outputs must not overlap each other or an input (one at the same address is
+ * refused).
  * lse [B][H][Tq] float, optional in the forward pass.  table [n_buckets][H]
  * float and map as rel_bias_expand, or NULL, NULL, 0, 0 without a bias.
  * 0 <= p < 1; 2^-64 <= scale <= 2^64.

@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call, so invalid calls touch nothing.
 #include <math.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 
@@ -522,6 +523,19 @@ bool row_groups_ok(int64_t rows, int64_t cols) {
     return rows <= INT32_MAX && per_row <= INT32_MAX && rows * per_row <= INT32_MAX;
 }
 
+// Whether y's rows lie over p's without being them, as far as strides show: of
+// one stride, or from one address on.
+bool rows_cross(const void* y, int64_t ld_y, const void* p, int64_t ld_p, int64_t rows,
+                int64_t cols, size_t size) {
+    if (y == p) return ld_y != ld_p && rows > 1;
+    if (!p || ld_y != ld_p) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(y), b = reinterpret_cast<uintptr_t>(p);
+    const uint64_t apart = a < b ? b - a : a - b;  // bytes
+    const uint64_t pitch = (uint64_t)ld_y * size, width = (uint64_t)cols * size;
+    if (apart >= pitch * (uint64_t)(rows - 1) + width) return false;
+    return apart % pitch < width || pitch - apart % pitch < width;
+}
+
 int check_lengths(int32_t Tq, int32_t Tk) {
     return Tq < 0 || Tk < 0 || Tq > kMaxPositions || Tk > kMaxPositions ? ONEBIT_E_SIZE : ONEBIT_OK;
 }
@@ -557,8 +571,11 @@ int dropout_apply(const void* x, const void* residual, void* y, int32_t dtype, i
     if (ld_x < cols || ld_y < cols || (residual && ld_r < cols) || ld_x > kMaxLd || ld_y > kMaxLd ||
         (residual && ld_r > kMaxLd))
         return ONEBIT_E_SIZE;
-    if (!aligned(x, size) || !aligned(y, size) || !aligned(residual, size) || !aligned(step_dev, 4))
-        return ONEBIT_E_ALIGN;
+    if (!aligned(x, size) || !aligned(y, size) || !aligned(residual, size)) return ONEBIT_E_ALIGN;
+    if (rows_cross(y, ld_y, x, ld_x, rows, cols, size) ||
+        rows_cross(y, ld_y, residual, ld_r, rows, cols, size))
+        return ONEBIT_E_ARG;
+    if (!aligned(step_dev, 4)) return ONEBIT_E_ALIGN;
     drop_stale_error();
     return hip_status(launch_dropout(x, residual, y, dtype, rows, cols, ld_x, ld_r, ld_y, row0, p,
                                      seed, step, step_dev, stream));
@@ -641,6 +658,13 @@ int check_heads(const void* p, const int64_t s[3], int32_t B, int32_t T, int32_t
         span += dim[k][0] * (dim[k][1] - 1);
     }
     return aligned(p, 16) ? ONEBIT_OK : ONEBIT_E_ALIGN;
+}
+
+// An output over a tensor of the call (empty ones are passed as they come).
+bool written_over(const void* out, int32_t T, std::initializer_list<const void*> others) {
+    for (const void* x : others)
+        if (out == x && out && T > 0) return true;
+    return false;
 }
 
 Strides strides_of(const int64_t s[3]) { return Strides{s[0], s[1], s[2]}; }
@@ -770,6 +794,7 @@ int rel_attention_forward(const rel_attention_args* a, void* ws, size_t ws_bytes
         k.split_o = static_cast<float*>(ws);
         k.split_ml = reinterpret_cast<f4*>(static_cast<char*>(ws) + z.split_o);
     }
+    if (written_over(a->o, a->Tq, {a->q, a->k, a->v})) return ONEBIT_E_ARG;
     drop_stale_error();
     return hip_status(launch_attn_forward(k, a->dtype, stream));
 }
@@ -791,6 +816,10 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
         attn_sizes(a->B, a->H, a->Hkv, a->Tq, a->Tk, a->D, a->dtable ? a->radius : 0);
     if (!ws || ws_bytes < z.delta + z.partials) return ONEBIT_E_WORKSPACE;
     if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    if (a->B > 0 && (written_over(a->dq, a->Tq, {a->q, a->k, a->v, a->o, a->d_o}) ||
+                     written_over(a->dk, a->Tk, {a->q, a->k, a->v, a->o, a->d_o, a->dq}) ||
+                     written_over(a->dv, a->Tk, {a->q, a->k, a->v, a->o, a->d_o, a->dq, a->dk})))
+        return ONEBIT_E_ARG;
     AttnArgs k = attn_args(a);
     k.d_o = a->d_o;
     k.dq = a->dq;

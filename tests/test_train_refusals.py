@@ -48,6 +48,23 @@ def test_dropout_refusals(lib):
     assert call(cols=0) == ob.ONEBIT_OK
 
 
+def test_dropout_refuses_rows_over_rows(lib):
+    """In place and between the rows is allowed (the address of the device step,
+    which is checked next and not aligned here, stops those calls), crossing
+    rows are not."""
+    def call(y, ly, x=P, lx=32, r=None, lr=32, rows=4, cols=10, sd=P + 2):
+        return lib.dropout_apply(x, r, y, 0, rows, cols, lx, lr, ly, 0.1, 1, 1, sd, 0, None)
+
+    for y, ly in ((P, 40), (P + 4, 32), (P + 4 * 32, 32), (P + 4 * 95, 32), (P + 4 * 9, 32),
+                  (P + 4 * 23, 32), (P - 4, 32), (P - 4 * 23, 32), (P - 4 * 96, 32)):
+        assert call(y, ly) == ob.ONEBIT_E_ARG, (y - P, ly)
+        assert call(y, ly, x=4 * P, r=P) == ob.ONEBIT_E_ARG, (y - P, ly)
+    for y, ly in ((P, 32), (P + 4 * 10, 32), (P + 4 * 22, 32), (P - 4 * 10, 32), (P + 4 * 106, 32),
+                  (P - 4 * 106, 32)):
+        assert call(y, ly) == ob.ONEBIT_E_ALIGN, (y - P, ly)
+    assert call(P, 40, rows=1) == ob.ONEBIT_E_ALIGN
+
+
 def test_rel_bias_refusals(lib):
     def call(t=P, m=P, o=P, dt=0, H=2, nb=8, R=16, Tq=4, Tk=4, pos=0):
         return lib.rel_bias_expand(t, m, o, dt, H, nb, R, Tq, Tk, pos, None)
@@ -219,6 +236,26 @@ def test_attention_refusals(lib):
     assert lib.rel_attention_forward(ctypes.byref(a), None, 0, None) == ob.ONEBIT_E_WORKSPACE
     assert lib.rel_attention_forward(ctypes.byref(_args(Tq=0, q=None, o=None)), None, 0,
                                      None) == ob.ONEBIT_OK
+
+
+def test_attention_refuses_outputs_over_its_tensors(lib):
+    import ctypes
+
+    apart = dict(q=P, k=2 * P, v=3 * P, o=4 * P, d_o=5 * P, dq=6 * P, dk=7 * P, dv=8 * P)
+
+    def fwd(**kw):
+        a = _args(**{**apart, **kw})
+        return lib.rel_attention_forward(ctypes.byref(a), 16 * P, 1 << 30, None)
+
+    def bwd(**kw):
+        a = _args(**{**apart, **kw})
+        return lib.rel_attention_backward(ctypes.byref(a), 16 * P, 1 << 30, None)
+
+    for n in "qkv":
+        assert fwd(o=apart[n]) == ob.ONEBIT_E_ARG
+    for out, n in (("dq", 5), ("dk", 6), ("dv", 7)):
+        for other in list(apart)[:n]:
+            assert bwd(**{out: apart[other]}) == ob.ONEBIT_E_ARG, (out, other)
 
 
 def test_attention_workspace(lib):
