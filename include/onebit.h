@@ -529,7 +529,9 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  *           (all Tk without k_len) and, if causal, j <= i + pos_b
  *   P     = softmax over the seen keys;  lse_i = log sum_j exp s_ij
  *   keep_ij = 65536 / T or 0, the draw of dropout_apply for row
- *           (b H + h) Tq + i and column j
+ *           (b H + h) Tq + i and column j.  Rows count from the call's own first
+ *           sequence and head: a call on a part of a batch or of the heads draws
+ *           another mask than the whole, and parts take seeds of their own
  *   o_i   = sum_j P_ij keep_ij v_j
  * A query that sees no key has o = 0, lse = -inf and no gradient.  Query head
  * h reads key head h / (H / Hkv).
@@ -547,6 +549,8 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * gradients' products of up to 64 queries and keys take the rest as well).
  * dtable is summed in binary32 and binary64 from unrounded dS.  Sums run in
  * an order fixed by the sizes: the same call gives the same bits.
+ * In F16 that makes the type's range a bound for dS: below 2^-24 it is lost,
+ * past 65504 infinite, so gradients come scaled as for any product in F16.
  * Keys and values that no query of the sequence sees, from k_len[b] on or, if
  * causal, from pos_b + Tq on, are not read (dk and dv are 0 there); the values
  * of the others are multiplied by 0 for queries that the causal mask hides them
@@ -556,8 +560,8 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * A table value of -2^40 or less counts as -infinity, and so does one that
  * leaves binary32 when divided by the scale or multiplied by log2 e: its keys
  * have no weight.  Other large values are scores like any: a row whose seen
- * keys all carry one has the weights that it has without it, but for an error
- * of up to 2^-22 of the value in what the scores are rounded at.
+ * keys all carry one has the weights that it has without it, its scores rounded
+ * as if they were larger by 2^-22 of the value.
  *
  * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
  * heads; D a multiple of 8, 8 ... 128, its elements side by side, 16-byte

@@ -9,7 +9,8 @@ import torch
 def rel_bucket_map(n_buckets: int, max_distance: int, two_sided: bool,
                    device=None) -> torch.Tensor:
     """Bucket of each distance -max_distance ... max_distance (key position
-    minus query position), int32, as the bias calls take it.
+    minus query position), int32, as the bias calls take it: they take maps of
+    max_distance up to 1024.
 
     Two-sided, the upper half of the buckets serves the keys after the query;
     one-sided, those share bucket 0 with the query's own position.  On a side

@@ -180,7 +180,9 @@ __device__ __forceinline__ typename Mma<T>::x8 col_frag(const char* tile, int ro
 // Order of the LDS reads and matrix instructions of a block: AHEAD reads first,
 // then after each matrix instruction the reads of a later one.  Left alone they
 // come one or two instructions before their use, and a wave that has its SIMD
-// to itself waits out the LDS latency at every one.
+// to itself waits out the LDS latency at every one.  The compiler follows it
+// for the row reads and, in the key pass for heads of 128, for the transposing
+// ones; with heads of 64 those products still wait for their own two reads.
 template <int READS_PER_MMA, int MMAS, int AHEAD>
 __device__ __forceinline__ void read_ahead() {
     constexpr int kRead = 0x100, kMma = 0x8;
@@ -309,7 +311,8 @@ enum WorkOrder {
     kFalling,    // one workgroup a CU at a time: who is done takes the next size
     kFallingTwo  // two or more at a time: every second 32 (an XCD's CUs) in
                  // reverse, so that a large one has a small one beside it (a
-                 // prompt of 4093 tokens and 16 heads: 162 -> 123 us)
+                 // prompt of 4093 tokens and 16 heads: 99 us, kFalling 101,
+                 // kEven 124)
 };
 // False for a number past the work.
 __device__ __forceinline__ bool xcd_work(uint32_t groups, uint32_t per_group, WorkOrder order,

@@ -6,13 +6,12 @@
 // a sequence are split over workgroups and over their waves; a wave goes
 // through its part alone, 32 keys at a time, without barriers: whole rows come
 // in, through LDS of its own they become operands, the next 32 on their way
-// while these are used.  The waves of a workgroup are
-// joined in LDS, the workgroups by attn_join.
+// while these are used.  The waves of a workgroup are joined in LDS, the
+// workgroups by attn_join.
 //
 // Bound by memory: 32 sequences of 8192 keys, 4 key heads of 128 and 16 query
-// heads take 94 us without a bias (5.7 TB/s) and 97 with one, of 2048 ... 8192
-// keys 68 and 70 us (4.9 and 4.8 TB/s; the short sequences' workgroups end
-// first).  Loads past the caches, as each key is read once (113 and 79 us with a
+// heads take 93 us without a bias (5.8 TB/s) and 97 with one, of 2048 ... 8192
+// keys 71 us with one (4.7 TB/s; the short sequences' workgroups end first).  Loads past the caches, as each key is read once (113 and 79 us with a
 // bias through them).  One token of one sequence over 16384 keys takes 22 us,
 // most of it the latencies of two launches.
 #include <type_traits>

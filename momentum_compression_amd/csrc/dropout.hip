@@ -10,9 +10,10 @@
 // one 16-byte load and store.  Of binary32 a pair of lanes takes the 8 columns
 // of two groups, each one half of both, so that an access of the wave is still
 // one run; each draws for one group and they exchange half of their draws
-// (16411 x 4099: 79 us, 6.8 TB/s; with 8 columns a lane 93 us).  Measured with a
-// residual, bf16: 8192 x 1024 7.7 us, 65536 x 4096 259 us (6.2 TB/s); two groups
-// a lane took 7.3 and 278.
+// (16411 x 4099, three tensors in turn: 92 us, 5.8 TB/s; the same tensor over and
+// over, part of which stays in the last cache, 79, with 8 columns a lane 93).
+// With a residual, bf16, the same tensors over and over: 8192 x 1024 7.7 us (9.1
+// in turn), 65536 x 4096 259 us (6.2 TB/s); two groups a lane took 7.3 and 278.
 #include "philox.h"
 #include "train.h"
 
