@@ -561,7 +561,8 @@ size_t rel_bias_workspace_bytes(int32_t B, int32_t H, int32_t Tq, int32_t Tk, in
  * leaves binary32 when divided by the scale or multiplied by log2 e: its keys
  * have no weight.  Other large values are scores like any: a row whose seen
  * keys all carry one has the weights that it has without it, its scores rounded
- * as if they were larger by 2^-22 of the value.
+ * as if they were larger by 2^-22 of the value.  Scores count up to 2^40 in
+ * magnitude.
  *
  * q, o, d_o, dq: Tq tokens of H heads of D; k, v, dk, dv: Tk tokens of Hkv
  * heads; D a multiple of 8, 8 ... 128, its elements side by side, 16-byte

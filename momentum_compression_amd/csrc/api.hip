@@ -532,8 +532,8 @@ bool rows_cross(const void* y, int64_t ld_y, const void* p, int64_t ld_p, int64_
     const uintptr_t a = reinterpret_cast<uintptr_t>(y), b = reinterpret_cast<uintptr_t>(p);
     const uint64_t apart = a < b ? b - a : a - b;  // bytes
     const uint64_t pitch = (uint64_t)ld_y * size, width = (uint64_t)cols * size;
-    if (apart >= pitch * (uint64_t)(rows - 1) + width) return false;
-    return apart % pitch < width || pitch - apart % pitch < width;
+    const uint64_t down = apart / pitch, right = apart % pitch, last = (uint64_t)rows - 1;
+    return (down <= last && right < width) || (down < last && pitch - right < width);
 }
 
 int check_lengths(int32_t Tq, int32_t Tk) {

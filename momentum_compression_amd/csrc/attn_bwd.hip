@@ -240,7 +240,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_
     uint32_t k0 = a.drop.k0, k1 = a.drop.k1;
     asm volatile("" : "+s"(k0), "+s"(k1));
     const float base = again ? large_base(a.lse[i < a.Tq ? row : 0], a.scale) : 0.0f;
-    float m = -0x1p12f, l = 0.0f, norm = 0.0f;
+    float m = -INFINITY, l = 0.0f, norm = 0.0f;
     delta = sum = 0.0f;
     const auto sweep = [&](auto which) __attribute__((always_inline)) {
         constexpr int pass = decltype(which)::value;
@@ -280,10 +280,11 @@ __global__ __launch_bounds__(kThreads, DP == 64 && !SHORT ? 3 : 2) void attn_dq_
                         mx = fmaxf(mx, s[r]);
                     }
                     const float m_new = fmaxf(m, fmaxf(mx, other_half(mx)));
-                    l *= __builtin_amdgcn_exp2f(m - m_new);
+                    const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                    l *= __builtin_amdgcn_exp2f(m - m_use);
                     m = m_new;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) l += __builtin_amdgcn_exp2f(s[r] - m);
+                    for (int r = 0; r < 16; ++r) l += __builtin_amdgcn_exp2f(s[r] - m_use);
                     continue;
                 }
 #pragma unroll

@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     // once more: what the products add to scores of that size is lost.
     if (__builtin_expect(__any(is_large(m)), 0)) {
         base = is_large(m) ? m : 0.0f;
-        m = base != 0.0f ? -0x1p12f : -INFINITY;  // above what far lower keys have
+        m = -INFINITY;
         pass(std::true_type());
     }
 

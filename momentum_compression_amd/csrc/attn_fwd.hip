@@ -180,9 +180,9 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
         else write_rows<T, DP>(a, acc, b, h, i, row, 0.0f, m, l, half);
     }
 
-    // Rows of large references once more: the reference is what holds of them.
-    // It becomes the base, and m starts low, but above what far lower keys
-    // have.  32 keys at a time, a tile after the other.
+    // Rows of large references once more: the reference is what holds of them,
+    // and becomes the base.  Scores are rounded before the maximum comes off, so
+    // that no weight passes 1.  32 keys at a time, a tile after the other.
     __shared__ uint32_t waves_large[kWaves];
     if (lane == 0) waves_large[wave] = __any(again);
     __syncthreads();  // the tiles are read, too
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
     uint32_t k0 = a.drop.k0, k1 = a.drop.k1;
     asm volatile("" : "+s"(k0), "+s"(k1));
     const float base = again ? m / scale2 : 0.0f;
-    m = -0x1p12f;
+    m = -INFINITY;
     l = 0.0f;
 #pragma unroll
     for (int d = 0; d < db_n; ++d) acc[d] = f32x16{};

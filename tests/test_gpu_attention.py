@@ -390,7 +390,7 @@ def test_a_row_of_one_key_has_no_score_gradient(dtype, p):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("low", [-1e4, -1e6, -1e9, 1e9])
+@pytest.mark.parametrize("low", [-1e4, -1e6, -1e9, 1e9, 5e11, -1e12])
 def test_rows_of_one_large_bias(low, dtype):
     """A softmax does not change when all its scores do: a head whose table
     holds one large number has the outputs and gradients of a head without a
@@ -474,10 +474,10 @@ def test_large_biases_far_away(low, dtype):
             assert torch.equal(got[n], want[n]), n
 
 
-@pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("far", [3e2, 1e4])
-def test_large_products(far, dtype):
-    """Scores of up to 10^8 and more: each row's weight lies on one key to more
+@pytest.mark.parametrize("dtype,far", [("bf16", 3e2), ("f16", 3e2), ("bf16", 1e4), ("f16", 1e4),
+                                       ("bf16", 1e5)])
+def test_large_products(dtype, far):
+    """Scores of up to 10^10 and more: each row's weight lies on one key to more
     than binary32 shows (its margin is checked), so o is that key's value, dv
     takes the rows' gradients whole, and no score has a gradient but for the
     rounding of delta."""
@@ -509,8 +509,12 @@ def test_large_products(far, dtype):
         err = (got["dv"][0, :, 0].double() - dv).abs()
         assert bool((err <= half_step(dtype) * dv.abs() + 2 * Tq * e * size_dv).all())
         # dP is known to (D + 2) e of its terms, and delta adds one of a few
-        # roundings more: dS = dP - delta of that key alone
-        ds = ((D + 8) * e * (do64.abs() @ v64.abs().transpose(1, 2)).amax(2)) * 4
+        # roundings more: dS = dP - delta of that key alone.  The row's normaliser
+        # lies above a base that lse gives: as far as the scores are off, times
+        # log2 e, and lse is rounded; it is rounded itself, e of that in the
+        # weight, which delta takes times the distance of two dP
+        high = 1.5 * (off + 4 * e * lse.abs()) + 30
+        ds = (4 * (D + 8) + 2 * high) * e * (do64.abs() @ v64.abs().transpose(1, 2)).amax(2)
         dq = got["dq"][0].double().transpose(0, 1)
         bound = D ** -0.5 * ds[..., None] * k64.abs().amax((1, 2))
         assert bool((dq.abs() <= bound + _tiny(dtype)).all())

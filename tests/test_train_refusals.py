@@ -60,8 +60,12 @@ def test_dropout_refuses_rows_over_rows(lib):
         assert call(y, ly) == ob.ONEBIT_E_ARG, (y - P, ly)
         assert call(y, ly, x=4 * P, r=P) == ob.ONEBIT_E_ARG, (y - P, ly)
     for y, ly in ((P, 32), (P + 4 * 10, 32), (P + 4 * 22, 32), (P - 4 * 10, 32), (P + 4 * 106, 32),
-                  (P - 4 * 106, 32)):
+                  (P - 4 * 106, 32), (P + 4 * (96 + 23), 32), (P - 4 * 128, 32)):
         assert call(y, ly) == ob.ONEBIT_E_ALIGN, (y - P, ly)
+    # strides and rows whose product passes 64 bits
+    far = dict(lx=1 << 40, ly=1 << 40, rows=1 << 29)
+    assert call(P + 4 * 9, **far) == call(P + 4 * ((1 << 40) - 9), **far) == ob.ONEBIT_E_ARG
+    assert call(P + 4 * 10, **far) == call(P + 4 * ((1 << 40) - 10), **far) == ob.ONEBIT_E_ALIGN
     assert call(P, 40, rows=1) == ob.ONEBIT_E_ALIGN
 
 
