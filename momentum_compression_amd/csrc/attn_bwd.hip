@@ -37,24 +37,23 @@ __device__ __forceinline__ typename Mma<T>::x8 pack_rest(const float* p,
     return r;
 }
 
-// Queries as columns: dq and, for the second pass, delta in binary32.  With any
-// value delta' near it, delta = delta' + sum P (dP - delta') / sum P; the sum of
-// dS comes beside dS, and the sum of P is 1 but for the roundings of lse: 5 times
-// 2^-24 of it, 2^-12 at the largest that rows without a base have, of a correction
-// that is itself 2^-8 of delta (summed and divided by, it took 3 % longer).  dq itself takes delta' = dO . o of the rounded output, which
-// is there before the pass: off by half a step of the element type times the
-// row's output.  That is small beside what dS is rounded by where many keys
-// share the weight, but not where few do, so workgroups with at most kTwice keys
-// make the pass twice, the first time for the sums alone and from the first key's
-// dP: a query that sees one key then has delta = dP to the bit, and dS = 0 in
-// both passes over the scores.  (Over more keys a query whose weight lies on one
-// of them by its scores keeps the half step times that key in dq, where dk and
-// dtable have the exact delta.)  Measured error of dq against 64 bits, in units
-// of the output's own rounding, with one pass and with two: 37 keys 1.51 and
-// 1.41, 256 keys 1.47 and 1.43, fp16 rows of at most 5 keys 2.9 and 1.4; with
-// one pass 512 keys 1.46, 1000 keys 1.44.  Two passes up to 512 keys would take
-// 69 instead of 50 us for 16 sequences of up to 512 keys and 16 heads of 64; one
-// pass always, 46.
+// Queries as columns: dq and, for the second pass, delta in binary32.  With any value
+// delta' near it, delta = delta' + sum P (dP - delta') / sum P; the sum of dS comes
+// beside dS, and the sum of P is 1 but for the roundings of lse: 5 times 2^-24 of it,
+// 2^-12 at the largest that rows without a base have, of a correction that is itself
+// 2^-8 of delta (summed and divided by, it took 3 % longer).  dq itself takes delta' =
+// dO . o of the rounded output, which is there before the pass: off by half a step of
+// the element type times the row's output.  That is small beside what dS is rounded by
+// where many keys share the weight, but not where few do, so workgroups with at most
+// kTwice keys make the pass twice, the first time for the sums alone and from the first
+// key's dP: a query that sees one key then has delta = dP to the bit, and dS = 0 in
+// both passes over the scores.  (Over more keys a query whose weight lies on one of
+// them by its scores keeps the half step times that key in dq, where dk and dtable have
+// the exact delta.)  Measured error of dq against 64 bits, in units of the output's own
+// rounding, with one pass and with two: 37 keys 1.51 and 1.41, 256 keys 1.47 and 1.43,
+// fp16 rows of at most 5 keys 2.9 and 1.4; with one pass 512 keys 1.46, 1000 keys 1.44.
+// Two passes up to 512 keys would take 69 instead of 50 us for 16 sequences of up to
+// 512 keys and 16 heads of 64; one pass always, 46.
 //
 // The kept share's scale is common to all dP: dS here is P (keep dP' - delta')
 // with dP' and delta' before it, and it enters once, with the result's scale.

@@ -9,11 +9,12 @@
 // while these are used.  The waves of a workgroup are joined in LDS, the
 // workgroups by attn_join.
 //
-// Bound by memory: 32 sequences of 8192 keys, 4 key heads of 128 and 16 query
-// heads take 93 us without a bias (5.8 TB/s) and 97 with one, of 2048 ... 8192
-// keys 71 us with one (4.7 TB/s; the short sequences' workgroups end first).  Loads past the caches, as each key is read once (113 and 79 us with a
-// bias through them).  One token of one sequence over 16384 keys takes 22 us,
-// most of it the latencies of two launches.
+// Bound by memory: 32 sequences of 8192 keys, 4 key heads of 128 and 16 query heads
+// take 93 us without a bias (5.8 TB/s) and 97 with one, of 2048 ... 8192 keys 71 us
+// with one (4.7 TB/s; the short sequences' workgroups end first).  Loads past the
+// caches, as each key is read once (113 and 79 us with a bias through them).  One
+// token of one sequence over 16384 keys takes 22 us, most of it the latencies of
+// two launches.
 #include <type_traits>
 
 #include "attention.h"
@@ -195,11 +196,21 @@ __global__ __launch_bounds__(kThreads, 2) void attn_few_kernel(AttnArgs a) {
     pass(std::false_type());
 
     // Large references become the rows' bases, and the wave goes through its keys
-    // once more: what the products add to scores of that size is lost.
+    // once more: what the products add to scores of that size is lost.  (Not
+    // where the wave has keys of a low bias alone, but the row's nearest key has
+    // another: they hardly count then, and their weights are right as they are.)
     if (__builtin_expect(__any(is_large(m)), 0)) {
-        base = is_large(m) ? m : 0.0f;
-        m = -INFINITY;
-        pass(std::true_type());
+        bool far = is_large(m);
+        if (BIAS && m < 0.0f) {
+            const Place q = place(lane);
+            const int32_t at = q.i + pos, last = n_keys - 1;
+            if (!is_large(bias_at(at < 0 ? -at : (at > last ? last - at : 0), q.h))) far = false;
+        }
+        if (__any(far)) {
+            base = far ? m : 0.0f;
+            m = -INFINITY;
+            pass(std::true_type());
+        }
     }
 
     // the waves' references and sums, then their rows, two waves at a time

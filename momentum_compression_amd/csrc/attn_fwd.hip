@@ -174,7 +174,31 @@ __global__ __launch_bounds__(kThreads, DP == 64 ? 4 : 2) void attn_fwd_kernel(At
 
     l += other_half(l);
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
-    const bool again = is_large(m);
+    bool again = is_large(m);
+    if (SPLIT && BIAS && __builtin_expect(__any(again), 0)) {
+        // A split of keys with a low bias alone: the row's nearest key, in some
+        // split, may lie so far above that these have no weight.
+        const int32_t j = i + pos < limit ? (i + pos > 0 ? i + pos : 0) : (limit > 0 ? limit : 0);
+        x8 kf[kc_n];
+        load_frags<T, DP>(kf, kp, a.sk.t, j, true, a.D, lane);
+        float near = 0.0f;
+#pragma unroll
+        for (int kc = 0; kc < kc_n; ++kc)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                near = __builtin_fmaf((float)qf[kc][e], (float)kf[kc][e], near);
+        near += other_half(near);
+        int32_t d = j - i - pos;
+        d = d < -R ? -R : (d > R ? R : d);
+        near = (near + window[d + R + kPad]) * scale2;
+        if (again && near > m + 256.0f) {
+            again = false;
+            m = -INFINITY;
+            if (l == l) l = 0.0f;
+#pragma unroll
+            for (int x = 0; x < db_n; ++x) acc[x] = f32x16{};
+        }
+    }
     if (i < a.Tq && !again) {
         if (SPLIT) write_split<DP>(a, acc, row, split, 0.0f, m, l, half);
         else write_rows<T, DP>(a, acc, b, h, i, row, 0.0f, m, l, half);

@@ -400,20 +400,21 @@ def test_rows_of_one_large_bias(low, dtype):
     and many go through different kernels."""
     dev = device()
     rest = abs(low) * 2.0 ** -22
-    for Tq, Tk, D, p, k_len in ((1, 300, 64, 0.0, None), (3, 2000, 128, 0.2, (1500,)),
-                                (50, 80, 64, 0.2, None), (150, 400, 128, 0.0, (333,)),
-                                (40, 1100, 64, 0.0, None), (130, 64, 80, 0.1, None)):
+    for n, (Tq, Tk, D, p, k_len) in enumerate((
+            (1, 300, 64, 0.0, None), (3, 2000, 128, 0.2, (1500,)), (50, 80, 64, 0.2, None),
+            (150, 400, 128, 0.0, (333,)), (40, 1100, 64, 0.0, None), (130, 64, 80, 0.1, None),
+            (1, 5000, 128, 0.1, None), (200, 300, 64, 0.1, None))):
         g = gen(Tq + D, dev)
         q, k, v = make(dtype, 1, 2, 1, Tq, Tk, D, g, dev)
         do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
         table = torch.randn((32, 2), generator=g, device=dev)
-        how = dict(scale=D ** -0.5, causal=False, q_pos=Tk - Tq, k_len=None,
+        how = dict(scale=D ** -0.5, causal=n % 2 == 1, q_pos=Tk - Tq if n < 7 else 40, k_len=None,
                    bucket_map=rel_bucket_map(32, 40, True, dev), p=p, seed=SEED, step=17)
         if k_len is not None:
             how["k_len"] = torch.tensor(k_len, dtype=torch.int32, device=dev)
-        table[:, 1] = rest
+        table[:, 1] = -rest
         want, tol = _oracle(q, k, v, do, dict(table=table, **how), dtype)
-        want["lse"][:, 1] += low - rest
+        want["lse"][:, 1] += low + rest
         tol["lse"][:, 1] += 4 * 2.0 ** -24 * abs(low)
         table[:, 1] = low
         dtable = torch.full_like(table, 9.0)
@@ -446,6 +447,30 @@ def test_rows_hidden_whole(low, dtype):
         want = _backward(q, k, v, dict(table=table, **how), do, torch.full_like(table, 9))
         for n in want:
             assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Tq", [1, 40, 150])
+def test_low_biases_over_lower_products(Tq, dtype):
+    """Far keys of a low bias hold all the weight where the products with the
+    near keys are lower still."""
+    dev = device()
+    g = gen(Tq, dev)
+    Tk, D = 1500, 64
+    q = torch.full((1, Tq, 2, D), 8.0, device=dev).to(TYPES[dtype])
+    k = torch.randn((1, Tk, 2, D), generator=g, device=dev).to(TYPES[dtype]) / 8
+    v = torch.randn((1, Tk, 2, D), generator=g, device=dev).to(TYPES[dtype])
+    k[:, Tk - Tq - 40:] = -64.0  # scores of -4096
+    do = torch.randn(q.shape, generator=g, device=dev).to(TYPES[dtype])
+    bmap = rel_bucket_map(8, 20, False, dev)
+    table = torch.randn((8, 2), generator=g, device=dev)
+    table[bmap[0]] = -2000.0
+    how = dict(scale=D ** -0.5, causal=True, q_pos=Tk - Tq, k_len=None, table=table,
+               bucket_map=bmap, p=0.1, seed=SEED, step=17)
+    want, tol = _oracle(q, k, v, do, how, dtype)
+    assert float(np.abs(want["lse"] + 2000).max()) < 100
+    got = _backward(q, k, v, how, do, torch.empty_like(table))
+    check(got, want, tol, ("o", "lse", "dq", "dk", "dv", "dtable"), _tiny(dtype))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
