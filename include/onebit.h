@@ -6,8 +6,8 @@
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument is a DEVICE pointer owned by the caller, except
- *   the argument structs of frozen_v_step and rel_attention_* (host memory,
- *   read during the call).
+ *   the argument structs of frozen_v_step, rel_attention_* and linear_* and
+ *   what adamw_plan takes (host memory, read during the call).
  *   The library never allocates, frees or synchronises; it validates
  *   arguments on the host (before any HIP call) and enqueues kernels on
  *   `stream` only.  Results are ready when the stream reaches them.
@@ -615,6 +615,173 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
  * the sizes are invalid. */
 size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t Tq, int32_t Tk,
                                      int32_t D, int32_t radius, int32_t backward);
+
+/*
+ * Layer norm over the rows of a matrix:
+ *   mean_r = sum_c x[r][c] / cols,  v_r = sum_c (x[r][c] - mean_r)^2 / cols
+ *   rstd_r = 1 / sqrt(v_r + eps)
+ *   y[r][c] = (x[r][c] - mean_r) rstd_r weight[c] + bias[c]
+ * in binary32 (the mean corrected by the mean of the deviations from it), y
+ * rounded once to the element type.  weight and bias [cols], both of w_dtype
+ * (ONEBIT_F32 or the element type), may each be NULL (1 and 0).  mean and rstd
+ * [rows] float, each NULL unless wanted: the backward pass reads them.
+ *
+ * x, y: rows of `cols` elements, ld_* elements apart (ld >= cols, up to 2^40),
+ * aligned to their element.  y may be x itself (same ld); where its rows lie over
+ * x's otherwise the call is refused.  cols up to 2^29, eps >= 0 and finite.  No
+ * rows or columns: a no-op.
+ */
+int layer_norm_forward(const void* x, void* y, int32_t dtype, int64_t rows, int64_t cols,
+                       int64_t ld_x, int64_t ld_y, const void* weight, const void* bias,
+                       int32_t w_dtype, float eps, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * The gradients of layer_norm_forward from dy, x and the forward call's mean and
+ * rstd:
+ *   h = (x - mean) rstd,  u = dy weight
+ *   dx = rstd (u - sum_c u / cols - h (sum_c u h) / cols)
+ *   dweight[c] = (accumulate ? dweight[c] : 0) + sum_r dy h
+ *   dbias[c]   = (accumulate ? dbias[c] : 0) + sum_r dy
+ * dx (of the element type), dweight and dbias [cols] float may each be NULL.  dx
+ * may be x or dy itself (same ld).  The sums over rows are binary32 within a
+ * workgroup and binary64 over workgroups, in an order fixed by the sizes.  With
+ * no rows they are 0.
+ * ws: at least layer_norm_workspace_bytes(rows, cols) bytes, 256-byte aligned,
+ * scratch; not needed (NULL, 0) without dweight and dbias.
+ */
+int layer_norm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                        void* dx, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_dy,
+                        int64_t ld_x, int64_t ld_dx, const void* weight, int32_t w_dtype,
+                        float* dweight, float* dbias, int32_t accumulate, void* ws,
+                        size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of layer_norm_backward (0 if the sizes are invalid). */
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * A linear layer with bias, activation and residual, forward and backward, for
+ * one row to whole batches:
+ *   z[m][n] = sum_k x[m][k] w[n][k] + bias[n]
+ *   pre = z,  y = act(z) + residual
+ * with act one of
+ */
+typedef enum {
+    ONEBIT_NONE = 0,       /* z                                               */
+    ONEBIT_RELU = 1,       /* max(z, 0), slope 0 at 0                         */
+    ONEBIT_GELU = 2,       /* z Phi(z), Phi the normal distribution's integral
+                              (to 1e-7)                                       */
+    ONEBIT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    ONEBIT_SILU = 4        /* z / (1 + exp(-z))                               */
+} onebit_activation;
+/*
+ * Elements are BF16 or F16.  Products are summed in binary32, in an order fixed
+ * by the sizes; bias, activation and residual follow in binary32, and y and pre
+ * are rounded once.  bias [N] of bias_dtype (ONEBIT_F32 or the element type),
+ * residual and pre are optional (NULL).
+ *
+ * backward, with dz = dy act'(pre):
+ *   dx[m][k] = sum_n dz[m][n] w[n][k]
+ *   dw[n][k] = (accumulate ? dw[n][k] : 0) + sum_m dz[m][n] x[m][k]
+ *   dbias[n] = (accumulate ? dbias[n] : 0) + sum_m dz[m][n]
+ * The residual's gradient is dy.  dx, dw and dbias may each be NULL.  dw is of
+ * dw_dtype (ONEBIT_F32 or the element type), dbias float.  With an activation, dz
+ * is rounded to the element type for the two products (dbias takes it unrounded):
+ * as much error as the rounding of a 16-bit dx or dw.  pre is read with an
+ * activation only.
+ *
+ * x, dx [M][K], w, dw [N][K], y, pre, residual, dy [M][N]: rows ld_* elements
+ * apart (ld >= the row's length, up to 2^40), aligned to their element.  M up to
+ * 2^31 - 1, N and K up to 2^22, ceil(max(M, N) / 128) ceil(max(N, K) / 128) up to
+ * 2^22.  Rows that start and end on 16 bytes (address, length and ld) are read as
+ * they are; other operands are laid out anew in the workspace first.  y may be
+ * residual itself (same ld); where an output's rows lie over those of another
+ * argument otherwise, as far as strides show, the call is refused.  With K = 0 z
+ * is the bias; with M or N = 0 sums over nothing are 0.
+ * ws: at least linear_workspace_bytes(...) bytes, 256-byte aligned, scratch.
+ */
+typedef struct linear_args {
+    int32_t dtype, activation;
+    int64_t M, N, K;
+    const void *x, *w;
+    int64_t ld_x, ld_w;
+    const void* bias;          /* forward; or NULL                              */
+    const void* residual;      /* forward; or NULL                              */
+    void* pre;                 /* out of the forward pass, read by the backward */
+    void* y;
+    int64_t ld_residual, ld_pre, ld_y;
+    int32_t bias_dtype;
+    int32_t dw_dtype;          /* from here on: backward pass only              */
+    const void* dy;
+    void *dx, *dw;
+    float* dbias;
+    int64_t ld_dy, ld_dx, ld_dw;
+    int32_t accumulate;
+} linear_args;
+
+int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream);
+
+int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of linear_forward (backward 0) or linear_backward (1), whatever
+ * the layout of the operands.  0 if the sizes are invalid. */
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward);
+
+/*
+ * AdamW over many tensors in one launch.  For tensor i and element J, with t =
+ * step and every operation rounded once to binary32 (bc1 = 1 / (1 - beta1^t) and
+ * bc2 = 1 / sqrt(1 - beta2^t) once from binary64):
+ *   g  = g_scale ? *g_scale g : g
+ *   m  = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) (g g)
+ *   l  = lr lr_scale_i
+ *   x  = x (1 - l weight_decay_i) - (l bc1) (m / (sqrt(v) bc2 + eps))
+ *   copy = x                                  (rounded to copy_dtype)
+ * states in 32 bits: m and v float.
+ * states in 8 bits: each 256 consecutive elements of a tensor (the last ones may
+ * be fewer) have a scale, a power of two, and m = scale times an e4m3 number
+ * (sign, 4 bits of exponent, 3 of mantissa; bias 7), v = scale times an e5m2
+ * number (bias 15).  The step computes m, v and x from those values as above; then
+ * the scale becomes the power of two that puts the block's largest finite
+ * magnitude into [2^7, 2^8) for m and [2^14, 2^15) for v (2^-126 at least), and the
+ * value over it is cut off to the format after adding
+ *   (u + 1/2) / 65536 of the format's step,  u = half word J & 7 (low half of a
+ *   word first) of Philox4x32-10(counter = (J / 8, i, 0, t), key = (seed lo32,
+ *   seed hi32 xor 0x41444D57)),
+ * so that its mean over the draws is the value (below the format's normal numbers
+ * it counts to 2^-20 of a step).  A v above 0 gets the smallest
+ * number above 0 at least; what is not finite becomes NaN.  Zero codes and any
+ * scale are a fresh state.
+ *
+ * The tensors are given once, in a plan: adamw_plan writes it to host memory, and
+ * the caller copies its bytes to the device (256-byte aligned) and keeps them
+ * there.  Every tensor's buffers are aligned to their element; what the step
+ * writes must not overlap anything else it reads or writes (such lists are
+ * refused).  g is of g_dtype; copy of copy_dtype (BF16 or F16; ONEBIT_F32: no
+ * copies).  n up to 2^34 elements a tensor, weight_decay and lr_scale finite.
+ */
+typedef struct adamw_tensor {
+    float* x;
+    const void* g;
+    void* copy;
+    void *m, *v;                /* float, or 8-bit codes                        */
+    float *m_scale, *v_scale;   /* [ceil(n / 256)] with 8-bit states            */
+    int64_t n;
+    float lr_scale, weight_decay;
+} adamw_tensor;
+
+/* Bytes of the plan and, where `tiles` is not NULL, the step's workgroups; 0 if
+ * n_tensors < 0 or a size is invalid. */
+size_t adamw_plan_bytes(const adamw_tensor* tensors, int32_t n_tensors, int64_t* tiles);
+
+/* tensors and plan are HOST memory; no HIP call is made. */
+int adamw_plan(const adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
+               int32_t g_dtype, int32_t copy_dtype, void* plan, size_t plan_bytes);
+
+/* One step.  plan: the device copy; n_tensors, tiles and the types as the plan was
+ * made with.  1 <= step, 0 <= beta < 1, eps >= 0, lr finite.  g_scale: device
+ * float or NULL.  A captured call replays its own step number and lr. */
+int adamw_step(const void* plan, int32_t n_tensors, int64_t tiles, int32_t state_bits,
+               int32_t g_dtype, int32_t copy_dtype, float lr, float beta1, float beta2, float eps,
+               uint32_t step, uint64_t seed, const float* g_scale, hipStream_t stream);
 
 /* Static description of a status code. */
 const char* onebit_strerror(int status);

@@ -34,4 +34,12 @@ from .onebit import (  # noqa: F401
     rel_attention_backward,
     rel_attention_forward,
     rel_attention_workspace_bytes,
+    layer_norm_backward,
+    layer_norm_forward,
+    layer_norm_workspace_bytes,
+    linear_backward,
+    linear_forward,
+    linear_workspace_bytes,
+    AdamWPlan,
+    adamw_step,
 )

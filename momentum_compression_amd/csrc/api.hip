@@ -2,9 +2,12 @@
 // Every check runs before the first HIP call, so invalid calls touch nothing.
 #include <math.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <mutex>
+#include <new>
 #include <utility>
+#include <vector>
 
 #include "attention.h"
 #include "common.h"
@@ -834,6 +837,501 @@ int rel_attention_backward(const rel_attention_args* a, void* ws, size_t ws_byte
     k.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + z.delta);
     drop_stale_error();
     return hip_status(launch_attn_backward(k, a->dtype, a->dtable, a->accumulate != 0, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- layer norm
+
+namespace {
+
+constexpr int64_t kMaxNormCols = (int64_t)1 << 29;
+constexpr int64_t kMaxRows = (int64_t)1 << 40;
+
+int check_norm(int32_t dtype, int32_t w_dtype, int64_t rows, int64_t cols) {
+    if (!type_size(dtype) || (w_dtype != dtype && w_dtype != ONEBIT_F32)) return ONEBIT_E_ARG;
+    if (rows < 0 || rows > kMaxRows || cols < 0 || cols > kMaxNormCols) return ONEBIT_E_SIZE;
+    return ONEBIT_OK;
+}
+
+bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
+
+}  // namespace
+
+extern "C" {
+
+int layer_norm_forward(const void* x, void* y, int32_t dtype, int64_t rows, int64_t cols,
+                       int64_t ld_x, int64_t ld_y, const void* weight, const void* bias,
+                       int32_t w_dtype, float eps, float* mean, float* rstd, hipStream_t stream) {
+    const int st = check_norm(dtype, w_dtype, rows, cols);
+    if (st) return st;
+    if (!(eps >= 0.0f && eps < INFINITY)) return ONEBIT_E_ARG;
+    if (rows == 0 || cols == 0) return ONEBIT_OK;
+    if (!x || !y) return ONEBIT_E_NULL;
+    if (!ld_ok(ld_x, cols) || !ld_ok(ld_y, cols)) return ONEBIT_E_SIZE;
+    const size_t size = type_size(dtype), w_size = type_size(w_dtype);
+    if (!aligned(x, size) || !aligned(y, size) || !aligned(weight, w_size) ||
+        !aligned(bias, w_size) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return ONEBIT_E_ALIGN;
+    if (rows_cross(y, ld_y, x, ld_x, rows, cols, size) || y == weight || y == bias ||
+        (mean && (mean == rstd || mean == x || mean == y)) || (rstd && (rstd == x || rstd == y)))
+        return ONEBIT_E_ARG;
+    NormArgs a = {};
+    a.x = x;
+    a.y = y;
+    a.weight = weight;
+    a.bias = bias;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_x = ld_x;
+    a.ld_y = ld_y;
+    a.eps = eps;
+    a.dtype = dtype;
+    a.w_wide = w_dtype == ONEBIT_F32;
+    drop_stale_error();
+    return hip_status(launch_layer_norm(a, stream));
+}
+
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (check_norm(ONEBIT_F32, ONEBIT_F32, rows, cols)) return 0;
+    const size_t need = round_up((size_t)norm_parts(rows, cols) * 2 * cols * sizeof(float));
+    return need ? need : 256;
+}
+
+int layer_norm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                        void* dx, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_dy,
+                        int64_t ld_x, int64_t ld_dx, const void* weight, int32_t w_dtype,
+                        float* dweight, float* dbias, int32_t accumulate, void* ws,
+                        size_t ws_bytes, hipStream_t stream) {
+    const int st = check_norm(dtype, w_dtype, rows, cols);
+    if (st) return st;
+    if (accumulate != 0 && accumulate != 1) return ONEBIT_E_ARG;
+    if (cols == 0) return ONEBIT_OK;
+    const bool sums = dweight || dbias;
+    const size_t size = type_size(dtype);
+    if (rows > 0) {
+        if (!dy || !x || !mean || !rstd) return ONEBIT_E_NULL;
+        if (!ld_ok(ld_dy, cols) || !ld_ok(ld_x, cols) || (dx && !ld_ok(ld_dx, cols)))
+            return ONEBIT_E_SIZE;
+    }
+    if (!aligned(dy, size) || !aligned(x, size) || !aligned(dx, size) ||
+        !aligned(weight, type_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+        !aligned(dweight, 4) || !aligned(dbias, 4))
+        return ONEBIT_E_ALIGN;
+    if (rows > 0 && dx &&
+        (rows_cross(dx, ld_dx, x, ld_x, rows, cols, size) ||
+         rows_cross(dx, ld_dx, dy, ld_dy, rows, cols, size) || dx == weight || dx == mean ||
+         dx == rstd || dx == dweight || dx == dbias))
+        return ONEBIT_E_ARG;
+    for (const void* out : {(const void*)dweight, (const void*)dbias})
+        if (out && (out == x || out == dy || out == weight || out == mean || out == rstd))
+            return ONEBIT_E_ARG;
+    if (dweight && dweight == dbias) return ONEBIT_E_ARG;
+    if (sums) {
+        if (!ws || ws_bytes < layer_norm_workspace_bytes(rows, cols)) return ONEBIT_E_WORKSPACE;
+        if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    }
+    if (!sums && (rows == 0 || !dx)) return ONEBIT_OK;
+    NormArgs a = {};
+    a.x = x;
+    a.dy = dy;
+    a.dx = dx;
+    a.weight = weight;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.partials = sums ? static_cast<float*>(ws) : nullptr;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_x = ld_x;
+    a.ld_dy = ld_dy;
+    a.ld_dx = ld_dx;
+    a.dtype = dtype;
+    a.w_wide = w_dtype == ONEBIT_F32;
+    drop_stale_error();
+    return hip_status(launch_layer_norm_grad(a, dweight, dbias, accumulate != 0, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- linear layer
+
+namespace {
+
+constexpr int64_t kMaxFeatures = (int64_t)1 << 22;  // a tile's rows within 2^31 bytes
+
+int check_linear_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > kMaxFeatures || K > kMaxFeatures)
+        return ONEBIT_E_SIZE;
+    // tiles of a launch (their threads counted in 32 bits), also of dw [N][K]
+    const int64_t rows = M > N ? M : N, cols = N > K ? N : K;
+    if (ceil_div(rows, 128) * ceil_div(cols, 128) > ((int64_t)1 << 22)) return ONEBIT_E_SIZE;
+    return ONEBIT_OK;
+}
+
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Rows that start and end on 16 bytes, in a buffer whose tiles 32 bits address.
+bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    return aligned(p, 16) && cols % 8 == 0 && ((ld % 8 == 0 && ld <= kMaxFeatures) || rows <= 1);
+}
+
+// Workspace in the order it is carved: operands laid out anew, dz, the partial
+// sums of dbias, the parts of a divided product.
+struct LinearSizes {
+    size_t x, w, dz, sums, parts;
+    size_t all() const { return x + w + dz + sums + parts; }
+};
+
+LinearSizes linear_sizes(int64_t M, int64_t N, int64_t K, bool backward) {
+    LinearSizes z = {};
+    z.x = round_up((size_t)M * padded(K) * 2);
+    z.w = round_up((size_t)N * padded(K) * 2);
+    if (!backward) {
+        z.parts = round_up(product_plan(M, N, K).bytes);
+        return z;
+    }
+    z.dz = round_up((size_t)M * padded(N) * 2);
+    z.sums = round_up((size_t)slope_parts(M, N) * N * sizeof(float));
+    const size_t dx = product_plan(M, K, N).bytes, dw = product_plan(N, K, M).bytes;
+    z.parts = round_up(dx > dw ? dx : dw);
+    return z;
+}
+
+int check_linear(const linear_args* a) {
+    if (!a) return ONEBIT_E_NULL;
+    if (a->dtype != ONEBIT_BF16 && a->dtype != ONEBIT_F16) return ONEBIT_E_ARG;
+    if (a->activation < ONEBIT_NONE || a->activation > ONEBIT_SILU) return ONEBIT_E_ARG;
+    return check_linear_sizes(a->M, a->N, a->K);
+}
+
+// A matrix argument: NULL where nothing is read or written of it.
+int check_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t size) {
+    if (rows == 0 || cols == 0) return ONEBIT_OK;
+    if (!p) return ONEBIT_E_NULL;
+    if (!ld_ok(ld, cols)) return ONEBIT_E_SIZE;
+    return aligned(p, size) ? ONEBIT_OK : ONEBIT_E_ALIGN;
+}
+
+struct Matrix {
+    const void* p;
+    int64_t ld, rows, cols;
+    size_t size;
+};
+
+// An output's rows over another matrix's, as far as strides show: from one address
+// on, of one stride in bytes, or starting inside a matrix without gaps.
+bool lies_over(const Matrix& out, const Matrix& in) {
+    if (!out.p || !in.p || out.rows == 0 || out.cols == 0 || in.rows == 0 || in.cols == 0)
+        return false;
+    const bool after = (uintptr_t)out.p > (uintptr_t)in.p;
+    const Matrix& first = after ? in : out;
+    const Matrix& second = after ? out : in;
+    const uint64_t apart = (uintptr_t)second.p - (uintptr_t)first.p;
+    if (apart == 0) return true;
+    const uint64_t width = (uint64_t)first.cols * first.size;
+    const uint64_t pitch = (uint64_t)first.ld * first.size;
+    if (first.rows == 1 || first.ld == first.cols) return apart < width * (uint64_t)first.rows;
+    if (pitch != (uint64_t)second.ld * second.size && second.rows > 1) return false;
+    const uint64_t down = apart / pitch, right = apart % pitch;
+    return (down < (uint64_t)first.rows && right < width) ||
+           (down + 1 < (uint64_t)first.rows && pitch - right < (uint64_t)second.cols * second.size);
+}
+
+// The operand as the product reads it, laid out anew at `room` if need be.
+hipError_t operand(ProductIn& in, const void* p, int64_t ld, int64_t rows, int64_t cols, char* room,
+                   hipStream_t st) {
+    if (rows == 0 || cols == 0 || whole_chunks(p, ld, rows, cols)) {
+        in = ProductIn{p, rows <= 1 ? padded(cols) : ld};
+        return hipSuccess;
+    }
+    in = ProductIn{room, padded(cols)};
+    return launch_pad_rows(p, ld, room, padded(cols), rows, cols, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward) {
+    if (check_linear_sizes(M, N, K)) return 0;
+    const size_t need = linear_sizes(M, N, K, backward != 0).all();
+    return need ? need : 256;
+}
+
+int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_linear(a);
+    if (st) return st;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    if (M == 0 || N == 0) return ONEBIT_OK;
+    if (a->bias && a->bias_dtype != ONEBIT_F32 && a->bias_dtype != a->dtype) return ONEBIT_E_ARG;
+    if ((st = check_matrix(a->x, a->ld_x, M, K, 2)) || (st = check_matrix(a->w, a->ld_w, N, K, 2)) ||
+        (st = check_matrix(a->y, a->ld_y, M, N, 2)) ||
+        (a->pre && (st = check_matrix(a->pre, a->ld_pre, M, N, 2))) ||
+        (a->residual && (st = check_matrix(a->residual, a->ld_residual, M, N, 2))))
+        return st;
+    if (a->bias && !aligned(a->bias, type_size(a->bias_dtype))) return ONEBIT_E_ALIGN;
+    const Matrix x{a->x, a->ld_x, M, K, 2}, w{a->w, a->ld_w, N, K, 2}, y{a->y, a->ld_y, M, N, 2},
+        pre{a->pre, a->ld_pre, M, N, 2}, r{a->residual, a->ld_residual, M, N, 2},
+        b{a->bias, N, 1, N, a->bias ? type_size(a->bias_dtype) : 2};
+    const bool in_place = a->residual && a->y == a->residual && a->ld_y == a->ld_residual;
+    for (const Matrix& in : {x, w, b})
+        if (lies_over(y, in) || lies_over(pre, in)) return ONEBIT_E_ARG;
+    if (lies_over(y, pre) || lies_over(pre, r) || (!in_place && lies_over(y, r)))
+        return ONEBIT_E_ARG;
+    if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 0)) return ONEBIT_E_WORKSPACE;
+    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    const LinearSizes z = linear_sizes(M, N, K, false);
+    char* room = static_cast<char*>(ws);
+    drop_stale_error();
+    ProductIn xs, wi;
+    hipError_t e = operand(xs, a->x, a->ld_x, M, K, room, stream);
+    if (e == hipSuccess) e = operand(wi, a->w, a->ld_w, N, K, room + z.x, stream);
+    if (e != hipSuccess) return ONEBIT_E_HIP;
+    ProductOut o = {};
+    o.out = a->y;
+    o.bias = a->bias;
+    o.residual = a->residual;
+    o.pre = a->pre;
+    o.rows = M;
+    o.cols = N;
+    o.ld = a->ld_y;
+    o.ld_r = a->ld_residual;
+    o.ld_pre = a->ld_pre;
+    o.type = a->dtype;
+    o.act = a->activation;
+    o.bias_wide = a->bias_dtype == ONEBIT_F32;
+    return hip_status(launch_product(a->dtype, wi, true, xs, true, K, o,
+                                     reinterpret_cast<float*>(room + z.x + z.w), stream));
+}
+
+int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+    int st = check_linear(a);
+    if (st) return st;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    if (a->accumulate != 0 && a->accumulate != 1) return ONEBIT_E_ARG;
+    if (a->dw && a->dw_dtype != ONEBIT_F32 && a->dw_dtype != a->dtype) return ONEBIT_E_ARG;
+    const size_t dw_size = a->dw ? type_size(a->dw_dtype) : 2;
+    const bool act = a->activation != ONEBIT_NONE;
+    if ((st = check_matrix(a->dy, a->ld_dy, M, N, 2)) ||
+        (act && (st = check_matrix(a->pre, a->ld_pre, M, N, 2))) ||
+        (a->dw && ((st = check_matrix(a->x, a->ld_x, M, K, 2)) ||
+                   (st = check_matrix(a->dw, a->ld_dw, N, K, dw_size)))) ||
+        (a->dx && ((st = check_matrix(a->w, a->ld_w, N, K, 2)) ||
+                   (st = check_matrix(a->dx, a->ld_dx, M, K, 2)))))
+        return st;
+    if (!aligned(a->dbias, 4)) return ONEBIT_E_ALIGN;
+    const Matrix dy{a->dy, a->ld_dy, M, N, 2}, pre{act ? a->pre : nullptr, a->ld_pre, M, N, 2},
+        x{a->x, a->ld_x, M, K, 2}, w{a->w, a->ld_w, N, K, 2}, dx{a->dx, a->ld_dx, M, K, 2},
+        dw{a->dw, a->ld_dw, N, K, dw_size}, db{a->dbias, N, 1, N, 4};
+    for (const Matrix& in : {dy, pre, x, w})
+        if (lies_over(dx, in) || lies_over(dw, in) || lies_over(db, in)) return ONEBIT_E_ARG;
+    if (lies_over(dx, dw) || lies_over(dx, db) || lies_over(dw, db)) return ONEBIT_E_ARG;
+    if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 1)) return ONEBIT_E_WORKSPACE;
+    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    const LinearSizes z = linear_sizes(M, N, K, true);
+    char* x_room = static_cast<char*>(ws);
+    char* w_room = x_room + z.x;
+    char* dz_room = w_room + z.w;
+    float* sums = reinterpret_cast<float*>(dz_room + z.dz);
+    float* parts = reinterpret_cast<float*>(dz_room + z.dz + z.sums);
+    drop_stale_error();
+    hipError_t e = hipSuccess;
+    ProductIn dz{a->dy, M <= 1 ? padded(N) : a->ld_dy};
+    const bool products = a->dx || a->dw;
+    const bool anew = products && (act || !whole_chunks(a->dy, a->ld_dy, M, N));
+    if (N > 0) {
+        if (M > 0 && (anew || a->dbias)) {
+            SlopeArgs s = {};
+            s.dy = a->dy;
+            s.pre = a->pre;
+            s.dz = anew ? dz_room : nullptr;
+            s.partials = a->dbias ? sums : nullptr;
+            s.rows = M;
+            s.cols = N;
+            s.ld_dy = a->ld_dy;
+            s.ld_pre = a->ld_pre;
+            s.padded = padded(N);
+            s.act = a->activation;
+            s.dtype = a->dtype;
+            e = launch_slope(s, stream);
+            if (anew) dz = ProductIn{dz_room, padded(N)};
+        }
+        if (e == hipSuccess && a->dbias)
+            e = launch_column_join(sums, M > 0 ? slope_parts(M, N) : 0, N, N, a->dbias, nullptr,
+                                   a->accumulate != 0, stream);
+    }
+    if (e == hipSuccess && a->dx && M > 0 && K > 0) {
+        ProductIn wi;
+        e = operand(wi, a->w, a->ld_w, N, K, w_room, stream);
+        ProductOut o = {};
+        o.out = a->dx;
+        o.rows = M;
+        o.cols = K;
+        o.ld = a->ld_dx;
+        o.type = a->dtype;
+        if (e == hipSuccess) e = launch_product(a->dtype, wi, false, dz, true, N, o, parts, stream);
+    }
+    if (e == hipSuccess && a->dw && N > 0 && K > 0) {
+        ProductIn xs;
+        e = operand(xs, a->x, a->ld_x, M, K, x_room, stream);
+        ProductOut o = {};
+        o.out = a->dw;
+        o.rows = N;
+        o.cols = K;
+        o.ld = a->ld_dw;
+        o.type = a->dw_dtype;
+        o.accumulate = a->accumulate != 0;
+        if (e == hipSuccess)
+            e = launch_product(a->dtype, xs, false, dz, false, M, o, parts, stream);
+    }
+    return hip_status(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- AdamW
+
+namespace {
+
+constexpr int64_t kMaxTensor = (int64_t)1 << 34;
+
+size_t plan_tensors_bytes(int32_t n_tensors) {
+    return round_up((size_t)n_tensors * sizeof(AdamWTensor));
+}
+
+struct Range {
+    uintptr_t begin, end;
+    bool written;
+};
+
+void add_range(std::vector<Range>& all, const void* p, int64_t bytes, bool written) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (bytes > 0) all.push_back(Range{at, at + (uintptr_t)bytes, written});
+}
+
+// Whether something written lies over another range.
+bool overlapping(std::vector<Range>& all) {
+    std::sort(all.begin(), all.end(),
+              [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    uintptr_t end = 0, written_end = 0;  // of the ranges before
+    for (const Range& r : all) {
+        if (r.begin < written_end || (r.written && r.begin < end)) return true;
+        if (r.end > end) end = r.end;
+        if (r.written && r.end > written_end) written_end = r.end;
+    }
+    return false;
+}
+
+int check_adamw_types(int32_t state_bits, int32_t g_dtype, int32_t copy_dtype) {
+    return (state_bits != 8 && state_bits != 32) || !type_size(g_dtype) || !type_size(copy_dtype)
+               ? ONEBIT_E_ARG
+               : ONEBIT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t adamw_plan_bytes(const adamw_tensor* tensors, int32_t n_tensors, int64_t* tiles) {
+    if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return 0;
+    int64_t all = 0;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        if (tensors[i].n < 0 || tensors[i].n > kMaxTensor) return 0;
+        all += ceil_div(tensors[i].n, kAdamWTile);
+        if (!groups_ok(all)) return 0;
+    }
+    if (tiles) *tiles = all;
+    const size_t need = plan_tensors_bytes(n_tensors) + (size_t)all * sizeof(int32_t);
+    return need ? round_up(need) : 256;
+}
+
+int adamw_plan(const adamw_tensor* tensors, int32_t n_tensors, int32_t state_bits,
+               int32_t g_dtype, int32_t copy_dtype, void* plan, size_t plan_bytes) {
+    if (check_adamw_types(state_bits, g_dtype, copy_dtype)) return ONEBIT_E_ARG;
+    if (n_tensors < 0) return ONEBIT_E_SIZE;
+    if ((n_tensors > 0 && !tensors) || !plan) return ONEBIT_E_NULL;
+    const size_t need = adamw_plan_bytes(tensors, n_tensors, nullptr);
+    if (!need) return ONEBIT_E_SIZE;
+    if (plan_bytes < need) return ONEBIT_E_WORKSPACE;
+    if (!aligned(plan, 8)) return ONEBIT_E_ALIGN;
+    const bool eight = state_bits == 8;
+    const size_t g_size = type_size(g_dtype), c_size = type_size(copy_dtype);
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const adamw_tensor& t = tensors[i];
+        if (!isfinite(t.lr_scale) || !isfinite(t.weight_decay)) return ONEBIT_E_ARG;
+        if (t.n == 0) continue;
+        if (!t.x || !t.g || !t.m || !t.v || (c_size == 2 && !t.copy) ||
+            (eight && (!t.m_scale || !t.v_scale)))
+            return ONEBIT_E_NULL;
+        if (!aligned(t.x, 4) || !aligned(t.g, g_size) || (c_size == 2 && !aligned(t.copy, 2)) ||
+            (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) ||
+            (eight && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+            return ONEBIT_E_ALIGN;
+    }
+    try {
+        std::vector<Range> all;
+        all.reserve((size_t)n_tensors * 7);
+        for (int32_t i = 0; i < n_tensors; ++i) {
+            const adamw_tensor& t = tensors[i];
+            const int64_t blocks = ceil_div(t.n, kStateBlock);
+            add_range(all, t.x, 4 * t.n, true);
+            add_range(all, t.g, (int64_t)g_size * t.n, false);
+            if (c_size == 2) add_range(all, t.copy, 2 * t.n, true);
+            add_range(all, t.m, (eight ? 1 : 4) * t.n, true);
+            add_range(all, t.v, (eight ? 1 : 4) * t.n, true);
+            if (eight) {
+                add_range(all, t.m_scale, 4 * blocks, true);
+                add_range(all, t.v_scale, 4 * blocks, true);
+            }
+        }
+        if (overlapping(all)) return ONEBIT_E_ARG;
+    } catch (const std::bad_alloc&) {
+        return ONEBIT_E_WORKSPACE;
+    }
+    AdamWTensor* to = static_cast<AdamWTensor*>(plan);
+    int32_t* tensor_of =
+        reinterpret_cast<int32_t*>(static_cast<char*>(plan) + plan_tensors_bytes(n_tensors));
+    int64_t tile = 0;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const adamw_tensor& t = tensors[i];
+        to[i] = AdamWTensor{t.x,       t.g,       t.copy, t.m,  t.v,        t.m_scale,
+                            t.v_scale, t.n,       tile,   t.lr_scale, t.weight_decay};
+        for (int64_t k = ceil_div(t.n, kAdamWTile); k > 0; --k) tensor_of[tile++] = i;
+    }
+    return ONEBIT_OK;
+}
+
+int adamw_step(const void* plan, int32_t n_tensors, int64_t tiles, int32_t state_bits,
+               int32_t g_dtype, int32_t copy_dtype, float lr, float beta1, float beta2, float eps,
+               uint32_t step, uint64_t seed, const float* g_scale, hipStream_t stream) {
+    if (check_adamw_types(state_bits, g_dtype, copy_dtype) || step < 1) return ONEBIT_E_ARG;
+    if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) ||
+        !(eps >= 0.0f && eps < INFINITY) || !isfinite(lr))
+        return ONEBIT_E_ARG;
+    if (n_tensors < 0 || !groups_ok(tiles)) return ONEBIT_E_SIZE;
+    if (tiles == 0) return ONEBIT_OK;
+    if (n_tensors == 0) return ONEBIT_E_SIZE;
+    if (!plan) return ONEBIT_E_NULL;
+    if (!aligned(plan, 256) || !aligned(g_scale, 4)) return ONEBIT_E_ALIGN;
+    AdamWArgs a = {};
+    a.tensors = static_cast<const AdamWTensor*>(plan);
+    a.tensor_of = reinterpret_cast<const int32_t*>(static_cast<const char*>(plan) +
+                                                   plan_tensors_bytes(n_tensors));
+    a.tiles = tiles;
+    a.g_scale = g_scale;
+    a.lr = lr;
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.eps = eps;
+    a.rate = (float)(1.0 / (1.0 - pow((double)beta1, (double)step)));
+    a.root = (float)(1.0 / sqrt(1.0 - pow((double)beta2, (double)step)));
+    a.k0 = (uint32_t)seed;
+    a.k1 = (uint32_t)(seed >> 32);
+    a.step = step;
+    drop_stale_error();
+    return hip_status(launch_adamw(a, state_bits, g_dtype, copy_dtype, stream));
 }
 
 }  // extern "C"

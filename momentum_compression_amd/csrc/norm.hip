@@ -1,0 +1,549 @@
+// Layer norm over the rows of a matrix, forward and backward.
+//
+// A row lies in the registers of `G` lanes, V groups of eight columns a lane
+// (group j of lane l: columns 8 (l + G j) ... + 7), so memory is read once and
+// written once: the kernels are bound by those bytes.  A workgroup takes rows in
+// turn and keeps what belongs to its columns in registers: the weights, and in
+// the backward pass the sums over rows.  Rows past kNormRow columns are
+// read again for each pass.
+#include <type_traits>
+
+#include "train.h"
+
+namespace onebit {
+namespace {
+
+// Sum over the lane's group of G lanes (a power of two up to 64), in every lane.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float x) {
+    auto dpp = [](float v, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp(
+            (int)__float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    if (G >= 2) x += dpp(x, std::integral_constant<int, 0xB1>{});    // lane ^ 1
+    if (G >= 4) x += dpp(x, std::integral_constant<int, 0x4E>{});    // lane ^ 2
+    if (G >= 8) x += dpp(x, std::integral_constant<int, 0x141>{});   // the other four of eight
+    if (G >= 16) x += dpp(x, std::integral_constant<int, 0x140>{});  // the other eight of 16
+    if (G >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x),
+                                                        false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (G >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x),
+                                                        false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return x;
+}
+
+// Sums of two values over the G threads of a row.  With more than a wave to a
+// row, every thread of the workgroup comes here, and `lds` (2 x 16 floats) is
+// another one at the next call.
+template <int G>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2* lds) {
+    constexpr int lanes = G < 64 ? G : 64;
+    a = lanes_sum<lanes>(a);
+    b = lanes_sum<lanes>(b);
+    if (G > 64) {
+        constexpr int waves = G / 64;
+        const int wave = threadIdx.x >> 6;
+        if (lane_id() == 0) lds[wave] = float2{a, b};
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int w = 0; w < waves; ++w) {
+            a += lds[w].x;
+            b += lds[w].y;
+        }
+    }
+}
+
+template <int G>
+constexpr int norm_threads() {
+    return G > 256 ? G : 256;
+}
+
+// Eight parameters from column c on, `n` of them there.
+__device__ __forceinline__ void load_params(float out[8], const void* p, bool wide, int32_t dtype,
+                                            int64_t c, int64_t n, float otherwise) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = otherwise;
+    if (!p || n <= 0) return;
+    if (wide) {
+        const auto x = n >= 8 ? load8((const float*)p + c) : load_tail((const float*)p + c, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = x.v[e];
+    } else if (dtype == ONEBIT_BF16) {
+        const auto x = n >= 8 ? load8((const bf16*)p + c) : load_tail((const bf16*)p + c, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = (float)x.v[e];
+    } else {
+        const auto x = n >= 8 ? load8((const f16*)p + c) : load_tail((const f16*)p + c, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = (float)x.v[e];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Vec8<T> load_part(const T* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) return load8(row + c);
+    return load_tail(row + c, cols - c);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_part(T* row, int64_t c, int64_t cols, const float v[8]) {
+    if (c + 8 <= cols) {
+        store8(row + c, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (c + e < cols) row[c + e] = (T)v[e];
+    }
+}
+
+// ---------------------------------------------------------------- forward
+// The mean in two steps: d = x - m1 with m1 the mean as binary32 sums leave it,
+// then what m1 is off, the mean of d.  A common offset of the row costs y
+// nothing then, and the variance is that of small numbers.
+struct Moments {
+    float shift, rest, rstd;  // mean = shift + rest
+};
+
+__device__ __forceinline__ Moments moments(float shift, float sum, float squares, float inv,
+                                           float eps) {
+    const float rest = sum * inv;
+    const float var = __builtin_fmaf(-rest, rest, squares * inv);
+    return Moments{shift, rest, 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps)};
+}
+
+template <typename T, int G, int V>
+__global__ __launch_bounds__(norm_threads<G>()) void layer_norm_kernel(NormArgs a) {
+    constexpr int per_block = norm_threads<G>() / G;
+    __shared__ float2 lds[3][16];
+    const int part = threadIdx.x % G;
+    const int64_t cols = a.cols, step = (int64_t)gridDim.x * per_block;
+    const float inv = 1.0f / (float)cols;
+    float w[V][8], b[V][8];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t c = 8 * (part + (int64_t)G * j);
+        load_params(w[j], a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+        load_params(b[j], a.bias, a.w_wide, a.dtype, c, cols - c, 0.0f);
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + threadIdx.x / G;
+        const bool ok = row < a.rows;
+        const T* x = (const T*)a.x + row * a.ld_x;
+        float d[V][8];
+        float sum = 0.0f, zero = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+            Vec8<T> v = {};
+            if (ok && c < cols) v = load_part(x, c, cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[j][e] = (float)v.v[e];
+            sum += ((d[j][0] + d[j][1]) + (d[j][2] + d[j][3])) +
+                   ((d[j][4] + d[j][5]) + (d[j][6] + d[j][7]));
+        }
+        row_sums<G>(sum, zero, lds[0]);
+        const float shift = sum * inv;
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[j][e] = c + e < cols ? d[j][e] - shift : 0.0f;
+                s1 += d[j][e];
+                s2 = __builtin_fmaf(d[j][e], d[j][e], s2);
+            }
+        }
+        row_sums<G>(s1, s2, lds[1]);
+        const Moments m = moments(shift, s1, s2, inv, a.eps);
+        if (ok && part == 0) {
+            if (a.mean) a.mean[row] = m.shift + m.rest;
+            if (a.rstd) a.rstd[row] = m.rstd;
+        }
+        T* y = (T*)a.y + row * a.ld_y;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+            if (!ok || c >= cols) continue;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = __builtin_fmaf((d[j][e] - m.rest) * m.rstd, w[j][e], b[j][e]);
+            store_part(y, c, cols, o);
+        }
+        if (G > 64) __syncthreads();  // lds is read
+    }
+}
+
+// Rows of any length: a workgroup a row, three passes over it.
+constexpr int kLong = 1024;
+
+template <typename T>
+__global__ __launch_bounds__(kLong) void layer_norm_long_kernel(NormArgs a) {
+    __shared__ float2 lds[2][16];
+    const int64_t cols = a.cols;
+    const float inv = 1.0f / (float)cols;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = (const T*)a.x + row * a.ld_x;
+        T* y = (T*)a.y + row * a.ld_y;
+        float sum = 0.0f, zero = 0.0f;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
+            const Vec8<T> v = load_part(x, c, cols);
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (float)v.v[e];
+            sum += s;
+        }
+        row_sums<kLong>(sum, zero, lds[0]);
+        const float shift = sum * inv;
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
+            const Vec8<T> v = load_part(x, c, cols);
+            float p = 0.0f, q = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = c + e < cols ? (float)v.v[e] - shift : 0.0f;
+                p += d;
+                q = __builtin_fmaf(d, d, q);
+            }
+            s1 += p;
+            s2 += q;
+        }
+        row_sums<kLong>(s1, s2, lds[1]);
+        const Moments m = moments(shift, s1, s2, inv, a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = m.shift + m.rest;
+            if (a.rstd) a.rstd[row] = m.rstd;
+        }
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
+            const Vec8<T> v = load_part(x, c, cols);
+            float w[8], b[8], o[8];
+            load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+            load_params(b, a.bias, a.w_wide, a.dtype, c, cols - c, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = __builtin_fmaf((((float)v.v[e] - m.shift) - m.rest) * m.rstd, w[e], b[e]);
+            store_part(y, c, cols, o);
+        }
+        __syncthreads();  // lds is read
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// dx = rstd (u - mean(u) - h mean(u h)) with u = dy w, h = (x - mean) rstd, and
+// the sums of dy h and dy over the workgroup's rows, kept by columns.  Groups of
+// lanes that hold the same columns are added at the end, in their order.
+template <typename T, int G, int V>
+__global__ __launch_bounds__(norm_threads<G>()) void layer_norm_grad_kernel(NormArgs a) {
+    constexpr int threads = norm_threads<G>(), per_block = threads / G;
+    __shared__ float2 lds[2][16];
+    __shared__ float share[per_block > 1 ? threads * 8 * V : 1];
+    const int part = threadIdx.x % G;
+    const int64_t cols = a.cols, step = (int64_t)gridDim.x * per_block;
+    const float inv = 1.0f / (float)cols;
+    float w[V][8], dw[V][8] = {}, db[V][8] = {};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t c = 8 * (part + (int64_t)G * j);
+        load_params(w[j], a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + threadIdx.x / G;
+        const bool ok = row < a.rows;
+        const T* x = (const T*)a.x + row * a.ld_x;
+        const T* dy = (const T*)a.dy + row * a.ld_dy;
+        const float mean = ok ? a.mean[row] : 0.0f, rstd = ok ? a.rstd[row] : 0.0f;
+        Vec8<T> xv[V], gv[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+            xv[j] = gv[j] = Vec8<T>{};
+            if (ok && c < cols) {
+                xv[j] = load_part(x, c, cols);
+                gv[j] = load_part(dy, c, cols);
+            }
+        }
+        float su = 0.0f, suh = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = c + e < cols ? ((float)xv[j].v[e] - mean) * rstd : 0.0f;
+                const float g = (float)gv[j].v[e], u = g * w[j][e];
+                dw[j][e] = __builtin_fmaf(g, h, dw[j][e]);
+                db[j][e] += g;
+                su += u;
+                suh = __builtin_fmaf(u, h, suh);
+            }
+        }
+        if (!a.dx) continue;  // the same for all
+        row_sums<G>(su, suh, lds[0]);
+        su *= inv;
+        suh *= inv;
+        T* dx = (T*)a.dx + row * a.ld_dx;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t c = 8 * (part + (int64_t)G * j);
+            if (!ok || c >= cols) continue;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = ((float)xv[j].v[e] - mean) * rstd;
+                const float u = (float)gv[j].v[e] * w[j][e];
+                o[e] = rstd * __builtin_fmaf(-h, suh, u - su);
+            }
+            store_part(dx, c, cols, o);
+        }
+        if (G > 64) __syncthreads();  // lds is read
+    }
+    if (!a.partials) return;
+    float* to = a.partials + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (per_block == 1) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int64_t c = 8 * (part + (int64_t)G * j);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < cols) to[s * cols + c + e] = s ? db[j][e] : dw[j][e];
+            }
+            continue;
+        }
+        if (s) __syncthreads();  // the first sums are read
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                share[(threadIdx.x / G) * (8 * G * V) + 8 * (part + G * j) + e] =
+                    s ? db[j][e] : dw[j][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 8 * G * V && c < cols; c += threads) {
+            float t = 0.0f;
+            for (int p = 0; p < per_block; ++p) t += share[p * (8 * G * V) + c];
+            to[s * cols + c] = t;
+        }
+    }
+}
+
+// Rows of any length: first the sums over rows, a workgroup for 2048 columns of
+// a part of the rows, then dx with a workgroup a row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void layer_norm_grad_cols_kernel(NormArgs a, int64_t strips,
+                                                                        int64_t rows_of_part) {
+    const int64_t c = 8 * ((int64_t)(blockIdx.x % strips) * kThreads + threadIdx.x);
+    const int64_t part = blockIdx.x / strips, cols = a.cols;
+    if (c >= cols) return;
+    const int64_t end = (part + 1) * rows_of_part < a.rows ? (part + 1) * rows_of_part : a.rows;
+    float dw[8] = {}, db[8] = {};
+    for (int64_t row = part * rows_of_part; row < end; ++row) {
+        const Vec8<T> xv = load_part((const T*)a.x + row * a.ld_x, c, cols);
+        const Vec8<T> gv = load_part((const T*)a.dy + row * a.ld_dy, c, cols);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = (float)gv.v[e];
+            dw[e] = __builtin_fmaf(g, ((float)xv.v[e] - mean) * rstd, dw[e]);
+            db[e] += g;
+        }
+    }
+    float* to = a.partials + part * 2 * cols;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (c + e >= cols) break;
+        to[c + e] = dw[e];
+        to[cols + c + e] = db[e];
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kLong) void layer_norm_grad_rows_kernel(NormArgs a) {
+    __shared__ float2 lds[16];
+    const int64_t cols = a.cols;
+    const float inv = 1.0f / (float)cols;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* x = (const T*)a.x + row * a.ld_x;
+        const T* dy = (const T*)a.dy + row * a.ld_dy;
+        T* dx = (T*)a.dx + row * a.ld_dx;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float su = 0.0f, suh = 0.0f;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
+            const Vec8<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
+            float w[8], p = 0.0f, q = 0.0f;
+            load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = c + e < cols ? ((float)xv.v[e] - mean) * rstd : 0.0f;
+                const float u = (float)gv.v[e] * w[e];
+                p += u;
+                q = __builtin_fmaf(u, h, q);
+            }
+            su += p;
+            suh += q;
+        }
+        row_sums<kLong>(su, suh, lds);
+        su *= inv;
+        suh *= inv;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
+            const Vec8<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
+            float w[8], o[8];
+            load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = ((float)xv.v[e] - mean) * rstd;
+                o[e] = rstd * __builtin_fmaf(-h, suh, (float)gv.v[e] * w[e] - su);
+            }
+            store_part(dx, c, cols, o);
+        }
+        __syncthreads();  // lds is read
+    }
+}
+
+// Joins the workgroups' sums [parts][n] over their n columns in a fixed order,
+// in binary64, 64 columns to a workgroup, its 16 waves taking parts in turn.  The
+// first `cols` of the n go to out0, the others to out1.
+__global__ __launch_bounds__(1024) void column_join_kernel(const float* partials, int64_t parts,
+                                                           int64_t n, int64_t cols, float* out0,
+                                                           float* out1, bool accumulate) {
+    __shared__ double sums[16][64];
+    const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int wave = threadIdx.x >> 6;
+    double t = 0.0;
+    if (c < n)
+        for (int64_t p = wave; p < parts; p += 16) t += partials[p * n + c];
+    sums[wave][threadIdx.x & 63] = t;
+    __syncthreads();
+    if (wave != 0 || c >= n) return;
+    for (int w = 1; w < 16; ++w) t += sums[w][threadIdx.x];
+    float* out = c < cols ? out0 : out1;
+    if (!out) return;
+    const int64_t at = c < cols ? c : c - cols;
+    out[at] = (float)(accumulate ? (double)out[at] + t : t);
+}
+
+template <typename F>
+hipError_t with_type(int32_t dtype, F&& f) {
+    if (dtype == ONEBIT_F32) f(float{});
+    else if (dtype == ONEBIT_BF16) f(bf16{});
+    else f(f16{});
+    return hipGetLastError();
+}
+
+// The lanes of a row and its groups of columns a lane.
+struct Shape {
+    int G, V;
+};
+
+Shape shape_of(int64_t rows, int64_t cols, bool grad) {
+    if (cols <= 8) return {1, 1};
+    if (cols <= 32) return {4, 1};
+    if (cols <= 128) return {16, 1};
+    if (cols <= 512) return {64, 1};
+    if (!grad && rows <= 1024 && cols <= 2048) return {256, 1};
+    if (cols <= 1024) return {64, 2};
+    if (cols <= 2048) return {64, 4};
+    if (cols <= 4096) return {256, 2};
+    if (cols <= 8192) return {256, 4};
+    if (cols <= kNormRow) return {1024, 2};
+    return {0, 0};
+}
+
+constexpr int64_t kNormBlocks = 512;      // workgroups of a backward pass, at most
+constexpr int64_t kLongParts = 64;        // parts of the rows, at most
+
+template <typename F>
+void with_shape(const Shape& s, F&& f) {
+    auto is = [&](int G, int V) { return s.G == G && s.V == V; };
+#define ONEBIT_SHAPE(G, V) \
+    if (is(G, V)) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{})
+    ONEBIT_SHAPE(1, 1);
+    ONEBIT_SHAPE(4, 1);
+    ONEBIT_SHAPE(16, 1);
+    ONEBIT_SHAPE(64, 1);
+    ONEBIT_SHAPE(64, 2);
+    ONEBIT_SHAPE(64, 4);
+    ONEBIT_SHAPE(256, 1);
+    ONEBIT_SHAPE(256, 2);
+    ONEBIT_SHAPE(256, 4);
+    ONEBIT_SHAPE(1024, 2);
+#undef ONEBIT_SHAPE
+}
+
+int64_t row_blocks(const Shape& s, int64_t rows, int64_t most) {
+    const int64_t per = s.G ? (s.G > 256 ? 1 : 256 / s.G) : 1;
+    const int64_t need = (rows + per - 1) / per;
+    return need < most ? need : most;
+}
+
+}  // namespace
+
+int64_t norm_parts(int64_t rows, int64_t cols) {
+    const Shape s = shape_of(rows, cols, true);
+    if (s.G) return row_blocks(s, rows, kNormBlocks);
+    return rows < kLongParts ? rows : kLongParts;
+}
+
+hipError_t launch_column_join(const float* partials, int64_t parts, int64_t n, int64_t cols,
+                              float* out0, float* out1, bool accumulate, hipStream_t st) {
+    hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, st,
+                       partials, parts, n, cols, out0, out1, accumulate);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st) {
+    const Shape s = shape_of(a.rows, a.cols, false);
+    return with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        if (!s.G) {
+            hipLaunchKernelGGL((layer_norm_long_kernel<T>),
+                               dim3((unsigned)(a.rows < 4096 ? a.rows : 4096)), dim3(kLong), 0, st,
+                               a);
+            return;
+        }
+        with_shape(s, [&](auto G, auto V) {
+            hipLaunchKernelGGL((layer_norm_kernel<T, G.value, V.value>),
+                               dim3((unsigned)row_blocks(s, a.rows, 2048)),
+                               dim3(norm_threads<G.value>()), 0, st, a);
+        });
+    });
+}
+
+hipError_t launch_layer_norm_grad(const NormArgs& a, float* dweight, float* dbias, bool accumulate,
+                                  hipStream_t st) {
+    const Shape s = shape_of(a.rows, a.cols, true);
+    const int64_t parts = norm_parts(a.rows, a.cols);
+    hipError_t e = hipSuccess;
+    if (a.rows > 0)
+        e = with_type(a.dtype, [&](auto t) {
+            using T = decltype(t);
+            if (s.G) {
+                with_shape(s, [&](auto G, auto V) {
+                    hipLaunchKernelGGL((layer_norm_grad_kernel<T, G.value, V.value>),
+                                       dim3((unsigned)parts), dim3(norm_threads<G.value>()), 0, st,
+                                       a);
+                });
+                return;
+            }
+            if (a.partials) {
+                const int64_t strips = (a.cols + 8 * kThreads - 1) / (8 * kThreads);
+                const int64_t rows_of_part = (a.rows + parts - 1) / parts;
+                hipLaunchKernelGGL((layer_norm_grad_cols_kernel<T>), dim3((unsigned)(strips * parts)),
+                                   dim3(kThreads), 0, st, a, strips, rows_of_part);
+            }
+            if (a.dx)
+                hipLaunchKernelGGL((layer_norm_grad_rows_kernel<T>),
+                                   dim3((unsigned)(a.rows < 4096 ? a.rows : 4096)), dim3(kLong), 0,
+                                   st, a);
+        });
+    if (e != hipSuccess || !a.partials) return e;
+    return launch_column_join(a.partials, parts, 2 * a.cols, a.cols, dweight, dbias, accumulate, st);
+}
+
+}  // namespace onebit

@@ -102,4 +102,114 @@ hipError_t launch_bias_join(const float* partials, const int32_t* map, float* dt
                             int64_t parts, int32_t n_buckets, int32_t radius, bool accumulate,
                             hipStream_t st);
 
+// ---------------------------------------------------------------- layer norm
+constexpr int64_t kNormRow = 16384;  // columns of a row that stays in registers
+
+struct NormArgs {
+    const void *x, *dy;
+    void *y, *dx;            // dx may be nullptr
+    const void *weight, *bias;  // or nullptr
+    float *mean, *rstd;      // [rows]; outputs of the forward pass, or nullptr
+    float* partials;         // [norm_parts][2][cols] of the backward pass, or nullptr
+    int64_t rows, cols, ld_x, ld_y, ld_dy, ld_dx;
+    float eps;
+    int32_t dtype;
+    bool w_wide;             // weight and bias are binary32
+};
+
+// Workgroups whose sums over rows the backward pass joins.
+int64_t norm_parts(int64_t rows, int64_t cols);
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st);
+hipError_t launch_layer_norm_grad(const NormArgs& a, float* dweight, float* dbias, bool accumulate,
+                                  hipStream_t st);
+
+// Sums partials [parts][n] over the parts; the first `cols` columns go to out0,
+// the others to out1 (either may be nullptr).
+hipError_t launch_column_join(const float* partials, int64_t parts, int64_t n, int64_t cols,
+                              float* out0, float* out1, bool accumulate, hipStream_t st);
+
+// ---------------------------------------------------------------- AdamW
+constexpr int64_t kAdamWTile = 4096;  // elements of a workgroup
+constexpr int64_t kStateBlock = 256;  // elements that share a scale of the 8-bit states
+
+// A tensor in the plan that the kernel reads.
+struct AdamWTensor {
+    float* x;
+    const void* g;
+    void* copy;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+    int64_t first_tile;
+    float lr_scale, weight_decay;
+};
+
+struct AdamWArgs {
+    const AdamWTensor* tensors;
+    const int32_t* tensor_of;   // [tiles]
+    int64_t tiles;
+    const float* g_scale;       // or nullptr
+    float lr, beta1, beta2, eps;
+    float rate, root;           // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    uint32_t k0, k1, step;      // of the rounding draws
+};
+
+hipError_t launch_adamw(const AdamWArgs& a, int32_t state_bits, int32_t g_dtype, int32_t copy_dtype,
+                        hipStream_t st);
+
+// ---------------------------------------------------------------- matrix products
+// Where a product's sums go: [rows][cols] of `type`, through
+//   z = sum + bias[col];  pre = z;  out = (accumulate ? out : 0) + act(z) + residual
+struct ProductOut {
+    void* out;
+    const void *bias, *residual;  // or nullptr
+    void* pre;                    // or nullptr
+    int64_t rows, cols, ld, ld_r, ld_pre;
+    int32_t type;                 // of out, residual and pre
+    int32_t act;
+    bool bias_wide;               // bias is binary32
+    bool accumulate;
+};
+
+// An operand: element (i, k) of the product's index i and the summed index k is
+// at p[i ld + k] (by rows) or p[k ld + i].
+struct ProductIn {
+    const void* p;
+    int64_t ld;
+};
+
+// How a product is divided: tiles of `tile` x `tile`, the sum over `splits` parts.
+struct ProductPlan {
+    int32_t tile;
+    int32_t splits;
+    size_t bytes;  // workspace of the parts
+};
+ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth);
+
+// out[r][c] = sum over k < depth of rows_in(r, k) cols_in(c, k).  The operand
+// types: by_rows says whether k is the contiguous index.  (cols_in, rows_in) is
+// (true, true), (false, true) or (false, false).  Contiguous indices and strides
+// are multiples of 8 and the addresses of 16 bytes.
+hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
+                          const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
+                          const ProductOut& out, float* parts, hipStream_t st);
+
+// to[r][c] = from[r][c], columns cols ... padded - 1 are 0 (16-bit elements).
+hipError_t launch_pad_rows(const void* from, int64_t ld, void* to, int64_t padded, int64_t rows,
+                           int64_t cols, hipStream_t st);
+
+// dz = dy act'(pre), rounded to the element type, into `dz` (rows of `padded`
+// elements, zeros at their end) where given, and its unrounded sums over parts of
+// the rows into partials [slope_parts][cols] where given.
+struct SlopeArgs {
+    const void *dy, *pre;
+    void* dz;
+    float* partials;
+    int64_t rows, cols, ld_dy, ld_pre, padded;
+    int32_t act, dtype;
+};
+int64_t slope_parts(int64_t rows, int64_t cols);
+hipError_t launch_slope(const SlopeArgs& a, hipStream_t st);
+
 }  // namespace onebit

@@ -72,6 +72,28 @@ class RelAttentionArgs(ctypes.Structure):
     ]
 
 
+class LinearArgs(ctypes.Structure):
+    """Mirror of linear_args."""
+
+    _fields_ = [
+        ("dtype", _c_i32), ("activation", _c_i32), ("M", _c_i64), ("N", _c_i64), ("K", _c_i64),
+        ("x", _c_p), ("w", _c_p), ("ld_x", _c_i64), ("ld_w", _c_i64), ("bias", _c_p),
+        ("residual", _c_p), ("pre", _c_p), ("y", _c_p), ("ld_residual", _c_i64),
+        ("ld_pre", _c_i64), ("ld_y", _c_i64), ("bias_dtype", _c_i32), ("dw_dtype", _c_i32),
+        ("dy", _c_p), ("dx", _c_p), ("dw", _c_p), ("dbias", _c_p), ("ld_dy", _c_i64),
+        ("ld_dx", _c_i64), ("ld_dw", _c_i64), ("accumulate", _c_i32),
+    ]
+
+
+class AdamWTensor(ctypes.Structure):
+    """Mirror of adamw_tensor."""
+
+    _fields_ = [
+        ("x", _c_p), ("g", _c_p), ("copy", _c_p), ("m", _c_p), ("v", _c_p), ("m_scale", _c_p),
+        ("v_scale", _c_p), ("n", _c_i64), ("lr_scale", _c_f), ("weight_decay", _c_f),
+    ]
+
+
 _SIGNATURES = {
     "onebit_compress": (_c_i32, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_f, _c_i32, _c_p, _c_p,
                                  _c_i32, _c_p, _c_sz, _c_p]),
@@ -111,6 +133,19 @@ _SIGNATURES = {
     "rel_attention_forward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
     "rel_attention_backward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
     "rel_attention_workspace_bytes": (_c_sz, [_c_i32] * 8),
+    "layer_norm_forward": (_c_i32, [_c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p,
+                                    _c_i32, _c_f, _c_p, _c_p, _c_p]),
+    "layer_norm_backward": (_c_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64,
+                                     _c_i64, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_i32, _c_p, _c_sz,
+                                     _c_p]),
+    "layer_norm_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "linear_forward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
+    "linear_backward": (_c_i32, [_c_p, _c_p, _c_sz, _c_p]),
+    "linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "adamw_plan_bytes": (_c_sz, [_c_p, _c_i32, _c_p]),
+    "adamw_plan": (_c_i32, [_c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_p, _c_sz]),
+    "adamw_step": (_c_i32, [_c_p, _c_i32, _c_i64, _c_i32, _c_i32, _c_i32, _c_f, _c_f, _c_f, _c_f,
+                            _c_u32, _c_u64, _c_p, _c_p]),
     "onebit_strerror": (ctypes.c_char_p, [_c_i32]),
 }
 
@@ -167,7 +202,8 @@ def _on_gpu(t) -> bool:
 # element kinds of the C ABI's buffers and the tensor dtypes that carry them
 _KINDS = {"f32": ("float32",), "u32": ("int32", "uint32"), "i64": ("int64",),
           "i8": ("int8",), "u8": ("uint8",), "i32": ("int32",),
-          "bf16": ("bfloat16",), "f16": ("float16",)}
+          "bf16": ("bfloat16",), "f16": ("float16",),
+          "e4m3": ("uint8", "float8_e4m3fn"), "e5m2": ("uint8", "float8_e5m2")}
 
 # element types of the training operators
 _DTYPES = {"float32": ("f32", ONEBIT_F32), "bfloat16": ("bf16", ONEBIT_BF16),
@@ -633,3 +669,236 @@ def rel_attention_backward(q, k, v, o, lse, do, dq, dk, dv, dtable=None, accumul
     _check("rel_attention_backward", load().rel_attention_backward(
         a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(stream, q, lse, dtable, q_pos, k_len, table, bucket_map, step_dev, ws)))
+
+
+# ---------------------------------------------------------------- layer norm
+
+
+def _params(weight, bias, cols: int, code: int):
+    """(weight, bias, their C ABI type): float32 or the rows' own type."""
+    wp = bp = None
+    w_code = None
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        k, c = _dtype(t, name)
+        if c != ONEBIT_F32 and c != code:
+            raise ValueError(f"{name} must be float32 or the rows' type (got {t.dtype})")
+        if w_code not in (None, c):
+            raise ValueError("weight and bias must be of one type")
+        w_code = c
+        if name == "weight":
+            wp = _buf(t, cols, k, name)
+        else:
+            bp = _buf(t, cols, k, name)
+    return wp, bp, ONEBIT_F32 if w_code is None else w_code
+
+
+def layer_norm_forward(x, y, rows: int, cols: int, eps: float, weight=None, bias=None, mean=None,
+                       rstd=None, stream=None) -> None:
+    """y = (x - mean) rstd weight + bias by rows; mean and rstd [rows] are written
+    where given."""
+    kind, code = _dtype(x, "x")
+    xp, ld_x = _rows(x, rows, cols, kind, "x")
+    yp, ld_y = _rows(y, rows, cols, kind, "y")
+    wp, bp, w_code = _params(weight, bias, cols, code)
+    _check("layer_norm_forward", load().layer_norm_forward(
+        xp, yp, code, rows, cols, ld_x, ld_y, wp, bp, w_code, eps, _buf(mean, rows, "f32", "mean"),
+        _buf(rstd, rows, "f32", "rstd"), _stream_of(stream, x, y, weight, bias, mean, rstd)))
+
+
+def layer_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().layer_norm_workspace_bytes(rows, cols))
+
+
+def layer_norm_backward(dy, x, mean, rstd, rows: int, cols: int, dx=None, weight=None,
+                        dweight=None, dbias=None, accumulate: bool = False, ws=None,
+                        stream=None) -> None:
+    """dx, and dweight and dbias [cols] float32, each where given, from dy, x and
+    the forward call's mean and rstd."""
+    kind, code = _dtype(x, "x")
+    gp, ld_dy = _rows(dy, rows, cols, kind, "dy")
+    xp, ld_x = _rows(x, rows, cols, kind, "x")
+    dp, ld_dx = _rows(dx, rows, cols, kind, "dx")
+    wp, _, w_code = _params(weight, None, cols, code)
+    _check("layer_norm_backward", load().layer_norm_backward(
+        gp, xp, _buf(mean, rows, "f32", "mean"), _buf(rstd, rows, "f32", "rstd"), dp, code, rows,
+        cols, ld_dy, ld_x, ld_dx, wp, w_code, _buf(dweight, cols, "f32", "dweight"),
+        _buf(dbias, cols, "f32", "dbias"), int(bool(accumulate)), _buf(ws, 0, "u8", "ws"),
+        _nbytes(ws) if ws is not None else 0,
+        _stream_of(stream, dy, x, mean, rstd, dx, weight, dweight, dbias, ws)))
+
+
+# ---------------------------------------------------------------- linear layer
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+# linear_args as one packing (its size and offsets are checked against the
+# declaration by the tests)
+_LINEAR = struct.Struct("<2i3q2Q2q4Q3q2i4Q3qi4x")
+
+
+def _activation(name: str) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)} (got {name!r})")
+    return code
+
+
+def _matrix(x, shape, dtype, device: int, name: str):
+    """(device pointer, elements between rows) of a matrix of contiguous rows, on
+    the device of the call's others; (0, 0) for None."""
+    if x is None:
+        return 0, 0
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, the call needs {tuple(shape)}")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, not with the call's others")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} (got {x.dtype})")
+    rows, cols = shape
+    step, one = x.stride()
+    if (one != 1 and cols > 1 or step < cols and rows > 1) and rows and cols:
+        raise ValueError(f"{name} must have contiguous, disjoint rows")
+    return x.data_ptr(), step if rows > 1 else cols
+
+
+def linear_workspace_bytes(M: int, N: int, K: int, backward: bool = False) -> int:
+    return int(load().linear_workspace_bytes(M, N, K, int(bool(backward))))
+
+
+def _linear_sizes(x, w, name: str):
+    M, K = _shape(x, 2, name)
+    N, k = _shape(w, 2, "w")
+    if k != K:
+        raise ValueError(f"w has {k} columns, {name} has {K}")
+    kind, code = _dtype(x, name)
+    if kind == "f32":
+        raise ValueError("a linear layer takes bfloat16 or float16 (got torch.float32)")
+    if not _on_gpu(x):
+        raise ValueError(f"{name} must be a device tensor (got {x.device})")
+    return M, N, K, code
+
+
+def linear_forward(x, w, y, bias=None, activation: str = "none", residual=None, pre=None, ws=None,
+                   stream=None) -> None:
+    """y [M, N] = act(x [M, K] w [N, K]^T + bias) + residual; the sum before the
+    activation goes to pre where given."""
+    M, N, K, code = _linear_sizes(x, w, "x")
+    dt, dev, out = x.dtype, x.get_device(), (M, N)
+    xp, wp = _matrix(x, x.shape, dt, dev, "x"), _matrix(w, w.shape, dt, dev, "w")
+    yp, pp = _matrix(y, out, dt, dev, "y"), _matrix(pre, out, dt, dev, "pre")
+    rp = _matrix(residual, out, dt, dev, "residual")
+    _, bp, b_code = _params(None, bias, N, code)
+    a = _LINEAR.pack(code, _activation(activation), M, N, K, xp[0], wp[0], xp[1], wp[1], bp or 0,
+                     rp[0], pp[0], yp[0], rp[1], pp[1], yp[1], b_code, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _check("linear_forward", load().linear_forward(
+        a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        _stream_of(stream, x, bias, ws)))
+
+
+def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, activation: str = "none", pre=None,
+                    accumulate: bool = False, ws=None, stream=None) -> None:
+    """dx [M, K], dw [N, K] (float32 or the elements' type) and dbias [N] float32,
+    each where given, from dy [M, N] and, with an activation, the forward call's
+    pre; accumulate adds dw and dbias to what they hold."""
+    M, N, K, code = _linear_sizes(x, w, "x")
+    dt, dev, out = x.dtype, x.get_device(), (M, N)
+    act = _activation(activation)
+    if act and pre is None:
+        raise ValueError("the gradient of an activation needs pre")
+    xp, wp = _matrix(x, x.shape, dt, dev, "x"), _matrix(w, w.shape, dt, dev, "w")
+    gp, pp = _matrix(dy, out, dt, dev, "dy"), _matrix(pre, out, dt, dev, "pre")
+    dxp = _matrix(dx, x.shape, dt, dev, "dx")
+    dw_code = ONEBIT_F32
+    if dw is not None:
+        dw_code = _dtype(dw, "dw")[1]
+        if dw_code != ONEBIT_F32 and dw_code != code:
+            raise ValueError(f"dw must be float32 or the elements' type (got {dw.dtype})")
+    dwp = _matrix(dw, w.shape, dw.dtype if dw is not None else dt, dev, "dw")
+    a = _LINEAR.pack(code, act, M, N, K, xp[0], wp[0], xp[1], wp[1], 0, 0, pp[0], 0, 0, pp[1], 0,
+                     0, dw_code, gp[0], dxp[0], dwp[0], _buf(dbias, N, "f32", "dbias") or 0, gp[1],
+                     dxp[1], dwp[1], 1 if accumulate else 0)
+    _check("linear_backward", load().linear_backward(
+        a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
+        _stream_of(stream, x, dbias, ws)))
+
+
+# ---------------------------------------------------------------- AdamW
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step as adamw_step reads them, on the device.
+
+    Holds the tensors, so that their memory stays.  Tensors are flat or of any
+    contiguous shape; x float32, g one type of float32, bfloat16 and float16,
+    copies (or None) one of the 16-bit types; m and v float32, or 8-bit values
+    (uint8, or float8_e4m3fn and float8_e5m2) with a float32 scale for each 256
+    elements."""
+
+    def __init__(self, x, g, m, v, m_scale=None, v_scale=None, copies=None, lr_scale=None,
+                 weight_decay=None):
+        import torch
+
+        n = len(x)
+        lists = dict(g=g, m=m, v=v, m_scale=m_scale, v_scale=v_scale, copies=copies,
+                     lr_scale=lr_scale, weight_decay=weight_decay)
+        for name, some in lists.items():
+            if some is not None and len(some) != n:
+                raise ValueError(f"{name} has {len(some)} entries, x has {n}")
+        self.state_bits = 32 if m_scale is None else 8
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("8-bit states need both scales")
+        self.tensors = [t for t in (x, g, m, v, m_scale, v_scale, copies) if t is not None]
+        self.tensors = [list(t) for t in self.tensors]
+        g_kind, self.g_dtype = _dtype(g[0], "g") if n else ("f32", ONEBIT_F32)
+        c_kind, self.copy_dtype = _dtype(copies[0], "copies") if copies else ("f32", ONEBIT_F32)
+        if copies and c_kind == "f32":
+            raise ValueError("copies must be bfloat16 or float16 (got torch.float32)")
+        eight = self.state_bits == 8
+        dev = x[0].get_device() if n else torch.cuda.current_device()
+        table = (AdamWTensor * max(n, 1))()
+
+        def at(t, count, kind, name):
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, not with x[0]")
+            if t.numel() != count:
+                raise ValueError(f"{name} has {t.numel()} elements, the call needs {count}")
+            return _buf(t, count, kind, name)
+
+        for i in range(n):
+            e, count = table[i], x[i].numel()
+            blocks = -(-count // 256)
+            e.x = at(x[i], count, "f32", f"x[{i}]")
+            e.g = at(g[i], count, g_kind, f"g[{i}]")
+            e.m = at(m[i], count, "e4m3" if eight else "f32", f"m[{i}]")
+            e.v = at(v[i], count, "e5m2" if eight else "f32", f"v[{i}]")
+            if eight:
+                e.m_scale = at(m_scale[i], blocks, "f32", f"m_scale[{i}]")
+                e.v_scale = at(v_scale[i], blocks, "f32", f"v_scale[{i}]")
+            if copies:
+                e.copy = at(copies[i], count, c_kind, f"copies[{i}]")
+            e.n = count
+            e.lr_scale = 1.0 if lr_scale is None else lr_scale[i]
+            e.weight_decay = 0.0 if weight_decay is None else weight_decay[i]
+        self.n_tensors, self.device = n, dev
+        tiles = _c_i64(0)
+        nbytes = int(load().adamw_plan_bytes(table, n, ctypes.byref(tiles)))
+        if nbytes == 0:
+            raise OnebitError("adamw_plan_bytes", ONEBIT_E_SIZE)
+        self.tiles = tiles.value
+        room = torch.empty(nbytes, dtype=torch.uint8)
+        _check("adamw_plan", load().adamw_plan(table, n, self.state_bits, self.g_dtype,
+                                               self.copy_dtype, room.data_ptr(), nbytes))
+        self.plan = room.to(f"cuda:{dev}")
+
+
+def adamw_step(plan: AdamWPlan, lr: float, beta1: float, beta2: float, eps: float, step: int,
+               seed: int = 0, grad_scale=None, stream=None) -> None:
+    """One step of AdamW on the plan's tensors; step counts from 1."""
+    if not 1 <= step < 1 << 32:
+        raise ValueError(f"step = {step} does not lie in 1 ... 2^32 - 1")
+    _check("adamw_step", load().adamw_step(
+        plan.plan.data_ptr(), plan.n_tensors, plan.tiles, plan.state_bits, plan.g_dtype,
+        plan.copy_dtype, lr, beta1, beta2, eps, step, seed & 0xFFFFFFFFFFFFFFFF,
+        _buf(grad_scale, 1, "f32", "grad_scale"), _stream_of(stream, plan.plan, grad_scale)))

@@ -19,7 +19,7 @@ Buffers (n workers, N elements per worker row, chunk L = N / n):
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Dict, Mapping, Optional
+from typing import Dict, List, Mapping, Optional
 
 import torch
 
@@ -390,3 +390,120 @@ def momentum_scale(m: torch.Tensor, seg_off: torch.Tensor, stream=None) -> torch
     k = torch.empty(S, dtype=torch.float32, device=m.device)
     ob.lamb_momentum_scale(m, N, seg_off, S, k, ws, stream=stream)
     return k
+
+
+_STATE_BLOCK = 256  # elements that share a scale of the 8-bit states
+
+
+@dataclass
+class AdamW:
+    """AdamW over a model's tensors where they lie, all in one launch a step
+    (bias-corrected, decoupled weight decay), with states in 32 or 8 bits, and
+    16-bit copies of the float32 parameters if wanted."""
+
+    params: List[torch.Tensor]             # float32
+    grads: List[torch.Tensor]              # float32, bfloat16 or float16
+    m: List[torch.Tensor]                  # float32, or uint8 codes (e4m3)
+    v: List[torch.Tensor]                  # float32, or uint8 codes (e5m2)
+    m_scale: Optional[List[torch.Tensor]]  # 8-bit states: float32, one for 256 elements
+    v_scale: Optional[List[torch.Tensor]]
+    copies: Optional[List[torch.Tensor]]
+    lr_scale: List[float]
+    weight_decay: List[float]
+    seed: int
+    plan: ob.AdamWPlan
+    steps: int = 0
+
+    @classmethod
+    def create(cls, params, grads, copies=None, weight_decay=0.0, lr_scale=1.0, bits: int = 32,
+               seed: int = 0, state: Optional[Mapping[str, List[torch.Tensor]]] = None,
+               steps: int = 0) -> "AdamW":
+        """weight_decay and lr_scale: a number, or one for each tensor.  The states
+        start at 0 unless `state` has them ("m", "v", and with 8 bits "m_scale" and
+        "v_scale", a list each), after `steps` steps."""
+        params, grads = list(params), list(grads)
+        each = [[float(a)] * len(params) if isinstance(a, (int, float)) else [float(b) for b in a]
+                for a in (lr_scale, weight_decay)]
+        if bits not in (8, 32):
+            raise ValueError(f"states have 8 or 32 bits (got {bits})")
+        if state is None:
+            state = cls._fresh(params, bits)
+        parts = {k: list(state[k]) for k in ("m", "v")}
+        for k in ("m_scale", "v_scale"):
+            parts[k] = list(state[k]) if bits == 8 else None
+        copies = None if copies is None else list(copies)
+        plan = ob.AdamWPlan(params, grads, copies=copies, lr_scale=each[0], weight_decay=each[1],
+                            **parts)
+        return cls(params=params, grads=grads, copies=copies, lr_scale=each[0],
+                   weight_decay=each[1], seed=seed, plan=plan, steps=int(steps), **parts)
+
+    @staticmethod
+    def _fresh(params, bits: int) -> Dict[str, List[torch.Tensor]]:
+        """Zero states, each kind in one buffer with every tensor's part from a
+        whole block on."""
+        sizes = [p.numel() for p in params]
+        blocks = [-(-n // _STATE_BLOCK) for n in sizes]
+        dev = params[0].device if params else None
+
+        def parts(dtype, per_block, counts):
+            flat = torch.zeros(sum(blocks) * per_block, dtype=dtype, device=dev)
+            out, at = [], 0
+            for n, b in zip(counts, blocks):
+                out.append(flat[at:at + n])
+                at += b * per_block
+            return out
+
+        kind = torch.float32 if bits == 32 else torch.uint8
+        state = {k: parts(kind, _STATE_BLOCK, sizes) for k in ("m", "v")}
+        if bits == 8:
+            state.update({k: parts(torch.float32, 1, blocks) for k in ("m_scale", "v_scale")})
+        return state
+
+    def set_grads(self, grads) -> None:
+        """Take the gradients from other tensors from now on (a new plan)."""
+        grads = list(grads)
+        self.plan = ob.AdamWPlan(self.params, grads, self.m, self.v, self.m_scale, self.v_scale,
+                                 self.copies, self.lr_scale, self.weight_decay)
+        self.grads = grads
+
+    def step(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step; grad_scale (a device float) multiplies the gradients first."""
+        ob.adamw_step(self.plan, lr, beta1, beta2, eps, self.steps + 1, seed=self.seed,
+                      grad_scale=grad_scale, stream=stream)
+        self.steps += 1
+
+    def state_values(self, i: int):
+        """m and v of tensor i in float32, whatever they are held in."""
+        if self.m_scale is None:
+            return self.m[i].clone(), self.v[i].clone()
+        n = self.m[i].numel()
+        out = []
+        for codes, scale, kind in ((self.m[i], self.m_scale[i], torch.float8_e4m3fn),
+                                   (self.v[i], self.v_scale[i], torch.float8_e5m2)):
+            of = scale.repeat_interleave(_STATE_BLOCK)[:n]
+            out.append(codes.reshape(-1).view(kind).float() * of)
+        return tuple(out)
+
+    def state_dict(self) -> Dict[str, torch.Tensor]:
+        """Carried tensors; the step count and the seed go with the checkpoint's
+        meta."""
+        kinds = {"x": self.params, "m": self.m, "v": self.v, "m_scale": self.m_scale,
+                 "v_scale": self.v_scale}
+        return {f"{k}.{i}": t.view(torch.uint8) if t.element_size() == 1 else t
+                for k, some in kinds.items() if some is not None for i, t in enumerate(some)}
+
+    @classmethod
+    def from_state(cls, tensors: Mapping[str, torch.Tensor], grads, steps: int, seed: int = 0,
+                   copies=None, weight_decay=0.0, lr_scale=1.0) -> "AdamW":
+        """The optimizer that state_dict describes, on its parameters ("x.0", ...)."""
+        n = sum(k.startswith("x.") for k in tensors)
+        bits = 8 if "m_scale.0" in tensors else 32
+        names = ("m", "v", "m_scale", "v_scale") if bits == 8 else ("m", "v")
+        state = {k: [tensors[f"{k}.{i}"] for i in range(n)] for k in names}
+        opt = cls.create([tensors[f"x.{i}"] for i in range(n)], grads, copies, weight_decay,
+                         lr_scale, bits, seed, state, steps)
+        if copies is not None:
+            for c, p in zip(opt.copies, opt.params):
+                c.copy_(p)
+        return opt
