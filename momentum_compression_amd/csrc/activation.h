@@ -51,6 +51,22 @@ __device__ __forceinline__ float activate(float z, int32_t act) {
     }
 }
 
+// Eight at once: one branch on the kind.
+template <int ACT>
+__device__ __forceinline__ void activate8_as(float z[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = activate(z[e], ACT);
+}
+__device__ __forceinline__ void activate8(float z[8], int32_t act) {
+    switch (act) {
+        case ONEBIT_RELU: return activate8_as<ONEBIT_RELU>(z);
+        case ONEBIT_GELU: return activate8_as<ONEBIT_GELU>(z);
+        case ONEBIT_GELU_TANH: return activate8_as<ONEBIT_GELU_TANH>(z);
+        case ONEBIT_SILU: return activate8_as<ONEBIT_SILU>(z);
+        default: return;
+    }
+}
+
 __device__ __forceinline__ float slope(float z, int32_t act) {
     switch (act) {
         case ONEBIT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
@@ -71,6 +87,21 @@ __device__ __forceinline__ float slope(float z, int32_t act) {
             return rest == 0.0f ? s : __builtin_fmaf(z, rest, s);
         }
         default: return 1.0f;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void times_slope8_as(float d[8], const float z[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= slope(z[e], ACT);
+}
+__device__ __forceinline__ void times_slope8(float d[8], const float z[8], int32_t act) {
+    switch (act) {
+        case ONEBIT_RELU: return times_slope8_as<ONEBIT_RELU>(d, z);
+        case ONEBIT_GELU: return times_slope8_as<ONEBIT_GELU>(d, z);
+        case ONEBIT_GELU_TANH: return times_slope8_as<ONEBIT_GELU_TANH>(d, z);
+        case ONEBIT_SILU: return times_slope8_as<ONEBIT_SILU>(d, z);
+        default: return;
     }
 }
 

@@ -12,7 +12,15 @@
 namespace onebit {
 namespace {
 
-constexpr int kDeep = 64;  // of the summed index a tile
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+// Orders a wave's own writes to LDS before its reads of what other lanes wrote.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+constexpr int kDeep = 64;  // of the summed index a tile: rows of a whole cache line
 
 // Eight values of a row of the result, `n` of them inside.
 template <typename S>
@@ -40,7 +48,6 @@ __device__ __forceinline__ void store_row8(S* p, const float v[8], int64_t n) {
 template <typename S, typename T>
 __device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c, float z[8]) {
     const int64_t n = o.cols - c;
-    if (n <= 0) return;
     if (o.bias) {
         float b[8];
         if (o.bias_wide) load_row8(b, (const float*)o.bias + c, n);
@@ -49,10 +56,7 @@ __device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c,
         for (int e = 0; e < 8; ++e) z[e] += b[e];
     }
     if (o.pre) store_row8((S*)o.pre + r * o.ld_pre + c, z, n);
-    if (o.act != ONEBIT_NONE) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = activate(z[e], o.act);
-    }
+    activate8(z, o.act);
     if (o.residual) {
         float v[8];
         load_row8(v, (const S*)o.residual + r * o.ld_r + c, n);
@@ -69,24 +73,30 @@ __device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c,
     store_row8(to, z, n);
 }
 
-// One operand's tiles, memory to LDS without registers between.  By rows: TILE
-// rows of kDeep elements, laid out as tile_at<64>; otherwise kDeep rows of TILE
-// elements, with the 16-byte chunks of a row xored as in tile_at<128>.  What lies
-// past the matrix reads as 0: such chunks get an offset past the buffer's end.
+// One operand's tiles: TILE of its index by kDeep of the summed one.  By rows: TILE
+// rows of kDeep elements in LDS; otherwise kDeep rows of TILE elements.  The 16-byte
+// chunks of a row are xored with bits of the row's number, so that a read of 16
+// rows' chunks, or a transposing read of 4 rows by 4 chunks, meets every bank once.
+// A tile comes in pieces of 16 bytes a lane, which lie side by side in LDS: the
+// lane asks for the chunk that the xor puts there.  What lies past the matrix reads
+// as 0: such chunks get an offset past the buffer's end.
 template <typename T, bool ROWS, int TILE, int WAVES>
 struct Operand {
     static constexpr int kChunks = ROWS ? kDeep / 8 : TILE / 8;  // of a row in LDS
     static constexpr int kRowsAtOnce = 64 / kChunks * WAVES;
     static constexpr int kPer = TILE * kDeep * 2 / (1024 * WAVES);
     static constexpr int kBytes = TILE * kDeep * 2;
+    static constexpr int kPeriod = ROWS ? 16 : 4;  // of the xor, in rows
+    static_assert(kPer >= 1 && 64 % kChunks == 0 && kRowsAtOnce % kPeriod == 0, "whole pieces");
+    static_assert(ROWS ? kChunks == 8 : kChunks >= 16, "the xor's layouts");
     const char* base;
     uint32_t stride, at;  // in bytes
-    int32_t count;        // rows (by rows), else columns from `first` on
+    int32_t count;        // of the operand's index from the tile's first on
     int32_t mine;         // by rows: the lane's first k in a tile
 
     static __device__ __forceinline__ int swizzled(int row, int chunk) {
-        return ROWS ? chunk ^ swizzle<64>(row)
-                    : TILE == 64 ? chunk ^ swizzle<64>(row) : chunk ^ swizzle<128>(row);
+        if (!ROWS) return chunk ^ ((row & 3) << 2);
+        return chunk ^ swizzle<64>(row);
     }
     __device__ __forceinline__ Operand(const ProductIn& in, int64_t first, int64_t extent, int wave,
                                        int lane) {
@@ -100,7 +110,9 @@ struct Operand {
         mine = 8 * chunk;
         if (!ROWS && 8 * chunk >= count) at = 0x80000000u;
     }
-    __device__ __forceinline__ void load(char* tile, int64_t k0, int64_t depth, int wave) const {
+    // The buffer of the tile from k0 on and the lane's offset in it.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int64_t k0, int64_t depth,
+                                                             uint32_t& off) const {
         const int64_t left = depth - k0;
         const char* from = base + (ROWS ? k0 * 2 : k0 * stride);
         const int32_t deep = left < kDeep ? (int32_t)left : kDeep;
@@ -109,15 +121,23 @@ struct Operand {
             deep <= 0 ? 0u
             : ROWS    ? (uint32_t)(count - 1) * stride + (uint32_t)((deep + 7) & ~7) * 2
                       : (uint32_t)(deep - 1) * stride + (uint32_t)((count + 7) & ~7) * 2;
-        const __amdgpu_buffer_rsrc_t rsrc =
-            __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, (int)bytes, 0x00027000);
-        const uint32_t off = ROWS && mine >= deep ? 0x80000000u : at;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc,
-                (__attribute__((address_space(3))) void*)(tile + (x * WAVES + wave) * 1024), 16,
-                (int)(off + (uint32_t)(x * kRowsAtOnce) * stride), 0, 0, 0);
+        off = ROWS && mine >= deep ? 0x80000000u : at;
+        return __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, (int)bytes, 0x00027000);
+    }
+    // Piece x of a tile, memory to LDS without registers between.
+    __device__ __forceinline__ void load(char* tile, int x, __amdgpu_buffer_rsrc_t rsrc,
+                                         uint32_t off, int wave) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (__attribute__((address_space(3))) void*)(tile + (x * WAVES + wave) * 1024), 16,
+            (int)(off + (uint32_t)(x * kRowsAtOnce) * stride), 0, 0, 0);
+    }
+    // The same into registers.
+    __device__ __forceinline__ u32x4 fetch(int x, __amdgpu_buffer_rsrc_t rsrc, uint32_t off) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(
+            rsrc, (int)(off + (uint32_t)(x * kRowsAtOnce) * stride), 0, 0);
+    }
+    static __device__ __forceinline__ void put(char* tile, int x, u32x4 held, int wave, int lane) {
+        *reinterpret_cast<u32x4*>(tile + (x * WAVES + wave) * 1024 + lane * 16) = held;
     }
     // 32 of the operand's index from `first` on, k from 16 kc on; PERM: the
     // order of perm_row().
@@ -146,25 +166,77 @@ struct Operand {
 struct ProductArgs {
     ProductIn a, b;       // columns' and rows' operand
     ProductOut out;
-    float* parts;         // [splits][rows][cols padded] of a divided sum, or nullptr
+    float* parts;         // [splits][rows][padded] of a divided sum, or nullptr
     int64_t depth, padded;
     int32_t tiles_a, tiles_b, splits;
 };
 
-// WA x WB waves of TILE x TILE results.
-template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TILE, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void product_kernel(ProductArgs p) {
-    constexpr int waves = WA * WB, na = TILE / WA / 32, nb = TILE / WB / 32;
-    using A = Operand<T, A_ROWS, TILE, waves>;
-    using B = Operand<T, B_ROWS, TILE, waves>;
+// A workgroup's tile.  Workgroups go to the 8 XCDs in turn: those of one XCD get
+// consecutive tiles, and consecutive tiles are blocks of kBand columns' tiles, so
+// that an XCD's L2 serves both operands several times.
+constexpr uint32_t kBand = 8;
+__device__ __forceinline__ void tile_of(const ProductArgs& p, uint32_t& ta, uint32_t& tb,
+                                        uint32_t& split) {
+    const uint32_t tiles = (uint32_t)p.tiles_a * p.tiles_b;
+    split = blockIdx.x / tiles;
+    uint32_t id = blockIdx.x % tiles;
+    const uint32_t even = tiles / 8;
+    if (id < even * 8) id = (id & 7) * even + (id >> 3);
+    const uint32_t band = id / (kBand * p.tiles_b), left = p.tiles_a - band * kBand;
+    const uint32_t wide = left < kBand ? left : kBand, in = id - band * kBand * p.tiles_b;
+    ta = band * kBand + in % wide;
+    tb = in / wide;
+}
+
+// What a wave has issued to LDS is there for all that pass: its own loads into LDS
+// (DIRECT) have to have come before the barrier.
+template <bool DIRECT>
+__device__ __forceinline__ void step_barrier() {
+    if (DIRECT) tiles_barrier();
+    else __syncthreads();
+}
+
+// Rows of a wave's part of the result on their way through LDS: the floats between
+// two of them, so that 16 rows' pieces of 16 bytes meet every bank once.
+template <int COLS>
+constexpr int out_pitch() {
+    return COLS + 4;
+}
+
+template <int TA, int TB, int WA, int WB>
+constexpr size_t product_lds() {
+    const size_t tiles = (size_t)(TA + TB) * kDeep * 2 * 2;
+    const size_t rows = (size_t)WA * WB * 32 * out_pitch<TA / WA>() * sizeof(float);
+    return tiles > rows ? tiles : rows;
+}
+
+// WA x WB waves of TA columns by TB rows of the result, two tiles of kDeep in LDS.
+//
+// A step multiplies a tile in parts of 16 k; the fragments of a part are read
+// between the products of the part before it, the first of a tile after the step's
+// one barrier, which stands before the last part of the tile before.  Behind that
+// barrier the tile that was read is replaced, half of it among the products of that
+// part and half among those of the next: a burst of loads would hold up the waves,
+// as the loads of a CU pass at 64 bytes a cycle.  With both operands by rows tiles
+// go from memory to LDS directly.  Transposing reads are not told apart from such
+// loads by the compiler, which waits for all of them before the first read; with
+// those a tile goes through registers, one tile further ahead.
+template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p) {
+    constexpr int waves = WA * WB, ca = TA / WA, rb = TB / WB, na = ca / 32, nb = rb / 32;
+    constexpr bool direct = A_ROWS && B_ROWS;
+    using A = Operand<T, A_ROWS, TA, waves>;
+    using B = Operand<T, B_ROWS, TB, waves>;
+    constexpr int bytes = A::kBytes + B::kBytes;
     extern __shared__ __align__(16) char lds[];
     const int wave = wave_id(), lane = lane_id();
     const int wa = wave % WA, wb = wave / WA;
-    const uint32_t tiles = (uint32_t)p.tiles_a * p.tiles_b;
-    const uint32_t tile = blockIdx.x % tiles, split = blockIdx.x / tiles;
-    const int64_t a0 = (int64_t)(tile % p.tiles_a) * TILE, b0 = (int64_t)(tile / p.tiles_a) * TILE;
-    const int64_t steps = (p.depth + kDeep - 1) / kDeep;
-    const int64_t first = steps * split / p.splits, last = steps * (split + 1) / p.splits;
+    uint32_t ta, tb, split;
+    tile_of(p, ta, tb, split);
+    const int64_t a0 = (int64_t)ta * TA, b0 = (int64_t)tb * TB;
+    const int32_t steps = (int32_t)((p.depth + kDeep - 1) / kDeep);
+    const int32_t first = (int32_t)((int64_t)steps * split / p.splits);
+    const int32_t last = (int32_t)((int64_t)steps * (split + 1) / p.splits);
     const A as(p.a, a0, p.out.cols, wave, lane);
     const B bs(p.b, b0, p.out.rows, wave, lane);
     f32x16 acc[na][nb];
@@ -172,56 +244,136 @@ __global__ __launch_bounds__(64 * WA * WB) void product_kernel(ProductArgs p) {
     for (int i = 0; i < na; ++i)
 #pragma unroll
         for (int j = 0; j < nb; ++j) acc[i][j] = f32x16{};
+    constexpr int kcs = kDeep / 16, pieces = A::kPer + B::kPer;
+    typename Mma<T>::x8 af[2][na], bf[2][nb];
+    // fragment x of the products' operands, the rows' first
+    auto read = [&](int x, int to, const char* tile, int kc) {
+        if (x < nb)
+            bf[to][x] = B::template frag<false>(tile + A::kBytes, wb * rb + 32 * x, kc, lane);
+        else
+            af[to][x - nb] = A::template frag<true>(tile, wa * ca + 32 * (x - nb), kc, lane);
+    };
+    u32x4 held[direct ? 1 : pieces];
+    __amdgpu_buffer_rsrc_t ar, br;
+    uint32_t ao = 0, bo = 0;
+    auto aim = [&](int32_t step) {
+        ar = as.buffer((int64_t)step * kDeep, p.depth, ao);
+        br = bs.buffer((int64_t)step * kDeep, p.depth, bo);
+    };
+    // piece x of the tile that was aimed at
+    auto start = [&](int x, char* tile) {
+        if constexpr (direct) {
+            if (x < A::kPer) as.load(tile, x, ar, ao, wave);
+            else bs.load(tile + A::kBytes, x - A::kPer, br, bo, wave);
+        } else {
+            held[x] = x < A::kPer ? as.fetch(x, ar, ao) : bs.fetch(x - A::kPer, br, bo);
+        }
+    };
+    auto finish = [&](int x, char* tile) {
+        if constexpr (!direct) {
+            if (x < A::kPer) A::put(tile, x, held[x], wave, lane);
+            else B::put(tile + A::kBytes, x - A::kPer, held[x], wave, lane);
+        }
+    };
     if (first < last) {
-        as.load(lds, first * kDeep, p.depth, wave);
-        bs.load(lds + A::kBytes, first * kDeep, p.depth, wave);
-    }
-    int buf = 0;
-    for (int64_t s = first; s < last; ++s, buf ^= 1) {
-        const char* at = lds + buf * (A::kBytes + B::kBytes);
-        const char* bt = at + A::kBytes;
-        tiles_barrier();  // this tile is there, and the other buffer is read
-        if (s + 1 < last) {
-            char* next = lds + (buf ^ 1) * (A::kBytes + B::kBytes);
-            as.load(next, (s + 1) * kDeep, p.depth, wave);
-            bs.load(next + A::kBytes, (s + 1) * kDeep, p.depth, wave);
+        char* tile = lds;
+        char* other = lds + bytes;
+        constexpr int early = pieces / 2;
+        aim(first);
+#pragma unroll
+        for (int x = 0; x < pieces; ++x) start(x, tile);
+#pragma unroll
+        for (int x = 0; x < pieces; ++x) finish(x, tile);
+        aim(first + 1);
+        if (direct) {
+            tiles_barrier();
+#pragma unroll
+            for (int x = 0; x < early; ++x) start(x, other);
+        } else {
+#pragma unroll
+            for (int x = 0; x < pieces; ++x) start(x, other);
+#pragma unroll
+            for (int x = 0; x < early; ++x) finish(x, other);
+            aim(first + 2);
+#pragma unroll
+            for (int x = 0; x < early; ++x) start(x, other);
+            __syncthreads();
         }
 #pragma unroll
-        for (int kc = 0; kc < kDeep / 16; ++kc) {
-            typename Mma<T>::x8 af[na], bf[nb];
+        for (int x = 0; x < na + nb; ++x) read(x, 0, tile, 0);
+        for (int32_t s = first; s < last; ++s) {
 #pragma unroll
-            for (int i = 0; i < na; ++i)
-                af[i] = A::template frag<true>(at, wa * (TILE / WA) + 32 * i, kc, lane);
+            for (int kc = 0; kc < kcs; ++kc) {
+                const bool end = kc + 1 == kcs;
+                char* from = end ? other : tile;
+                if (end) {
+                    // the next tile is there, and this one is read
+                    step_barrier<direct>();
+                    aim(s + (direct ? 2 : 3));
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < nb; ++j)
-                bf[j] = B::template frag<false>(bt, wb * (TILE / WB) + 32 * j, kc, lane);
+                for (int i = 0; i < na; ++i) {
 #pragma unroll
-            for (int i = 0; i < na; ++i)
+                    for (int j = 0; j < nb; ++j)
+                        acc[i][j] = Mma<T>::mul(af[kc & 1][i], bf[kc & 1][j], acc[i][j]);
+                    // between the products what later ones need: fragments of
+                    // the next 16 k, and pieces of the tile that takes the place
+                    // of the one read last
 #pragma unroll
-                for (int j = 0; j < nb; ++j) acc[i][j] = Mma<T>::mul(af[i], bf[j], acc[i][j]);
+                    for (int x = 0; x < na + nb; ++x)
+                        if (x * na / (na + nb) == i) read(x, (kc + 1) & 1, from, end ? 0 : kc + 1);
+#pragma unroll
+                    for (int x = 0; x < pieces; ++x)
+                        if ((end && x < early && x * na / early == i) ||
+                            (kc == 0 && x >= early && (x - early) * na / (pieces - early) == i)) {
+                            finish(x, end ? tile : other);
+                            start(x, end ? tile : other);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            char* t = tile;
+            tile = other;
+            other = t;
         }
+        step_barrier<direct>();  // nothing is under way to the tiles, and they are read
     }
+
+    // The result through LDS, 32 rows of the wave's at a time, so that a row's
+    // columns leave side by side.
+    constexpr int pitch = out_pitch<ca>(), lanes = ca / 8, at_once = 64 / lanes;
+    float* stage = reinterpret_cast<float*>(lds) + wave * (32 * pitch);
+    const int64_t c = a0 + wa * ca + 8 * (lane % lanes);
 #pragma unroll
     for (int j = 0; j < nb; ++j) {
-        const int64_t r = b0 + wb * (TILE / WB) + 32 * j + (lane & 31);
-        if (r >= p.out.rows) continue;
+        wave_fence();
 #pragma unroll
         for (int i = 0; i < na; ++i)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int64_t c = a0 + wa * (TILE / WA) + 32 * i + 16 * g + 8 * (lane >> 5);
-                if (c >= p.out.cols) continue;
-                float z[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = acc[i][j][8 * g + e];
-                if (!p.parts) {
-                    emit8<S, T>(p.out, r, c, z);
-                } else {
-                    float* to = p.parts + ((int64_t)split * p.out.rows + r) * p.padded + c;
-                    *reinterpret_cast<f4*>(to) = f4{z[0], z[1], z[2], z[3]};
-                    *reinterpret_cast<f4*>(to + 4) = f4{z[4], z[5], z[6], z[7]};
-                }
+            for (int g = 0; g < 4; ++g) {
+                float* to = stage + (lane & 31) * pitch + 32 * i + 16 * (g >> 1) +
+                            8 * (lane >> 5) + 4 * (g & 1);
+                *reinterpret_cast<f4*>(to) = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                                acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
             }
+        wave_fence();
+        const int64_t r0 = b0 + wb * rb + 32 * j;
+#pragma unroll 1
+        for (int r = lane / lanes; r < 32; r += at_once) {
+            if (r0 + r >= p.out.rows || c >= p.out.cols) continue;
+            const float* from = stage + r * pitch + 8 * (lane % lanes);
+            const f4 lo = *reinterpret_cast<const f4*>(from);
+            const f4 hi = *reinterpret_cast<const f4*>(from + 4);
+            if (p.parts) {
+                float* to = p.parts + ((int64_t)split * p.out.rows + r0 + r) * p.padded + c;
+                *reinterpret_cast<f4*>(to) = lo;
+                *reinterpret_cast<f4*>(to + 4) = hi;
+            } else {
+                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                emit8<S, T>(p.out, r0 + r, c, z);
+            }
+        }
     }
 }
 
@@ -278,8 +430,7 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
         if (a.act != ONEBIT_NONE) {
             float z[8];
             load_row8(z, (const T*)a.pre + r * a.ld_pre + c, n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = d[e] * slope(z[e], a.act);
+            times_slope8(d, z, a.act);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[e] += d[e];
@@ -296,17 +447,18 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
         if (e < n) a.partials[part * a.cols + c + e] = sums[e];
 }
 
-constexpr int kTileBig = 256, kTileSmall = 128;
+template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB>
+void launch_tile(const ProductArgs& p, hipStream_t st) {
+    hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, TA, TB, WA, WB>),
+                       dim3((unsigned)((int64_t)p.tiles_a * p.tiles_b * p.splits)),
+                       dim3(64 * WA * WB), (product_lds<TA, TB, WA, WB>()), st, p);
+}
 
 template <typename T, typename S, bool A_ROWS, bool B_ROWS>
-void launch_tiles(const ProductArgs& p, int32_t tile, hipStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)p.tiles_a * p.tiles_b * p.splits);
-    if (tile == kTileBig)
-        hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, kTileBig, 2, 4>), dim3(grid),
-                           dim3(512), 4 * kTileBig * kDeep * 2, st, p);
-    else
-        hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, kTileSmall, 2, 2>), dim3(grid),
-                           dim3(256), 4 * kTileSmall * kDeep * 2, st, p);
+void launch_tiles(const ProductArgs& p, const ProductPlan& plan, hipStream_t st) {
+    if (plan.tile_b == 256) launch_tile<T, S, A_ROWS, B_ROWS, 256, 256, 2, 4>(p, st);
+    else if (plan.tile_a == 256) launch_tile<T, S, A_ROWS, B_ROWS, 256, 128, 4, 2>(p, st);
+    else launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 2>(p, st);
     if (p.parts) {
         const int64_t groups = (p.out.rows * (p.padded / 8) + kThreads - 1) / kThreads;
         hipLaunchKernelGGL((product_join_kernel<T, S>), dim3((unsigned)(groups < 4096 ? groups : 4096)),
@@ -314,37 +466,58 @@ void launch_tiles(const ProductArgs& p, int32_t tile, hipStream_t st) {
     }
 }
 
-template <typename T, typename S>
-void launch_operands(const ProductArgs& p, bool a_rows, bool b_rows, int32_t tile,
-                     hipStream_t st) {
-    if (a_rows) launch_tiles<T, S, true, true>(p, tile, st);
-    else if (b_rows) launch_tiles<T, S, false, true>(p, tile, st);
-    else launch_tiles<T, S, false, false>(p, tile, st);
-}
-
+// Binary32 results are those of dw, whose operands both come by their own index.
 template <typename T>
-void launch_typed(const ProductArgs& p, bool a_rows, bool b_rows, int32_t tile, hipStream_t st) {
-    if (p.out.type == ONEBIT_F32) launch_operands<T, float>(p, a_rows, b_rows, tile, st);
-    else launch_operands<T, T>(p, a_rows, b_rows, tile, st);
+void launch_typed(const ProductArgs& p, bool a_rows, bool b_rows, const ProductPlan& plan,
+                  hipStream_t st) {
+    if (a_rows) launch_tiles<T, T, true, true>(p, plan, st);
+    else if (b_rows) launch_tiles<T, T, false, true>(p, plan, st);
+    else if (p.out.type == ONEBIT_F32) launch_tiles<T, float, false, false>(p, plan, st);
+    else launch_tiles<T, T, false, false>(p, plan, st);
 }
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
 }  // namespace
 
+// The division that a model of the kernels' times takes for the fastest: rounds of
+// resident workgroups, each the longer the deeper it is, and the join of parts.
+// Microseconds as measured (8192^3: 856, 1043 and 988 with tiles of 256 x 256, 256 x
+// 128 and 128 x 128; 4096 x 1024 over 8192: 141, 94 and 77).
 ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth) {
-    ProductPlan plan;
-    const int64_t big = tiles_of(rows, kTileBig) * tiles_of(cols, kTileBig);
-    plan.tile = big >= 256 ? kTileBig : kTileSmall;
-    const int64_t tiles = tiles_of(rows, plan.tile) * tiles_of(cols, plan.tile);
+    struct Tile {
+        int32_t a, b, places;  // places: workgroups at once
+        double per_k, half_per_k, fixed;  // half: with at most half of the places taken
+    };
+    static const Tile kinds[] = {{256, 256, 256, 0.026, 0.018, 9.0},
+                                 {256, 128, 256, 0.0159, 0.0118, 6.0},
+                                 {128, 128, 512, 0.0150, 0.0092, 5.0}};
+    ProductPlan best = {};
+    double least = 0.0;
     const int64_t steps = tiles_of(depth, kDeep);
-    int64_t splits = tiles > 0 ? 256 / tiles : 1;
-    if (splits > steps / 4) splits = steps / 4;
-    plan.splits = (int32_t)(splits < 1 ? 1 : splits);
-    plan.bytes = plan.splits > 1
-                     ? (size_t)plan.splits * rows * ((cols + 7) / 8 * 8) * sizeof(float)
+    for (const Tile& t : kinds) {
+        const int64_t tiles = tiles_of(rows, t.b) * tiles_of(cols, t.a);
+        for (int64_t splits = 1; splits <= 32; ++splits) {
+            if (splits > 1 && (tiles * splits > t.places || splits * 4 > steps)) break;
+            const int64_t rounds = tiles_of(tiles * splits, t.places);
+            const double per_k = tiles * splits * 2 <= t.places ? t.half_per_k : t.per_k;
+            const double deep = (double)tiles_of(steps, splits) * kDeep;
+            // the parts are written and read at 4 bytes per ns and GPU
+            const double join =
+                splits > 1 ? 6.0 + (double)(2 * splits * rows * cols * 4) / 4.0e6 : 0.0;
+            const double time = (double)rounds * (deep * per_k + t.fixed) + join;
+            if (best.splits == 0 || time < least) {
+                least = time;
+                best.tile_a = t.a;
+                best.tile_b = t.b;
+                best.splits = (int32_t)splits;
+            }
+        }
+    }
+    best.bytes = best.splits > 1
+                     ? (size_t)best.splits * rows * ((cols + 7) / 8 * 8) * sizeof(float)
                      : 0;
-    return plan;
+    return best;
 }
 
 hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
@@ -359,11 +532,11 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
     p.parts = plan.splits > 1 ? parts : nullptr;
     p.depth = depth;
     p.padded = (out.cols + 7) / 8 * 8;
-    p.tiles_a = (int32_t)tiles_of(out.cols, plan.tile);
-    p.tiles_b = (int32_t)tiles_of(out.rows, plan.tile);
+    p.tiles_a = (int32_t)tiles_of(out.cols, plan.tile_a);
+    p.tiles_b = (int32_t)tiles_of(out.rows, plan.tile_b);
     p.splits = plan.splits;
-    if (dtype == ONEBIT_BF16) launch_typed<bf16>(p, cols_by_rows, rows_by_rows, plan.tile, st);
-    else launch_typed<f16>(p, cols_by_rows, rows_by_rows, plan.tile, st);
+    if (dtype == ONEBIT_BF16) launch_typed<bf16>(p, cols_by_rows, rows_by_rows, plan, st);
+    else launch_typed<f16>(p, cols_by_rows, rows_by_rows, plan, st);
     return hipGetLastError();
 }
 

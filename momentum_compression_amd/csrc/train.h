@@ -179,9 +179,10 @@ struct ProductIn {
     int64_t ld;
 };
 
-// How a product is divided: tiles of `tile` x `tile`, the sum over `splits` parts.
+// How a product is divided: tiles of tile_a columns by tile_b rows of the result,
+// the sum over `splits` parts.
 struct ProductPlan {
-    int32_t tile;
+    int32_t tile_a, tile_b;
     int32_t splits;
     size_t bytes;  // workspace of the parts
 };
