@@ -6,6 +6,8 @@
 // perm_row() order.  Each operand comes with k contiguous (read as rows of the
 // tile in LDS) or with its own index contiguous (read by transposing LDS reads),
 // so the product of a layer and both of its gradients need no transposed copies.
+#include <type_traits>
+
 #include "activation.h"
 #include "attention.h"
 
@@ -44,19 +46,26 @@ __device__ __forceinline__ void store_row8(S* p, const float v[8], int64_t n) {
         if (e < n) p[e] = (S)v[e];
 }
 
-// The epilogue for columns c ... c + 7 of row r.
-template <typename S, typename T>
-__device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c, float z[8]) {
-    const int64_t n = o.cols - c;
-    if (o.bias) {
-        float b[8];
-        if (o.bias_wide) load_row8(b, (const float*)o.bias + c, n);
-        else load_row8(b, (const T*)o.bias + c, n);
+// The bias of columns c ... c + 7.
+template <typename T>
+__device__ __forceinline__ void load_bias(float b[8], const ProductOut& o, int64_t c) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += b[e];
-    }
+    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+    if (!o.bias || c >= o.cols) return;
+    if (o.bias_wide) load_row8(b, (const float*)o.bias + c, o.cols - c);
+    else load_row8(b, (const T*)o.bias + c, o.cols - c);
+}
+
+// The epilogue for columns c ... c + 7 of row r.
+template <int ACT, typename S>
+__device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c, const float b[8],
+                                      float z[8]) {
+    const int64_t n = o.cols - c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += b[e];
     if (o.pre) store_row8((S*)o.pre + r * o.ld_pre + c, z, n);
-    activate8(z, o.act);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = activate<ACT>(z[e]);
     if (o.residual) {
         float v[8];
         load_row8(v, (const S*)o.residual + r * o.ld_r + c, n);
@@ -71,6 +80,18 @@ __device__ __forceinline__ void emit8(const ProductOut& o, int64_t r, int64_t c,
         for (int e = 0; e < 8; ++e) z[e] += v[e];
     }
     store_row8(to, z, n);
+}
+
+// f with the activation as a constant.
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int32_t act, F&& f) {
+    switch (act) {
+        case ONEBIT_RELU: return f(std::integral_constant<int, ONEBIT_RELU>{});
+        case ONEBIT_GELU: return f(std::integral_constant<int, ONEBIT_GELU>{});
+        case ONEBIT_GELU_TANH: return f(std::integral_constant<int, ONEBIT_GELU_TANH>{});
+        case ONEBIT_SILU: return f(std::integral_constant<int, ONEBIT_SILU>{});
+        default: return f(std::integral_constant<int, ONEBIT_NONE>{});
+    }
 }
 
 // One operand's tiles: TILE of its index by kDeep of the summed one.  By rows: TILE
@@ -345,6 +366,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
     constexpr int pitch = out_pitch<ca>(), lanes = ca / 8, at_once = 64 / lanes;
     float* stage = reinterpret_cast<float*>(lds) + wave * (32 * pitch);
     const int64_t c = a0 + wa * ca + 8 * (lane % lanes);
+    float bias[8];
+    load_bias<T>(bias, p.out, p.parts ? p.out.cols : c);
 #pragma unroll
     for (int j = 0; j < nb; ++j) {
         wave_fence();
@@ -359,21 +382,28 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
             }
         wave_fence();
         const int64_t r0 = b0 + wb * rb + 32 * j;
-#pragma unroll 1
-        for (int r = lane / lanes; r < 32; r += at_once) {
-            if (r0 + r >= p.out.rows || c >= p.out.cols) continue;
-            const float* from = stage + r * pitch + 8 * (lane % lanes);
-            const f4 lo = *reinterpret_cast<const f4*>(from);
-            const f4 hi = *reinterpret_cast<const f4*>(from + 4);
-            if (p.parts) {
-                float* to = p.parts + ((int64_t)split * p.out.rows + r0 + r) * p.padded + c;
-                *reinterpret_cast<f4*>(to) = lo;
-                *reinterpret_cast<f4*>(to + 4) = hi;
-            } else {
-                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                emit8<S, T>(p.out, r0 + r, c, z);
+        const int32_t left = (int32_t)(p.out.rows - r0 < 32 ? p.out.rows - r0 : 32);
+        if (c >= p.out.cols) continue;
+        const float* from = stage + 8 * (lane % lanes);
+        if (p.parts) {
+            float* to = p.parts + ((int64_t)split * p.out.rows + r0) * p.padded + c;
+            for (int r = lane / lanes; r < left; r += at_once) {
+                *reinterpret_cast<f4*>(to + r * p.padded) =
+                    *reinterpret_cast<const f4*>(from + r * pitch);
+                *reinterpret_cast<f4*>(to + r * p.padded + 4) =
+                    *reinterpret_cast<const f4*>(from + r * pitch + 4);
             }
+            continue;
         }
+        with_act(p.out.act, [&](auto act) {
+#pragma unroll 2
+            for (int r = lane / lanes; r < left; r += at_once) {
+                const f4 lo = *reinterpret_cast<const f4*>(from + r * pitch);
+                const f4 hi = *reinterpret_cast<const f4*>(from + r * pitch + 4);
+                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                emit8<act.value, S>(p.out, r0 + r, c, bias, z);
+            }
+        });
     }
 }
 
@@ -395,7 +425,9 @@ __global__ __launch_bounds__(kThreads) void product_join_kernel(ProductArgs p) {
                 z[4 + e] += hi[e];
             }
         }
-        emit8<S, T>(p.out, r, c, z);
+        float b[8];
+        load_bias<T>(b, p.out, c);
+        with_act(p.out.act, [&](auto act) { emit8<act.value, S>(p.out, r, c, b, z); });
     }
 }
 
@@ -415,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t* from
 
 // ---------------------------------------------------------------- the activation's slope
 // A thread has eight columns of a part of the rows.
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t groups,
                                                          int64_t rows_of_part) {
     const int64_t strips = (groups + kThreads - 1) / kThreads;
@@ -427,10 +459,11 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
     for (int64_t r = part * rows_of_part; r < end; ++r) {
         float d[8];
         load_row8(d, (const T*)a.dy + r * a.ld_dy + c, n);
-        if (a.act != ONEBIT_NONE) {
+        if (ACT != ONEBIT_NONE) {
             float z[8];
             load_row8(z, (const T*)a.pre + r * a.ld_pre + c, n);
-            times_slope8(d, z, a.act);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] *= slope<ACT>(z[e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[e] += d[e];
@@ -562,10 +595,14 @@ hipError_t launch_slope(const SlopeArgs& a, hipStream_t st) {
     const int64_t parts = slope_parts(a.rows, a.cols);
     const dim3 grid((unsigned)(strips * parts)), block(kThreads);
     const int64_t rows_of_part = tiles_of(a.rows, parts);
-    if (a.dtype == ONEBIT_BF16)
-        hipLaunchKernelGGL((slope_kernel<bf16>), grid, block, 0, st, a, groups, rows_of_part);
-    else
-        hipLaunchKernelGGL((slope_kernel<f16>), grid, block, 0, st, a, groups, rows_of_part);
+    with_act(a.act, [&](auto act) {
+        if (a.dtype == ONEBIT_BF16)
+            hipLaunchKernelGGL((slope_kernel<bf16, act.value>), grid, block, 0, st, a, groups,
+                               rows_of_part);
+        else
+            hipLaunchKernelGGL((slope_kernel<f16, act.value>), grid, block, 0, st, a, groups,
+                               rows_of_part);
+    });
     return hipGetLastError();
 }
 
