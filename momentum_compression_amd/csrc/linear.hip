@@ -456,6 +456,7 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
     if (n <= 0) return;
     const int64_t end = (part + 1) * rows_of_part < a.rows ? (part + 1) * rows_of_part : a.rows;
     float sums[8] = {};
+#pragma unroll 4
     for (int64_t r = part * rows_of_part; r < end; ++r) {
         float d[8];
         load_row8(d, (const T*)a.dy + r * a.ld_dy + c, n);

@@ -4,8 +4,8 @@
 // (group j of lane l: columns 8 (l + G j) ... + 7), so memory is read once and
 // written once: the kernels are bound by those bytes.  A workgroup takes rows in
 // turn and keeps what belongs to its columns in registers: the weights, and in
-// the backward pass the sums over rows.  Rows past kNormRow columns are
-// read again for each pass.
+// the backward pass the sums over rows.  Rows of more columns
+// than that holds are read again for each pass.
 #include <type_traits>
 
 #include "train.h"
@@ -59,6 +59,13 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2* lds) {
     }
 }
 
+// The group of lanes that the thread is in; a wave's or more as a scalar, so that
+// rows' addresses are.
+template <int G>
+__device__ __forceinline__ int group_id() {
+    return G >= 64 ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x / G)) : (int)threadIdx.x / G;
+}
+
 template <int G>
 constexpr int norm_threads() {
     return G > 256 ? G : 256;
@@ -85,10 +92,45 @@ __device__ __forceinline__ void load_params(float out[8], const void* p, bool wi
     }
 }
 
+// Eight elements of a row in whole 32-bit words: as single elements the compiler
+// gives each a register of its own.
 template <typename T>
-__device__ __forceinline__ Vec8<T> load_part(const T* row, int64_t c, int64_t cols) {
-    if (c + 8 <= cols) return load8(row + c);
-    return load_tail(row + c, cols - c);
+struct Part {
+    typedef uint32_t Words __attribute__((ext_vector_type(2 * sizeof(T))));
+    Words w;
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else return (float)__builtin_bit_cast(T, (uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+    }
+    // The same bits, of which the compiler knows nothing.
+    __device__ __forceinline__ void hide() {
+#pragma unroll
+        for (unsigned k = 0; k < 2 * sizeof(T); ++k) {
+            uint32_t x = w[k];
+            asm volatile("" : "+v"(x));
+            w[k] = x;
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ Part<T> load_whole(const T* p) {
+    typedef typename Part<T>::Words Any __attribute__((aligned(sizeof(T))));
+    return Part<T>{*reinterpret_cast<const Any*>(p)};
+}
+
+template <typename T>
+__device__ __forceinline__ Part<T> load_part(const T* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) return load_whole(row + c);
+    Part<T> x;
+    x.w = 0;
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (c + e < cols) {
+            if constexpr (sizeof(T) == 4) x.w[e] = __float_as_uint(row[c + e]);
+            else x.w[e >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + e]) << (16 * (e & 1));
+        }
+    return x;
 }
 
 template <typename T>
@@ -122,37 +164,40 @@ __global__ __launch_bounds__(norm_threads<G>()) void layer_norm_kernel(NormArgs 
     constexpr int per_block = norm_threads<G>() / G;
     __shared__ float2 lds[3][16];
     const int part = threadIdx.x % G;
-    const int64_t cols = a.cols, step = (int64_t)gridDim.x * per_block;
+    const int cols = (int)a.cols;
+    const int64_t step = (int64_t)gridDim.x * per_block;
     const float inv = 1.0f / (float)cols;
-    float w[V][8], b[V][8];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int64_t c = 8 * (part + (int64_t)G * j);
-        load_params(w[j], a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
-        load_params(b[j], a.bias, a.w_wide, a.dtype, c, cols - c, 0.0f);
-    }
-    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
-        const int64_t row = r0 + threadIdx.x / G;
-        const bool ok = row < a.rows;
+    // the next row is on its way while one is computed
+    Part<T> next[V];
+    auto fetch = [&](int64_t row) {
         const T* x = (const T*)a.x + row * a.ld_x;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = 8 * (part + G * j);
+            next[j].w = 0;
+            if (row < a.rows && c < cols) next[j] = load_part(x, c, cols);
+        }
+    };
+    fetch((int64_t)blockIdx.x * per_block + group_id<G>());
+    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + group_id<G>();
+        const bool ok = row < a.rows;
         float d[V][8];
         float sum = 0.0f, zero = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
-            Vec8<T> v = {};
-            if (ok && c < cols) v = load_part(x, c, cols);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[j][e] = (float)v.v[e];
+            for (int e = 0; e < 8; ++e) d[j][e] = next[j][e];
             sum += ((d[j][0] + d[j][1]) + (d[j][2] + d[j][3])) +
                    ((d[j][4] + d[j][5]) + (d[j][6] + d[j][7]));
         }
+        fetch(row + step);
         row_sums<G>(sum, zero, lds[0]);
         const float shift = sum * inv;
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
+            const int c = 8 * (part + G * j);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 d[j][e] = c + e < cols ? d[j][e] - shift : 0.0f;
@@ -169,12 +214,16 @@ __global__ __launch_bounds__(norm_threads<G>()) void layer_norm_kernel(NormArgs 
         T* y = (T*)a.y + row * a.ld_y;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
+            const int c = 8 * (part + G * j);
             if (!ok || c >= cols) continue;
-            float o[8];
+            // from the caches for each row: in registers they would halve the
+            // rows under way
+            float w[8], b[8], o[8];
+            load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+            load_params(b, a.bias, a.w_wide, a.dtype, c, cols - c, 0.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = __builtin_fmaf((d[j][e] - m.rest) * m.rstd, w[j][e], b[j][e]);
+                o[e] = __builtin_fmaf((d[j][e] - m.rest) * m.rstd, w[e], b[e]);
             store_part(y, c, cols, o);
         }
         if (G > 64) __syncthreads();  // lds is read
@@ -194,21 +243,21 @@ __global__ __launch_bounds__(kLong) void layer_norm_long_kernel(NormArgs a) {
         T* y = (T*)a.y + row * a.ld_y;
         float sum = 0.0f, zero = 0.0f;
         for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
-            const Vec8<T> v = load_part(x, c, cols);
+            const Part<T> v = load_part(x, c, cols);
             float s = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += (float)v.v[e];
+            for (int e = 0; e < 8; ++e) s += v[e];
             sum += s;
         }
         row_sums<kLong>(sum, zero, lds[0]);
         const float shift = sum * inv;
         float s1 = 0.0f, s2 = 0.0f;
         for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
-            const Vec8<T> v = load_part(x, c, cols);
+            const Part<T> v = load_part(x, c, cols);
             float p = 0.0f, q = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = c + e < cols ? (float)v.v[e] - shift : 0.0f;
+                const float d = c + e < cols ? v[e] - shift : 0.0f;
                 p += d;
                 q = __builtin_fmaf(d, d, q);
             }
@@ -222,13 +271,13 @@ __global__ __launch_bounds__(kLong) void layer_norm_long_kernel(NormArgs a) {
             if (a.rstd) a.rstd[row] = m.rstd;
         }
         for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
-            const Vec8<T> v = load_part(x, c, cols);
+            const Part<T> v = load_part(x, c, cols);
             float w[8], b[8], o[8];
             load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
             load_params(b, a.bias, a.w_wide, a.dtype, c, cols - c, 0.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = __builtin_fmaf((((float)v.v[e] - m.shift) - m.rest) * m.rstd, w[e], b[e]);
+                o[e] = __builtin_fmaf(((v[e] - m.shift) - m.rest) * m.rstd, w[e], b[e]);
             store_part(y, c, cols, o);
         }
         __syncthreads();  // lds is read
@@ -239,67 +288,106 @@ __global__ __launch_bounds__(kLong) void layer_norm_long_kernel(NormArgs a) {
 // dx = rstd (u - mean(u) - h mean(u h)) with u = dy w, h = (x - mean) rstd, and
 // the sums of dy h and dy over the workgroup's rows, kept by columns.  Groups of
 // lanes that hold the same columns are added at the end, in their order.
+//
+// Where a row ends inside a lane's eight columns, the lane reads the row's last
+// eight, and those that belong to the lane before it have weight 0 here (no
+// branches to load single elements, which cost 40 registers for every eight
+// columns).
 template <typename T, int G, int V>
-__global__ __launch_bounds__(norm_threads<G>()) void layer_norm_grad_kernel(NormArgs a) {
+__global__ __launch_bounds__(norm_threads<G>(), 2) void layer_norm_grad_kernel(NormArgs a) {
     constexpr int threads = norm_threads<G>(), per_block = threads / G;
-    __shared__ float2 lds[2][16];
+    __shared__ float2 lds[16];
     __shared__ float share[per_block > 1 ? threads * 8 * V : 1];
-    const int part = threadIdx.x % G;
-    const int64_t cols = a.cols, step = (int64_t)gridDim.x * per_block;
+    const int part = threadIdx.x % G, cols = (int)a.cols;
+    const int64_t step = (int64_t)gridDim.x * per_block;
     const float inv = 1.0f / (float)cols;
+    int at[V], low[V], high[V];  // the lane's columns at + low ... at + high - 1
     float w[V][8], dw[V][8] = {}, db[V][8] = {};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t c = 8 * (part + (int64_t)G * j);
-        load_params(w[j], a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
+        const int c = 8 * (part + G * j);
+        at[j] = G > 1 && c + 8 > cols ? cols - 8 : c;
+        low[j] = c - at[j];
+        high[j] = c >= cols ? 0 : G > 1 ? 8 : cols;
+        load_params(w[j], a.weight, a.w_wide, a.dtype, at[j], high[j], 1.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[j][e] = e >= low[j] && e < high[j] ? w[j][e] : 0.0f;
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
-        const int64_t row = r0 + threadIdx.x / G;
+    // the next row is on its way while one is computed, where there is room for it
+    constexpr bool ahead = V * sizeof(T) <= 8;
+    Part<T> xv[V], gv[V], xn[V], gn[V];
+    float mean = 0.0f, rstd = 0.0f, mean_next = 0.0f, rstd_next = 0.0f;
+    auto fetch = [&](int64_t row, Part<T>(&xs)[V], Part<T>(&gs)[V], float& m, float& r) {
         const bool ok = row < a.rows;
         const T* x = (const T*)a.x + row * a.ld_x;
         const T* dy = (const T*)a.dy + row * a.ld_dy;
-        const float mean = ok ? a.mean[row] : 0.0f, rstd = ok ? a.rstd[row] : 0.0f;
-        Vec8<T> xv[V], gv[V];
+        m = ok ? a.mean[row] : 0.0f;
+        r = ok ? a.rstd[row] : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
-            xv[j] = gv[j] = Vec8<T>{};
-            if (ok && c < cols) {
-                xv[j] = load_part(x, c, cols);
-                gv[j] = load_part(dy, c, cols);
+            xs[j].w = gs[j].w = 0;
+            if (ok && high[j] > 0) {
+                xs[j] = G > 1 ? load_whole(x + at[j]) : load_part(x, 0, cols);
+                gs[j] = G > 1 ? load_whole(dy + at[j]) : load_part(dy, 0, cols);
             }
+        }
+    };
+    if (ahead)
+        fetch((int64_t)blockIdx.x * per_block + group_id<G>(), xn, gn, mean_next, rstd_next);
+    for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + group_id<G>();
+        const bool ok = row < a.rows;
+        if (ahead) {
+            mean = mean_next;
+            rstd = rstd_next;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                xv[j] = xn[j];
+                gv[j] = gn[j];
+            }
+            fetch(row + step, xn, gn, mean_next, rstd_next);
+        } else {
+            fetch(row, xv, gv, mean, rstd);
         }
         float su = 0.0f, suh = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = c + e < cols ? ((float)xv[j].v[e] - mean) * rstd : 0.0f;
-                const float g = (float)gv[j].v[e], u = g * w[j][e];
+                const float h = (xv[j][e] - mean) * rstd, g = gv[j][e], u = g * w[j][e];
                 dw[j][e] = __builtin_fmaf(g, h, dw[j][e]);
                 db[j][e] += g;
                 su += u;
                 suh = __builtin_fmaf(u, h, suh);
             }
+            __builtin_amdgcn_sched_barrier(0);  // one group's values at a time
         }
         if (!a.dx) continue;  // the same for all
-        row_sums<G>(su, suh, lds[0]);
+        row_sums<G>(su, suh, lds);
         su *= inv;
         suh *= inv;
         T* dx = (T*)a.dx + row * a.ld_dx;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = 8 * (part + (int64_t)G * j);
-            if (!ok || c >= cols) continue;
+            if (!ok || high[j] == 0) continue;
+            // what the first pass made of them is not kept: registers are rows
+            // under way
+            xv[j].hide();
+            gv[j].hide();
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = ((float)xv[j].v[e] - mean) * rstd;
-                const float u = (float)gv[j].v[e] * w[j][e];
+                const float h = (xv[j][e] - mean) * rstd, u = gv[j][e] * w[j][e];
                 o[e] = rstd * __builtin_fmaf(-h, suh, u - su);
             }
-            store_part(dx, c, cols, o);
+            if (low[j] == 0 && high[j] == 8) {
+                store8(dx + at[j], o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= low[j] && e < high[j]) dx[at[j] + e] = (T)o[e];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (G > 64) __syncthreads();  // lds is read
     }
@@ -307,25 +395,16 @@ __global__ __launch_bounds__(norm_threads<G>()) void layer_norm_grad_kernel(Norm
     float* to = a.partials + (int64_t)blockIdx.x * 2 * cols;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        if (per_block == 1) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int64_t c = 8 * (part + (int64_t)G * j);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < cols) to[s * cols + c + e] = s ? db[j][e] : dw[j][e];
-            }
-            continue;
-        }
-        if (s) __syncthreads();  // the first sums are read
+        if (s && per_block > 1) __syncthreads();  // the first sums are read
+        float* out = per_block > 1 ? share + (group_id<G>()) * (8 * G * V) : to + s * cols;
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                share[(threadIdx.x / G) * (8 * G * V) + 8 * (part + G * j) + e] =
-                    s ? db[j][e] : dw[j][e];
+                if (e >= low[j] && e < high[j]) out[at[j] + e] = s ? db[j][e] : dw[j][e];
+        if (per_block == 1) continue;
         __syncthreads();
-        for (int c = threadIdx.x; c < 8 * G * V && c < cols; c += threads) {
+        for (int c = threadIdx.x; c < cols; c += threads) {
             float t = 0.0f;
             for (int p = 0; p < per_block; ++p) t += share[p * (8 * G * V) + c];
             to[s * cols + c] = t;
@@ -344,13 +423,13 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_cols_kernel(NormArgs
     const int64_t end = (part + 1) * rows_of_part < a.rows ? (part + 1) * rows_of_part : a.rows;
     float dw[8] = {}, db[8] = {};
     for (int64_t row = part * rows_of_part; row < end; ++row) {
-        const Vec8<T> xv = load_part((const T*)a.x + row * a.ld_x, c, cols);
-        const Vec8<T> gv = load_part((const T*)a.dy + row * a.ld_dy, c, cols);
+        const Part<T> xv = load_part((const T*)a.x + row * a.ld_x, c, cols);
+        const Part<T> gv = load_part((const T*)a.dy + row * a.ld_dy, c, cols);
         const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float g = (float)gv.v[e];
-            dw[e] = __builtin_fmaf(g, ((float)xv.v[e] - mean) * rstd, dw[e]);
+            const float g = gv[e];
+            dw[e] = __builtin_fmaf(g, (xv[e] - mean) * rstd, dw[e]);
             db[e] += g;
         }
     }
@@ -375,13 +454,13 @@ __global__ __launch_bounds__(kLong) void layer_norm_grad_rows_kernel(NormArgs a)
         const float mean = a.mean[row], rstd = a.rstd[row];
         float su = 0.0f, suh = 0.0f;
         for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
-            const Vec8<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
+            const Part<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
             float w[8], p = 0.0f, q = 0.0f;
             load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = c + e < cols ? ((float)xv.v[e] - mean) * rstd : 0.0f;
-                const float u = (float)gv.v[e] * w[e];
+                const float h = c + e < cols ? (xv[e] - mean) * rstd : 0.0f;
+                const float u = gv[e] * w[e];
                 p += u;
                 q = __builtin_fmaf(u, h, q);
             }
@@ -392,13 +471,13 @@ __global__ __launch_bounds__(kLong) void layer_norm_grad_rows_kernel(NormArgs a)
         su *= inv;
         suh *= inv;
         for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * kLong) {
-            const Vec8<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
+            const Part<T> xv = load_part(x, c, cols), gv = load_part(dy, c, cols);
             float w[8], o[8];
             load_params(w, a.weight, a.w_wide, a.dtype, c, cols - c, 1.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = ((float)xv.v[e] - mean) * rstd;
-                o[e] = rstd * __builtin_fmaf(-h, suh, (float)gv.v[e] * w[e] - su);
+                const float h = (xv[e] - mean) * rstd;
+                o[e] = rstd * __builtin_fmaf(-h, suh, gv[e] * w[e] - su);
             }
             store_part(dx, c, cols, o);
         }
@@ -416,8 +495,17 @@ __global__ __launch_bounds__(1024) void column_join_kernel(const float* partials
     const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
     const int wave = threadIdx.x >> 6;
     double t = 0.0;
-    if (c < n)
-        for (int64_t p = wave; p < parts; p += 16) t += partials[p * n + c];
+    if (c < n) {
+        int64_t p = wave;
+        for (; p + 7 * 16 < parts; p += 8 * 16) {  // eight loads at once
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = partials[(p + 16 * k) * n + c];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t += v[k];
+        }
+        for (; p < parts; p += 16) t += partials[p * n + c];
+    }
     sums[wave][threadIdx.x & 63] = t;
     __syncthreads();
     if (wave != 0 || c >= n) return;
@@ -436,7 +524,11 @@ hipError_t with_type(int32_t dtype, F&& f) {
     return hipGetLastError();
 }
 
-// The lanes of a row and its groups of columns a lane.
+// The lanes of a row and its groups of columns a lane; {0, 0}: a row that is read
+// again for each pass.  The fewer groups the more rows are under way; the backward
+// pass keeps 24 registers a group for its sums and weights, and with 1024 lanes of
+// two groups (not enough registers) takes 122 us where reading again takes 90
+// (2048 x 16384 bf16).
 struct Shape {
     int G, V;
 };
@@ -446,16 +538,19 @@ Shape shape_of(int64_t rows, int64_t cols, bool grad) {
     if (cols <= 32) return {4, 1};
     if (cols <= 128) return {16, 1};
     if (cols <= 512) return {64, 1};
+    // few rows: a workgroup each
     if (!grad && rows <= 1024 && cols <= 2048) return {256, 1};
     if (cols <= 1024) return {64, 2};
-    if (cols <= 2048) return {64, 4};
+    if (cols <= 2048) return grad ? Shape{256, 1} : Shape{64, 4};
     if (cols <= 4096) return {256, 2};
-    if (cols <= 8192) return {256, 4};
-    if (cols <= kNormRow) return {1024, 2};
+    if (cols <= 8192) return grad ? Shape{1024, 1} : Shape{256, 4};
+    if (cols <= 16384 && !grad) return {1024, 2};
     return {0, 0};
 }
 
-constexpr int64_t kNormBlocks = 512;      // workgroups of a backward pass, at most
+// Workgroups at most.  The backward pass's sums are joined: with 512, 1024 and 2048
+// of them 16384 x 2048 takes 49, 53 and 64 us.
+constexpr int64_t kForwardBlocks = 4096, kNormBlocks = 512;
 constexpr int64_t kLongParts = 64;        // parts of the rows, at most
 
 template <typename F>
@@ -472,6 +567,7 @@ void with_shape(const Shape& s, F&& f) {
     ONEBIT_SHAPE(256, 1);
     ONEBIT_SHAPE(256, 2);
     ONEBIT_SHAPE(256, 4);
+    ONEBIT_SHAPE(1024, 1);
     ONEBIT_SHAPE(1024, 2);
 #undef ONEBIT_SHAPE
 }
@@ -509,7 +605,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st) {
         }
         with_shape(s, [&](auto G, auto V) {
             hipLaunchKernelGGL((layer_norm_kernel<T, G.value, V.value>),
-                               dim3((unsigned)row_blocks(s, a.rows, 2048)),
+                               dim3((unsigned)row_blocks(s, a.rows, kForwardBlocks)),
                                dim3(norm_threads<G.value>()), 0, st, a);
         });
     });

@@ -103,8 +103,6 @@ hipError_t launch_bias_join(const float* partials, const int32_t* map, float* dt
                             hipStream_t st);
 
 // ---------------------------------------------------------------- layer norm
-constexpr int64_t kNormRow = 16384;  // columns of a row that stays in registers
-
 struct NormArgs {
     const void *x, *dy;
     void *y, *dx;            // dx may be nullptr
