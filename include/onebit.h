@@ -746,10 +746,9 @@ size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward)
  *   (u + 1/2) / 65536 of the format's step,  u = half word J & 7 (low half of a
  *   word first) of Philox4x32-10(counter = (J / 8, i, 0, t), key = (seed lo32,
  *   seed hi32 xor 0x41444D57)),
- * so that its mean over the draws is the value (below the format's normal numbers
- * it counts to 2^-20 of a step).  A v above 0 gets the smallest
- * number above 0 at least; what is not finite becomes NaN.  Zero codes and any
- * scale are a fresh state.
+ * so that its mean over the draws is the value.  A v above 0 gets the smallest
+ * number above 0 at least; an infinite m becomes NaN, an infinite v stays so.  Zero
+ * codes and any scale are a fresh state.
  *
  * The tensors are given once, in a plan: adamw_plan writes it to host memory, and
  * the caller copies its bytes to the device (256-byte aligned) and keeps them

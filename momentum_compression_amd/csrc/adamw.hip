@@ -12,8 +12,8 @@
 // mantissa give sqrt(v) the steps that three give m).  Values are rounded up or
 // down with the probabilities that keep their mean: with rounding to nearest a
 // state that decays by 1 - beta2 = 0.001 a step would stay where it is for good.
-// The draw is added below the kept bits of the binary32 pattern and the rest cut
-// off, which is exact for every binade.
+// The conversion adds the draw below the kept bits and cuts the rest off, which is
+// exact for every binade and below the normal numbers.
 #include <type_traits>
 
 #include "philox.h"
@@ -23,6 +23,7 @@ namespace onebit {
 namespace {
 
 constexpr uint32_t kTag = 0x41444D57u;
+constexpr uint32_t kInfinite = 0x7F800000u;
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
@@ -43,42 +44,47 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
     return h[0] > h[1] ? h[0] : h[1];
 }
 
-// A format's codes: normal values from 2^kLeast on, kDigits bits of mantissa, the
-// block's largest value in [2^kTop, 2^(kTop + 1)).
-template <int TOP, int LEAST, int DIGITS>
-struct Code {
-    static constexpr int kDrop = 23 - DIGITS;
-    static constexpr uint32_t kNan = DIGITS == 3 ? 0x7F : 0x7E;
+// Exponent (with the bias of binary32) of a block's power of two, which puts the
+// pattern of its largest finite magnitude into [2^TOP, 2^(TOP + 1)).
+constexpr uint32_t kTopM = 7, kTopV = 14;
+template <uint32_t TOP>
+__device__ __forceinline__ uint32_t scale_exponent(uint32_t most) {
+    const uint32_t e = most >> 23;
+    return (e > TOP + 1 ? e : TOP + 1) - TOP;
+}
 
-    // Exponent of the block's power of two (with the bias of binary32), from the
-    // pattern of its largest finite magnitude.
-    static __device__ __forceinline__ uint32_t scale_exponent(uint32_t most) {
-        const uint32_t e = most >> 23;
-        return (e > TOP + 1 ? e : TOP + 1) - TOP;
-    }
-    // y >= 0, below 2^(TOP + 1); 16 bits of draw
-    static __device__ __forceinline__ uint32_t encode(float y, uint32_t draw) {
-        const bool tiny = y < __uint_as_float((uint32_t)(127 + LEAST) << 23);
-        // below the normal values the grid is that of the first binade: there the
-        // sum's pattern counts it
-        const float z = tiny ? y + __uint_as_float((uint32_t)(127 + LEAST) << 23) : y;
-        const uint32_t noise = (draw << (kDrop - 16)) + (1u << (kDrop - 17)) -
-                               ((uint32_t)(126 + LEAST) << 23);
-        return ((__float_as_uint(z) + noise) >> kDrop) - (tiny ? 1u << DIGITS : 0u);
-    }
-    static __device__ __forceinline__ float decode(uint32_t code) {
-        const uint32_t at = code & 0x7F;
-        const float y = __uint_as_float(at << kDrop) *
-                        __uint_as_float((uint32_t)(253 + LEAST) << 23);
-        const float s = __uint_as_float(__float_as_uint(y) | (code & 0x80) << 24);
-        return DIGITS == 3 ? (at == 0x7F ? __builtin_nanf("") : s)
-                           : (at >= 0x7C ? (at == 0x7C ? INFINITY : __builtin_nanf("")) : s);
-    }
-};
-using CodeM = Code<7, -6, 3>;
-using CodeV = Code<14, -14, 2>;
+__device__ __forceinline__ float power_of_two(uint32_t e) { return __uint_as_float(e << 23); }
 
-__device__ __forceinline__ bool finite(uint32_t magnitude) { return magnitude < 0x7F800000u; }
+// The values of four codes.
+template <bool M>
+__device__ __forceinline__ void decode4(float out[4], uint32_t codes, float scale) {
+    const auto lo = M ? __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false)
+                      : __builtin_amdgcn_cvt_pk_f32_bf8((int)codes, false);
+    const auto hi = M ? __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true)
+                      : __builtin_amdgcn_cvt_pk_f32_bf8((int)codes, true);
+    out[0] = lo[0] * scale;
+    out[1] = lo[1] * scale;
+    out[2] = hi[0] * scale;
+    out[3] = hi[1] * scale;
+}
+
+// Square root of a number within 2^-100 ... 2^90, correctly rounded: one correction
+// from the exact remainder (compared with sqrtf for every mantissa of both
+// parities of the exponent, over that range).  Eight issue slots to its twenty.
+__device__ __forceinline__ float root_of(float v) {
+    const float y = __builtin_amdgcn_rsqf(v), s = v * y;
+    return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
+}
+
+// m / d, correctly rounded, where neither they nor the quotient come near the ends
+// of the range: the usual sequence without its scaling.
+__device__ __forceinline__ float quotient_of(float m, float d) {
+    const float y0 = __builtin_amdgcn_rcpf(d);
+    const float y = __builtin_fmaf(__builtin_fmaf(-d, y0, 1.0f), y0, y0);
+    float q = m * y;
+    q = __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
+    return __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
+}
 
 // Four consecutive elements at any element address, `n` of them there.
 template <typename T>
@@ -127,7 +133,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t n) {
 
 __device__ __forceinline__ void store_codes(uint8_t* p, uint32_t x, int64_t n) {
     if (n >= 4) {
-        __builtin_nontemporal_store(x, reinterpret_cast<u32_any*>(p));
+        *reinterpret_cast<u32_any*>(p) = x;  // a store past the caches would go by bytes
         return;
     }
 #pragma unroll
@@ -167,28 +173,51 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs a) {
             load4(g[s], (const G*)t.g + at, n);
             if (EIGHT) {
                 const float ms = t.m_scale[first / kStateBlock], vs = t.v_scale[first / kStateBlock];
-                const uint32_t mc = load_codes((const uint8_t*)t.m + at, n);
-                const uint32_t vc = load_codes((const uint8_t*)t.v + at, n);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    m[s][e] = CodeM::decode(mc >> (8 * e) & 0xFF) * ms;
-                    v[s][e] = CodeV::decode(vc >> (8 * e) & 0xFF) * vs;
-                }
+                decode4<true>(m[s], load_codes((const uint8_t*)t.m + at, n), ms);
+                decode4<false>(v[s], load_codes((const uint8_t*)t.v + at, n), vs);
             } else {
                 load4(m[s], (const float*)t.m + at, n);
                 load4(v[s], (const float*)t.v + at, n);
             }
         }
+        float m_most[kSets], v_most[kSets];  // of the lane, NaN left out
+        uint32_t m_least = ~0u, v_least = ~0u, v_last = 0u;  // patterns; zeros of m left out
 #pragma unroll
         for (int s = 0; s < kSets; ++s) {
-            const int64_t at = base + s * kStateBlock + 4 * lane, n = t.n - at;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (a.g_scale) g[s][e] = g[s][e] * g_scale;
                 m[s][e] = a.beta1 * m[s][e] + omb1 * g[s][e];
                 v[s][e] = a.beta2 * v[s][e] + omb2 * (g[s][e] * g[s][e]);
-                x[s][e] = x[s][e] * decay - rate * (m[s][e] / (sqrtf(v[s][e]) * a.root + a.eps));
+                const uint32_t mb = (__float_as_uint(m[s][e]) & 0x7FFFFFFFu) - 1u;
+                const uint32_t vb = __float_as_uint(v[s][e]);
+                m_least = mb < m_least ? mb : m_least;
+                v_least = vb < v_least ? vb : v_least;
+                v_last = vb > v_last ? vb : v_last;
             }
+            m_most[s] = fmaxf(fmaxf(__builtin_fabsf(m[s][0]), __builtin_fabsf(m[s][1])),
+                              fmaxf(__builtin_fabsf(m[s][2]), __builtin_fabsf(m[s][3])));
+            v_most[s] = fmaxf(fmaxf(v[s][0], v[s][1]), fmaxf(v[s][2], v[s][3]));
+        }
+        const bool usual = m_least >= (27u << 23) - 1u && fmaxf(m_most[0], m_most[1]) <= 0x1p90f &&
+                           v_least >= 27u << 23 && v_last <= 217u << 23;
+        if (__all(usual)) {
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[s][e] = x[s][e] * decay -
+                              rate * quotient_of(m[s][e], root_of(v[s][e]) * a.root + a.eps);
+        } else {
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[s][e] = x[s][e] * decay - rate * (m[s][e] / (sqrtf(v[s][e]) * a.root + a.eps));
+        }
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const int64_t at = base + s * kStateBlock + 4 * lane, n = t.n - at;
             if (n <= 0) continue;
             store4(t.x + at, x[s], n);
             if (sizeof(C) == 2) store4((C*)t.copy + at, x[s], n);
@@ -216,44 +245,48 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs a) {
             const int64_t first = base + s * kStateBlock, at = first + 4 * lane, n = t.n - at;
             if (first >= t.n) continue;  // the same for the wave
             // elements past the tensor's end are 0 and count for nothing
-            uint32_t m_most = 0, v_most = 0;
+            uint32_t mm = block_max(__float_as_uint(m_most[s]));
+            uint32_t vm = block_max(__float_as_uint(v_most[s]));
+            if (__builtin_expect(mm >= kInfinite || vm >= kInfinite, 0)) {
+                // infinities count for nothing either
+                mm = vm = 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t mb = __float_as_uint(m[s][e]) & 0x7FFFFFFFu;
-                const uint32_t vb = __float_as_uint(v[s][e]) & 0x7FFFFFFFu;
-                m_most = finite(mb) && mb > m_most ? mb : m_most;
-                v_most = finite(vb) && vb > v_most ? vb : v_most;
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t mb = __float_as_uint(m[s][e]) & 0x7FFFFFFFu;
+                    const uint32_t vb = __float_as_uint(v[s][e]) & 0x7FFFFFFFu;
+                    mm = mb < kInfinite && mb > mm ? mb : mm;
+                    vm = vb < kInfinite && vb > vm ? vb : vm;
+                }
+                mm = block_max(mm);
+                vm = block_max(vm);
             }
-            const uint32_t me = CodeM::scale_exponent(block_max(m_most));
-            const uint32_t ve = CodeV::scale_exponent(block_max(v_most));
-            const float m_inv = __uint_as_float((254 - me) << 23);
-            const float v_inv = __uint_as_float((254 - ve) << 23);
-            uint32_t mc = 0, vc = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // one draw for both states: each alone keeps its mean
+            const uint32_t me = scale_exponent<kTopM>(mm), ve = scale_exponent<kTopV>(vm);
+            const float m_inv = power_of_two(254 - me), v_inv = power_of_two(254 - ve);
+            int mc = 0, vc = 0;
+            auto encode = [&](auto at_byte) {
+                constexpr int e = decltype(at_byte)::value;
+                // one draw for both states: each alone keeps its mean.  Half a
+                // draw's step is added, so that 0 and 65535 are alike.
                 const uint32_t word = draws[s][e >> 1];
-                const uint32_t draw = (e & 1) ? word >> 16 : word & 0xFFFFu;
-                const uint32_t bits = __float_as_uint(m[s][e]);
-                uint32_t c = finite(bits & 0x7FFFFFFFu)
-                                 ? CodeM::encode(__uint_as_float(bits & 0x7FFFFFFFu) * m_inv, draw)
-                                 : CodeM::kNan;
-                c |= (bits >> 24) & 0x80;
-                mc |= c << (8 * e);
+                const uint32_t noise = ((e & 1) ? word & 0xFFFF0000u : word << 16) | 0x8000u;
+                mc = __builtin_amdgcn_cvt_sr_fp8_f32(m[s][e] * m_inv, noise, mc, e);
                 // a variance above 0 stays above 0, or its element's next step
                 // would be divided by eps alone
-                uint32_t d = CodeV::encode(v[s][e] * v_inv, draw);
-                d = v[s][e] > 0.0f && d == 0u ? 1u : d;
-                d = finite(__float_as_uint(v[s][e])) ? d : CodeV::kNan;
-                vc |= d << (8 * e);
-            }
+                const float y = v[s][e] * v_inv;
+                vc = __builtin_amdgcn_cvt_sr_bf8_f32(
+                    v[s][e] > 0.0f && y < 0x1p-16f ? 0x1p-16f : y, noise, vc, e);
+            };
+            encode(std::integral_constant<int, 0>{});
+            encode(std::integral_constant<int, 1>{});
+            encode(std::integral_constant<int, 2>{});
+            encode(std::integral_constant<int, 3>{});
             if (n > 0) {
-                store_codes((uint8_t*)t.m + at, mc, n);
-                store_codes((uint8_t*)t.v + at, vc, n);
+                store_codes((uint8_t*)t.m + at, (uint32_t)mc, n);
+                store_codes((uint8_t*)t.v + at, (uint32_t)vc, n);
             }
             if (lane == 0) {
-                t.m_scale[first / kStateBlock] = __uint_as_float(me << 23);
-                t.v_scale[first / kStateBlock] = __uint_as_float(ve << 23);
+                t.m_scale[first / kStateBlock] = power_of_two(me);
+                t.v_scale[first / kStateBlock] = power_of_two(ve);
             }
         }
     }

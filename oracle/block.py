@@ -124,9 +124,6 @@ def encode(x, u, digits, positive):
         e = max(math.frexp(most)[1] - 1 - top if most > 0 else -126, -126)
         scales[b] = F32(math.ldexp(1.0, e))
         y = np.ldexp(np.abs(np.where(ok, v, 0)).astype(np.float64), -e)
-        # below the normal numbers the value counts to 2^-23 of the least of them
-        low = math.ldexp(1.0, least)
-        y = np.where(y < low, (y + low).astype(F32).astype(np.float64) - low, y)
         step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, least) - digits)
         r = np.floor(y / step + (u[s] + 0.5) / 65536.0) * step
         f, k = np.frexp(r)
@@ -136,7 +133,7 @@ def encode(x, u, digits, positive):
         c = (field << digits) + (whole.astype(np.int64) & ((1 << digits) - 1))
         if positive:
             c = np.where((v > 0) & (c == 0), 1, c)
-        c = np.where(ok, c, nan)
+        c = np.where(ok, c, np.where(np.isinf(v) & positive, 0x7C, nan))
         codes[s] = c | (np.signbit(v).astype(np.int64) << 7 if not positive else 0)
     return codes, scales
 
