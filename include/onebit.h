@@ -697,7 +697,8 @@ typedef enum {
  * residual itself (same ld); where an output's rows lie over those of another
  * argument otherwise, as far as strides show, the call is refused.  With K = 0 z
  * is the bias; with M or N = 0 sums over nothing are 0.
- * ws: at least linear_workspace_bytes(...) bytes, 256-byte aligned, scratch.
+ * ws: at least linear_workspace_bytes(...) bytes, 256-byte aligned, scratch (a
+ * forward call of up to 64 rows takes NULL too).
  */
 typedef struct linear_args {
     int32_t dtype, activation;

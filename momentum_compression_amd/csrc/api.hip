@@ -989,12 +989,14 @@ LinearSizes linear_sizes(int64_t M, int64_t N, int64_t K, bool backward) {
     z.x = round_up((size_t)M * padded(K) * 2);
     z.w = round_up((size_t)N * padded(K) * 2);
     if (!backward) {
-        z.parts = round_up(product_plan(M, N, K).bytes);
+        if (product_few(M)) return LinearSizes{};
+        z.parts = round_up(product_plan(M, N, K, true, true).bytes);
         return z;
     }
     z.dz = round_up((size_t)M * padded(N) * 2);
     z.sums = round_up((size_t)slope_parts(M, N) * N * sizeof(float));
-    const size_t dx = product_plan(M, K, N).bytes, dw = product_plan(N, K, M).bytes;
+    const size_t dx = product_plan(M, K, N, false, true).bytes,
+                 dw = product_plan(N, K, M, false, false).bytes;
     z.parts = round_up(dx > dw ? dx : dw);
     return z;
 }
@@ -1039,15 +1041,15 @@ bool lies_over(const Matrix& out, const Matrix& in) {
            (down + 1 < (uint64_t)first.rows && pitch - right < (uint64_t)second.cols * second.size);
 }
 
-// The operand as the product reads it, laid out anew at `room` if need be.
-hipError_t operand(ProductIn& in, const void* p, int64_t ld, int64_t rows, int64_t cols, char* room,
-                   hipStream_t st) {
-    if (rows == 0 || cols == 0 || whole_chunks(p, ld, rows, cols)) {
-        in = ProductIn{p, rows <= 1 ? padded(cols) : ld};
-        return hipSuccess;
-    }
-    in = ProductIn{room, padded(cols)};
-    return launch_pad_rows(p, ld, room, padded(cols), rows, cols, st);
+// The operand as the product reads it; `anew` says how it is laid out at `room`
+// first, if need be.
+ProductIn operand(const void* p, int64_t ld, int64_t rows, int64_t cols, char* room,
+                  PadRows& anew) {
+    anew = PadRows{};
+    if (rows == 0 || cols == 0 || whole_chunks(p, ld, rows, cols))
+        return ProductIn{p, rows <= 1 ? padded(cols) : ld};
+    anew = PadRows{p, room, ld, padded(cols), rows, cols};
+    return ProductIn{room, padded(cols)};
 }
 
 }  // namespace
@@ -1080,15 +1082,13 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
         if (lies_over(y, in) || lies_over(pre, in)) return ONEBIT_E_ARG;
     if (lies_over(y, pre) || lies_over(pre, r) || (!in_place && lies_over(y, r)))
         return ONEBIT_E_ARG;
-    if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 0)) return ONEBIT_E_WORKSPACE;
-    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    if (!product_few(M)) {
+        if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 0)) return ONEBIT_E_WORKSPACE;
+        if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    }
     const LinearSizes z = linear_sizes(M, N, K, false);
     char* room = static_cast<char*>(ws);
     drop_stale_error();
-    ProductIn xs, wi;
-    hipError_t e = operand(xs, a->x, a->ld_x, M, K, room, stream);
-    if (e == hipSuccess) e = operand(wi, a->w, a->ld_w, N, K, room + z.x, stream);
-    if (e != hipSuccess) return ONEBIT_E_HIP;
     ProductOut o = {};
     o.out = a->y;
     o.bias = a->bias;
@@ -1102,6 +1102,13 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
     o.type = a->dtype;
     o.act = a->activation;
     o.bias_wide = a->bias_dtype == ONEBIT_F32;
+    if (product_few(M))
+        return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w},
+                                             ProductIn{a->x, a->ld_x}, K, o, stream));
+    PadRows x_anew, w_anew;
+    const ProductIn xs = operand(a->x, a->ld_x, M, K, room, x_anew);
+    const ProductIn wi = operand(a->w, a->ld_w, N, K, room + z.x, w_anew);
+    if (launch_pad_rows(x_anew, w_anew, stream) != hipSuccess) return ONEBIT_E_HIP;
     return hip_status(launch_product(a->dtype, wi, true, xs, true, K, o,
                                      reinterpret_cast<float*>(room + z.x + z.w), stream));
 }
@@ -1162,20 +1169,22 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
             e = launch_column_join(sums, M > 0 ? slope_parts(M, N) : 0, N, N, a->dbias, nullptr,
                                    a->accumulate != 0, stream);
     }
-    if (e == hipSuccess && a->dx && M > 0 && K > 0) {
-        ProductIn wi;
-        e = operand(wi, a->w, a->ld_w, N, K, w_room, stream);
+    const bool want_dx = a->dx && M > 0 && K > 0, want_dw = a->dw && N > 0 && K > 0;
+    PadRows x_anew = {}, w_anew = {};
+    ProductIn xs = {}, wi = {};
+    if (want_dx) wi = operand(a->w, a->ld_w, N, K, w_room, w_anew);
+    if (want_dw) xs = operand(a->x, a->ld_x, M, K, x_room, x_anew);
+    if (e == hipSuccess) e = launch_pad_rows(x_anew, w_anew, stream);
+    if (e == hipSuccess && want_dx) {
         ProductOut o = {};
         o.out = a->dx;
         o.rows = M;
         o.cols = K;
         o.ld = a->ld_dx;
         o.type = a->dtype;
-        if (e == hipSuccess) e = launch_product(a->dtype, wi, false, dz, true, N, o, parts, stream);
+        e = launch_product(a->dtype, wi, false, dz, true, N, o, parts, stream);
     }
-    if (e == hipSuccess && a->dw && N > 0 && K > 0) {
-        ProductIn xs;
-        e = operand(xs, a->x, a->ld_x, M, K, x_room, stream);
+    if (e == hipSuccess && want_dw) {
         ProductOut o = {};
         o.out = a->dw;
         o.rows = N;
@@ -1183,8 +1192,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
         o.ld = a->ld_dw;
         o.type = a->dw_dtype;
         o.accumulate = a->accumulate != 0;
-        if (e == hipSuccess)
-            e = launch_product(a->dtype, xs, false, dz, false, M, o, parts, stream);
+        e = launch_product(a->dtype, xs, false, dz, false, M, o, parts, stream);
     }
     return hip_status(e);
 }

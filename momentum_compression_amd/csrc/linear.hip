@@ -23,22 +23,39 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 constexpr int kDeep = 64;  // of the summed index a tile: rows of a whole cache line
+constexpr int64_t kCUs = 256;
 
-// Eight values of a row of the result, `n` of them inside.
+// Eight values of a row of the result, `n` of them inside, at any element address.
+// Whole 32-bit words are moved: what single elements are merged with is moved by
+// elements.
+template <typename S>
+struct Words8 {
+    typedef uint32_t Any __attribute__((ext_vector_type(2 * sizeof(S)), aligned(sizeof(S))));
+};
+
 template <typename S>
 __device__ __forceinline__ void load_row8(float out[8], const S* p, int64_t n) {
-    const Vec8<S> x = n >= 8 ? load8(p) : load_tail(p, n);
+    if (n >= 8) {
+        const auto w = *reinterpret_cast<const typename Words8<S>::Any*>(p);
+        S x[8];
+        __builtin_memcpy(x, &w, sizeof(x));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = (float)x.v[e];
+        for (int e = 0; e < 8; ++e) out[e] = (float)x[e];
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = e < 7 && e < n ? (float)p[e] : 0.0f;
 }
 
 template <typename S>
 __device__ __forceinline__ void store_row8(S* p, const float v[8], int64_t n) {
     if (n >= 8) {
-        Vec8<S> x;
+        S x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x.v[e] = (S)v[e];
-        *reinterpret_cast<Vec8<S>*>(p) = x;
+        for (int e = 0; e < 8; ++e) x[e] = (S)v[e];
+        typename Words8<S>::Any w;
+        __builtin_memcpy(&w, x, sizeof(x));
+        *reinterpret_cast<typename Words8<S>::Any*>(p) = w;
         return;
     }
 #pragma unroll
@@ -209,12 +226,13 @@ __device__ __forceinline__ void tile_of(const ProductArgs& p, uint32_t& ta, uint
     tb = in / wide;
 }
 
-// What a wave has issued to LDS is there for all that pass: its own loads into LDS
-// (DIRECT) have to have come before the barrier.
-template <bool DIRECT>
+// A barrier that shows all waves the tiles whose loads they issued before, but for
+// the last LOADS of each: a wave waits for its own first.
+template <int LOADS>
 __device__ __forceinline__ void step_barrier() {
-    if (DIRECT) tiles_barrier();
-    else __syncthreads();
+    // its reads of LDS too: other waves replace what they read
+    __builtin_amdgcn_s_waitcnt(0x0070 | (LOADS & 15) | ((LOADS >> 4) << 14));
+    __syncthreads();
 }
 
 // Rows of a wave's part of the result on their way through LDS: the floats between
@@ -224,9 +242,10 @@ constexpr int out_pitch() {
     return COLS + 4;
 }
 
+constexpr int kAhead = 4;  // tiles in LDS of a product that does not fill the GPU
 template <int TA, int TB, int WA, int WB>
-constexpr size_t product_lds() {
-    const size_t tiles = (size_t)(TA + TB) * kDeep * 2 * 2;
+constexpr size_t product_lds(bool ahead) {
+    const size_t tiles = (size_t)(TA + TB) * kDeep * 2 * (ahead ? kAhead : 2);
     const size_t rows = (size_t)WA * WB * 32 * out_pitch<TA / WA>() * sizeof(float);
     return tiles > rows ? tiles : rows;
 }
@@ -242,7 +261,14 @@ constexpr size_t product_lds() {
 // go from memory to LDS directly.  Transposing reads are not told apart from such
 // loads by the compiler, which waits for all of them before the first read; with
 // those a tile goes through registers, one tile further ahead.
-template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB>
+//
+// WHOLE: for products whose workgroups do not fill the GPU.  With a workgroup or less
+// a CU nothing hides the latency of LDS, so the fragments of a whole tile are read
+// during the step before (a step of 128 x 128 x 64 took 1400 cycles for 512 of
+// products, however many tiles were on their way), and with both operands by rows
+// kAhead tiles are on their way.
+template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB,
+          bool WHOLE>
 __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p) {
     constexpr int waves = WA * WB, ca = TA / WA, rb = TB / WB, na = ca / 32, nb = rb / 32;
     constexpr bool direct = A_ROWS && B_ROWS;
@@ -266,13 +292,15 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
 #pragma unroll
         for (int j = 0; j < nb; ++j) acc[i][j] = f32x16{};
     constexpr int kcs = kDeep / 16, pieces = A::kPer + B::kPer;
-    typename Mma<T>::x8 af[2][na], bf[2][nb];
-    // fragment x of the products' operands, the rows' first
+    constexpr int parts = WHOLE ? kcs : 1, places = WHOLE && direct ? kAhead : 2;
+    typename Mma<T>::x8 af[2][parts][na], bf[2][parts][nb];
+    // fragment x of a part's operands, the rows' first
     auto read = [&](int x, int to, const char* tile, int kc) {
+        const int part = WHOLE ? kc : 0;
         if (x < nb)
-            bf[to][x] = B::template frag<false>(tile + A::kBytes, wb * rb + 32 * x, kc, lane);
+            bf[to][part][x] = B::template frag<false>(tile + A::kBytes, wb * rb + 32 * x, kc, lane);
         else
-            af[to][x - nb] = A::template frag<true>(tile, wa * ca + 32 * (x - nb), kc, lane);
+            af[to][part][x - nb] = A::template frag<true>(tile, wa * ca + 32 * (x - nb), kc, lane);
     };
     u32x4 held[direct ? 1 : pieces];
     __amdgpu_buffer_rsrc_t ar, br;
@@ -296,48 +324,118 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
             else B::put(tile + A::kBytes, x - A::kPer, held[x], wave, lane);
         }
     };
-    if (first < last) {
-        char* tile = lds;
-        char* other = lds + bytes;
+    auto place = [&](int at) { return lds + at * bytes; };
+    if constexpr (WHOLE) {
+        constexpr int reads = kcs * (na + nb), products = kcs * na * nb;
+        if (first < last) {
+            // past the end zeros come
+#pragma unroll
+            for (int t = 0; t < places; ++t) {
+                aim(first + t);
+#pragma unroll
+                for (int x = 0; x < pieces; ++x) start(x, place(t));
+#pragma unroll
+                for (int x = 0; x < pieces; ++x) finish(x, place(t));
+            }
+            if constexpr (direct) {
+                step_barrier<(places - 1) * pieces>();
+            } else {
+                aim(first + 2);
+#pragma unroll
+                for (int x = 0; x < pieces; ++x) start(x, place(0));
+                __syncthreads();
+            }
+            int at = 0, next = 1;
+#pragma unroll
+            for (int x = 0; x < reads; ++x) read(x % (na + nb), 0, place(0), x / (na + nb));
+            auto step = [&](auto parity, int32_t s) {
+                constexpr int now = decltype(parity)::value;
+                // the next tile is there, and this one is read
+                if constexpr (direct) step_barrier<(places - 2) * pieces>();
+                else step_barrier<63>();
+                aim(s + (direct ? places : 3));
+                char* from = place(next);
+                char* to = place(at);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < products; ++m) {
+                    const int kc = m / (na * nb), i = m / nb % na, j = m % nb;
+                    acc[i][j] = Mma<T>::mul(af[now][kc][i], bf[now][kc][j], acc[i][j]);
+                    // the reads in the first half, so that they are there in time
+#pragma unroll
+                    for (int x = 0; x < reads; ++x)
+                        if (x * (products / 2) / reads == m)
+                            read(x % (na + nb), now ^ 1, from, x / (na + nb));
+#pragma unroll
+                    for (int x = 0; x < pieces; ++x)
+                        if (x * products / pieces == m) {
+                            finish(x, to);
+                            start(x, to);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                at = next;
+                next = next + 1 < places ? next + 1 : 0;
+            };
+            int32_t s = first;
+            for (; s + 1 < last; s += 2) {
+                step(std::integral_constant<int, 0>{}, s);
+                step(std::integral_constant<int, 1>{}, s + 1);
+            }
+            if (s < last) step(std::integral_constant<int, 0>{}, s);
+            step_barrier<0>();  // nothing is under way to the tiles, and they are read
+        }
+    } else if (first < last) {
         constexpr int early = pieces / 2;
-        aim(first);
+        if constexpr (direct) {
+            // past the end zeros come
 #pragma unroll
-        for (int x = 0; x < pieces; ++x) start(x, tile);
+            for (int t = 0; t + 1 < places; ++t) {
+                aim(first + t);
 #pragma unroll
-        for (int x = 0; x < pieces; ++x) finish(x, tile);
-        aim(first + 1);
-        if (direct) {
-            tiles_barrier();
+                for (int x = 0; x < pieces; ++x) start(x, place(t));
+            }
+            step_barrier<(places - 2) * pieces>();
+            aim(first + places - 1);
 #pragma unroll
-            for (int x = 0; x < early; ++x) start(x, other);
+            for (int x = 0; x < early; ++x) start(x, place(places - 1));
         } else {
+            aim(first);
 #pragma unroll
-            for (int x = 0; x < pieces; ++x) start(x, other);
+            for (int x = 0; x < pieces; ++x) start(x, place(0));
 #pragma unroll
-            for (int x = 0; x < early; ++x) finish(x, other);
+            for (int x = 0; x < pieces; ++x) finish(x, place(0));
+            aim(first + 1);
+#pragma unroll
+            for (int x = 0; x < pieces; ++x) start(x, place(1));
+#pragma unroll
+            for (int x = 0; x < early; ++x) finish(x, place(1));
             aim(first + 2);
 #pragma unroll
-            for (int x = 0; x < early; ++x) start(x, other);
+            for (int x = 0; x < early; ++x) start(x, place(1));
             __syncthreads();
         }
+        int at = 0, next = 1, before = places - 1;  // places of this tile and its neighbours
 #pragma unroll
-        for (int x = 0; x < na + nb; ++x) read(x, 0, tile, 0);
+        for (int x = 0; x < na + nb; ++x) read(x, 0, place(at), 0);
         for (int32_t s = first; s < last; ++s) {
 #pragma unroll
             for (int kc = 0; kc < kcs; ++kc) {
                 const bool end = kc + 1 == kcs;
-                char* from = end ? other : tile;
                 if (end) {
                     // the next tile is there, and this one is read
-                    step_barrier<direct>();
-                    aim(s + (direct ? 2 : 3));
+                    if (direct) step_barrier<(places - 2) * pieces>();
+                    else __syncthreads();
+                    aim(s + (direct ? places : 3));
                 }
+                char* from = place(end ? next : at);
+                char* to = place(end ? at : before);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < na; ++i) {
 #pragma unroll
                     for (int j = 0; j < nb; ++j)
-                        acc[i][j] = Mma<T>::mul(af[kc & 1][i], bf[kc & 1][j], acc[i][j]);
+                        acc[i][j] = Mma<T>::mul(af[kc & 1][0][i], bf[kc & 1][0][j], acc[i][j]);
                     // between the products what later ones need: fragments of
                     // the next 16 k, and pieces of the tile that takes the place
                     // of the one read last
@@ -348,17 +446,17 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
                     for (int x = 0; x < pieces; ++x)
                         if ((end && x < early && x * na / early == i) ||
                             (kc == 0 && x >= early && (x - early) * na / (pieces - early) == i)) {
-                            finish(x, end ? tile : other);
-                            start(x, end ? tile : other);
+                            finish(x, to);
+                            start(x, to);
                         }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            char* t = tile;
-            tile = other;
-            other = t;
+            before = at;
+            at = next;
+            next = next + 1 < places ? next + 1 : 0;
         }
-        step_barrier<direct>();  // nothing is under way to the tiles, and they are read
+        step_barrier<0>();  // nothing is under way to the tiles, and they are read
     }
 
     // The result through LDS, 32 rows of the wave's at a time, so that a row's
@@ -431,17 +529,159 @@ __global__ __launch_bounds__(kThreads) void product_join_kernel(ProductArgs p) {
     }
 }
 
+// ---------------------------------------------------------------- few rows
+// With few rows the time is that of reading the columns' operand (the weights)
+// once.  A workgroup has 16 columns and all rows; its waves share the sum, each
+// reading its part of the weights' rows straight into the operands of 16 x 16 x 32
+// products, and are joined in LDS.  A lane takes 32 bytes of a row at a time, four
+// lanes a cache line; the order of k within a product is free as long as both
+// operands have the same.  Rows may lie anywhere: nothing is laid out anew.
+template <typename T>
+struct Mma16;
+template <>
+struct Mma16<bf16> {
+    static __device__ __forceinline__ f4 mul(Mma<bf16>::x8 a, Mma<bf16>::x8 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma16<f16> {
+    static __device__ __forceinline__ f4 mul(Mma<f16>::x8 a, Mma<f16>::x8 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::x8 load_any(const T* p) {
+    typedef u32x4 Any __attribute__((aligned(2)));
+    return __builtin_bit_cast(typename Mma<T>::x8, *reinterpret_cast<const Any*>(p));
+}
+
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::x8 load_end(const T* p, int64_t n) {
+    typename Mma<T>::x8 x = {};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n) x[e] = p[e];
+    return x;
+}
+
+// Columns of a workgroup, rows at most (8192 columns over 2048: 16, 32, 48 and 64 rows
+// 9.8, 13.5, 17 and 21 us; by tiles 12.6, 14.2, 15.2 and 15.7).
+constexpr int kFewCols = 16, kFewRows = 32;
+
+template <typename T, int RB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void product_few_kernel(ProductArgs p) {
+    __shared__ float sums[WAVES][16 * RB][kFewCols + 1];
+    using x8 = typename Mma<T>::x8;
+    const int wave = wave_id(), lane = lane_id(), i = lane & 15, q = lane >> 4;
+    const int64_t c0 = (int64_t)blockIdx.x * kFewCols;
+    const int64_t c = c0 + i < p.out.cols ? c0 + i : p.out.cols - 1;  // what is past the last
+                                                                       // is not stored
+    const T* w = (const T*)p.a.p + c * p.a.ld + 16 * q;
+    const T* x[RB];
+    bool ok[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        ok[b] = 16 * b + i < p.out.rows;
+        x[b] = (const T*)p.b.p + (ok[b] ? 16 * b + i : 0) * p.b.ld + 16 * q;
+    }
+    const int64_t blocks = (p.depth + 63) / 64, whole = p.depth / 64;
+    const int64_t first = blocks * wave / WAVES, last = blocks * (wave + 1) / WAVES;
+    const int64_t end = last < whole ? last : whole;
+    f4 acc[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[b] = f4{};
+    int64_t t = first;
+    constexpr int kAtOnce = 4;
+    for (; t + kAtOnce <= end; t += kAtOnce) {
+        x8 wf[2 * kAtOnce], xf[RB][2 * kAtOnce];
+#pragma unroll
+        for (int u = 0; u < 2 * kAtOnce; ++u)
+            wf[u] = load_any(w + 64 * (t + u / 2) + 8 * (u & 1));
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int u = 0; u < 2 * kAtOnce; ++u)
+                xf[b][u] = ok[b] ? load_any(x[b] + 64 * (t + u / 2) + 8 * (u & 1)) : x8{};
+#pragma unroll
+        for (int u = 0; u < 2 * kAtOnce; ++u)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) acc[b] = Mma16<T>::mul(wf[u], xf[b][u], acc[b]);
+    }
+    for (; t < last; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = 64 * t + 8 * h, n = p.depth - k - 16 * q;
+            const x8 wf = n >= 8 ? load_any(w + k) : load_end(w + k, n);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                x8 xf = {};
+                if (ok[b]) xf = n >= 8 ? load_any(x[b] + k) : load_end(x[b] + k, n);
+                acc[b] = Mma16<T>::mul(wf, xf, acc[b]);
+            }
+        }
+    }
+    // a lane has columns 4 q ... + 3 of row i
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave][16 * b + i][4 * q + e] = acc[b][e];
+    __syncthreads();
+    const ProductOut& o = p.out;
+    for (int at = threadIdx.x; at < 16 * RB * kFewCols; at += 64 * WAVES) {
+        const int r = at / kFewCols, k = at % kFewCols;
+        const int64_t col = c0 + k;
+        if (r >= o.rows || col >= o.cols) continue;
+        float z = 0.0f;
+#pragma unroll
+        for (int s = 0; s < WAVES; ++s) z += sums[s][r][k];
+        if (o.bias) z += o.bias_wide ? ((const float*)o.bias)[col] : (float)((const T*)o.bias)[col];
+        if (o.pre) ((T*)o.pre)[r * o.ld_pre + col] = (T)z;
+        with_act(o.act, [&](auto act) { z = activate<act.value>(z); });
+        if (o.residual) z += (float)((const T*)o.residual)[r * o.ld_r + col];
+        ((T*)o.out)[r * o.ld + col] = (T)z;
+    }
+}
+
+template <typename T, int RB>
+void launch_few_waves(const ProductArgs& p, hipStream_t st) {
+    const int64_t groups = (p.out.cols + kFewCols - 1) / kFewCols, blocks = (p.depth + 63) / 64;
+    const dim3 grid((unsigned)groups);
+    // enough waves for the memory's latency, each with a few blocks of k
+    if (groups >= 512 || blocks <= 8)
+        hipLaunchKernelGGL((product_few_kernel<T, RB, 4>), grid, dim3(256), 0, st, p);
+    else if (groups >= 256 || blocks <= 16)
+        hipLaunchKernelGGL((product_few_kernel<T, RB, 8>), grid, dim3(512), 0, st, p);
+    else
+        hipLaunchKernelGGL((product_few_kernel<T, RB, 16>), grid, dim3(1024), 0, st, p);
+}
+
+template <typename T>
+void launch_few(const ProductArgs& p, hipStream_t st) {
+    if (p.out.rows <= 16) launch_few_waves<T, 1>(p, st);
+    else launch_few_waves<T, 2>(p, st);
+}
+
 // ---------------------------------------------------------------- operands laid out anew
-__global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t* from, int64_t ld,
-                                                            uint16_t* to, int64_t padded,
-                                                            int64_t rows, int64_t cols) {
-    const int64_t groups = padded / 8, all = rows * groups;
+__global__ __launch_bounds__(kThreads) void pad_rows_kernel(PadRows one, PadRows two) {
+    const int64_t first = one.rows * (one.padded / 8);
+    const int64_t all = first + two.rows * (two.padded / 8);
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all;
          i += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = i / groups, c = (i % groups) * 8;
-        const uint16_t* p = from + r * ld + c;
-        const Vec8<uint16_t> x = c + 8 <= cols ? load8(p) : load_tail(p, cols - c);
-        *reinterpret_cast<Vec8<uint16_t>*>(to + r * padded + c) = x;
+        const PadRows& a = i < first ? one : two;
+        const int64_t groups = a.padded / 8, at = i < first ? i : i - first;
+        const int64_t r = at / groups, c = (at % groups) * 8;
+        const uint16_t* p = (const uint16_t*)a.from + r * a.ld + c;
+        u32x4 x = {};
+        if (c + 8 <= a.cols) {
+            x = *reinterpret_cast<const Words8<uint16_t>::Any*>(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + e < a.cols) x[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
+        *reinterpret_cast<u32x4*>((uint16_t*)a.to + r * a.padded + c) = x;
     }
 }
 
@@ -481,18 +721,33 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
         if (e < n) a.partials[part * a.cols + c + e] = sums[e];
 }
 
-template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB>
+template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB,
+          bool WHOLE>
 void launch_tile(const ProductArgs& p, hipStream_t st) {
-    hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, TA, TB, WA, WB>),
+    hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, TA, TB, WA, WB, WHOLE>),
                        dim3((unsigned)((int64_t)p.tiles_a * p.tiles_b * p.splits)),
-                       dim3(64 * WA * WB), (product_lds<TA, TB, WA, WB>()), st, p);
+                       dim3(64 * WA * WB),
+                       (product_lds<TA, TB, WA, WB>(WHOLE && A_ROWS && B_ROWS)), st, p);
+}
+
+// (tiles of 64 rows have their operand by rows: product_plan)
+template <typename T, typename S, bool A_ROWS, bool B_ROWS>
+void launch_narrow(const ProductArgs& p, hipStream_t st) {
+    if constexpr (B_ROWS) launch_tile<T, S, A_ROWS, B_ROWS, 128, 64, 2, 2, true>(p, st);
 }
 
 template <typename T, typename S, bool A_ROWS, bool B_ROWS>
 void launch_tiles(const ProductArgs& p, const ProductPlan& plan, hipStream_t st) {
-    if (plan.tile_b == 256) launch_tile<T, S, A_ROWS, B_ROWS, 256, 256, 2, 4>(p, st);
-    else if (plan.tile_a == 256) launch_tile<T, S, A_ROWS, B_ROWS, 256, 128, 4, 2>(p, st);
-    else launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 2>(p, st);
+    if (plan.tile_b == 256)
+        launch_tile<T, S, A_ROWS, B_ROWS, 256, 256, 2, 4, false>(p, st);
+    else if (plan.tile_a == 256)
+        launch_tile<T, S, A_ROWS, B_ROWS, 256, 128, 4, 2, false>(p, st);
+    else if (plan.tile_b == 64)
+        launch_narrow<T, S, A_ROWS, B_ROWS>(p, st);
+    else if ((int64_t)p.tiles_a * p.tiles_b * p.splits <= kCUs)
+        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 4, true>(p, st);
+    else
+        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 2, false>(p, st);
     if (p.parts) {
         const int64_t groups = (p.out.rows * (p.padded / 8) + kThreads - 1) / kThreads;
         hipLaunchKernelGGL((product_join_kernel<T, S>), dim3((unsigned)(groups < 4096 ? groups : 4096)),
@@ -517,28 +772,36 @@ int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 // The division that a model of the kernels' times takes for the fastest: rounds of
 // resident workgroups, each the longer the deeper it is, and the join of parts.
 // Microseconds as measured (8192^3: 856, 1043 and 988 with tiles of 256 x 256, 256 x
-// 128 and 128 x 128; 4096 x 1024 over 8192: 141, 94 and 77).
-ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth) {
+// 128 and 128 x 128; 4096 x 1024 over 8192: 141, 94 and 77).  Workgroups that do not
+// fill the GPU take as long as a CU's loads, 60 bytes a ns: 32 KB a step of 128 x 128,
+// 24 KB of 128 x 64 (256 x 1024 over 4096: 40 and 32 us).
+ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by_rows,
+                         bool rows_by_rows) {
     struct Tile {
-        int32_t a, b, places;  // places: workgroups at once
-        double per_k, half_per_k, fixed;  // half: with at most half of the places taken
+        int32_t a, b, places;       // places: workgroups at once
+        double direct, registers;   // microseconds for one of k, by the tiles' way to LDS
+        double half, fixed;         // half: with at most half of the places taken
     };
-    static const Tile kinds[] = {{256, 256, 256, 0.026, 0.018, 9.0},
-                                 {256, 128, 256, 0.0159, 0.0118, 6.0},
-                                 {128, 128, 512, 0.0150, 0.0092, 5.0}};
+    static const Tile kinds[] = {{256, 256, 256, 0.0260, 0.0272, 0.0180, 9.0},
+                                 {256, 128, 256, 0.0159, 0.0164, 0.0118, 6.0},
+                                 {128, 128, 512, 0.0150, 0.0175, 0.0086, 5.0},
+                                 {128, 64, 256, 0.0072, 0.0072, 0.0066, 4.5}};
     ProductPlan best = {};
     double least = 0.0;
     const int64_t steps = tiles_of(depth, kDeep);
     for (const Tile& t : kinds) {
+        if (t.b == 64 && !rows_by_rows) continue;
         const int64_t tiles = tiles_of(rows, t.b) * tiles_of(cols, t.a);
         for (int64_t splits = 1; splits <= 32; ++splits) {
             if (splits > 1 && (tiles * splits > t.places || splits * 4 > steps)) break;
             const int64_t rounds = tiles_of(tiles * splits, t.places);
-            const double per_k = tiles * splits * 2 <= t.places ? t.half_per_k : t.per_k;
+            const double per_k = tiles * splits * 2 <= t.places ? t.half
+                                 : cols_by_rows                 ? t.direct
+                                                                : t.registers;
             const double deep = (double)tiles_of(steps, splits) * kDeep;
             // the parts are written and read at 4 bytes per ns and GPU
             const double join =
-                splits > 1 ? 6.0 + (double)(2 * splits * rows * cols * 4) / 4.0e6 : 0.0;
+                splits > 1 ? 4.0 + (double)(2 * splits * rows * cols * 4) / 4.0e6 : 0.0;
             const double time = (double)rounds * (deep * per_k + t.fixed) + join;
             if (best.splits == 0 || time < least) {
                 least = time;
@@ -554,11 +817,26 @@ ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth) {
     return best;
 }
 
+bool product_few(int64_t rows) { return rows <= kFewRows; }
+
+hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const ProductIn& rows_in,
+                              int64_t depth, const ProductOut& out, hipStream_t st) {
+    if (out.rows == 0 || out.cols == 0) return hipSuccess;
+    ProductArgs p = {};
+    p.a = cols_in;
+    p.b = rows_in;
+    p.out = out;
+    p.depth = depth;
+    if (dtype == ONEBIT_BF16) launch_few<bf16>(p, st);
+    else launch_few<f16>(p, st);
+    return hipGetLastError();
+}
+
 hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
                           const ProductOut& out, float* parts, hipStream_t st) {
     if (out.rows == 0 || out.cols == 0) return hipSuccess;
-    const ProductPlan plan = product_plan(out.rows, out.cols, depth);
+    const ProductPlan plan = product_plan(out.rows, out.cols, depth, cols_by_rows, rows_by_rows);
     ProductArgs p = {};
     p.a = cols_in;
     p.b = rows_in;
@@ -574,13 +852,12 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
     return hipGetLastError();
 }
 
-hipError_t launch_pad_rows(const void* from, int64_t ld, void* to, int64_t padded, int64_t rows,
-                           int64_t cols, hipStream_t st) {
-    const int64_t groups = (rows * (padded / 8) + kThreads - 1) / kThreads;
+hipError_t launch_pad_rows(const PadRows& one, const PadRows& two, hipStream_t st) {
+    const int64_t all = one.rows * (one.padded / 8) + two.rows * (two.padded / 8);
+    const int64_t groups = tiles_of(all, kThreads);
     if (groups == 0) return hipSuccess;
     hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)(groups < 8192 ? groups : 8192)),
-                       dim3(kThreads), 0, st, (const uint16_t*)from, ld, (uint16_t*)to, padded,
-                       rows, cols);
+                       dim3(kThreads), 0, st, one, two);
     return hipGetLastError();
 }
 

@@ -185,7 +185,8 @@ struct ProductPlan {
     int32_t splits;
     size_t bytes;  // workspace of the parts
 };
-ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth);
+ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by_rows,
+                         bool rows_by_rows);
 
 // out[r][c] = sum over k < depth of rows_in(r, k) cols_in(c, k).  The operand
 // types: by_rows says whether k is the contiguous index.  (cols_in, rows_in) is
@@ -195,9 +196,20 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
                           const ProductOut& out, float* parts, hipStream_t st);
 
-// to[r][c] = from[r][c], columns cols ... padded - 1 are 0 (16-bit elements).
-hipError_t launch_pad_rows(const void* from, int64_t ld, void* to, int64_t padded, int64_t rows,
-                           int64_t cols, hipStream_t st);
+// Whether a product of both operands by rows goes by launch_product_few, for which
+// they may lie anywhere.
+bool product_few(int64_t rows);
+hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const ProductIn& rows_in,
+                              int64_t depth, const ProductOut& out, hipStream_t st);
+
+// to[r][c] = from[r][c], columns cols ... padded - 1 are 0 (16-bit elements).  Two
+// matrices in one launch; rows 0 for none.
+struct PadRows {
+    const void* from;
+    void* to;
+    int64_t ld, padded, rows, cols;
+};
+hipError_t launch_pad_rows(const PadRows& one, const PadRows& two, hipStream_t st);
 
 // dz = dy act'(pre), rounded to the element type, into `dz` (rows of `padded`
 // elements, zeros at their end) where given, and its unrounded sums over parts of
