@@ -242,7 +242,7 @@ constexpr int out_pitch() {
     return COLS + 4;
 }
 
-constexpr int kAhead = 4;  // tiles in LDS of a product that does not fill the GPU
+constexpr int kAhead = 3;  // tiles in LDS of a product that does not fill the GPU
 template <int TA, int TB, int WA, int WB>
 constexpr size_t product_lds(bool ahead) {
     const size_t tiles = (size_t)(TA + TB) * kDeep * 2 * (ahead ? kAhead : 2);
@@ -785,7 +785,7 @@ ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by
     static const Tile kinds[] = {{256, 256, 256, 0.0260, 0.0272, 0.0180, 9.0},
                                  {256, 128, 256, 0.0159, 0.0164, 0.0118, 6.0},
                                  {128, 128, 512, 0.0150, 0.0175, 0.0086, 5.0},
-                                 {128, 64, 256, 0.0072, 0.0072, 0.0066, 4.5}};
+                                 {128, 64, 512, 0.0110, 0.0110, 0.0066, 4.5}};
     ProductPlan best = {};
     double least = 0.0;
     const int64_t steps = tiles_of(depth, kDeep);
