@@ -1041,13 +1041,22 @@ bool lies_over(const Matrix& out, const Matrix& in) {
            (down + 1 < (uint64_t)first.rows && pitch - right < (uint64_t)second.cols * second.size);
 }
 
+// Rows that a product that takes operands anywhere takes as they are.
+bool any_rows(int64_t ld, int64_t rows, int64_t cols) {
+    return cols >= 8 && (ld <= kMaxFeatures || rows <= 1);
+}
+
 // The operand as the product reads it; `anew` says how it is laid out at `room`
-// first, if need be.
+// first, if need be, `any` that its rows are not whole chunks.
 ProductIn operand(const void* p, int64_t ld, int64_t rows, int64_t cols, char* room,
-                  PadRows& anew) {
+                  bool takes_any, PadRows& anew, bool& any) {
     anew = PadRows{};
     if (rows == 0 || cols == 0 || whole_chunks(p, ld, rows, cols))
         return ProductIn{p, rows <= 1 ? padded(cols) : ld};
+    if (takes_any && any_rows(ld, rows, cols)) {
+        any = true;
+        return ProductIn{p, rows <= 1 ? padded(cols) : ld};
+    }
     anew = PadRows{p, room, ld, padded(cols), rows, cols};
     return ProductIn{room, padded(cols)};
 }
@@ -1105,11 +1114,13 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
     if (product_few(M))
         return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w},
                                              ProductIn{a->x, a->ld_x}, K, o, stream));
+    const bool takes_any = product_any(product_plan(M, N, K, true, true));
     PadRows x_anew, w_anew;
-    const ProductIn xs = operand(a->x, a->ld_x, M, K, room, x_anew);
-    const ProductIn wi = operand(a->w, a->ld_w, N, K, room + z.x, w_anew);
+    bool any = false;
+    const ProductIn xs = operand(a->x, a->ld_x, M, K, room, takes_any, x_anew, any);
+    const ProductIn wi = operand(a->w, a->ld_w, N, K, room + z.x, takes_any, w_anew, any);
     if (launch_pad_rows(x_anew, w_anew, stream) != hipSuccess) return ONEBIT_E_HIP;
-    return hip_status(launch_product(a->dtype, wi, true, xs, true, K, o,
+    return hip_status(launch_product(a->dtype, wi, true, xs, true, K, o, any,
                                      reinterpret_cast<float*>(room + z.x + z.w), stream));
 }
 
@@ -1146,8 +1157,15 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
     drop_stale_error();
     hipError_t e = hipSuccess;
     ProductIn dz{a->dy, M <= 1 ? padded(N) : a->ld_dy};
-    const bool products = a->dx || a->dw;
-    const bool anew = products && (act || !whole_chunks(a->dy, a->ld_dy, M, N));
+    const bool want_dx = a->dx && M > 0 && K > 0, want_dw = a->dw && N > 0 && K > 0;
+    const bool dx_any = product_any(product_plan(M, K, N, false, true));
+    const bool dw_any = product_any(product_plan(N, K, M, false, false));
+    // dz is laid out anew for the activation, or where a product does not take it
+    const bool chunks = M == 0 || N == 0 || whole_chunks(a->dy, a->ld_dy, M, N);
+    const bool anew = (want_dx || want_dw) &&
+                      (act || (!chunks && (!any_rows(a->ld_dy, M, N) || (want_dx && !dx_any) ||
+                                           (want_dw && !dw_any))));
+    const bool dz_any = !anew && !chunks;
     if (N > 0) {
         if (M > 0 && (anew || a->dbias)) {
             SlopeArgs s = {};
@@ -1169,11 +1187,11 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
             e = launch_column_join(sums, M > 0 ? slope_parts(M, N) : 0, N, N, a->dbias, nullptr,
                                    a->accumulate != 0, stream);
     }
-    const bool want_dx = a->dx && M > 0 && K > 0, want_dw = a->dw && N > 0 && K > 0;
     PadRows x_anew = {}, w_anew = {};
     ProductIn xs = {}, wi = {};
-    if (want_dx) wi = operand(a->w, a->ld_w, N, K, w_room, w_anew);
-    if (want_dw) xs = operand(a->x, a->ld_x, M, K, x_room, x_anew);
+    bool w_any = dz_any, x_any = dz_any;
+    if (want_dx) wi = operand(a->w, a->ld_w, N, K, w_room, dx_any, w_anew, w_any);
+    if (want_dw) xs = operand(a->x, a->ld_x, M, K, x_room, dw_any, x_anew, x_any);
     if (e == hipSuccess) e = launch_pad_rows(x_anew, w_anew, stream);
     if (e == hipSuccess && want_dx) {
         ProductOut o = {};
@@ -1182,7 +1200,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
         o.cols = K;
         o.ld = a->ld_dx;
         o.type = a->dtype;
-        e = launch_product(a->dtype, wi, false, dz, true, N, o, parts, stream);
+        e = launch_product(a->dtype, wi, false, dz, true, N, o, w_any, parts, stream);
     }
     if (e == hipSuccess && want_dw) {
         ProductOut o = {};
@@ -1192,7 +1210,8 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
         o.ld = a->ld_dw;
         o.type = a->dw_dtype;
         o.accumulate = a->accumulate != 0;
-        e = launch_product(a->dtype, xs, false, dz, false, M, o, parts, stream);
+        e = launch_product(a->dtype, xs, false, dz, false, M, o, x_any, parts,
+                           stream);
     }
     return hip_status(e);
 }

@@ -131,6 +131,8 @@ struct Operand {
     uint32_t stride, at;  // in bytes
     int32_t count;        // of the operand's index from the tile's first on
     int32_t mine;         // by rows: the lane's first k in a tile
+    int32_t row0;         // the lane's first row in LDS
+    int32_t past;         // else: of its eight columns, those past the last one
 
     static __device__ __forceinline__ int swizzled(int row, int chunk) {
         if (!ROWS) return chunk ^ ((row & 3) << 2);
@@ -146,6 +148,8 @@ struct Operand {
         base = (const char*)in.p + (ROWS ? first * in.ld * 2 : first * 2);
         at = (uint32_t)row * stride + 16 * chunk;
         mine = 8 * chunk;
+        row0 = row;
+        past = mine + 8 > count ? mine + 8 - count : 0;
         if (!ROWS && 8 * chunk >= count) at = 0x80000000u;
     }
     // The buffer of the tile from k0 on and the lane's offset in it.
@@ -173,6 +177,43 @@ struct Operand {
     __device__ __forceinline__ u32x4 fetch(int x, __amdgpu_buffer_rsrc_t rsrc, uint32_t off) const {
         return __builtin_amdgcn_raw_buffer_load_b128(
             rsrc, (int)(off + (uint32_t)(x * kRowsAtOnce) * stride), 0, 0);
+    }
+    // Rows that lie anywhere and end anywhere (of eight elements or more): how many
+    // of the lane's eight elements lie past the row's end, in the tile from k0 on.
+    __device__ __forceinline__ int32_t over_of(int64_t k0, int64_t depth) const {
+        if (!ROWS) return past;
+        const int64_t over = k0 + mine + 8 - depth;
+        return over <= 0 ? 0 : over < 8 ? (int32_t)over : 8;
+    }
+    // Piece x of such a tile: where a row ends inside the lane's eight elements, the
+    // row's last eight.
+    __device__ __forceinline__ u32x4 fetch_any(int x, int64_t k0, int64_t depth,
+                                               int32_t over) const {
+        const int row = row0 + x * kRowsAtOnce;
+        u32x4 v = {};
+        if (over < 8 && (ROWS ? row < count : k0 + row < depth)) {
+            typedef u32x4 Any __attribute__((aligned(2)));
+            const char* from = base + (ROWS ? k0 * 2 : k0 * stride) + ((int64_t)row * stride) +
+                               2 * (mine - over);
+            v = *reinterpret_cast<const Any*>(from);
+        }
+        return v;
+    }
+    // What fetch_any brought, moved down by `over` elements, zeros behind them.  Not
+    // before it is needed: it waits for the load.
+    static __device__ __forceinline__ u32x4 moved(u32x4 v, int32_t over) {
+        if (!__any(over > 0 && over < 8)) return v;
+        uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+        if (over >= 4) {
+            lo = hi;
+            hi = 0;
+        }
+        const int bits = 16 * (over & 3);
+        if (bits) {
+            lo = lo >> bits | hi << (64 - bits);
+            hi >>= bits;
+        }
+        return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
     }
     static __device__ __forceinline__ void put(char* tile, int x, u32x4 held, int wave, int lane) {
         *reinterpret_cast<u32x4*>(tile + (x * WAVES + wave) * 1024 + lane * 16) = held;
@@ -267,11 +308,13 @@ constexpr size_t product_lds(bool ahead) {
 // during the step before (a step of 128 x 128 x 64 took 1400 cycles for 512 of
 // products, however many tiles were on their way), and with both operands by rows
 // kAhead tiles are on their way.
+//
+// ANY: operands whose rows are not whole 16-byte chunks, through registers.
 template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB,
-          bool WHOLE>
+          bool WHOLE, bool ANY>
 __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p) {
     constexpr int waves = WA * WB, ca = TA / WA, rb = TB / WB, na = ca / 32, nb = rb / 32;
-    constexpr bool direct = A_ROWS && B_ROWS;
+    constexpr bool direct = A_ROWS && B_ROWS && !ANY;
     using A = Operand<T, A_ROWS, TA, waves>;
     using B = Operand<T, B_ROWS, TB, waves>;
     constexpr int bytes = A::kBytes + B::kBytes;
@@ -305,7 +348,18 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
     u32x4 held[direct ? 1 : pieces];
     __amdgpu_buffer_rsrc_t ar, br;
     uint32_t ao = 0, bo = 0;
+    int64_t aimed = 0;
+    // of ANY, past the rows' ends: in the tile that is fetched and the one before it
+    int32_t a_over[2] = {}, b_over[2] = {};
     auto aim = [&](int32_t step) {
+        if constexpr (ANY) {
+            aimed = (int64_t)step * kDeep;
+            a_over[1] = a_over[0];
+            b_over[1] = b_over[0];
+            a_over[0] = as.over_of(aimed, p.depth);
+            b_over[0] = bs.over_of(aimed, p.depth);
+            return;
+        }
         ar = as.buffer((int64_t)step * kDeep, p.depth, ao);
         br = bs.buffer((int64_t)step * kDeep, p.depth, bo);
     };
@@ -314,11 +368,17 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
         if constexpr (direct) {
             if (x < A::kPer) as.load(tile, x, ar, ao, wave);
             else bs.load(tile + A::kBytes, x - A::kPer, br, bo, wave);
+        } else if constexpr (ANY) {
+            held[x] = x < A::kPer ? as.fetch_any(x, aimed, p.depth, a_over[0])
+                                  : bs.fetch_any(x - A::kPer, aimed, p.depth, b_over[0]);
         } else {
             held[x] = x < A::kPer ? as.fetch(x, ar, ao) : bs.fetch(x - A::kPer, br, bo);
         }
     };
-    auto finish = [&](int x, char* tile) {
+    // and into LDS, of the tile aimed at `ago` aims before
+    auto finish = [&](int x, char* tile, int ago) {
+        if constexpr (ANY)
+            held[x] = x < A::kPer ? A::moved(held[x], a_over[ago]) : B::moved(held[x], b_over[ago]);
         if constexpr (!direct) {
             if (x < A::kPer) A::put(tile, x, held[x], wave, lane);
             else B::put(tile + A::kBytes, x - A::kPer, held[x], wave, lane);
@@ -335,7 +395,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
 #pragma unroll
                 for (int x = 0; x < pieces; ++x) start(x, place(t));
 #pragma unroll
-                for (int x = 0; x < pieces; ++x) finish(x, place(t));
+                for (int x = 0; x < pieces; ++x) finish(x, place(t), 0);
             }
             if constexpr (direct) {
                 step_barrier<(places - 1) * pieces>();
@@ -369,7 +429,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
 #pragma unroll
                     for (int x = 0; x < pieces; ++x)
                         if (x * products / pieces == m) {
-                            finish(x, to);
+                            finish(x, to, 1);
                             start(x, to);
                         }
                     __builtin_amdgcn_sched_barrier(0);
@@ -404,12 +464,12 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
 #pragma unroll
             for (int x = 0; x < pieces; ++x) start(x, place(0));
 #pragma unroll
-            for (int x = 0; x < pieces; ++x) finish(x, place(0));
+            for (int x = 0; x < pieces; ++x) finish(x, place(0), 0);
             aim(first + 1);
 #pragma unroll
             for (int x = 0; x < pieces; ++x) start(x, place(1));
 #pragma unroll
-            for (int x = 0; x < early; ++x) finish(x, place(1));
+            for (int x = 0; x < early; ++x) finish(x, place(1), 0);
             aim(first + 2);
 #pragma unroll
             for (int x = 0; x < early; ++x) start(x, place(1));
@@ -446,7 +506,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
                     for (int x = 0; x < pieces; ++x)
                         if ((end && x < early && x * na / early == i) ||
                             (kc == 0 && x >= early && (x - early) * na / (pieces - early) == i)) {
-                            finish(x, to);
+                            finish(x, to, 1);
                             start(x, to);
                         }
                     __builtin_amdgcn_sched_barrier(0);
@@ -722,32 +782,36 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
 }
 
 template <typename T, typename S, bool A_ROWS, bool B_ROWS, int TA, int TB, int WA, int WB,
-          bool WHOLE>
+          bool WHOLE, bool ANY>
 void launch_tile(const ProductArgs& p, hipStream_t st) {
-    hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, TA, TB, WA, WB, WHOLE>),
+    hipLaunchKernelGGL((product_kernel<T, S, A_ROWS, B_ROWS, TA, TB, WA, WB, WHOLE, ANY>),
                        dim3((unsigned)((int64_t)p.tiles_a * p.tiles_b * p.splits)),
                        dim3(64 * WA * WB),
-                       (product_lds<TA, TB, WA, WB>(WHOLE && A_ROWS && B_ROWS)), st, p);
+                       (product_lds<TA, TB, WA, WB>(WHOLE && A_ROWS && B_ROWS && !ANY)), st, p);
 }
 
 // (tiles of 64 rows have their operand by rows: product_plan)
-template <typename T, typename S, bool A_ROWS, bool B_ROWS>
-void launch_narrow(const ProductArgs& p, hipStream_t st) {
-    if constexpr (B_ROWS) launch_tile<T, S, A_ROWS, B_ROWS, 128, 64, 2, 2, true>(p, st);
+template <typename T, typename S, bool A_ROWS, bool B_ROWS, bool ANY>
+void launch_small(const ProductArgs& p, const ProductPlan& plan, hipStream_t st) {
+    if (plan.tile_b == 64) {
+        if constexpr (B_ROWS) launch_tile<T, S, A_ROWS, B_ROWS, 128, 64, 2, 2, true, ANY>(p, st);
+    } else if ((int64_t)p.tiles_a * p.tiles_b * p.splits <= kCUs) {
+        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 4, true, ANY>(p, st);
+    } else {
+        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 2, false, ANY>(p, st);
+    }
 }
 
 template <typename T, typename S, bool A_ROWS, bool B_ROWS>
-void launch_tiles(const ProductArgs& p, const ProductPlan& plan, hipStream_t st) {
+void launch_tiles(const ProductArgs& p, const ProductPlan& plan, bool any, hipStream_t st) {
     if (plan.tile_b == 256)
-        launch_tile<T, S, A_ROWS, B_ROWS, 256, 256, 2, 4, false>(p, st);
+        launch_tile<T, S, A_ROWS, B_ROWS, 256, 256, 2, 4, false, false>(p, st);
     else if (plan.tile_a == 256)
-        launch_tile<T, S, A_ROWS, B_ROWS, 256, 128, 4, 2, false>(p, st);
-    else if (plan.tile_b == 64)
-        launch_narrow<T, S, A_ROWS, B_ROWS>(p, st);
-    else if ((int64_t)p.tiles_a * p.tiles_b * p.splits <= kCUs)
-        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 4, true>(p, st);
+        launch_tile<T, S, A_ROWS, B_ROWS, 256, 128, 4, 2, false, false>(p, st);
+    else if (any)
+        launch_small<T, S, A_ROWS, B_ROWS, true>(p, plan, st);
     else
-        launch_tile<T, S, A_ROWS, B_ROWS, 128, 128, 2, 2, false>(p, st);
+        launch_small<T, S, A_ROWS, B_ROWS, false>(p, plan, st);
     if (p.parts) {
         const int64_t groups = (p.out.rows * (p.padded / 8) + kThreads - 1) / kThreads;
         hipLaunchKernelGGL((product_join_kernel<T, S>), dim3((unsigned)(groups < 4096 ? groups : 4096)),
@@ -758,11 +822,11 @@ void launch_tiles(const ProductArgs& p, const ProductPlan& plan, hipStream_t st)
 // Binary32 results are those of dw, whose operands both come by their own index.
 template <typename T>
 void launch_typed(const ProductArgs& p, bool a_rows, bool b_rows, const ProductPlan& plan,
-                  hipStream_t st) {
-    if (a_rows) launch_tiles<T, T, true, true>(p, plan, st);
-    else if (b_rows) launch_tiles<T, T, false, true>(p, plan, st);
-    else if (p.out.type == ONEBIT_F32) launch_tiles<T, float, false, false>(p, plan, st);
-    else launch_tiles<T, T, false, false>(p, plan, st);
+                  bool any, hipStream_t st) {
+    if (a_rows) launch_tiles<T, T, true, true>(p, plan, any, st);
+    else if (b_rows) launch_tiles<T, T, false, true>(p, plan, any, st);
+    else if (p.out.type == ONEBIT_F32) launch_tiles<T, float, false, false>(p, plan, any, st);
+    else launch_tiles<T, T, false, false>(p, plan, any, st);
 }
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
@@ -817,6 +881,8 @@ ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by
     return best;
 }
 
+bool product_any(const ProductPlan& plan) { return plan.tile_a == 128; }
+
 bool product_few(int64_t rows) { return rows <= kFewRows; }
 
 hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const ProductIn& rows_in,
@@ -834,7 +900,7 @@ hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const Pro
 
 hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
-                          const ProductOut& out, float* parts, hipStream_t st) {
+                          const ProductOut& out, bool any, float* parts, hipStream_t st) {
     if (out.rows == 0 || out.cols == 0) return hipSuccess;
     const ProductPlan plan = product_plan(out.rows, out.cols, depth, cols_by_rows, rows_by_rows);
     ProductArgs p = {};
@@ -847,8 +913,8 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
     p.tiles_a = (int32_t)tiles_of(out.cols, plan.tile_a);
     p.tiles_b = (int32_t)tiles_of(out.rows, plan.tile_b);
     p.splits = plan.splits;
-    if (dtype == ONEBIT_BF16) launch_typed<bf16>(p, cols_by_rows, rows_by_rows, plan, st);
-    else launch_typed<f16>(p, cols_by_rows, rows_by_rows, plan, st);
+    if (dtype == ONEBIT_BF16) launch_typed<bf16>(p, cols_by_rows, rows_by_rows, plan, any, st);
+    else launch_typed<f16>(p, cols_by_rows, rows_by_rows, plan, any, st);
     return hipGetLastError();
 }
 

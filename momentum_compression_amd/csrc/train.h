@@ -188,13 +188,18 @@ struct ProductPlan {
 ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by_rows,
                          bool rows_by_rows);
 
+// Whether the division's kernels take operands that lie anywhere; the larger tiles,
+// whose work is worth a copy of the operands, take rows of whole 16-byte chunks.
+bool product_any(const ProductPlan& plan);
+
 // out[r][c] = sum over k < depth of rows_in(r, k) cols_in(c, k).  The operand
 // types: by_rows says whether k is the contiguous index.  (cols_in, rows_in) is
 // (true, true), (false, true) or (false, false).  Contiguous indices and strides
-// are multiples of 8 and the addresses of 16 bytes.
+// are multiples of 8 and the addresses of 16 bytes; with `any` (product_any)
+// contiguous indices are 8 or more.
 hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
-                          const ProductOut& out, float* parts, hipStream_t st);
+                          const ProductOut& out, bool any, float* parts, hipStream_t st);
 
 // Whether a product of both operands by rows goes by launch_product_few, for which
 // they may lie anywhere.
