@@ -749,7 +749,7 @@ size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward)
  *   seed hi32 xor 0x41444D57)),
  * so that its mean over the draws is the value.  A v above 0 gets the smallest
  * number above 0 at least; an infinite m becomes NaN, an infinite v stays so.  Zero
- * codes and any scale are a fresh state.
+ * codes and any finite scale are a fresh state.
  *
  * The tensors are given once, in a plan: adamw_plan writes it to host memory, and
  * the caller copies its bytes to the device (256-byte aligned) and keeps them

@@ -68,7 +68,7 @@ __device__ __forceinline__ void decode4(float out[4], uint32_t codes, float scal
     out[3] = hi[1] * scale;
 }
 
-// Square root of a number within 2^-100 ... 2^90, correctly rounded: one correction
+// Square root of a number within 2^-100 ... 2^60, correctly rounded: one correction
 // from the exact remainder (compared with sqrtf for every mantissa of both
 // parities of the exponent, over that range).  Eight issue slots to its twenty.
 __device__ __forceinline__ float root_of(float v) {
@@ -196,8 +196,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs a) {
                           fmaxf(__builtin_fabsf(m[s][2]), __builtin_fabsf(m[s][3])));
         v_most[s] = fmaxf(fmaxf(v[s][0], v[s][1]), fmaxf(v[s][2], v[s][3]));
     }
-    const bool usual = m_least >= (27u << 23) - 1u && fmaxf(m_most[0], m_most[1]) <= 0x1p90f &&
-                       v_least >= 27u << 23 && v_last <= 217u << 23;
+    // m of 2^-60 ... 2^60 or 0, v of 2^-100 ... 2^60, a divisor of 2^-50 ... 2^43
+    const bool usual = m_least >= (67u << 23) - 1u && fmaxf(m_most[0], m_most[1]) <= 0x1p60f &&
+                       v_least >= 27u << 23 && v_last <= 187u << 23 && a.eps <= 1.0f;
     if (__all(usual)) {
 #pragma unroll
         for (int s = 0; s < kSets; ++s)

@@ -1091,11 +1091,11 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
         if (lies_over(y, in) || lies_over(pre, in)) return ONEBIT_E_ARG;
     if (lies_over(y, pre) || lies_over(pre, r) || (!in_place && lies_over(y, r)))
         return ONEBIT_E_ARG;
-    if (!product_few(M)) {
-        if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 0)) return ONEBIT_E_WORKSPACE;
+    const LinearSizes z = linear_sizes(M, N, K, false);
+    if (z.all()) {
+        if (!ws || ws_bytes < z.all()) return ONEBIT_E_WORKSPACE;
         if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     }
-    const LinearSizes z = linear_sizes(M, N, K, false);
     char* room = static_cast<char*>(ws);
     drop_stale_error();
     ProductOut o = {};
@@ -1146,9 +1146,11 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
     for (const Matrix& in : {dy, pre, x, w})
         if (lies_over(dx, in) || lies_over(dw, in) || lies_over(db, in)) return ONEBIT_E_ARG;
     if (lies_over(dx, dw) || lies_over(dx, db) || lies_over(dw, db)) return ONEBIT_E_ARG;
-    if (!ws || ws_bytes < linear_workspace_bytes(M, N, K, 1)) return ONEBIT_E_WORKSPACE;
-    if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
     const LinearSizes z = linear_sizes(M, N, K, true);
+    if (z.all()) {
+        if (!ws || ws_bytes < z.all()) return ONEBIT_E_WORKSPACE;
+        if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
+    }
     char* x_room = static_cast<char*>(ws);
     char* w_room = x_room + z.x;
     char* dz_room = w_room + z.w;

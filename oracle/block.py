@@ -85,11 +85,11 @@ def linear_grad(dy, x, w, act, pre):
 
 
 # ---------------------------------------------------------------- AdamW
-def draws(n, tensor, step, seed):
-    """The 16-bit draws of a tensor's n elements."""
+def draws(n, tensor, step, seed, first=0):
+    """The 16-bit draws of n elements of a tensor, from `first` (a multiple of 8) on."""
     groups = (n + 7) // 8
     ctr = np.zeros((groups, 4), dtype=np.uint32)
-    ctr[:, 0] = np.arange(groups, dtype=np.uint32)
+    ctr[:, 0] = np.arange(groups, dtype=np.uint32) + np.uint32(first // 8)
     ctr[:, 1] = tensor
     ctr[:, 3] = np.uint32(step & _MASK)
     key = np.array([seed & _MASK, ((seed >> 32) & _MASK) ^ KEY_TAG], dtype=np.uint32)
