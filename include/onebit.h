@@ -627,8 +627,8 @@ size_t rel_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t 
  * [rows] float, each NULL unless wanted: the backward pass reads them.
  *
  * x, y: rows of `cols` elements, ld_* elements apart (ld >= cols, up to 2^40),
- * aligned to their element.  y may be x itself (same ld); where its rows lie over
- * x's otherwise the call is refused.  cols up to 2^29, eps >= 0 and finite.  No
+ * aligned to their element.  y may be x itself (same ld); where an output lies over
+ * another argument otherwise, as far as strides show, the call is refused.  cols up to 2^29, eps >= 0 and finite.  No
  * rows or columns: a no-op.
  */
 int layer_norm_forward(const void* x, void* y, int32_t dtype, int64_t rows, int64_t cols,
@@ -643,7 +643,8 @@ int layer_norm_forward(const void* x, void* y, int32_t dtype, int64_t rows, int6
  *   dweight[c] = (accumulate ? dweight[c] : 0) + sum_r dy h
  *   dbias[c]   = (accumulate ? dbias[c] : 0) + sum_r dy
  * dx (of the element type), dweight and dbias [cols] float may each be NULL.  dx
- * may be x or dy itself (same ld).  The sums over rows are binary32 within a
+ * may be x or dy itself (same ld); other overlaps are refused as in the forward
+ * call.  The sums over rows are binary32 within a
  * workgroup and binary64 over workgroups, in an order fixed by the sizes.  With
  * no rows they are 0.
  * ws: at least layer_norm_workspace_bytes(rows, cols) bytes, 256-byte aligned,
@@ -693,12 +694,13 @@ typedef enum {
  * apart (ld >= the row's length, up to 2^40), aligned to their element.  M up to
  * 2^31 - 1, N and K up to 2^22, ceil(max(M, N) / 128) ceil(max(N, K) / 128) up to
  * 2^22.  Rows that start and end on 16 bytes (address, length and ld) are read as
- * they are; other operands are laid out anew in the workspace first.  y may be
+ * they are, and so are any rows in small products; where a large product has other
+ * operands they are laid out anew in the workspace first.  y may be
  * residual itself (same ld); where an output's rows lie over those of another
  * argument otherwise, as far as strides show, the call is refused.  With K = 0 z
  * is the bias; with M or N = 0 sums over nothing are 0.
  * ws: at least linear_workspace_bytes(...) bytes, 256-byte aligned, scratch (a
- * forward call of up to 64 rows takes NULL too).
+ * forward call of up to 32 rows takes NULL too).
  */
 typedef struct linear_args {
     int32_t dtype, activation;

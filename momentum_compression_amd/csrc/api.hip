@@ -856,6 +856,31 @@ int check_norm(int32_t dtype, int32_t w_dtype, int64_t rows, int64_t cols) {
 
 bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
 
+struct Matrix {
+    const void* p;
+    int64_t ld, rows, cols;
+    size_t size;
+};
+
+// An output's rows over another matrix's, as far as strides show: from one address
+// on, of one stride in bytes, or starting inside a matrix without gaps.
+bool lies_over(const Matrix& out, const Matrix& in) {
+    if (!out.p || !in.p || out.rows == 0 || out.cols == 0 || in.rows == 0 || in.cols == 0)
+        return false;
+    const bool after = (uintptr_t)out.p > (uintptr_t)in.p;
+    const Matrix& first = after ? in : out;
+    const Matrix& second = after ? out : in;
+    const uint64_t apart = (uintptr_t)second.p - (uintptr_t)first.p;
+    if (apart == 0) return true;
+    const uint64_t width = (uint64_t)first.cols * first.size;
+    const uint64_t pitch = (uint64_t)first.ld * first.size;
+    if (first.rows == 1 || first.ld == first.cols) return apart < width * (uint64_t)first.rows;
+    if (pitch != (uint64_t)second.ld * second.size && second.rows > 1) return false;
+    const uint64_t down = apart / pitch, right = apart % pitch;
+    return (down < (uint64_t)first.rows && right < width) ||
+           (down + 1 < (uint64_t)first.rows && pitch - right < (uint64_t)second.cols * second.size);
+}
+
 }  // namespace
 
 extern "C" {
@@ -873,9 +898,16 @@ int layer_norm_forward(const void* x, void* y, int32_t dtype, int64_t rows, int6
     if (!aligned(x, size) || !aligned(y, size) || !aligned(weight, w_size) ||
         !aligned(bias, w_size) || !aligned(mean, 4) || !aligned(rstd, 4))
         return ONEBIT_E_ALIGN;
-    if (rows_cross(y, ld_y, x, ld_x, rows, cols, size) || y == weight || y == bias ||
-        (mean && (mean == rstd || mean == x || mean == y)) || (rstd && (rstd == x || rstd == y)))
-        return ONEBIT_E_ARG;
+    const Matrix xs{x, ld_x, rows, cols, size}, ys{y, ld_y, rows, cols, size},
+        w{weight, cols, 1, cols, w_size}, b{bias, cols, 1, cols, w_size},
+        means{mean, rows, 1, rows, 4}, rstds{rstd, rows, 1, rows, 4};
+    if (lies_over(ys, xs) && !(y == x && (ld_y == ld_x || rows == 1))) return ONEBIT_E_ARG;
+    for (const Matrix& in : {w, b})
+        if (lies_over(ys, in)) return ONEBIT_E_ARG;
+    for (const Matrix& out : {means, rstds})
+        for (const Matrix& other : {xs, ys, w, b})
+            if (lies_over(out, other)) return ONEBIT_E_ARG;
+    if (lies_over(means, rstds)) return ONEBIT_E_ARG;
     NormArgs a = {};
     a.x = x;
     a.y = y;
@@ -920,15 +952,20 @@ int layer_norm_backward(const void* dy, const void* x, const float* mean, const 
         !aligned(weight, type_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) ||
         !aligned(dweight, 4) || !aligned(dbias, 4))
         return ONEBIT_E_ALIGN;
-    if (rows > 0 && dx &&
-        (rows_cross(dx, ld_dx, x, ld_x, rows, cols, size) ||
-         rows_cross(dx, ld_dx, dy, ld_dy, rows, cols, size) || dx == weight || dx == mean ||
-         dx == rstd || dx == dweight || dx == dbias))
-        return ONEBIT_E_ARG;
-    for (const void* out : {(const void*)dweight, (const void*)dbias})
-        if (out && (out == x || out == dy || out == weight || out == mean || out == rstd))
+    const size_t w_size = type_size(w_dtype);
+    const Matrix dys{dy, ld_dy, rows, cols, size}, xs{x, ld_x, rows, cols, size},
+        dxs{dx, ld_dx, rows, cols, size}, w{weight, cols, 1, cols, w_size},
+        means{mean, rows, 1, rows, 4}, rstds{rstd, rows, 1, rows, 4},
+        dws{dweight, cols, 1, cols, 4}, dbs{dbias, cols, 1, cols, 4};
+    for (const Matrix& in : {dys, xs})
+        if (lies_over(dxs, in) && !(dx == in.p && (ld_dx == in.ld || rows == 1)))
             return ONEBIT_E_ARG;
-    if (dweight && dweight == dbias) return ONEBIT_E_ARG;
+    for (const Matrix& in : {w, means, rstds})
+        if (lies_over(dxs, in)) return ONEBIT_E_ARG;
+    for (const Matrix& out : {dws, dbs})
+        for (const Matrix& other : {dys, xs, dxs, w, means, rstds})
+            if (lies_over(out, other)) return ONEBIT_E_ARG;
+    if (lies_over(dws, dbs)) return ONEBIT_E_ARG;
     if (sums) {
         if (!ws || ws_bytes < layer_norm_workspace_bytes(rows, cols)) return ONEBIT_E_WORKSPACE;
         if (!aligned(ws, 256)) return ONEBIT_E_ALIGN;
@@ -1014,31 +1051,6 @@ int check_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t s
     if (!p) return ONEBIT_E_NULL;
     if (!ld_ok(ld, cols)) return ONEBIT_E_SIZE;
     return aligned(p, size) ? ONEBIT_OK : ONEBIT_E_ALIGN;
-}
-
-struct Matrix {
-    const void* p;
-    int64_t ld, rows, cols;
-    size_t size;
-};
-
-// An output's rows over another matrix's, as far as strides show: from one address
-// on, of one stride in bytes, or starting inside a matrix without gaps.
-bool lies_over(const Matrix& out, const Matrix& in) {
-    if (!out.p || !in.p || out.rows == 0 || out.cols == 0 || in.rows == 0 || in.cols == 0)
-        return false;
-    const bool after = (uintptr_t)out.p > (uintptr_t)in.p;
-    const Matrix& first = after ? in : out;
-    const Matrix& second = after ? out : in;
-    const uint64_t apart = (uintptr_t)second.p - (uintptr_t)first.p;
-    if (apart == 0) return true;
-    const uint64_t width = (uint64_t)first.cols * first.size;
-    const uint64_t pitch = (uint64_t)first.ld * first.size;
-    if (first.rows == 1 || first.ld == first.cols) return apart < width * (uint64_t)first.rows;
-    if (pitch != (uint64_t)second.ld * second.size && second.rows > 1) return false;
-    const uint64_t down = apart / pitch, right = apart % pitch;
-    return (down < (uint64_t)first.rows && right < width) ||
-           (down + 1 < (uint64_t)first.rows && pitch - right < (uint64_t)second.cols * second.size);
 }
 
 // Rows that a product that takes operands anywhere takes as they are.

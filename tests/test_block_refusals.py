@@ -75,6 +75,19 @@ def test_layer_norm_backward_refusals(lib):
     assert _norm_grad(lib, cols=0) == ob.ONEBIT_OK
 
 
+def test_layer_norm_partial_overlaps(lib):
+    """Outputs that start inside another argument, or that another starts inside."""
+    # x: 4 rows of 40 bytes from P on
+    for bad in (dict(mean=P + 156), dict(mean=P - 12), dict(rstd=P + 40), dict(w=4 * P + 8),
+                dict(b=4 * P + 156), dict(mean=8 * P, rstd=8 * P + 12),
+                dict(mean=8 * P, w=8 * P - 36), dict(y=P + 156), dict(y=P - 156)):
+        assert _norm(lib, **bad) == ob.ONEBIT_E_ARG, bad
+    # dw, db: 40 bytes from 6 P and 7 P on
+    for bad in (dict(db=6 * P + 36), dict(db=6 * P - 36), dict(dw=5 * P + 156), dict(dw=3 * P + 12),
+                dict(dx=3 * P - 156), dict(w=7 * P + 20), dict(dx=P + 156)):
+        assert _norm_grad(lib, **bad) == ob.ONEBIT_E_ARG, bad
+
+
 def test_layer_norm_workspace():
     f = ob.layer_norm_workspace_bytes
     assert f(0, 100) == 256 and f(-1, 100) == f(10, -1) == 0
