@@ -4,7 +4,9 @@
 The compute lives in libonebit.so (hand-written HIP for gfx950, C ABI in
 include/onebit.h); ``momentum_compression_amd.onebit`` is its ctypes binding
 and ``momentum_compression_amd.state`` allocates the buffers one simulated
-data-parallel group needs and drives one step through the binding.
+data-parallel group needs and drives one step through the binding.  Operators of
+the models that it trains stand beside it: dropout, position bias, attention,
+layer norm, linear layers and an AdamW step over many tensors.
 """
 
 from . import onebit  # noqa: F401

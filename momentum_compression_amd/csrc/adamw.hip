@@ -4,8 +4,10 @@
 // workgroup names (one scalar load; a search over the tensors' offsets would be
 // nine in a row).  A wave has two blocks of 256 elements at a time, a lane four
 // consecutive elements of each.  The kernel
-// moves what the step cannot do without, 28 + g + copy bytes an element with
-// 32-bit states and 12 + g + copy with 8-bit ones, and is bound by them.
+// moves what the step cannot do without, 24 + g + copy bytes an element with
+// 32-bit states and 12 + g + copy with 8-bit ones, and is bound by them: 302 tensors
+// of 336 million elements in 1484 to 1671 us (9.41 GB, 5.6 to 6.3 TB/s, one GPU or
+// another), with 8-bit states in 868 to 893 (5.40 GB, 6.0 to 6.2 TB/s).
 //
 // 8-bit states.  256 consecutive elements share a power of two; over it, m is an
 // e4m3 number and v an e5m2 one (v spans the square of what m does: two bits of

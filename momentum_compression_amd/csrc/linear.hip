@@ -298,7 +298,10 @@ constexpr size_t product_lds(bool ahead) {
 // one barrier, which stands before the last part of the tile before.  Behind that
 // barrier the tile that was read is replaced, half of it among the products of that
 // part and half among those of the next: a burst of loads would hold up the waves,
-// as the loads of a CU pass at 64 bytes a cycle.  With both operands by rows tiles
+// as the loads of a CU pass at 64 bytes a cycle.  (8192^3 bf16: 814 to 850 us, 1290 to
+// 1350 TFLOP/s, the matrix unit busy three quarters of the time; 8192 x 4096 over 1024:
+// 69 to 73 us; with a GELU and `pre` 86, as nothing runs beside the epilogue of a CU's
+// one workgroup.)  With both operands by rows tiles
 // go from memory to LDS directly.  Transposing reads are not told apart from such
 // loads by the compiler, which waits for all of them before the first read; with
 // those a tile goes through registers, one tile further ahead.
@@ -746,7 +749,8 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(PadRows one, PadRows
 }
 
 // ---------------------------------------------------------------- the activation's slope
-// A thread has eight columns of a part of the rows.
+// A thread has eight columns of a part of the rows.  Bound by the slope's arithmetic
+// as much as by the bytes (8192 x 4096 with a GELU: 47 us, 31 for its 201 MB).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t groups,
                                                          int64_t rows_of_part) {
