@@ -996,8 +996,6 @@ int layer_norm_backward(const void* dy, const void* x, const float* mean, const 
 
 namespace {
 
-constexpr int64_t kMaxFeatures = (int64_t)1 << 22;  // a tile's rows within 2^31 bytes
-
 int check_linear_sizes(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > kMaxFeatures || K > kMaxFeatures)
         return ONEBIT_E_SIZE;
@@ -1005,13 +1003,6 @@ int check_linear_sizes(int64_t M, int64_t N, int64_t K) {
     const int64_t rows = M > N ? M : N, cols = N > K ? N : K;
     if (ceil_div(rows, 128) * ceil_div(cols, 128) > ((int64_t)1 << 22)) return ONEBIT_E_SIZE;
     return ONEBIT_OK;
-}
-
-int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
-
-// Rows that start and end on 16 bytes, in a buffer whose tiles 32 bits address.
-bool whole_chunks(const void* p, int64_t ld, int64_t rows, int64_t cols) {
-    return aligned(p, 16) && cols % 8 == 0 && ((ld % 8 == 0 && ld <= kMaxFeatures) || rows <= 1);
 }
 
 // Workspace in the order it is carved: operands laid out anew, dz, the partial
@@ -1051,26 +1042,6 @@ int check_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t s
     if (!p) return ONEBIT_E_NULL;
     if (!ld_ok(ld, cols)) return ONEBIT_E_SIZE;
     return aligned(p, size) ? ONEBIT_OK : ONEBIT_E_ALIGN;
-}
-
-// Rows that a product that takes operands anywhere takes as they are.
-bool any_rows(int64_t ld, int64_t rows, int64_t cols) {
-    return cols >= 8 && (ld <= kMaxFeatures || rows <= 1);
-}
-
-// The operand as the product reads it; `anew` says how it is laid out at `room`
-// first, if need be, `any` that its rows are not whole chunks.
-ProductIn operand(const void* p, int64_t ld, int64_t rows, int64_t cols, char* room,
-                  bool takes_any, PadRows& anew, bool& any) {
-    anew = PadRows{};
-    if (rows == 0 || cols == 0 || whole_chunks(p, ld, rows, cols))
-        return ProductIn{p, rows <= 1 ? padded(cols) : ld};
-    if (takes_any && any_rows(ld, rows, cols)) {
-        any = true;
-        return ProductIn{p, rows <= 1 ? padded(cols) : ld};
-    }
-    anew = PadRows{p, room, ld, padded(cols), rows, cols};
-    return ProductIn{room, padded(cols)};
 }
 
 }  // namespace
@@ -1124,8 +1095,8 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
     o.act = a->activation;
     o.bias_wide = a->bias_dtype == ONEBIT_F32;
     if (product_few(M))
-        return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w},
-                                             ProductIn{a->x, a->ld_x}, K, o, stream));
+        return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w, K},
+                                             ProductIn{a->x, a->ld_x, K}, K, o, stream));
     const bool takes_any = product_any(product_plan(M, N, K, true, true));
     PadRows x_anew, w_anew;
     bool any = false;
@@ -1170,22 +1141,17 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
     float* parts = reinterpret_cast<float*>(dz_room + z.dz + z.sums);
     drop_stale_error();
     hipError_t e = hipSuccess;
-    ProductIn dz{a->dy, M <= 1 ? padded(N) : a->ld_dy};
     const bool want_dx = a->dx && M > 0 && K > 0, want_dw = a->dw && N > 0 && K > 0;
-    const bool dx_any = product_any(product_plan(M, K, N, false, true));
-    const bool dw_any = product_any(product_plan(N, K, M, false, false));
-    // dz is laid out anew for the activation, or where a product does not take it
-    const bool chunks = M == 0 || N == 0 || whole_chunks(a->dy, a->ld_dy, M, N);
-    const bool anew = (want_dx || want_dw) &&
-                      (act || (!chunks && (!any_rows(a->ld_dy, M, N) || (want_dx && !dx_any) ||
-                                           (want_dw && !dw_any))));
-    const bool dz_any = !anew && !chunks;
+    const GradIn g = grad_operands(GradShape{
+        a->dy, a->x, a->w, M, N, K, a->ld_dy, a->ld_x, a->ld_w, act, want_dx, want_dw,
+        product_any(product_plan(M, K, N, false, true)),
+        product_any(product_plan(N, K, M, false, false)), x_room, w_room, dz_room});
     if (N > 0) {
-        if (M > 0 && (anew || a->dbias)) {
+        if (M > 0 && (g.dz_anew || a->dbias)) {
             SlopeArgs s = {};
             s.dy = a->dy;
             s.pre = a->pre;
-            s.dz = anew ? dz_room : nullptr;
+            s.dz = g.dz_anew ? dz_room : nullptr;
             s.partials = a->dbias ? sums : nullptr;
             s.rows = M;
             s.cols = N;
@@ -1195,18 +1161,12 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
             s.act = a->activation;
             s.dtype = a->dtype;
             e = launch_slope(s, stream);
-            if (anew) dz = ProductIn{dz_room, padded(N)};
         }
         if (e == hipSuccess && a->dbias)
             e = launch_column_join(sums, M > 0 ? slope_parts(M, N) : 0, N, N, a->dbias, nullptr,
                                    a->accumulate != 0, stream);
     }
-    PadRows x_anew = {}, w_anew = {};
-    ProductIn xs = {}, wi = {};
-    bool w_any = dz_any, x_any = dz_any;
-    if (want_dx) wi = operand(a->w, a->ld_w, N, K, w_room, dx_any, w_anew, w_any);
-    if (want_dw) xs = operand(a->x, a->ld_x, M, K, x_room, dw_any, x_anew, x_any);
-    if (e == hipSuccess) e = launch_pad_rows(x_anew, w_anew, stream);
+    if (e == hipSuccess) e = launch_pad_rows(g.x_anew, g.w_anew, stream);
     if (e == hipSuccess && want_dx) {
         ProductOut o = {};
         o.out = a->dx;
@@ -1214,7 +1174,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
         o.cols = K;
         o.ld = a->ld_dx;
         o.type = a->dtype;
-        e = launch_product(a->dtype, wi, false, dz, true, N, o, w_any, parts, stream);
+        e = launch_product(a->dtype, g.w, false, g.dz, true, N, o, g.dx_any, parts, stream);
     }
     if (e == hipSuccess && want_dw) {
         ProductOut o = {};
@@ -1224,8 +1184,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
         o.ld = a->ld_dw;
         o.type = a->dw_dtype;
         o.accumulate = a->accumulate != 0;
-        e = launch_product(a->dtype, xs, false, dz, false, M, o, x_any, parts,
-                           stream);
+        e = launch_product(a->dtype, g.x, false, g.dz, false, M, o, g.dw_any, parts, stream);
     }
     return hip_status(e);
 }

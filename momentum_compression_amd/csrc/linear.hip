@@ -132,7 +132,8 @@ struct Operand {
     int32_t count;        // of the operand's index from the tile's first on
     int32_t mine;         // by rows: the lane's first k in a tile
     int32_t row0;         // the lane's first row in LDS
-    int32_t past;         // else: of its eight columns, those past the last one
+    int32_t past;         // else: of its eight columns, those past the row's end
+    int64_t length;       // of a contiguous row: elements that may be read
 
     static __device__ __forceinline__ int swizzled(int row, int chunk) {
         if (!ROWS) return chunk ^ ((row & 3) << 2);
@@ -149,7 +150,8 @@ struct Operand {
         at = (uint32_t)row * stride + 16 * chunk;
         mine = 8 * chunk;
         row0 = row;
-        past = mine + 8 > count ? mine + 8 - count : 0;
+        length = in.row;
+        past = past_end(first + mine, length);
         if (!ROWS && 8 * chunk >= count) at = 0x80000000u;
     }
     // The buffer of the tile from k0 on and the lane's offset in it.
@@ -180,10 +182,8 @@ struct Operand {
     }
     // Rows that lie anywhere and end anywhere (of eight elements or more): how many
     // of the lane's eight elements lie past the row's end, in the tile from k0 on.
-    __device__ __forceinline__ int32_t over_of(int64_t k0, int64_t depth) const {
-        if (!ROWS) return past;
-        const int64_t over = k0 + mine + 8 - depth;
-        return over <= 0 ? 0 : over < 8 ? (int32_t)over : 8;
+    __device__ __forceinline__ int32_t over_of(int64_t k0) const {
+        return ROWS ? past_end(k0 + mine, length) : past;
     }
     // Piece x of such a tile: where a row ends inside the lane's eight elements, the
     // row's last eight.
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
             aimed = (int64_t)step * kDeep;
             a_over[1] = a_over[0];
             b_over[1] = b_over[0];
-            a_over[0] = as.over_of(aimed, p.depth);
-            b_over[0] = bs.over_of(aimed, p.depth);
+            a_over[0] = as.over_of(aimed);
+            b_over[0] = bs.over_of(aimed);
             return;
         }
         ar = as.buffer((int64_t)step * kDeep, p.depth, ao);
@@ -906,6 +906,8 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
                           const ProductOut& out, bool any, float* parts, hipStream_t st) {
     if (out.rows == 0 || out.cols == 0) return hipSuccess;
+    // what past_end() needs
+    if (any && depth > 0 && (cols_in.row < 8 || rows_in.row < 8)) return hipErrorInvalidValue;
     const ProductPlan plan = product_plan(out.rows, out.cols, depth, cols_by_rows, rows_by_rows);
     ProductArgs p = {};
     p.a = cols_in;

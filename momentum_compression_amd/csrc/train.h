@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.h"
+#include "operands.h"
 
 namespace onebit {
 
@@ -171,13 +172,6 @@ struct ProductOut {
     bool accumulate;
 };
 
-// An operand: element (i, k) of the product's index i and the summed index k is
-// at p[i ld + k] (by rows) or p[k ld + i].
-struct ProductIn {
-    const void* p;
-    int64_t ld;
-};
-
 // How a product is divided: tiles of tile_a columns by tile_b rows of the result,
 // the sum over `splits` parts.
 struct ProductPlan {
@@ -196,7 +190,7 @@ bool product_any(const ProductPlan& plan);
 // types: by_rows says whether k is the contiguous index.  (cols_in, rows_in) is
 // (true, true), (false, true) or (false, false).  Contiguous indices and strides
 // are multiples of 8 and the addresses of 16 bytes; with `any` (product_any)
-// contiguous indices are 8 or more.
+// contiguous rows have 8 elements or more, and others are refused.
 hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_rows,
                           const ProductIn& rows_in, bool rows_by_rows, int64_t depth,
                           const ProductOut& out, bool any, float* parts, hipStream_t st);
@@ -207,13 +201,7 @@ bool product_few(int64_t rows);
 hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const ProductIn& rows_in,
                               int64_t depth, const ProductOut& out, hipStream_t st);
 
-// to[r][c] = from[r][c], columns cols ... padded - 1 are 0 (16-bit elements).  Two
-// matrices in one launch; rows 0 for none.
-struct PadRows {
-    const void* from;
-    void* to;
-    int64_t ld, padded, rows, cols;
-};
+// Two matrices in one launch.
 hipError_t launch_pad_rows(const PadRows& one, const PadRows& two, hipStream_t st);
 
 // dz = dy act'(pre), rounded to the element type, into `dz` (rows of `padded`
