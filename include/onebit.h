@@ -685,9 +685,12 @@ typedef enum {
  *   dw[n][k] = (accumulate ? dw[n][k] : 0) + sum_m dz[m][n] x[m][k]
  *   dbias[n] = (accumulate ? dbias[n] : 0) + sum_m dz[m][n]
  * The residual's gradient is dy.  dx, dw and dbias may each be NULL.  dw is of
- * dw_dtype (ONEBIT_F32 or the element type), dbias float.  With an activation, dz
- * is rounded to the element type for the two products (dbias takes it unrounded):
- * as much error as the rounding of a 16-bit dx or dw.  pre is read with an
+ * dw_dtype (ONEBIT_F32 or the element type), dbias float.  With GELU, GELU_TANH or
+ * SILU the two products take dz as the sum of two numbers of the element type (to
+ * 2^-15 of it in BF16, 2^-21 or 2^-25 absolute in F16, and 2^-14 past F16's range).
+ * With round_dz = 1 they take it rounded once to the element type: about half the products'
+ * time, for as much error again as the rounding of a 16-bit dx or dw, and infinite
+ * where dz passes F16's range.  dbias takes dz unrounded.  pre is read with an
  * activation only.
  *
  * x, dx [M][K], w, dw [N][K], y, pre, residual, dy [M][N]: rows ld_* elements
@@ -719,6 +722,7 @@ typedef struct linear_args {
     float* dbias;
     int64_t ld_dy, ld_dx, ld_dw;
     int32_t accumulate;
+    int32_t round_dz;          /* 0 or 1                                        */
 } linear_args;
 
 int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream);

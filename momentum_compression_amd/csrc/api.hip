@@ -1005,7 +1005,7 @@ int check_linear_sizes(int64_t M, int64_t N, int64_t K) {
     return ONEBIT_OK;
 }
 
-// Workspace in the order it is carved: operands laid out anew, dz, the partial
+// Workspace in the order it is carved: operands laid out anew, dz's parts, the partial
 // sums of dbias, the parts of a divided product.
 struct LinearSizes {
     size_t x, w, dz, sums, parts;
@@ -1021,11 +1021,13 @@ LinearSizes linear_sizes(int64_t M, int64_t N, int64_t K, bool backward) {
         z.parts = round_up(product_plan(M, N, K, true, true).bytes);
         return z;
     }
-    z.dz = round_up((size_t)M * padded(N) * 2);
+    z.dz = round_up((size_t)M * padded(N) * 2 * 2);
     z.sums = round_up((size_t)slope_parts(M, N) * N * sizeof(float));
-    const size_t dx = product_plan(M, K, N, false, true).bytes,
-                 dw = product_plan(N, K, M, false, false).bytes;
-    z.parts = round_up(dx > dw ? dx : dw);
+    for (const bool two : {false, true}) {
+        const size_t dx = product_plan(M, K, product_depth(N, two), false, true).bytes,
+                     dw = product_plan(N, K, product_depth(M, two), false, false).bytes;
+        z.parts = std::max(z.parts, round_up(std::max(dx, dw)));
+    }
     return z;
 }
 
@@ -1095,8 +1097,8 @@ int linear_forward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t 
     o.act = a->activation;
     o.bias_wide = a->bias_dtype == ONEBIT_F32;
     if (product_few(M))
-        return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w, K},
-                                             ProductIn{a->x, a->ld_x, K}, K, o, stream));
+        return hip_status(launch_product_few(a->dtype, ProductIn{a->w, a->ld_w, K, 0},
+                                             ProductIn{a->x, a->ld_x, K, 0}, K, o, stream));
     const bool takes_any = product_any(product_plan(M, N, K, true, true));
     PadRows x_anew, w_anew;
     bool any = false;
@@ -1112,6 +1114,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
     if (st) return st;
     const int64_t M = a->M, N = a->N, K = a->K;
     if (a->accumulate != 0 && a->accumulate != 1) return ONEBIT_E_ARG;
+    if (a->round_dz != 0 && a->round_dz != 1) return ONEBIT_E_ARG;
     if (a->dw && a->dw_dtype != ONEBIT_F32 && a->dw_dtype != a->dtype) return ONEBIT_E_ARG;
     const size_t dw_size = a->dw ? type_size(a->dw_dtype) : 2;
     const bool act = a->activation != ONEBIT_NONE;
@@ -1142,10 +1145,12 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
     drop_stale_error();
     hipError_t e = hipSuccess;
     const bool want_dx = a->dx && M > 0 && K > 0, want_dw = a->dw && N > 0 && K > 0;
+    const bool two = !a->round_dz && !slope_exact(a->activation);
     const GradIn g = grad_operands(GradShape{
-        a->dy, a->x, a->w, M, N, K, a->ld_dy, a->ld_x, a->ld_w, act, want_dx, want_dw,
-        product_any(product_plan(M, K, N, false, true)),
-        product_any(product_plan(N, K, M, false, false)), x_room, w_room, dz_room});
+        a->dy, a->x, a->w, M, N, K, a->ld_dy, a->ld_x, a->ld_w, act, two, want_dx, want_dw,
+        product_any(product_plan(M, K, product_depth(N, two), false, true)),
+        product_any(product_plan(N, K, product_depth(M, two), false, false)), x_room, w_room,
+        dz_room});
     if (N > 0) {
         if (M > 0 && (g.dz_anew || a->dbias)) {
             SlopeArgs s = {};
@@ -1158,6 +1163,7 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
             s.ld_dy = a->ld_dy;
             s.ld_pre = a->ld_pre;
             s.padded = padded(N);
+            s.rest = g.dz.rest;
             s.act = a->activation;
             s.dtype = a->dtype;
             e = launch_slope(s, stream);

@@ -129,6 +129,7 @@ struct Operand {
     static_assert(ROWS ? kChunks == 8 : kChunks >= 16, "the xor's layouts");
     const char* base;
     uint32_t stride, at;  // in bytes
+    int64_t rest;         // from the first part to the second
     int32_t count;        // of the operand's index from the tile's first on
     int32_t mine;         // by rows: the lane's first k in a tile
     int32_t row0;         // the lane's first row in LDS
@@ -146,6 +147,7 @@ struct Operand {
         stride = (uint32_t)in.ld * 2;
         const int64_t left = extent - first;
         count = left < TILE ? (int32_t)left : TILE;
+        rest = in.rest;
         base = (const char*)in.p + (ROWS ? first * in.ld * 2 : first * 2);
         at = (uint32_t)row * stride + 16 * chunk;
         mine = 8 * chunk;
@@ -154,11 +156,15 @@ struct Operand {
         past = past_end(first + mine, length);
         if (!ROWS && 8 * chunk >= count) at = 0x80000000u;
     }
-    // The buffer of the tile from k0 on and the lane's offset in it.
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int64_t k0, int64_t depth,
+    // Where the tile from k0 on begins, in the first part or the second.
+    __device__ __forceinline__ const char* start(int64_t k0, bool second) const {
+        return base + (ROWS ? k0 * 2 : k0 * stride) + (second ? rest : 0);
+    }
+    // The buffer of that tile and the lane's offset in it.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int64_t k0, bool second, int64_t depth,
                                                              uint32_t& off) const {
         const int64_t left = depth - k0;
-        const char* from = base + (ROWS ? k0 * 2 : k0 * stride);
+        const char* from = start(k0, second);
         const int32_t deep = left < kDeep ? (int32_t)left : kDeep;
         // rows are made of whole chunks
         const uint32_t bytes =
@@ -187,14 +193,13 @@ struct Operand {
     }
     // Piece x of such a tile: where a row ends inside the lane's eight elements, the
     // row's last eight.
-    __device__ __forceinline__ u32x4 fetch_any(int x, int64_t k0, int64_t depth,
+    __device__ __forceinline__ u32x4 fetch_any(int x, int64_t k0, bool second, int64_t depth,
                                                int32_t over) const {
         const int row = row0 + x * kRowsAtOnce;
         u32x4 v = {};
         if (over < 8 && (ROWS ? row < count : k0 + row < depth)) {
             typedef u32x4 Any __attribute__((aligned(2)));
-            const char* from = base + (ROWS ? k0 * 2 : k0 * stride) + ((int64_t)row * stride) +
-                               2 * (mine - over);
+            const char* from = start(k0, second) + (int64_t)row * stride + 2 * (mine - over);
             v = *reinterpret_cast<const Any*>(from);
         }
         return v;
@@ -247,6 +252,7 @@ struct ProductArgs {
     ProductOut out;
     float* parts;         // [splits][rows][padded] of a divided sum, or nullptr
     int64_t depth, padded;
+    int32_t steps, half;  // of kDeep in the whole sum and in its first parts
     int32_t tiles_a, tiles_b, splits;
 };
 
@@ -327,9 +333,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
     uint32_t ta, tb, split;
     tile_of(p, ta, tb, split);
     const int64_t a0 = (int64_t)ta * TA, b0 = (int64_t)tb * TB;
-    const int32_t steps = (int32_t)((p.depth + kDeep - 1) / kDeep);
-    const int32_t first = (int32_t)((int64_t)steps * split / p.splits);
-    const int32_t last = (int32_t)((int64_t)steps * (split + 1) / p.splits);
+    const int32_t first = (int32_t)((int64_t)p.steps * split / p.splits);
+    const int32_t last = (int32_t)((int64_t)p.steps * (split + 1) / p.splits);
     const A as(p.a, a0, p.out.cols, wave, lane);
     const B bs(p.b, b0, p.out.rows, wave, lane);
     f32x16 acc[na][nb];
@@ -352,19 +357,21 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
     __amdgpu_buffer_rsrc_t ar, br;
     uint32_t ao = 0, bo = 0;
     int64_t aimed = 0;
+    bool second = false;
     // of ANY, past the rows' ends: in the tile that is fetched and the one before it
     int32_t a_over[2] = {}, b_over[2] = {};
     auto aim = [&](int32_t step) {
+        second = step >= p.half;
+        aimed = (int64_t)(second ? step - p.half : step) * kDeep;
         if constexpr (ANY) {
-            aimed = (int64_t)step * kDeep;
             a_over[1] = a_over[0];
             b_over[1] = b_over[0];
             a_over[0] = as.over_of(aimed);
             b_over[0] = bs.over_of(aimed);
             return;
         }
-        ar = as.buffer((int64_t)step * kDeep, p.depth, ao);
-        br = bs.buffer((int64_t)step * kDeep, p.depth, bo);
+        ar = as.buffer(aimed, second, p.depth, ao);
+        br = bs.buffer(aimed, second, p.depth, bo);
     };
     // piece x of the tile that was aimed at
     auto start = [&](int x, char* tile) {
@@ -372,8 +379,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void product_kernel(ProductArgs p)
             if (x < A::kPer) as.load(tile, x, ar, ao, wave);
             else bs.load(tile + A::kBytes, x - A::kPer, br, bo, wave);
         } else if constexpr (ANY) {
-            held[x] = x < A::kPer ? as.fetch_any(x, aimed, p.depth, a_over[0])
-                                  : bs.fetch_any(x - A::kPer, aimed, p.depth, b_over[0]);
+            held[x] = x < A::kPer ? as.fetch_any(x, aimed, second, p.depth, a_over[0])
+                                  : bs.fetch_any(x - A::kPer, aimed, second, p.depth, b_over[0]);
         } else {
             held[x] = x < A::kPer ? as.fetch(x, ar, ao) : bs.fetch(x - A::kPer, br, bo);
         }
@@ -749,9 +756,31 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(PadRows one, PadRows
 }
 
 // ---------------------------------------------------------------- the activation's slope
+// d as the sum of two numbers of the element type: to 2^-15 of it (bfloat16), or to
+// 2^-21 or 2^-25 absolute (float16; 2^-14 past the type's range, where a slope above 1
+// may lead).  The first is cut off below d's magnitude, never d itself, so that both have its
+// sign (from 2^-116 and from 2^-23 on) and an infinity in the other operand meets no 0
+// and no opposite number.
+__device__ __forceinline__ float below(float d) {  // of d >= 0
+    const uint32_t u = __float_as_uint(d);
+    return __uint_as_float(u - (u ? 1u : 0u));
+}
+__device__ __forceinline__ void two_parts(float d, bf16& first, bf16& rest) {
+    const float cut = below(__builtin_fabsf(d));
+    first = __builtin_bit_cast(bf16, (uint16_t)(__float_as_uint(__builtin_copysignf(cut, d)) >> 16));
+    rest = (bf16)(d - (float)first);
+}
+__device__ __forceinline__ void two_parts(float d, f16& first, f16& rest) {
+    // the rest is a float16 number above 0, so it is 2^-24 at least
+    const float most = __builtin_fabsf(d);
+    const float cut = fminf(below(most), fmaxf(most - 0x1p-24f, 0.0f));
+    first = (f16)__builtin_amdgcn_cvt_pkrtz(__builtin_copysignf(cut, d), 0.0f)[0];
+    rest = (f16)(d - (float)first);
+}
+
 // A thread has eight columns of a part of the rows.  Bound by the slope's arithmetic
 // as much as by the bytes (8192 x 4096 with a GELU: 47 us, 31 for its 201 MB).
-template <typename T, int ACT>
+template <typename T, int ACT, bool TWO>
 __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t groups,
                                                          int64_t rows_of_part) {
     const int64_t strips = (groups + kThreads - 1) / kThreads;
@@ -776,7 +805,16 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t gr
             // the rest of the last group is zeros
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = e < n ? d[e] : 0.0f;
-            store_row8((T*)a.dz + r * a.padded + c, d, 8);
+            T* to = (T*)a.dz + r * a.padded + c;
+            if constexpr (TWO) {
+                T first[8], rest[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) two_parts(d[e], first[e], rest[e]);
+                *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, first);
+                *reinterpret_cast<u32x4*>((char*)to + a.rest) = __builtin_bit_cast(u32x4, rest);
+            } else {
+                store_row8(to, d, 8);
+            }
         }
     }
     if (!a.partials) return;
@@ -885,6 +923,10 @@ ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by
     return best;
 }
 
+int64_t product_depth(int64_t depth, bool two) {
+    return two ? 2 * tiles_of(depth, kDeep) * kDeep : depth;
+}
+
 bool product_any(const ProductPlan& plan) { return plan.tile_a == 128; }
 
 bool product_few(int64_t rows) { return rows <= kFewRows; }
@@ -908,13 +950,17 @@ hipError_t launch_product(int32_t dtype, const ProductIn& cols_in, bool cols_by_
     if (out.rows == 0 || out.cols == 0) return hipSuccess;
     // what past_end() needs
     if (any && depth > 0 && (cols_in.row < 8 || rows_in.row < 8)) return hipErrorInvalidValue;
-    const ProductPlan plan = product_plan(out.rows, out.cols, depth, cols_by_rows, rows_by_rows);
+    const bool two = cols_in.rest || rows_in.rest;
+    const ProductPlan plan =
+        product_plan(out.rows, out.cols, product_depth(depth, two), cols_by_rows, rows_by_rows);
     ProductArgs p = {};
     p.a = cols_in;
     p.b = rows_in;
     p.out = out;
     p.parts = plan.splits > 1 ? parts : nullptr;
     p.depth = depth;
+    p.half = two ? (int32_t)tiles_of(depth, kDeep) : INT32_MAX;
+    p.steps = (int32_t)tiles_of(product_depth(depth, two), kDeep);
     p.padded = (out.cols + 7) / 8 * 8;
     p.tiles_a = (int32_t)tiles_of(out.cols, plan.tile_a);
     p.tiles_b = (int32_t)tiles_of(out.rows, plan.tile_b);
@@ -948,13 +994,19 @@ hipError_t launch_slope(const SlopeArgs& a, hipStream_t st) {
     const int64_t parts = slope_parts(a.rows, a.cols);
     const dim3 grid((unsigned)(strips * parts)), block(kThreads);
     const int64_t rows_of_part = tiles_of(a.rows, parts);
-    with_act(a.act, [&](auto act) {
+    auto launch = [&](auto act, auto two) {
         if (a.dtype == ONEBIT_BF16)
-            hipLaunchKernelGGL((slope_kernel<bf16, act.value>), grid, block, 0, st, a, groups,
-                               rows_of_part);
+            hipLaunchKernelGGL((slope_kernel<bf16, act.value, two.value>), grid, block, 0, st, a,
+                               groups, rows_of_part);
         else
-            hipLaunchKernelGGL((slope_kernel<f16, act.value>), grid, block, 0, st, a, groups,
-                               rows_of_part);
+            hipLaunchKernelGGL((slope_kernel<f16, act.value, two.value>), grid, block, 0, st, a,
+                               groups, rows_of_part);
+    };
+    with_act(a.act, [&](auto act) {
+        if constexpr (!slope_exact(act.value)) {
+            if (a.dz && a.rest) return launch(act, std::true_type{});
+        }
+        launch(act, std::false_type{});
     });
     return hipGetLastError();
 }

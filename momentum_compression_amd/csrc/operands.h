@@ -13,10 +13,14 @@ constexpr int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 
 // An operand: element (i, k) of the product's index i and the summed index k is
 // at p[i ld + k] (by rows) or p[k ld + i].  Of a contiguous row `row` elements may be
-// read: the matrix's own, or of rows laid out anew also the zeros behind them.
+// read: the matrix's own, or of rows laid out anew also the zeros behind them.  Where
+// one operand of a product is the sum of two parts of the same layout, the second
+// `rest` bytes behind the first, the sum over k goes over the first parts and then over
+// the rest (0 bytes for the other operand).
 struct ProductIn {
     const void* p;
     int64_t ld, row;
+    int64_t rest;
 };
 
 // Of the eight elements of a row from `at` on, those past its end; 8: none is read.
@@ -46,7 +50,7 @@ inline bool any_rows(int64_t ld, int64_t rows, int64_t cols) {
 }
 
 inline ProductIn as_it_is(const void* p, int64_t ld, int64_t rows, int64_t cols) {
-    return ProductIn{p, rows <= 1 ? padded(cols) : ld, cols};
+    return ProductIn{p, rows <= 1 ? padded(cols) : ld, cols, 0};
 }
 
 // The operand as the product reads it; `anew` says how it is laid out at `room`
@@ -61,20 +65,20 @@ inline ProductIn operand(const void* p, int64_t ld, int64_t rows, int64_t cols, 
         return as_it_is(p, ld, rows, cols);
     }
     anew = PadRows{p, room, ld, padded(cols), rows, cols};
-    return ProductIn{room, padded(cols), padded(cols)};
+    return ProductIn{room, padded(cols), padded(cols), 0};
 }
 
 // What the backward pass's products read: dx from dz and w, dw from dz and x.
 struct GradShape {
     const void *dy, *x, *w;
     int64_t M, N, K, ld_dy, ld_x, ld_w;
-    bool act, want_dx, want_dw;
+    bool act, two_parts, want_dx, want_dw;
     bool dx_takes_any, dw_takes_any;
     char *x_room, *w_room, *dz_room;
 };
 
 struct GradIn {
-    bool dz_anew;  // dz is written to dz_room first
+    bool dz_anew;  // dz is written to dz_room first (its parts one behind the other)
     ProductIn dz, x, w;
     PadRows x_anew, w_anew;
     bool dx_any, dw_any;
@@ -88,7 +92,8 @@ inline GradIn grad_operands(const GradShape& s) {
                 (s.act || (!chunks && (!any_rows(s.ld_dy, s.M, s.N) ||
                                        (s.want_dx && !s.dx_takes_any) ||
                                        (s.want_dw && !s.dw_takes_any))));
-    g.dz = g.dz_anew ? ProductIn{s.dz_room, padded(s.N), padded(s.N)}
+    const int64_t rest = s.two_parts ? 2 * s.M * padded(s.N) : 0;
+    g.dz = g.dz_anew ? ProductIn{s.dz_room, padded(s.N), padded(s.N), rest}
                      : as_it_is(s.dy, s.ld_dy, s.M, s.N);
     g.dx_any = g.dw_any = !g.dz_anew && !chunks;
     if (s.want_dx)

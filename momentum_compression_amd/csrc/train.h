@@ -182,6 +182,9 @@ struct ProductPlan {
 ProductPlan product_plan(int64_t rows, int64_t cols, int64_t depth, bool cols_by_rows,
                          bool rows_by_rows);
 
+// The summed index's extent with an operand of two parts.
+int64_t product_depth(int64_t depth, bool two);
+
 // Whether the division's kernels take operands that lie anywhere; the larger tiles,
 // whose work is worth a copy of the operands, take rows of whole 16-byte chunks.
 bool product_any(const ProductPlan& plan);
@@ -204,14 +207,18 @@ hipError_t launch_product_few(int32_t dtype, const ProductIn& cols_in, const Pro
 // Two matrices in one launch.
 hipError_t launch_pad_rows(const PadRows& one, const PadRows& two, hipStream_t st);
 
-// dz = dy act'(pre), rounded to the element type, into `dz` (rows of `padded`
-// elements, zeros at their end) where given, and its unrounded sums over parts of
-// the rows into partials [slope_parts][cols] where given.
+// Whether dz is a number of the element type.
+constexpr bool slope_exact(int32_t act) { return act == ONEBIT_NONE || act == ONEBIT_RELU; }
+
+// dz = dy act'(pre) into `dz` (rows of `padded` elements, zeros at their end) where
+// given, rounded to the element type or, with `rest` bytes to the second, in two parts
+// of it, and its unrounded sums over parts of the rows into partials
+// [slope_parts][cols] where given.
 struct SlopeArgs {
     const void *dy, *pre;
     void* dz;
     float* partials;
-    int64_t rows, cols, ld_dy, ld_pre, padded;
+    int64_t rows, cols, ld_dy, ld_pre, padded, rest;
     int32_t act, dtype;
 };
 int64_t slope_parts(int64_t rows, int64_t cols);

@@ -81,7 +81,7 @@ class LinearArgs(ctypes.Structure):
         ("residual", _c_p), ("pre", _c_p), ("y", _c_p), ("ld_residual", _c_i64),
         ("ld_pre", _c_i64), ("ld_y", _c_i64), ("bias_dtype", _c_i32), ("dw_dtype", _c_i32),
         ("dy", _c_p), ("dx", _c_p), ("dw", _c_p), ("dbias", _c_p), ("ld_dy", _c_i64),
-        ("ld_dx", _c_i64), ("ld_dw", _c_i64), ("accumulate", _c_i32),
+        ("ld_dx", _c_i64), ("ld_dw", _c_i64), ("accumulate", _c_i32), ("round_dz", _c_i32),
     ]
 
 
@@ -735,7 +735,7 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # linear_args as one packing (its size and offsets are checked against the
 # declaration by the tests)
-_LINEAR = struct.Struct("<2i3q2Q2q4Q3q2i4Q3qi4x")
+_LINEAR = struct.Struct("<2i3q2Q2q4Q3q2i4Q3q2i")
 
 
 def _activation(name: str) -> int:
@@ -791,17 +791,21 @@ def linear_forward(x, w, y, bias=None, activation: str = "none", residual=None, 
     rp = _matrix(residual, out, dt, dev, "residual")
     _, bp, b_code = _params(None, bias, N, code)
     a = _LINEAR.pack(code, _activation(activation), M, N, K, xp[0], wp[0], xp[1], wp[1], bp or 0,
-                     rp[0], pp[0], yp[0], rp[1], pp[1], yp[1], b_code, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+                     rp[0], pp[0], yp[0], rp[1], pp[1], yp[1], b_code, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+                     0)
     _check("linear_forward", load().linear_forward(
         a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(stream, x, bias, ws)))
 
 
 def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, activation: str = "none", pre=None,
-                    accumulate: bool = False, ws=None, stream=None) -> None:
+                    accumulate: bool = False, ws=None, stream=None,
+                    round_dz: bool = False) -> None:
     """dx [M, K], dw [N, K] (float32 or the elements' type) and dbias [N] float32,
     each where given, from dy [M, N] and, with an activation, the forward call's
-    pre; accumulate adds dw and dbias to what they hold."""
+    pre; accumulate adds dw and dbias to what they hold; round_dz rounds
+    dy act'(pre) to the elements' type before the products, which halves their
+    time."""
     M, N, K, code = _linear_sizes(x, w, "x")
     dt, dev, out = x.dtype, x.get_device(), (M, N)
     act = _activation(activation)
@@ -818,7 +822,7 @@ def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, activation: str = "n
     dwp = _matrix(dw, w.shape, dw.dtype if dw is not None else dt, dev, "dw")
     a = _LINEAR.pack(code, act, M, N, K, xp[0], wp[0], xp[1], wp[1], 0, 0, pp[0], 0, 0, pp[1], 0,
                      0, dw_code, gp[0], dxp[0], dwp[0], _buf(dbias, N, "f32", "dbias") or 0, gp[1],
-                     dxp[1], dwp[1], 1 if accumulate else 0)
+                     dxp[1], dwp[1], 1 if accumulate else 0, 1 if round_dz else 0)
     _check("linear_backward", load().linear_backward(
         a, _buf(ws, 0, "u8", "ws"), _nbytes(ws) if ws is not None else 0,
         _stream_of(stream, x, dbias, ws)))

@@ -32,8 +32,8 @@ def test_the_check_sees_reads_in_front(tmp_path):
     """With rows laid out anew taken for as long as the matrix's own, reads start in
     front of them, and the check says so."""
     text = open(os.path.join(B.CSRC, "operands.h")).read()
-    short = text.replace("ProductIn{room, padded(cols), padded(cols)}",
-                         "ProductIn{room, padded(cols), cols}")
+    short = text.replace("ProductIn{room, padded(cols), padded(cols)",
+                         "ProductIn{room, padded(cols), cols")
     assert short != text
     (tmp_path / "operands.h").write_text(short)
     res = run(tmp_path, str(tmp_path))

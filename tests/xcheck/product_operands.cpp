@@ -51,7 +51,7 @@ int main() {
                         // what is padded by one starts on no 16 bytes
                         GradShape s = {on16(mem[0]) + 2 * (d == 1), on16(mem[1]) + 2 * (a == 1),
                                        on16(mem[2]) + 2 * (b == 1), M, N, K, N + pads[d],
-                                       K + pads[a], K + pads[b], (how & 1) != 0, (how & 2) != 0, (how & 4) != 0,
+                                       K + pads[a], K + pads[b], (how & 1) != 0, false, (how & 2) != 0, (how & 4) != 0,
                                        (how & 8) != 0, (how & 16) != 0, xr, wr, zr};
                         const GradIn g = grad_operands(s);
                         snprintf(what, sizeof(what), "M %ld N %ld K %ld layout %d how %d", (long)M,
