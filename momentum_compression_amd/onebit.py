@@ -838,7 +838,10 @@ class AdamWPlan:
     contiguous shape; x float32, g one type of float32, bfloat16 and float16,
     copies (or None) one of the 16-bit types; m and v float32, or 8-bit values
     (uint8, or float8_e4m3fn and float8_e5m2) with a float32 scale for each 256
-    elements."""
+    elements.  A plan may be dropped while a step on any stream still reads it (a
+    captured step needs it for as long as it is replayed); a stream given as a raw
+    handle outlives the plan.  Of the tensors, those of another stream than the step's
+    are the caller's to keep until the step is done."""
 
     def __init__(self, x, g, m, v, m_scale=None, v_scale=None, copies=None, lr_scale=None,
                  weight_decay=None):
@@ -895,6 +898,17 @@ class AdamWPlan:
         _check("adamw_plan", load().adamw_plan(table, n, self.state_bits, self.g_dtype,
                                                self.copy_dtype, room.data_ptr(), nbytes))
         self.plan = room.to(f"cuda:{dev}")
+        # streams that the allocator knows to use the plan: the one it was made on
+        self._streams = {torch._C._cuda_getCurrentRawStream(dev)}
+
+    def _used_on(self, stream: int) -> None:
+        """Before a step on a raw stream: the plan's memory, once dropped, is not given
+        to others until that stream's work at that time is done."""
+        import torch
+
+        if stream not in self._streams:
+            self.plan.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+            self._streams.add(stream)
 
 
 def adamw_step(plan: AdamWPlan, lr: float, beta1: float, beta2: float, eps: float, step: int,
@@ -902,7 +916,9 @@ def adamw_step(plan: AdamWPlan, lr: float, beta1: float, beta2: float, eps: floa
     """One step of AdamW on the plan's tensors; step counts from 1."""
     if not 1 <= step < 1 << 32:
         raise ValueError(f"step = {step} does not lie in 1 ... 2^32 - 1")
+    on = _stream_of(stream, plan.plan, grad_scale)
+    plan._used_on(on)
     _check("adamw_step", load().adamw_step(
         plan.plan.data_ptr(), plan.n_tensors, plan.tiles, plan.state_bits, plan.g_dtype,
         plan.copy_dtype, lr, beta1, beta2, eps, step, seed & 0xFFFFFFFFFFFFFFFF,
-        _buf(grad_scale, 1, "f32", "grad_scale"), _stream_of(stream, plan.plan, grad_scale)))
+        _buf(grad_scale, 1, "f32", "grad_scale"), on))

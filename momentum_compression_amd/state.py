@@ -460,8 +460,9 @@ class AdamW:
         return state
 
     def set_grads(self, grads) -> None:
-        """Take the gradients from other tensors from now on (a new plan; a captured
-        step still reads the old one, which its owner keeps)."""
+        """Take the gradients from other tensors from now on, whatever steps are still
+        under way on any stream (a new plan; a captured step still reads the old one,
+        which its owner keeps)."""
         grads = list(grads)
         self.plan = ob.AdamWPlan(self.params, grads, self.m, self.v, self.m_scale, self.v_scale,
                                  self.copies, self.lr_scale, self.weight_decay)

@@ -3,6 +3,7 @@ far as the C ABI decides them before any HIP call (the fake addresses are never
 dereferenced)."""
 
 import pytest
+import torch
 
 from momentum_compression_amd import onebit as ob
 from tests.test_block_refusals import P, _linear_args
@@ -21,3 +22,34 @@ def test_round_dz_is_a_truth_value(lib):
     for good in (0, 1):
         assert lib.linear_backward(_linear_args(round_dz=good), None, 0,
                                    None) == ob.ONEBIT_E_WORKSPACE
+
+
+def test_a_plan_is_known_on_the_streams_of_its_steps(monkeypatch):
+    """The allocator is told of each stream but the plan's own, once, before the step
+    is enqueued."""
+    said = []
+
+    class Memory:
+        def record_stream(self, stream):
+            said.append(("record", stream))
+
+        def data_ptr(self):
+            return P
+
+    class Lib:
+        @staticmethod
+        def adamw_step(*args):
+            said.append(("step", args[-1]))
+            return ob.ONEBIT_OK
+
+    plan = object.__new__(ob.AdamWPlan)
+    plan.plan, plan.device, plan._streams = Memory(), 0, {7}
+    plan.n_tensors = plan.tiles = 1
+    plan.state_bits, plan.g_dtype, plan.copy_dtype = 32, 0, 0
+    monkeypatch.setattr(ob, "load", lambda: Lib)
+    monkeypatch.setattr(ob, "_stream_of", lambda stream, *tensors: stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: (raw, device))
+    for on in (7, 9, 9, 8, 7):
+        ob.adamw_step(plan, 1e-3, 0.9, 0.99, 1e-8, 1, stream=on)
+    assert said == [("step", 7), ("record", (9, 0)), ("step", 9), ("step", 9),
+                    ("record", (8, 0)), ("step", 8), ("step", 7)]
