@@ -691,7 +691,7 @@ typedef enum {
  * With round_dz = 1 they take it rounded once to the element type: about half the products'
  * time, for as much error again as the rounding of a 16-bit dx or dw, and infinite
  * where dz passes F16's range.  dbias takes dz unrounded.  pre is read with an
- * activation only.
+ * activation only, x for dw and w for dx only: what is not read may be anything.
  *
  * x, dx [M][K], w, dw [N][K], y, pre, residual, dy [M][N]: rows ld_* elements
  * apart (ld >= the row's length, up to 2^40), aligned to their element.  M up to

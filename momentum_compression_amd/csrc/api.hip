@@ -1126,8 +1126,9 @@ int linear_backward(const linear_args* a, void* ws, size_t ws_bytes, hipStream_t
                    (st = check_matrix(a->dx, a->ld_dx, M, K, 2)))))
         return st;
     if (!aligned(a->dbias, 4)) return ONEBIT_E_ALIGN;
+    // what is not read may be anything, its ld too
     const Matrix dy{a->dy, a->ld_dy, M, N, 2}, pre{act ? a->pre : nullptr, a->ld_pre, M, N, 2},
-        x{a->x, a->ld_x, M, K, 2}, w{a->w, a->ld_w, N, K, 2}, dx{a->dx, a->ld_dx, M, K, 2},
+        x{a->dw ? a->x : nullptr, a->ld_x, M, K, 2}, w{a->dx ? a->w : nullptr, a->ld_w, N, K, 2}, dx{a->dx, a->ld_dx, M, K, 2},
         dw{a->dw, a->ld_dw, N, K, dw_size}, db{a->dbias, N, 1, N, 4};
     for (const Matrix& in : {dy, pre, x, w})
         if (lies_over(dx, in) || lies_over(dw, in) || lies_over(db, in)) return ONEBIT_E_ARG;

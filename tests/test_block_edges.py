@@ -53,3 +53,15 @@ def test_a_plan_is_known_on_the_streams_of_its_steps(monkeypatch):
         ob.adamw_step(plan, 1e-3, 0.9, 0.99, 1e-8, 1, stream=on)
     assert said == [("step", 7), ("record", (9, 0)), ("step", 9), ("step", 9),
                     ("record", (8, 0)), ("step", 8), ("step", 7)]
+
+
+def test_linear_backward_takes_anything_for_what_it_does_not_read(lib):
+    """x without dw and w without dx, and their strides, are not looked at (the
+    workspace, which is checked last, stops these calls)."""
+    for kw in (dict(dw=None, ld_x=0), dict(dx=None, ld_w=0), dict(dx=None, dw=None, ld_x=0, ld_w=0),
+               dict(dw=None, ld_x=-24), dict(dx=None, w=7 * P - 64, ld_w=1),
+               dict(dw=None, x=5 * P + 2), dict(dx=None, w=6 * P + 1), dict(dx=None, w=7 * P)):
+        assert lib.linear_backward(_linear_args(**kw), None, 0, None) == ob.ONEBIT_E_WORKSPACE, kw
+    # what is read is looked at
+    for kw in (dict(x=5 * P + 2), dict(w=6 * P + 2), dict(dw=None, w=5 * P), dict(dx=None, x=6 * P)):
+        assert lib.linear_backward(_linear_args(**kw), None, 0, None) == ob.ONEBIT_E_ARG, kw
