@@ -420,29 +420,32 @@ __global__ __launch_bounds__(norm_threads<G>(), 2) void layer_norm_grad_kernel(N
 // a part of the rows, then dx with a workgroup a row.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void layer_norm_grad_cols_kernel(NormArgs a, int64_t strips,
+                                                                        int64_t parts,
                                                                         int64_t rows_of_part) {
-    const int64_t c = 8 * ((int64_t)(blockIdx.x % strips) * kThreads + threadIdx.x);
-    const int64_t part = blockIdx.x / strips, cols = a.cols;
-    if (c >= cols) return;
-    const int64_t end = (part + 1) * rows_of_part < a.rows ? (part + 1) * rows_of_part : a.rows;
-    float dw[8] = {}, db[8] = {};
-    for (int64_t row = part * rows_of_part; row < end; ++row) {
-        const Part<T> xv = load_part((const T*)a.x + row * a.ld_x, c, cols);
-        const Part<T> gv = load_part((const T*)a.dy + row * a.ld_dy, c, cols);
-        const float mean = a.mean[row], rstd = a.rstd[row];
+    const int64_t cols = a.cols;
+    for (int64_t block = blockIdx.x; block < strips * parts; block += gridDim.x) {
+        const int64_t c = 8 * (block % strips * kThreads + threadIdx.x), part = block / strips;
+        if (c >= cols) continue;
+        const int64_t end = (part + 1) * rows_of_part < a.rows ? (part + 1) * rows_of_part : a.rows;
+        float dw[8] = {}, db[8] = {};
+        for (int64_t row = part * rows_of_part; row < end; ++row) {
+            const Part<T> xv = load_part((const T*)a.x + row * a.ld_x, c, cols);
+            const Part<T> gv = load_part((const T*)a.dy + row * a.ld_dy, c, cols);
+            const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = gv[e];
+                dw[e] = __builtin_fmaf(g, (xv[e] - mean) * rstd, dw[e]);
+                db[e] += g;
+            }
+        }
+        float* to = a.partials + part * 2 * cols;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float g = gv[e];
-            dw[e] = __builtin_fmaf(g, (xv[e] - mean) * rstd, dw[e]);
-            db[e] += g;
+            if (c + e >= cols) break;
+            to[c + e] = dw[e];
+            to[cols + c + e] = db[e];
         }
-    }
-    float* to = a.partials + part * 2 * cols;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (c + e >= cols) break;
-        to[c + e] = dw[e];
-        to[cols + c + e] = db[e];
     }
 }
 
@@ -496,28 +499,31 @@ __global__ __launch_bounds__(1024) void column_join_kernel(const float* partials
                                                            int64_t n, int64_t cols, float* out0,
                                                            float* out1, bool accumulate) {
     __shared__ double sums[16][64];
-    const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-    const int wave = threadIdx.x >> 6;
-    double t = 0.0;
-    if (c < n) {
-        int64_t p = wave;
-        for (; p + 7 * 16 < parts; p += 8 * 16) {  // eight loads at once
-            float v[8];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < n; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + lane;
+        double t = 0.0;
+        if (c < n) {
+            int64_t p = wave;
+            for (; p + 7 * 16 < parts; p += 8 * 16) {  // eight loads at once
+                float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = partials[(p + 16 * k) * n + c];
+                for (int k = 0; k < 8; ++k) v[k] = partials[(p + 16 * k) * n + c];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t += v[k];
+                for (int k = 0; k < 8; ++k) t += v[k];
+            }
+            for (; p < parts; p += 16) t += partials[p * n + c];
         }
-        for (; p < parts; p += 16) t += partials[p * n + c];
+        sums[wave][lane] = t;
+        __syncthreads();
+        float* out = c < cols ? out0 : out1;
+        if (wave == 0 && c < n && out) {
+            for (int w = 1; w < 16; ++w) t += sums[w][lane];
+            const int64_t at = c < cols ? c : c - cols;
+            out[at] = (float)(accumulate ? (double)out[at] + t : t);
+        }
+        __syncthreads();  // the sums are read
     }
-    sums[wave][threadIdx.x & 63] = t;
-    __syncthreads();
-    if (wave != 0 || c >= n) return;
-    for (int w = 1; w < 16; ++w) t += sums[w][threadIdx.x];
-    float* out = c < cols ? out0 : out1;
-    if (!out) return;
-    const int64_t at = c < cols ? c : c - cols;
-    out[at] = (float)(accumulate ? (double)out[at] + t : t);
 }
 
 template <typename F>
@@ -556,6 +562,8 @@ Shape shape_of(int64_t rows, int64_t cols, bool grad) {
 // of them 16384 x 2048 takes 49, 53 and 64 us.
 constexpr int64_t kForwardBlocks = 4096, kNormBlocks = 512;
 constexpr int64_t kLongParts = 64;        // parts of the rows, at most
+// a launch holds fewer than 2^32 threads, of 1024 a workgroup at most
+constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
 template <typename F>
 void with_shape(const Shape& s, F&& f) {
@@ -592,8 +600,9 @@ int64_t norm_parts(int64_t rows, int64_t cols) {
 
 hipError_t launch_column_join(const float* partials, int64_t parts, int64_t n, int64_t cols,
                               float* out0, float* out1, bool accumulate, hipStream_t st) {
-    hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, st,
-                       partials, parts, n, cols, out0, out1, accumulate);
+    const int64_t groups = (n + 63) / 64;
+    hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)(groups < kMostBlocks ? groups : kMostBlocks)),
+                       dim3(1024), 0, st, partials, parts, n, cols, out0, out1, accumulate);
     return hipGetLastError();
 }
 
@@ -634,8 +643,10 @@ hipError_t launch_layer_norm_grad(const NormArgs& a, float* dweight, float* dbia
             if (a.partials) {
                 const int64_t strips = (a.cols + 8 * kThreads - 1) / (8 * kThreads);
                 const int64_t rows_of_part = (a.rows + parts - 1) / parts;
-                hipLaunchKernelGGL((layer_norm_grad_cols_kernel<T>), dim3((unsigned)(strips * parts)),
-                                   dim3(kThreads), 0, st, a, strips, rows_of_part);
+                const int64_t blocks = strips * parts;
+                hipLaunchKernelGGL((layer_norm_grad_cols_kernel<T>),
+                                   dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)),
+                                   dim3(kThreads), 0, st, a, strips, parts, rows_of_part);
             }
             if (a.dx)
                 hipLaunchKernelGGL((layer_norm_grad_rows_kernel<T>),
