@@ -79,13 +79,16 @@ __device__ __forceinline__ float root_of(float v) {
 }
 
 // m / d, correctly rounded, where neither they nor the quotient come near the ends
-// of the range: the usual sequence without its scaling.
+// of the range.  The reciprocal is brought to half a step or so by one step of Newton's
+// iteration, and the quotient by two corrections with its exact remainder (Markstein's
+// method of division by fused multiply-adds).  With the remainder's sign the other way
+// round a quotient of -0 stays one.
 __device__ __forceinline__ float quotient_of(float m, float d) {
     const float y0 = __builtin_amdgcn_rcpf(d);
     const float y = __builtin_fmaf(__builtin_fmaf(-d, y0, 1.0f), y0, y0);
     float q = m * y;
-    q = __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
-    return __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
+    q = __builtin_fmaf(-__builtin_fmaf(d, q, -m), y, q);
+    return __builtin_fmaf(-__builtin_fmaf(d, q, -m), y, q);
 }
 
 // Four consecutive elements at any element address, `n` of them there.  Past the
