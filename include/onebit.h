@@ -670,7 +670,7 @@ typedef enum {
     ONEBIT_NONE = 0,       /* z                                               */
     ONEBIT_RELU = 1,       /* max(z, 0), slope 0 at 0                         */
     ONEBIT_GELU = 2,       /* z Phi(z), Phi the normal distribution's integral
-                              (to 1e-7)                                       */
+                              (to 2e-7, below 0 also to 2e-5 of itself)       */
     ONEBIT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
     ONEBIT_SILU = 4        /* z / (1 + exp(-z))                               */
 } onebit_activation;
