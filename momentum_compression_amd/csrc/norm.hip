@@ -565,7 +565,8 @@ constexpr int64_t kLongParts = 64;        // parts of the rows, at most
 // a launch holds fewer than 2^32 threads, of 1024 a workgroup at most
 constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
-template <typename F>
+// f with a shape that shape_of gives for the pass.
+template <bool GRAD, typename F>
 void with_shape(const Shape& s, F&& f) {
     auto is = [&](int G, int V) { return s.G == G && s.V == V; };
 #define ONEBIT_SHAPE(G, V) \
@@ -575,12 +576,15 @@ void with_shape(const Shape& s, F&& f) {
     ONEBIT_SHAPE(16, 1);
     ONEBIT_SHAPE(64, 1);
     ONEBIT_SHAPE(64, 2);
-    ONEBIT_SHAPE(64, 4);
     ONEBIT_SHAPE(256, 1);
     ONEBIT_SHAPE(256, 2);
-    ONEBIT_SHAPE(256, 4);
-    ONEBIT_SHAPE(1024, 1);
-    ONEBIT_SHAPE(1024, 2);
+    if constexpr (GRAD) {
+        ONEBIT_SHAPE(1024, 1);
+    } else {
+        ONEBIT_SHAPE(64, 4);
+        ONEBIT_SHAPE(256, 4);
+        ONEBIT_SHAPE(1024, 2);
+    }
 #undef ONEBIT_SHAPE
 }
 
@@ -616,7 +620,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st) {
                                a);
             return;
         }
-        with_shape(s, [&](auto G, auto V) {
+        with_shape<false>(s, [&](auto G, auto V) {
             hipLaunchKernelGGL((layer_norm_kernel<T, G.value, V.value>),
                                dim3((unsigned)row_blocks(s, a.rows, kForwardBlocks)),
                                dim3(norm_threads<G.value>()), 0, st, a);
@@ -633,7 +637,7 @@ hipError_t launch_layer_norm_grad(const NormArgs& a, float* dweight, float* dbia
         e = with_type(a.dtype, [&](auto t) {
             using T = decltype(t);
             if (s.G) {
-                with_shape(s, [&](auto G, auto V) {
+                with_shape<true>(s, [&](auto G, auto V) {
                     hipLaunchKernelGGL((layer_norm_grad_kernel<T, G.value, V.value>),
                                        dim3((unsigned)parts), dim3(norm_threads<G.value>()), 0, st,
                                        a);
