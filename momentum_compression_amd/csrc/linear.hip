@@ -306,7 +306,7 @@ constexpr size_t product_lds(bool ahead) {
 // part and half among those of the next: a burst of loads would hold up the waves,
 // as the loads of a CU pass at 64 bytes a cycle.  (8192^3 bf16: 814 to 850 us, 1290 to
 // 1350 TFLOP/s, the matrix unit busy three quarters of the time; 8192 x 4096 over 1024:
-// 69 to 73 us; with a GELU and `pre` 86, as nothing runs beside the epilogue of a CU's
+// 69 to 73 us; with a GELU and `pre` 86 to 92, as nothing runs beside the epilogue of a CU's
 // one workgroup.)  With both operands by rows tiles
 // go from memory to LDS directly.  Transposing reads are not told apart from such
 // loads by the compiler, which waits for all of them before the first read; with
@@ -778,8 +778,10 @@ __device__ __forceinline__ void two_parts(float d, f16& first, f16& rest) {
     rest = (f16)(d - (float)first);
 }
 
-// A thread has eight columns of a part of the rows.  Bound by the slope's arithmetic
-// as much as by the bytes (8192 x 4096 with a GELU: 47 us, 31 for its 201 MB).
+// A thread has eight columns of a part of the rows.  8192 x 4096 with a GELU takes 59 us
+// with dz in two parts (268 MB, 41 us at a copy's rate) and 47 rounded (201 MB, 31).
+// The vector unit is busy half of either time (instructions counted, one a cycle and CU)
+// and waves wait two thirds of theirs: bound by the loads under way.
 template <typename T, int ACT, bool TWO>
 __global__ __launch_bounds__(kThreads) void slope_kernel(SlopeArgs a, int64_t groups,
                                                          int64_t rows_of_part) {
@@ -982,7 +984,7 @@ hipError_t launch_pad_rows(const PadRows& one, const PadRows& two, hipStream_t s
 int64_t slope_parts(int64_t rows, int64_t cols) {
     const int64_t strips = tiles_of(tiles_of(cols, 8), kThreads);
     // the parts' column sums are joined, so few parts, and about four workgroups a CU:
-    // the backward pass of 8192 x 4096 x 1024 with a GELU 207 us, 210 with 2048
+    // the backward pass of 8192 x 4096 x 1024 with a GELU, dz rounded, 207 us, 210 with 2048
     // workgroups and half the rows read ahead, 223 with 4096
     int64_t parts = strips > 0 ? 1024 / strips : 1;
     if (parts > tiles_of(rows, 4)) parts = tiles_of(rows, 4);

@@ -8,8 +8,8 @@
 // than that holds are read again for each pass.
 //
 // Measured: forward 8192 x 1024 bf16 10.1 us (33.6 MB, 3.3 TB/s: two rounds of loads
-// and their latency), backward 16384 x 2048 bf16 44 us and 5.6 for the join (201 MB),
-// 16411 x 1003 float32 41 and 4.8 (198 MB): 4.6 to 4.8 TB/s.
+// and their latency), backward 16384 x 2048 bf16 44 us and 5 for the join (201 MB),
+// 16411 x 1003 float32 41 and 4.7 (198 MB): 4.6 to 4.8 TB/s.
 #include <type_traits>
 
 #include "train.h"

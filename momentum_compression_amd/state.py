@@ -470,7 +470,8 @@ class AdamW:
 
     def step(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
-        """One step; grad_scale (a device float) multiplies the gradients first."""
+        """One step; grad_scale (a device float) multiplies the gradients first.  A
+        captured step repeats its own number, lr and rounding draws at each replay."""
         ob.adamw_step(self.plan, lr, beta1, beta2, eps, self.steps + 1, seed=self.seed,
                       grad_scale=grad_scale, stream=stream)
         self.steps += 1
